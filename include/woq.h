@@ -88,8 +88,8 @@ typedef enum woq_status {
   WOQ_ERR_INTERNAL = 4
 } woq_status;
 
-/* Activation / output element type. */
-typedef enum woq_dtype { WOQ_F16 = 0, WOQ_BF16 = 1 } woq_dtype;
+/* Activation / output element type (WOQ_F32 only where an entry point says so). */
+typedef enum woq_dtype { WOQ_F16 = 0, WOQ_BF16 = 1, WOQ_F32 = 2 } woq_dtype;
 
 /* Layout version produced and consumed by this library (WOQ_LAYOUT_V2). */
 int32_t woq_layout_version(void);
@@ -284,6 +284,71 @@ woq_status woq_gptq_quantize_pack(const void* X, const void* W, int64_t T, int64
                                   int32_t bits, int32_t group_size, int32_t asymmetric, double damp,
                                   void* packed, void* scales, void* zeros,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Microscaled 4-bit floats (MXFP4, the OCP Microscaling Formats' MXFP4).
+ *
+ * Format of a matrix [M, K], K % 32 == 0.  32 consecutive elements of a row
+ * share one scale byte b, standing for 2^(b - 127) (255: the block is not a
+ * number); an element is a 4-bit float e2m1: bit 3 the sign, the low three
+ * bits 0 .. 7 the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   codes : uint8 [M, K/2], element k in byte k / 2, even k in the low nibble
+ *   scales: uint8 [M, K/32]
+ * Quantization of a block x:
+ *   b    = clamp(floor(log2 max|x|) - 2 + 127, 0, 254); 0 for a zero block
+ *   code = the value nearest to x / 2^(b - 127), ties to the even code,
+ *          magnitudes above 6 to 6; the sign is kept, a zero's too
+ * A block with an infinity or a NaN gives b = 255 and zero codes.
+ *
+ * For these entry points: codes, X and Y 16-byte aligned, scales of any
+ * alignment, everything else as for the calls above.  A block with b = 255
+ * makes every output that it takes part in a NaN. */
+
+/* x [M, K] of xdtype (WOQ_F16 or WOQ_BF16) -> codes, scales (weights or
+ * activations). */
+woq_status woq_mxfp4_quantize(const void* x, int32_t xdtype, int64_t M, int64_t K, void* codes, void* scales,
+                              void* stream);
+
+/* out [M, K] of outdtype (WOQ_F16, WOQ_BF16 or WOQ_F32): the values that codes
+ * and scales stand for.  Exact in fp32 and bf16 where they are in range; fp16
+ * rounds once (to nearest, ties to even). */
+woq_status woq_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, int32_t outdtype,
+                                void* out, void* stream);
+
+/* Y[m, n] = sum_k X[m, k] w[n, k] for microscaled weights w [N, K] and 16-bit
+ * X [M, K]; Y [M, N] of X's type, fp32 sums, rounded once.  M = 1 with
+ * K <= 16384 uses X as given.  Otherwise X is split, 32 elements at a time,
+ * into three 6-bit floats that hold each element to within 2^-13.9 of its
+ * block's largest magnitude (and 2^-126 where the block is below 2^-112).
+ *   workspace : device scratch of woq_mxfp4_gemm_workspace_bytes(M, N, K)
+ *               bytes, 256-byte aligned (NULL where that is 0; it is 0 for
+ *               invalid sizes too). */
+size_t woq_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+woq_status woq_mxfp4_gemm(const void* X, int32_t xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
+                          int64_t K, void* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Y[m, n] = sum_k a[m, k] w[n, k] for microscaled a [M, K] and w [N, K]; exact
+ * products, fp32 sums, Y [M, N] of ydtype (WOQ_F16 or WOQ_BF16) rounded once. */
+woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const void* codes, const void* scales,
+                             int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream);
+
+/* A mixture-of-experts layer on a few tokens (T <= 64, E <= 512):
+ *   logits[t, e] = sum_k X[t, k] router[e, k]   (fp32)
+ *   S(t)   = the top_k experts of t by descending logit, the lower index first
+ *            among equals (a NaN comes last)
+ *   p[t,e] = exp(logits[t, e]) / sum over S(t) of exp(logits[t, .])
+ *   h      = silu(X[t] . up[e, i]) (X[t] . up[e, I + i]),  silu(g) = g / (1 + exp(-g))
+ *   Y[t]   = sum over S(t) of p[t, e] sum_i h[t, e, i] down[e, ., i]
+ *   X [T, H], router [E, H], Y [T, H] of xdtype; up microscaled [E, 2 I, H]
+ *   (rows 0 .. I-1 gate, I .. 2I-1 up), down microscaled [E, H, I]; H and I
+ *   multiples of 32.
+ * X and p h are split into 6-bit pieces as in woq_mxfp4_gemm; sums over k and
+ * i, and the sum over experts, are fp32, Y is rounded once.  No atomics: the
+ * same inputs give the same bits.  workspace as above. */
+size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E);
+woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, const void* up_codes,
+                         const void* up_scales, const void* down_codes, const void* down_scales, int64_t T, int64_t H,
+                         int64_t I, int64_t E, int32_t top_k, void* Y, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 /* Measurement aids.  Not part of the method: they measure the ceilings the
  * quantized kernels are compared with.  A decode GEMV reads its weights once

@@ -20,6 +20,7 @@ WOQ_ERR_HIP = 3
 WOQ_ERR_INTERNAL = 4
 WOQ_F16 = 0
 WOQ_BF16 = 1
+WOQ_F32 = 2
 WOQ_LAYOUT_V2 = 2
 
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -50,6 +51,13 @@ SIGNATURES = {
     "woq_gptq_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "woq_gptq_quantize_pack": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, ctypes.c_double, _vp, _vp, _vp,
                                       _vp, _sz, _vp]),
+    "woq_mxfp4_quantize": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp]),
+    "woq_mxfp4_dequantize": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp]),
+    "woq_mxfp4_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "woq_mxfp4_gemm": (_i32, [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "woq_mxfp4_gemm_mx": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "woq_mxfp4_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "woq_mxfp4_moe": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     "woq_probe_stream_read": (_i32, [_vp, _sz, _i32, _i32, _i32, _vp, _i32, _vp]),
     "woq_probe_empty": (_i32, [_i32, _i32, _vp]),
     "woq_probe_mfma_rate": (_i32, [_vp, _i32, _i32, _vp, _i32, _vp]),

@@ -1,0 +1,182 @@
+// Microscaled 4-bit floats (MXFP4): quantization, its inverse, and the split
+// of 16-bit activations into 6-bit pieces for the products.
+//
+// Quantization of a block of 32 values x (format in mxfp4_device.h):
+//   b    = clamp(floor(log2 max|x|) - 2 + 127, 0, 254), 0 for a zero block
+//   code = the e2m1 value nearest to x / 2^(b - 127), ties to the even code,
+//          magnitudes above 6 to 6, the sign kept (a negative zero too)
+// A block holding an infinity or a NaN gets b = 255 and zero codes.  gfx950's
+// v_cvt_scalef32_pk_fp4_f32 does the scaling, rounding and saturation of two
+// elements in one instruction.
+//
+// Bound by memory: 2 + 0.5 + 1/32 bytes per element, a dozen VALU operations.
+// A lane takes 8 elements (one 16-byte load, one 4-byte store), four lanes a
+// block, so that loads and stores of a wave are contiguous.
+#include "mxfp4_device.h"
+#include "woq_internal.h"
+
+namespace woq {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Codes of 8 elements with scale byte b.  The 16-bit forms of the conversion
+// flush elements near the bottom of their type's range, so the elements go
+// through fp32, and blocks of scales below 2^-63 (bf16 only) are raised by 2^64
+// first, where no fp32 subnormal is left.  Both steps are exact.
+template <class XT>
+__device__ inline uint32_t to_fp4x8(u32x4_t w, uint32_t b) {
+  const bool low = b < 64u;
+  const float up = low ? 0x1p64f : 1.0f;
+  const float s = mx_pow2(low ? b + 64u : b);
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = XT::to_f32((uint16_t)(w[e] & 0xFFFFu)) * up;
+    v[2 * e + 1] = XT::to_f32((uint16_t)(w[e] >> 16)) * up;
+  }
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+  return c;
+}
+
+// units: 8-element pieces, a multiple of 4.
+template <class XT>
+__global__ __launch_bounds__(kThreads) void mxfp4_quantize_kernel(const u32x4_t* __restrict__ x, int64_t units,
+                                                                  uint32_t* __restrict__ codes,
+                                                                  uint8_t* __restrict__ scales) {
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < units; i += step) {
+    const u32x4_t w = x[i];
+    // the magnitudes of the 16-bit patterns order as the values do; a NaN is above infinity
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+      m = m > lo ? m : lo;
+      m = m > hi ? m : hi;
+    }
+    uint32_t o = (uint32_t)__shfl_xor((int)m, 1, 64);
+    m = m > o ? m : o;
+    o = (uint32_t)__shfl_xor((int)m, 2, 64);
+    m = m > o ? m : o;
+    const uint32_t b = mx_scale_byte(XT::to_f32((uint16_t)m));
+    const uint32_t c = to_fp4x8<XT>(w, b);
+    codes[i] = b == (uint32_t)kMxNan ? 0u : c;
+    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)b;
+  }
+}
+
+// out: 0 fp16, 1 bf16, 2 fp32.  The values are exact in bf16 and fp32 but for
+// an overflow (6 2^127); fp16 rounds what lies outside its range.
+template <int OUT>
+__global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32_t* __restrict__ codes,
+                                                                    const uint8_t* __restrict__ scales, int64_t units,
+                                                                    void* __restrict__ out) {
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < units; i += step) {
+    const uint32_t c = codes[i], b = scales[i >> 2];
+    const bool nan = b == (uint32_t)kMxNan;
+    const float s = nan ? 1.0f : mx_pow2(b);
+    if constexpr (OUT == 2) {
+      float2_t v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1),
+                       __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3)};
+      const float n = __builtin_bit_cast(float, 0x7FC00000u);
+      float4_t* const o = reinterpret_cast<float4_t*>(out) + 2 * i;
+      o[0] = nan ? float4_t{n, n, n, n} : float4_t{v[0][0], v[0][1], v[1][0], v[1][1]};
+      o[1] = nan ? float4_t{n, n, n, n} : float4_t{v[2][0], v[2][1], v[3][0], v[3][1]};
+    } else {
+      u32x4_t v;
+      if constexpr (OUT == 0) {
+        v = u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3))};
+      } else {
+        v = u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3))};
+      }
+      const uint32_t n2 = OUT == 0 ? 0x7E007E00u : 0x7FC07FC0u;
+      reinterpret_cast<u32x4_t*>(out)[i] = nan ? u32x4_t{n2, n2, n2, n2} : v;
+    }
+  }
+}
+
+// One wave per fragment of R rows x 2048 / R elements (layout in
+// mxfp4_device.h).
+template <class XT, int R>
+__global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* __restrict__ X, int M, int K,
+                                                               int ksteps, int frags, uint8_t* __restrict__ pieces,
+                                                               uint32_t* __restrict__ scales) {
+  const int f = (int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6);
+  if (f >= frags) return;
+  const int lane = threadIdx.x & 63;
+  const int row = (f / ksteps) * R + lane % R;
+  const int k = ((f % ksteps) * (64 / R) + lane / R) * kMxBlock;
+  float v[kMxBlock] = {};
+  if (row < M && k < K) mx_load_block<XT>(X + (int64_t)row * K + k, v);
+  const MxPieces s = mx_split(v);
+  mx_store_pieces(s, pieces + (int64_t)f * kMxFragBytes, scales + (int64_t)f * 64, lane);
+}
+
+unsigned grid_for(int64_t units) {
+  const int64_t b = (units + kThreads - 1) / kThreads;
+  return (unsigned)(b < 16384 ? b : 16384);
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_quantize(const void* x, int xdtype, int64_t M, int64_t K, void* codes, void* scales,
+                                 hipStream_t stream) {
+  const int64_t units = M * K / 8;
+  const auto* xp = static_cast<const u32x4_t*>(x);
+  auto* cp = static_cast<uint32_t*>(codes);
+  auto* sp = static_cast<uint8_t*>(scales);
+  if (xdtype == 0)
+    mxfp4_quantize_kernel<F16><<<grid_for(units), kThreads, 0, stream>>>(xp, units, cp, sp);
+  else
+    mxfp4_quantize_kernel<BF16><<<grid_for(units), kThreads, 0, stream>>>(xp, units, cp, sp);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, int outdtype,
+                                   void* out, hipStream_t stream) {
+  const int64_t units = M * K / 8;
+  const auto* cp = static_cast<const uint32_t*>(codes);
+  const auto* sp = static_cast<const uint8_t*>(scales);
+  if (outdtype == 0)
+    mxfp4_dequantize_kernel<0><<<grid_for(units), kThreads, 0, stream>>>(cp, sp, units, out);
+  else if (outdtype == 1)
+    mxfp4_dequantize_kernel<1><<<grid_for(units), kThreads, 0, stream>>>(cp, sp, units, out);
+  else
+    mxfp4_dequantize_kernel<2><<<grid_for(units), kThreads, 0, stream>>>(cp, sp, units, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_split(const void* X, int xdtype, int64_t M, int64_t K, int R, int64_t row_groups,
+                              int64_t ksteps, void* pieces, void* scales, hipStream_t stream) {
+  const int frags = (int)(row_groups * ksteps);
+  const unsigned grid = (unsigned)((frags + kThreads / 64 - 1) / (kThreads / 64));
+  const auto* xp = static_cast<const uint16_t*>(X);
+  auto* pp = static_cast<uint8_t*>(pieces);
+  auto* sp = static_cast<uint32_t*>(scales);
+  if (R == 32) {
+    if (xdtype == 0)
+      mxfp4_split_kernel<F16, 32><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
+    else
+      mxfp4_split_kernel<BF16, 32><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
+  } else {
+    if (xdtype == 0)
+      mxfp4_split_kernel<F16, 16><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
+    else
+      mxfp4_split_kernel<BF16, 16><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace woq

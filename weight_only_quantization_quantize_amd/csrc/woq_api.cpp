@@ -127,6 +127,65 @@ woq_status check_gptq(int64_t T, int64_t N, int64_t K, int32_t bits, int32_t gro
   return WOQ_OK;
 }
 
+// Sizes of a microscaled matrix [M, K].
+woq_status check_mxfp4_shape(int64_t M, int64_t K, const char* rows) {
+  if (M < 1) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s must be >= 1 (got %lld)", rows, (long long)M);
+  if (K < 32 || K % 32 != 0)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "the row length must be a positive multiple of 32 (got %lld)", (long long)K);
+  if (M > INT32_MAX / 2 || K > INT32_MAX / 2)
+    return fail(WOQ_ERR_UNSUPPORTED, "matrix too large for this library (%s=%lld, row length %lld)", rows,
+                (long long)M, (long long)K);
+  return WOQ_OK;
+}
+
+woq_status check_mxfp4_arrays(const void* codes, const void* scales, const char* name) {
+  if (!codes || !scales) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s codes and scales must not be NULL", name);
+  if (!aligned(codes, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s codes must be 16-byte aligned", name);
+  return WOQ_OK;
+}
+
+woq_status check_activations(const void* x, int32_t xdtype, const void* y) {
+  if (xdtype != WOQ_F16 && xdtype != WOQ_BF16)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "the element type must be WOQ_F16 or WOQ_BF16 (got %d)", xdtype);
+  if (!x || !y) return fail(WOQ_ERR_INVALID_ARGUMENT, "X and Y must not be NULL");
+  if (!aligned(x, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "X must be 16-byte aligned");
+  if (!aligned(y, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "Y must be 16-byte aligned");
+  return WOQ_OK;
+}
+
+woq_status check_workspace(const void* workspace, size_t workspace_bytes, size_t need) {
+  if (need == 0) return WOQ_OK;
+  if (!workspace || !aligned(workspace, 256))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "workspace too small (%zu bytes, need %zu)", workspace_bytes, need);
+  return WOQ_OK;
+}
+
+// The tile grid of a product: 2^16 - 1 tiles of 64 columns, and activations
+// whose fragments a 32-bit index counts.
+woq_status check_mxfp4_gemm(int64_t M, int64_t N, int64_t K) {
+  WOQ_TRY(check_mxfp4_shape(M, K, "M"));
+  WOQ_TRY(check_mxfp4_shape(N, K, "N"));
+  if (N > 65535 * (int64_t)64 || (M + 255) / 32 * (K / 64 + 2) > INT32_MAX)
+    return fail(WOQ_ERR_UNSUPPORTED, "product too large for this library (M=%lld, N=%lld, K=%lld)", (long long)M,
+                (long long)N, (long long)K);
+  return WOQ_OK;
+}
+
+woq_status check_mxfp4_moe(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k) {
+  WOQ_TRY(check_mxfp4_shape(T, H, "T"));
+  WOQ_TRY(check_mxfp4_shape(E, I, "E"));
+  if (top_k < 1 || top_k > E)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "top_k must be in [1, E] (got %d of %lld)", top_k, (long long)E);
+  if (T > woq::mxfp4_moe_max_tokens() || E > woq::mxfp4_moe_max_experts())
+    return fail(WOQ_ERR_UNSUPPORTED, "mxfp4_moe takes up to %d tokens and %d experts (got %lld, %lld)",
+                woq::mxfp4_moe_max_tokens(), woq::mxfp4_moe_max_experts(), (long long)T, (long long)E);
+  if (H > (1 << 20) || I > (1 << 20))
+    return fail(WOQ_ERR_UNSUPPORTED, "layer too large for this library (H=%lld, I=%lld)", (long long)H, (long long)I);
+  return WOQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -325,6 +384,86 @@ woq_status woq_gptq_quantize_pack(const void* X, const void* W, int64_t T, int64
   return from_hip(woq::launch_gptq(X, W, T, N, K, bits, group_size, asymmetric != 0, damp, packed, scales,
                                    zeros, workspace, static_cast<hipStream_t>(stream)),
                   "gptq launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_mxfp4_quantize(const void* x, int32_t xdtype, int64_t M, int64_t K, void* codes, void* scales,
+                              void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_mxfp4_shape(M, K, "M"));
+  if (xdtype != WOQ_F16 && xdtype != WOQ_BF16)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "xdtype must be WOQ_F16 or WOQ_BF16 (got %d)", xdtype);
+  if (!x || !aligned(x, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "x must be non-NULL and 16-byte aligned");
+  WOQ_TRY(check_mxfp4_arrays(codes, scales, "output"));
+  return from_hip(woq::launch_mxfp4_quantize(x, xdtype, M, K, codes, scales, static_cast<hipStream_t>(stream)),
+                  "mxfp4_quantize launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, int32_t outdtype,
+                                void* out, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_mxfp4_shape(M, K, "M"));
+  if (outdtype != WOQ_F16 && outdtype != WOQ_BF16 && outdtype != WOQ_F32)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "outdtype must be WOQ_F16, WOQ_BF16 or WOQ_F32 (got %d)", outdtype);
+  WOQ_TRY(check_mxfp4_arrays(codes, scales, "input"));
+  if (!out || !aligned(out, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "out must be non-NULL and 16-byte aligned");
+  return from_hip(woq::launch_mxfp4_dequantize(codes, scales, M, K, outdtype, out, static_cast<hipStream_t>(stream)),
+                  "mxfp4_dequantize launch");
+  WOQ_GUARD_END
+}
+
+size_t woq_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_mxfp4_gemm(M, N, K) != WOQ_OK) return 0;
+  return woq::mxfp4_gemm_workspace_bytes(M, N, K);
+}
+
+woq_status woq_mxfp4_gemm(const void* X, int32_t xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
+                          int64_t K, void* Y, void* workspace, size_t workspace_bytes, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_mxfp4_gemm(M, N, K));
+  WOQ_TRY(check_activations(X, xdtype, Y));
+  WOQ_TRY(check_mxfp4_arrays(codes, scales, "weight"));
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_gemm_workspace_bytes(M, N, K)));
+  return from_hip(woq::launch_mxfp4_gemm(X, xdtype, codes, scales, M, N, K, Y, workspace,
+                                         static_cast<hipStream_t>(stream)),
+                  "mxfp4_gemm launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const void* codes, const void* scales,
+                             int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_mxfp4_gemm(M, N, K));
+  WOQ_TRY(check_mxfp4_arrays(a_codes, a_scales, "activation"));
+  WOQ_TRY(check_mxfp4_arrays(codes, scales, "weight"));
+  WOQ_TRY(check_activations(a_codes, ydtype, Y));
+  return from_hip(woq::launch_mxfp4_gemm_mx(a_codes, a_scales, codes, scales, M, N, K, ydtype, Y,
+                                            static_cast<hipStream_t>(stream)),
+                  "mxfp4_gemm_mx launch");
+  WOQ_GUARD_END
+}
+
+size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E) {
+  if (check_mxfp4_moe(T, H, I, E, 1) != WOQ_OK) return 0;
+  return woq::mxfp4_moe_workspace_bytes(T, H, I, E);
+}
+
+woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, const void* up_codes,
+                         const void* up_scales, const void* down_codes, const void* down_scales, int64_t T, int64_t H,
+                         int64_t I, int64_t E, int32_t top_k, void* Y, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_mxfp4_moe(T, H, I, E, top_k));
+  WOQ_TRY(check_activations(X, xdtype, Y));
+  if (!router || !aligned(router, 16))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "router must be non-NULL and 16-byte aligned");
+  WOQ_TRY(check_mxfp4_arrays(up_codes, up_scales, "up"));
+  WOQ_TRY(check_mxfp4_arrays(down_codes, down_scales, "down"));
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_moe_workspace_bytes(T, H, I, E)));
+  return from_hip(woq::launch_mxfp4_moe(X, xdtype, router, up_codes, up_scales, down_codes, down_scales, T, H, I, E,
+                                        top_k, Y, workspace, static_cast<hipStream_t>(stream)),
+                  "mxfp4_moe launch");
   WOQ_GUARD_END
 }
 

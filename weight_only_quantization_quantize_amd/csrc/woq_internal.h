@@ -131,6 +131,34 @@ hipError_t launch_gptq(const void* X, const void* W, int64_t T, int64_t N, int64
                        bool asymmetric, double damp, void* packed, void* scales, void* zeros, void* workspace,
                        hipStream_t stream);
 
+// Microscaled 4-bit floats (MXFP4): codes [M, K / 2], one scale byte per 32
+// elements [M, K / 32].  xdtype / outdtype: 0 fp16, 1 bf16, 2 fp32 (outdtype).
+hipError_t launch_mxfp4_quantize(const void* x, int xdtype, int64_t M, int64_t K, void* codes, void* scales,
+                                 hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, int outdtype,
+                                   void* out, hipStream_t stream);
+// Splits 16-bit X [M, K] into 6-bit pieces, fragment-major: row_groups groups
+// of R rows (32 or 16) by ksteps steps of 2048 / R elements.
+hipError_t launch_mxfp4_split(const void* X, int xdtype, int64_t M, int64_t K, int R, int64_t row_groups,
+                              int64_t ksteps, void* pieces, void* scales, hipStream_t stream);
+// One row of activations, K <= mxfp4_gemv_max_k().
+int64_t mxfp4_gemv_max_k();
+hipError_t launch_mxfp4_gemv(const void* x, int xdtype, const void* codes, const void* scales, int64_t N, int64_t K,
+                             void* y, hipStream_t stream);
+// 16-bit activations by microscaled weights; microscaled by microscaled.
+size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
+                             int64_t K, void* Y, void* workspace, hipStream_t stream);
+hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
+                                int64_t K, int ydtype, void* Y, hipStream_t stream);
+// A mixture-of-experts layer on a few tokens.
+int mxfp4_moe_max_tokens();
+int mxfp4_moe_max_experts();
+size_t mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E);
+hipError_t launch_mxfp4_moe(const void* X, int xdtype, const void* router, const void* up_codes,
+                            const void* up_scales, const void* down_codes, const void* down_scales, int64_t T,
+                            int64_t H, int64_t I, int64_t E, int top_k, void* Y, void* workspace, hipStream_t stream);
+
 // Measurement aids (no quantization): a read-only stream over `bytes` bytes
 // with a given launch shape, an empty kernel, and back-to-back fp16 MFMAs.
 hipError_t launch_stream_read(const void* p, int64_t bytes, int blocks, int threads, int unroll, void* sink,

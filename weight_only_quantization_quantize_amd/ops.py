@@ -361,3 +361,182 @@ def gptq(
                    float(damp), packed.data_ptr(), scales.data_ptr(), _ptr(zeros), ws.data_ptr(), nbytes, _stream(X))
     _lib.check(st, "woq_gptq_quantize_pack")
     return packed, scales, zeros
+
+
+# ---------------------------------------------------------------------------
+# Microscaled 4-bit floats (MXFP4): codes uint8 [M, K/2] and scales uint8
+# [M, K/32], as include/woq.h defines them.
+# ---------------------------------------------------------------------------
+
+_MX_OUT = {torch.float16: _lib.WOQ_F16, torch.bfloat16: _lib.WOQ_BF16, torch.float32: _lib.WOQ_F32}
+
+
+def _check_mxfp4(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int = 2) -> Tuple[int, ...]:
+    """The matrix sizes of a microscaled set [..., M, K]."""
+    if codes.dtype != torch.uint8 or codes.dim() != dims or codes.shape[-1] < 16 or codes.shape[-1] % 16:
+        raise ValueError(f"{name} codes must be {dims}-D uint8 with K/2 columns, K a positive multiple of 32 "
+                         f"(got {codes.dtype}, {tuple(codes.shape)})")
+    shape = tuple(codes.shape)
+    if scales.dtype != torch.uint8 or tuple(scales.shape) != shape[:-1] + (shape[-1] // 16,):
+        raise ValueError(f"{name} scales must be uint8 of shape {shape[:-1] + (shape[-1] // 16,)} "
+                         f"(got {scales.dtype}, {tuple(scales.shape)})")
+    return shape[:-1] + (2 * shape[-1],)
+
+
+def _no_grad(*ts: torch.Tensor) -> None:
+    """These operators are for inference: a gradient asked of them is refused, not dropped."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in ts):
+        raise ValueError("the mxfp4 operators have no gradient (use torch.no_grad() or detach the input)")
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device made current for the launch."""
+    return torch.cuda.device(t.device)
+
+
+def mxfp4_quantize(
+    x: torch.Tensor,
+    out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Quantize x [M, K] (fp16 or bf16; weights or activations) to microscaled
+    4-bit floats -> (codes uint8 [M, K/2], scales uint8 [M, K/32])."""
+    if x.dtype not in _DTYPE or x.dim() != 2 or x.shape[1] < 32 or x.shape[1] % 32 or x.shape[0] < 1:
+        raise ValueError(f"x must be fp16/bf16 [M, K] with M >= 1 and K a positive multiple of 32 "
+                         f"(got {x.dtype}, {tuple(x.shape)})")
+    M, K = x.shape
+    _no_grad(x)
+    if out is None:
+        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    else:
+        codes, scales = out
+        _check_out(codes, (M, K // 2), torch.uint8, "out codes")
+        _check_out(scales, (M, K // 32), torch.uint8, "out scales")
+    _require_gpu(x, codes, scales)
+    with _on(x):
+        st = _lib.call("woq_mxfp4_quantize", x.data_ptr(), _DTYPE[x.dtype], M, K, codes.data_ptr(), scales.data_ptr(),
+                       _stream(x))
+    _lib.check(st, "woq_mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The values [M, K] that microscaled codes and scales stand for, in fp32, bf16 (both exact) or fp16."""
+    M, K = _check_mxfp4(codes, scales, "input")
+    if dtype not in _MX_OUT:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16 (got {dtype})")
+    if M < 1:
+        raise ValueError("need at least one row")
+    out = torch.empty((M, K), dtype=dtype, device=codes.device)
+    _require_gpu(codes, scales, out)
+    with _on(codes):
+        st = _lib.call("woq_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(), M, K, _MX_OUT[dtype],
+                       out.data_ptr(), _stream(codes))
+    _lib.check(st, "woq_mxfp4_dequantize")
+    return out
+
+
+def _mx_workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
+    """A call's own scratch.  It comes from PyTorch's allocator each time: the
+    allocator keeps it on this stream, and under graph capture in that graph's
+    pool, so no two calls that may run at once share it."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def mxfp4_gemm(
+    X: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Y [M, N] = X @ w^T for X [M, K] (fp16 or bf16) and microscaled weights w [N, K]."""
+    N, K = _check_mxfp4(codes, scales, "weight")
+    if X.dtype not in _DTYPE or X.dim() != 2 or X.shape[1] != K:
+        raise ValueError(f"X must be fp16/bf16 [M, {K}] (got {X.dtype}, {tuple(X.shape)})")
+    M = X.shape[0]
+    if M < 1 or N < 1:
+        raise ValueError("need at least one row of X and of the weights")
+    _no_grad(X)
+    if out is not None:
+        _check_out(out, (M, N), X.dtype, "out")
+    Y = out if out is not None else torch.empty((M, N), dtype=X.dtype, device=X.device)
+    _require_gpu(X, codes, scales, Y)
+    nbytes = int(_lib.call("woq_mxfp4_gemm_workspace_bytes", M, N, K))
+    with _on(X):
+        ws = _mx_workspace(X.device, nbytes)
+        st = _lib.call("woq_mxfp4_gemm", X.data_ptr(), _DTYPE[X.dtype], codes.data_ptr(), scales.data_ptr(), M, N, K,
+                       Y.data_ptr(), _ptr(ws), nbytes, _stream(X))
+    _lib.check(st, "woq_mxfp4_gemm")
+    return Y
+
+
+def mxfp4_gemm_mx(
+    a_codes: torch.Tensor,
+    a_scales: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    dtype: torch.dtype = torch.bfloat16,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Y [M, N] = a @ w^T of dtype (fp16 or bf16) for microscaled activations
+    a [M, K] (mxfp4_quantize) and microscaled weights w [N, K]."""
+    M, K = _check_mxfp4(a_codes, a_scales, "activation")
+    N, Kw = _check_mxfp4(codes, scales, "weight")
+    if K != Kw:
+        raise ValueError(f"activations and weights must share K (got {K} and {Kw})")
+    if dtype not in _DTYPE:
+        raise ValueError(f"dtype must be float16 or bfloat16 (got {dtype})")
+    if M < 1 or N < 1:
+        raise ValueError("need at least one row of activations and of weights")
+    if out is not None:
+        _check_out(out, (M, N), dtype, "out")
+    Y = out if out is not None else torch.empty((M, N), dtype=dtype, device=a_codes.device)
+    _require_gpu(a_codes, a_scales, codes, scales, Y)
+    with _on(a_codes):
+        st = _lib.call("woq_mxfp4_gemm_mx", a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(),
+                       scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr(), _stream(a_codes))
+    _lib.check(st, "woq_mxfp4_gemm_mx")
+    return Y
+
+
+def mxfp4_moe(
+    X: torch.Tensor,
+    router: torch.Tensor,
+    up_codes: torch.Tensor,
+    up_scales: torch.Tensor,
+    down_codes: torch.Tensor,
+    down_scales: torch.Tensor,
+    top_k: int,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """A mixture-of-experts layer on T <= 64 tokens X [T, H] (fp16 or bf16):
+    router [E, H] of X's type, up microscaled [E, 2 I, H] (gate rows, then up
+    rows), down microscaled [E, H, I] -> Y [T, H].  Softmax over the top_k
+    logits; silu(gate) * up; see woq_mxfp4_moe in include/woq.h."""
+    E, I2, H = _check_mxfp4(up_codes, up_scales, "up", 3)
+    I = I2 // 2
+    if I2 % 2 or _check_mxfp4(down_codes, down_scales, "down", 3) != (E, H, I):
+        raise ValueError(f"up must be [E, 2 I, H] and down [E, H, I] (got {(E, I2, H)} and "
+                         f"{tuple(down_codes.shape[:2]) + (2 * down_codes.shape[2],)})")
+    if X.dtype not in _DTYPE or X.dim() != 2 or X.shape[1] != H:
+        raise ValueError(f"X must be fp16/bf16 [T, {H}] (got {X.dtype}, {tuple(X.shape)})")
+    if router.dtype != X.dtype or tuple(router.shape) != (E, H):
+        raise ValueError(f"router must be {X.dtype} of shape {(E, H)} (got {router.dtype}, {tuple(router.shape)})")
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k must be in [1, {E}] (got {top_k})")
+    T = X.shape[0]
+    nbytes = int(_lib.call("woq_mxfp4_moe_workspace_bytes", T, H, I, E))
+    if nbytes == 0:
+        raise ValueError(f"mxfp4_moe takes 1 to 64 tokens and up to 512 experts (got T={T}, H={H}, I={I}, E={E})")
+    _no_grad(X, router)
+    if out is not None:
+        _check_out(out, (T, H), X.dtype, "out")
+    Y = out if out is not None else torch.empty((T, H), dtype=X.dtype, device=X.device)
+    _require_gpu(X, router, up_codes, up_scales, down_codes, down_scales, Y)
+    with _on(X):
+        ws = _mx_workspace(X.device, nbytes)
+        st = _lib.call("woq_mxfp4_moe", X.data_ptr(), _DTYPE[X.dtype], router.data_ptr(), up_codes.data_ptr(),
+                       up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k,
+                       Y.data_ptr(), _ptr(ws), nbytes, _stream(X))
+    _lib.check(st, "woq_mxfp4_moe")
+    return Y

@@ -31,19 +31,6 @@ __device__ inline void load_to_lds(const void* g, void* l) {
   __builtin_amdgcn_global_load_lds((glb_void*)g, (lds_void*)l, 16, 0, 0);
 }
 
-// The four scale bytes of a row's K tile starting at block b of nblk; past the
-// row's end 127, which the zero operand of those blocks makes harmless.
-__device__ inline uint32_t load_scales(const uint8_t* __restrict__ row, int b, int nblk) {
-  uint32_t v;
-  if (b + 4 <= nblk) {
-    __builtin_memcpy(&v, row + b, 4);
-  } else {
-    v = 0x7F7F7F7Fu;
-    for (int i = 0; b + i < nblk; ++i) v = (v & ~(0xFFu << (8 * i))) | ((uint32_t)row[b + i] << (8 * i));
-  }
-  return v;
-}
-
 template <class YT, int PIECES, int TM, int TN>
 __global__ __launch_bounds__(kThreads) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
                                                               const uint8_t* __restrict__ As,
@@ -97,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_gemm_kernel(const uint8_t* __r
       if constexpr (PIECES == 1) {
         int r = m0 + (wm * TM + i) * 32 + r32;
         r = r < M ? r : M - 1;
-        a[i] = load_scales(As + (int64_t)r * nblk, 4 * kt, nblk);
+        a[i] = mx_load_scales(As + (int64_t)r * nblk, 4 * kt, nblk);
       } else {
         const int64_t f = (int64_t)(m0 / 32 + wm * TM + i) * (2 * ktiles) + 2 * kt;
         a[2 * i] = reinterpret_cast<const uint32_t*>(As)[f * 64 + lane];
@@ -108,7 +95,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_gemm_kernel(const uint8_t* __r
     for (int j = 0; j < TN; ++j) {
       int r = n0 + (wn * TN + j) * 32 + r32;
       r = r < N ? r : N - 1;
-      b[j] = load_scales(Ws + (int64_t)r * nblk, 4 * kt, nblk);
+      b[j] = mx_load_scales(Ws + (int64_t)r * nblk, 4 * kt, nblk);
     }
   };
 
@@ -212,6 +199,9 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   return hipGetLastError();
 }
 
+constexpr int64_t kSkinnyRows = 64;     // up to here the weight-streaming kernel, 16-bit activations
+constexpr int64_t kSkinnyRowsMx = 64;   // and microscaled ones
+bool skinny(int64_t M, int64_t K, int64_t rows) { return M <= rows && K >= 128; }
 constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
 
 int64_t split_row_groups(int64_t M) { return (M + kRowPad - 1) / kRowPad * (kRowPad / 32); }
@@ -221,14 +211,22 @@ int64_t split_ksteps(int64_t K) { return (K + kBK - 1) / kBK * 2; }
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return 0;
+  if (skinny(M, K, kSkinnyRows)) return (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * (kMxFragBytes + kMxFragScaleBytes);
   return (size_t)(split_row_groups(M) * split_ksteps(K)) * (kMxFragBytes + kMxFragScaleBytes);
 }
 
 hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
                              int64_t K, void* Y, void* workspace, hipStream_t stream) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return launch_mxfp4_gemv(X, xdtype, codes, scales, N, K, Y, stream);
-  const int64_t rg = split_row_groups(M), ks = split_ksteps(K);
   uint8_t* const pieces = static_cast<uint8_t*>(workspace);
+  if (skinny(M, K, kSkinnyRows)) {
+    const int64_t steps = (K + 511) / 512 * 4, groups = (M + 15) / 16;
+    uint8_t* const ps = pieces + groups * steps * kMxFragBytes;
+    const hipError_t e = launch_mxfp4_split(X, xdtype, M, K, 16, groups, steps, pieces, ps, stream);
+    if (e != hipSuccess) return e;
+    return launch_mxfp4_skinny(pieces, ps, codes, scales, M, N, K, xdtype, Y, stream);
+  }
+  const int64_t rg = split_row_groups(M), ks = split_ksteps(K);
   uint8_t* const ps = pieces + rg * ks * kMxFragBytes;
   const hipError_t e = launch_mxfp4_split(X, xdtype, M, K, 32, rg, ks, pieces, ps, stream);
   if (e != hipSuccess) return e;
@@ -238,6 +236,7 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
 
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, hipStream_t stream) {
+  if (skinny(M, K, kSkinnyRowsMx)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
   return ydtype == 0 ? launch<F16, 1>(A, As, W, Ws, M, N, K, Y, stream) : launch<BF16, 1>(A, As, W, Ws, M, N, K, Y, stream);
 }
 

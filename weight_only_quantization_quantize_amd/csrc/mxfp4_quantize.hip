@@ -117,7 +117,9 @@ __global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* _
   if (f >= frags) return;
   const int lane = threadIdx.x & 63;
   const int row = (f / ksteps) * R + lane % R;
-  const int k = ((f % ksteps) * (64 / R) + lane / R) * kMxBlock;
+  const int ks = f % ksteps;
+  const int blk = R == 32 ? 2 * ks + lane / 32 : 16 * (ks / 4) + 4 * (lane / 16) + ks % 4;
+  const int k = blk * kMxBlock;
   float v[kMxBlock] = {};
   if (row < M && k < K) mx_load_block<XT>(X + (int64_t)row * K + k, v);
   const MxPieces s = mx_split(v);

@@ -151,6 +151,12 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
                              int64_t K, void* Y, void* workspace, hipStream_t stream);
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, hipStream_t stream);
+// The same for a few rows: 16-bit activations split in fragments of 16 rows
+// (M <= 16), microscaled activations (M <= 64).
+hipError_t launch_mxfp4_skinny(const void* pieces, const void* piece_scales, const void* codes, const void* scales,
+                               int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream);
+hipError_t launch_mxfp4_skinny_mx(const void* A, const void* As, const void* codes, const void* scales, int64_t M,
+                                  int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream);
 // A mixture-of-experts layer on a few tokens.
 int mxfp4_moe_max_tokens();
 int mxfp4_moe_max_experts();

@@ -389,9 +389,17 @@ def _no_grad(*ts: torch.Tensor) -> None:
         raise ValueError("the mxfp4 operators have no gradient (use torch.no_grad() or detach the input)")
 
 
-def _on(t: torch.Tensor):
-    """The tensor's device made current for the launch."""
-    return torch.cuda.device(t.device)
+def _launch(name: str, device: torch.device, *args) -> None:
+    """Calls an entry point on the device's current stream (appended to args),
+    the device made current where it is not, and raises on a failure."""
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        st = _lib.call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = _lib.call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, name)
 
 
 def mxfp4_quantize(
@@ -413,10 +421,7 @@ def mxfp4_quantize(
         _check_out(codes, (M, K // 2), torch.uint8, "out codes")
         _check_out(scales, (M, K // 32), torch.uint8, "out scales")
     _require_gpu(x, codes, scales)
-    with _on(x):
-        st = _lib.call("woq_mxfp4_quantize", x.data_ptr(), _DTYPE[x.dtype], M, K, codes.data_ptr(), scales.data_ptr(),
-                       _stream(x))
-    _lib.check(st, "woq_mxfp4_quantize")
+    _launch("woq_mxfp4_quantize", x.device, x.data_ptr(), _DTYPE[x.dtype], M, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -429,10 +434,8 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
         raise ValueError("need at least one row")
     out = torch.empty((M, K), dtype=dtype, device=codes.device)
     _require_gpu(codes, scales, out)
-    with _on(codes):
-        st = _lib.call("woq_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(), M, K, _MX_OUT[dtype],
-                       out.data_ptr(), _stream(codes))
-    _lib.check(st, "woq_mxfp4_dequantize")
+    _launch("woq_mxfp4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), M, K, _MX_OUT[dtype],
+            out.data_ptr())
     return out
 
 
@@ -462,11 +465,9 @@ def mxfp4_gemm(
     Y = out if out is not None else torch.empty((M, N), dtype=X.dtype, device=X.device)
     _require_gpu(X, codes, scales, Y)
     nbytes = int(_lib.call("woq_mxfp4_gemm_workspace_bytes", M, N, K))
-    with _on(X):
-        ws = _mx_workspace(X.device, nbytes)
-        st = _lib.call("woq_mxfp4_gemm", X.data_ptr(), _DTYPE[X.dtype], codes.data_ptr(), scales.data_ptr(), M, N, K,
-                       Y.data_ptr(), _ptr(ws), nbytes, _stream(X))
-    _lib.check(st, "woq_mxfp4_gemm")
+    ws = _mx_workspace(X.device, nbytes)
+    _launch("woq_mxfp4_gemm", X.device, X.data_ptr(), _DTYPE[X.dtype], codes.data_ptr(), scales.data_ptr(), M, N, K,
+            Y.data_ptr(), _ptr(ws), nbytes)
     return Y
 
 
@@ -492,10 +493,8 @@ def mxfp4_gemm_mx(
         _check_out(out, (M, N), dtype, "out")
     Y = out if out is not None else torch.empty((M, N), dtype=dtype, device=a_codes.device)
     _require_gpu(a_codes, a_scales, codes, scales, Y)
-    with _on(a_codes):
-        st = _lib.call("woq_mxfp4_gemm_mx", a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(),
-                       scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr(), _stream(a_codes))
-    _lib.check(st, "woq_mxfp4_gemm_mx")
+    _launch("woq_mxfp4_gemm_mx", a_codes.device, a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(),
+            scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr())
     return Y
 
 
@@ -533,10 +532,8 @@ def mxfp4_moe(
         _check_out(out, (T, H), X.dtype, "out")
     Y = out if out is not None else torch.empty((T, H), dtype=X.dtype, device=X.device)
     _require_gpu(X, router, up_codes, up_scales, down_codes, down_scales, Y)
-    with _on(X):
-        ws = _mx_workspace(X.device, nbytes)
-        st = _lib.call("woq_mxfp4_moe", X.data_ptr(), _DTYPE[X.dtype], router.data_ptr(), up_codes.data_ptr(),
-                       up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k,
-                       Y.data_ptr(), _ptr(ws), nbytes, _stream(X))
-    _lib.check(st, "woq_mxfp4_moe")
+    ws = _mx_workspace(X.device, nbytes)
+    _launch("woq_mxfp4_moe", X.device, X.data_ptr(), _DTYPE[X.dtype], router.data_ptr(), up_codes.data_ptr(),
+            up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k, Y.data_ptr(),
+            _ptr(ws), nbytes)
     return Y

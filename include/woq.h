@@ -327,9 +327,12 @@ woq_status woq_mxfp4_gemm(const void* X, int32_t xdtype, const void* codes, cons
                           int64_t K, void* Y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Y[m, n] = sum_k a[m, k] w[n, k] for microscaled a [M, K] and w [N, K]; exact
- * products, fp32 sums, Y [M, N] of ydtype (WOQ_F16 or WOQ_BF16) rounded once. */
+ * products, fp32 sums, Y [M, N] of ydtype (WOQ_F16 or WOQ_BF16) rounded once.
+ * workspace as above (M > 64: the scales in tile order). */
+size_t woq_mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K);
 woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const void* codes, const void* scales,
-                             int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream);
+                             int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* A mixture-of-experts layer on a few tokens (T <= 64, E <= 512):
  *   logits[t, e] = sum_k X[t, k] router[e, k]   (fp32)

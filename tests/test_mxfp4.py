@@ -222,9 +222,12 @@ def test_abi_gemm_refuses():
               (3, None, INVALID), (4, 0, INVALID), (5, 0, INVALID), (6, 40, INVALID), (7, None, INVALID),
               (7, FAKE + 2, INVALID), (8, None, INVALID), (8, FAKE + 128, INVALID), (9, need - 1, INVALID),
               (5, 1 << 29, UNSUPPORTED), (4, 1 << 40, UNSUPPORTED)])
-    _refused("woq_mxfp4_gemm_mx", [FAKE, FAKE, FAKE, FAKE, 4, 64, 64, 0, FAKE, None],
+    need = lib.woq_mxfp4_gemm_mx_workspace_bytes(4, 64, 64)
+    assert need > 0
+    _refused("woq_mxfp4_gemm_mx", [FAKE, FAKE, FAKE, FAKE, 4, 64, 64, 0, FAKE, FAKE, need, None],
              [(0, None, INVALID), (1, None, INVALID), (2, FAKE + 8, INVALID), (3, None, INVALID), (4, 0, INVALID),
-              (5, -5, INVALID), (6, 16, INVALID), (7, 2, INVALID), (8, None, INVALID)])
+              (5, -5, INVALID), (6, 16, INVALID), (7, 2, INVALID), (8, None, INVALID),
+              (9, None, INVALID), (9, FAKE + 64, INVALID), (10, need - 1, INVALID)])
 
 
 def test_abi_workspace_queries():

@@ -127,19 +127,6 @@ __device__ inline MxPieces mx_split(const float (&v)[kMxBlock]) {
   return r;
 }
 
-// The scale bytes of blocks b .. b + 3 of a row of nblk; past the row's end 127,
-// which the zero operand of those blocks makes harmless.
-__device__ inline uint32_t mx_load_scales(const uint8_t* __restrict__ row, int b, int nblk) {
-  uint32_t v;
-  if (b + 4 <= nblk) {
-    __builtin_memcpy(&v, row + b, 4);
-  } else {
-    v = 0x7F7F7F7Fu;
-    for (int i = 0; b + i < nblk; ++i) v = (v & ~(0xFFu << (8 * i))) | ((uint32_t)row[b + i] << (8 * i));
-  }
-  return v;
-}
-
 // Fragment-major storage of split activations.  A fragment is R rows (32 or
 // 16) by 2048 / R elements of K (2 or 4 blocks): lane l of a wave holds row
 // l % R, block l / R.  Per fragment and piece 64 lanes x 16 bytes, then 64

@@ -6,134 +6,274 @@
 // all of it inside v_mfma_scale_f32_32x32x64_f8f6f4: no element is decoded,
 // the products are exact and the sums are the matrix unit's fp32.
 //
-// A workgroup of 2 x 2 waves computes 64 TM x 64 TN of Y in K tiles of 128,
-// double-buffered in LDS by direct loads (16 bytes a lane).
+// Tile.  2 x 2 waves compute 64 TM x 64 TN of Y, a wave 32 TM x 32 TN.  Large
+// products take 256 x 128 (4-bit A) and 128 x 256 (three pieces: A is the
+// heavier operand, 2.25 bytes an element against 17/32, so it gets the shorter
+// side); two such workgroups share a compute unit, which hides the one's
+// barriers, prologue and stores behind the other's matrix instructions.
 //
-// LDS layout of a 4-bit operand: a row's 64 bytes of a K tile are four chunks
-// of one block each, chunk c at position c ^ ((row / 4) % 4), so that the 16
-// rows a quarter wave reads at one chunk lie in 16 different 16-byte slots of
-// the 256-byte bank row.
+// Pipeline.  K goes in stages of 64 KS (128; 64 for split activations), STAGES
+// of them in LDS, filled by direct loads (global_load_lds: no registers, no
+// instructions to write LDS).  At the top of a turn a wave waits until its own
+// loads of this stage are done, meets the others at the barrier, which also
+// says that everybody is through with the previous stage, starts the loads of
+// the stage STAGES - 1 ahead into that one's place, and multiplies.  The loads
+// are written out in assembly because the compiler would wait for all of them
+// before every read of LDS; their counter is waited for by hand, and there is
+// no other vector memory access inside the loop.
+//
+// Scales.  The 4-bit operands' scale bytes lie K/32 bytes apart from row to row
+// at any alignment, which direct loads cannot gather; a pass before the product
+// (mxfp4_scales_kernel) turns them into one dword per row and 128 of K, rows
+// contiguous, with 127 past the row's end.
+//
+// LDS layout of a 4-bit operand: a row's 32 KS bytes of a stage are chunks of
+// one block each, chunk c at position c ^ swizzle(row), so that 16 rows read at
+// one chunk lie in 16 different 16-byte slots of the 256-byte bank row.
+//
+// Tile order.  Workgroup b runs on XCD b % 8; each XCD takes one contiguous run
+// of tiles, M fastest, so that the tiles in flight there share few columns of W
+// and all of A in its L2.
+#include <type_traits>
+
 #include "mxfp4_device.h"
 #include "woq_internal.h"
 
 namespace woq {
 namespace {
 
-constexpr int kBK = 128;              // K per tile
-constexpr int kRowBytes = kBK / 2;    // of a 4-bit operand
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kXcds = 8;
+constexpr int kScalePad = 256;  // rows of a scale array are padded to the largest tile's and a workgroup's
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void glb_void;
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
-// 64 lanes x 16 bytes from per-lane addresses to consecutive LDS.
-__device__ inline void load_to_lds(const void* g, void* l) {
-  __builtin_amdgcn_global_load_lds((glb_void*)g, (lds_void*)l, 16, 0, 0);
+__device__ inline uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(const lds_byte*)p; }
+
+// Direct loads to LDS: lane l's 16 (4) bytes from base + offset go to to + 16 l
+// (4 l).  M0 holds the LDS address.  The five wait states cover the write of M0
+// and a base address that a vector instruction wrote just before.  The caller
+// waits for the data with wait_loads.
+__device__ inline void load_lds16(const uint8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ inline void load_lds4(const uint8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+// Until at most N of the wave's vector memory loads are under way and its LDS
+// reads are done.
+template <int N>
+__device__ inline void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <class YT, int PIECES, int TM, int TN>
-__global__ __launch_bounds__(kThreads) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
-                                                              const uint8_t* __restrict__ As,
-                                                              const uint8_t* __restrict__ W,
-                                                              const uint8_t* __restrict__ Ws, int M, int N, int K,
-                                                              uint16_t* __restrict__ Y) {
-  constexpr int BM = 64 * TM, BN = 64 * TN;
-  constexpr int kABytes = PIECES == 1 ? BM * kRowBytes : BM / 32 * 2 * kMxFragBytes;
-  constexpr int kBBytes = BN * kRowBytes;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kABytes + kBBytes];
+// Scale bytes [rows, nblk] -> dwords [ceil(nblk / 4)][rows_pad], 127 in the
+// place of rows and blocks that are not there.
+struct ScaleJob {
+  const uint8_t* scales;
+  uint32_t* out;
+  int rows, rows_pad;
+};
+__global__ __launch_bounds__(kThreads) void mxfp4_scales_kernel(ScaleJob w, ScaleJob a, int nblk, int wblocks) {
+  const bool first = (int)blockIdx.x < wblocks;
+  const ScaleJob j = first ? w : a;
+  const int64_t i = (int64_t)((int)blockIdx.x - (first ? 0 : wblocks)) * kThreads + threadIdx.x;
+  const int ktiles = (nblk + 3) >> 2;
+  // a thread takes 16 blocks of a row, a wave 64 rows: the writes are contiguous
+  const int row = (int)(i % j.rows_pad), g = (int)(i / j.rows_pad);
+  if (4 * g >= ktiles) return;
+  u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  if (row < j.rows) {
+    const uint8_t* const p = j.scales + (int64_t)row * nblk + 16 * g;
+    if (16 * g + 16 <= nblk) {
+      __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (16 * g + q < nblk) v[q / 4] = (v[q / 4] & ~(0xFFu << (8 * (q % 4)))) | ((uint32_t)p[q] << (8 * (q % 4)));
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (4 * g + q < ktiles) j.out[(int64_t)(4 * g + q) * j.rows_pad + row] = v[q];
+}
 
+// A 4-bit operand: ROWS rows, stages of 64 KS.  One load of a wave takes 16
+// rows (KS = 2) or 32 (KS = 1).
+template <int ROWS, int KS>
+struct Tile4 {
+  static constexpr int kRowBytes = 32 * KS;
+  static constexpr int kBytes = ROWS * kRowBytes;
+  static constexpr int kUnits = kBytes / 1024;
+  static constexpr int kScaleUnits = ROWS / 64;
+  static constexpr int kScaleBytes = ROWS * 4;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  uint32_t scale_step;  // bytes between K tiles of the scale dwords
+  int nblk, last, chunk;
+
+  __device__ static int swizzle(int row) { return KS == 2 ? (row >> 2) & 3 : (row >> 3) & 1; }
+  __device__ void start(const uint8_t* codes_, const uint8_t* scales_, int row0, int rows, int rows_pad, int nblk_, int) {
+    nblk = nblk_;
+    codes = codes_ + (int64_t)row0 * nblk * 16;
+    scales = scales_ + (int64_t)row0 * 4;
+    scale_step = (uint32_t)rows_pad * 4u;
+    last = rows - row0 - 1;
+    const int lane = threadIdx.x & 63;
+    chunk = (lane & (2 * KS - 1)) ^ swizzle(lane / (2 * KS));
+  }
+  __device__ void load(int unit, int h, uint32_t to) const {
+    const int lane = threadIdx.x & 63;
+    int r = unit * (32 / KS) + lane / (2 * KS);
+    r = r < last ? r : last;
+    int b = 2 * KS * h + chunk;
+    b = b < nblk ? b : nblk - 1;  // past the row's end: its last block, A is zeros there
+    load_lds16(codes, (uint32_t)(r * nblk + b) * 16u, to + 1024u * (uint32_t)unit);
+  }
+  __device__ void load_scales(int unit, int h, uint32_t to) const {
+    const int kt = KS == 2 ? h : h >> 1;
+    load_lds4(scales + (int64_t)kt * scale_step, 256u * (uint32_t)unit + 4u * (threadIdx.x & 63), to + 256u * (uint32_t)unit);
+  }
+  // lane (row, half) multiplies block 2 s + half of its row's stage
+  __device__ static u32x4_t fragment(const uint8_t* lds, int row, int s, int half) {
+    const int c = (2 * s + half) ^ swizzle(row);
+    return *reinterpret_cast<const u32x4_t*>(lds + row * kRowBytes + c * 16);
+  }
+  __device__ static int scale(const uint8_t* lds, int row, int s, int half, int h) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(lds + 4 * row);
+    return (int)(v >> (8 * (2 * (KS == 2 ? s : h & 1) + half)));
+  }
+};
+
+// Split activations: stages of one fragment (64 of K) of each 32 rows.
+template <int ROWS>
+struct TileSplit {
+  static constexpr int kBytes = ROWS / 32 * kMxFragBytes;
+  static constexpr int kUnits = kBytes / 1024;
+  static constexpr int kScaleUnits = ROWS / 32;
+  static constexpr int kScaleBytes = ROWS * 8;
+  static_assert(kBytes % 1024 == 0, "whole loads");
+  const uint8_t* pieces;
+  const uint8_t* scales;
+  uint32_t ksteps;
+
+  __device__ void start(const uint8_t* pieces_, const uint8_t* scales_, int row0, int, int, int, int ksteps_) {
+    ksteps = (uint32_t)ksteps_;
+    pieces = pieces_ + (int64_t)(row0 / 32) * ksteps * kMxFragBytes;
+    scales = scales_ + (int64_t)(row0 / 32) * ksteps * kMxFragScaleBytes;
+  }
+  __device__ void load(int unit, int h, uint32_t to) const {
+    const uint32_t o = 1024u * (uint32_t)unit + 16u * (threadIdx.x & 63);
+    const uint32_t rg = o / kMxFragBytes, in = o % kMxFragBytes;
+    load_lds16(pieces + (int64_t)h * kMxFragBytes, rg * ksteps * kMxFragBytes + in, to + 1024u * (uint32_t)unit);
+  }
+  __device__ void load_scales(int unit, int h, uint32_t to) const {
+    load_lds4(scales + (int64_t)h * kMxFragScaleBytes, (uint32_t)unit * ksteps * kMxFragScaleBytes + 4u * (threadIdx.x & 63),
+              to + 256u * (uint32_t)unit);
+  }
+};
+
+template <int PIECES, int TM, int TN>
+struct Config {
+  static constexpr bool kSplit = PIECES == kMxPieces;
+  static constexpr int kKS = kSplit ? 1 : 2;
+  static constexpr int BM = 64 * TM, BN = 64 * TN;
+  using TA = std::conditional_t<kSplit, TileSplit<BM>, Tile4<BM, kKS>>;
+  using TW = Tile4<BN, kKS>;
+  static constexpr int kStage = TA::kBytes + TW::kBytes + TA::kScaleBytes + TW::kScaleBytes;
+  // as many stages as leave room for a second workgroup, at most 4
+  static constexpr int kFit = 80 * 1024 / kStage;
+  static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
+  static constexpr int per_wave(int units) { return (units + kWaves - 1) / kWaves; }
+  static constexpr int kALoads = per_wave(TA::kUnits), kWLoads = per_wave(TW::kUnits);
+  static constexpr int kAScaleLoads = per_wave(TA::kScaleUnits), kWScaleLoads = per_wave(TW::kScaleUnits);
+  static constexpr int kLoads = kALoads + kWLoads + kAScaleLoads + kWScaleLoads;
+};
+
+template <class YT, int PIECES, int TM, int TN>
+__global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
+                                                                 const uint8_t* __restrict__ As,
+                                                                 const uint8_t* __restrict__ W,
+                                                                 const uint8_t* __restrict__ Ws, int M, int N,
+                                                                 int m_pad, int n_pad, int nblk, int mtiles, int tiles,
+                                                                 uint16_t* __restrict__ Y) {
+  using C = Config<PIECES, TM, TN>;
+  using TA = typename C::TA;
+  using TW = typename C::TW;
+  constexpr int kAt = TA::kBytes, kAsAt = kAt + TW::kBytes, kWsAt = kAsAt + TA::kScaleBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kStages][C::kStage];
+
+  const int per = (tiles + kXcds - 1) / kXcds;
+  const int tile = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  if (tile >= tiles) return;
+  const int m0 = tile % mtiles * C::BM, n0 = tile / mtiles * C::BN;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = (wave & 1) * TM, wn = (wave >> 1) * TN;  // in units of 32 rows
   const int half = lane >> 5, r32 = lane & 31;
-  const int nblk = K / kMxBlock, ktiles = (K + kBK - 1) / kBK;
-  const int m0 = (int)blockIdx.x * BM, n0 = (int)blockIdx.y * BN;
+  const int turns = (nblk + 2 * C::kKS - 1) / (2 * C::kKS);
 
-  // 4-bit operand tile: load j of a wave covers 16 rows, four lanes a row.
-  auto issue4 = [&](const uint8_t* P, int row0, int rows, int tile_rows, int kt, uint8_t* dst) {
-    const int sub = lane >> 2, pos = lane & 3;
+  TA ta;
+  TW tw;
+  ta.start(A, As, m0, M, m_pad, nblk, ((nblk + 3) >> 2) * 2);
+  tw.start(W, Ws, n0, N, n_pad, nblk, 0);
+  // every wave starts the same number of loads a stage: past an operand's units
+  // the last one is loaded again, past the last stage that stage
+  auto issue = [&](int h_, int buf) {
+    const int h = h_ < turns ? h_ : turns - 1;
+    const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_address(lds[0])) + (uint32_t)(buf * C::kStage);
+    auto unit = [&](int j, int units) {
+      const int u = wave + kWaves * j;
+      return u < units ? u : units - 1;
+    };
 #pragma unroll
-    for (int j = 0; j < tile_rows / 64; ++j) {
-      const int lr = (4 * j + wave) * 16 + sub;
-      int r = row0 + lr;
-      r = r < rows ? r : rows - 1;
-      int c = 4 * kt + (pos ^ ((lr >> 2) & 3));
-      c = c < nblk ? c : nblk - 1;  // past the row's end: any block, its partner operand is zeroed
-      load_to_lds(P + ((int64_t)r * nblk + c) * 16, dst + (4 * j + wave) * 1024);
-    }
-  };
-  auto issue = [&](int kt, int buf) {
-    uint8_t* const a = lds[buf];
-    if constexpr (PIECES == 1) {
-      issue4(A, m0, M, BM, kt, a);
-    } else {
-      // per 32 rows 2 fragments = 9 loads of 1 KB
-      constexpr int kLoads = BM / 32 * 9;
-      for (int j = wave; j < kLoads; j += kThreads / 64) {
-        const int rg = j / 9, part = j % 9;
-        const int64_t f = (int64_t)(m0 / 32 + rg) * (2 * ktiles) + 2 * kt;
-        load_to_lds(A + f * kMxFragBytes + part * 1024 + lane * 16, a + j * 1024);
-      }
-    }
-    issue4(W, n0, N, BN, kt, a + kABytes);
-  };
-  uint32_t sa[2][TM * (PIECES == 1 ? 1 : 2)], sb[2][TN];
-  auto issue_scales = [&](int kt, uint32_t* a, uint32_t* b) {
+    for (int j = 0; j < C::kALoads; ++j) ta.load(unit(j, TA::kUnits), h, to);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      if constexpr (PIECES == 1) {
-        int r = m0 + (wm * TM + i) * 32 + r32;
-        r = r < M ? r : M - 1;
-        a[i] = mx_load_scales(As + (int64_t)r * nblk, 4 * kt, nblk);
-      } else {
-        const int64_t f = (int64_t)(m0 / 32 + wm * TM + i) * (2 * ktiles) + 2 * kt;
-        a[2 * i] = reinterpret_cast<const uint32_t*>(As)[f * 64 + lane];
-        a[2 * i + 1] = reinterpret_cast<const uint32_t*>(As)[f * 64 + 64 + lane];
-      }
-    }
+    for (int j = 0; j < C::kWLoads; ++j) tw.load(unit(j, TW::kUnits), h, to + kAt);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      int r = n0 + (wn * TN + j) * 32 + r32;
-      r = r < N ? r : N - 1;
-      b[j] = mx_load_scales(Ws + (int64_t)r * nblk, 4 * kt, nblk);
-    }
+    for (int j = 0; j < C::kAScaleLoads; ++j) ta.load_scales(unit(j, TA::kScaleUnits), h, to + kAsAt);
+#pragma unroll
+    for (int j = 0; j < C::kWScaleLoads; ++j) tw.load_scales(unit(j, TW::kScaleUnits), h, to + kWsAt);
   };
 
   float16_t acc[TM][TN] = {};
-  auto frag4 = [&](const uint8_t* base, int row, int s) {
-    const int c = (2 * s + half) ^ ((row >> 2) & 3);
-    return *reinterpret_cast<const u32x4_t*>(base + row * kRowBytes + c * 16);
-  };
-  auto compute = [&](int kt, int buf, const uint32_t* a, const uint32_t* b) {
+  for (int st = 0; st + 1 < C::kStages; ++st) issue(st, st);
+  int buf = 0;
+  for (int h = 0; h < turns; ++h) {
+    wait_loads<(C::kStages - 2) * C::kLoads>();
+    __builtin_amdgcn_s_barrier();
+    issue(h + C::kStages - 1, buf == 0 ? C::kStages - 1 : buf - 1);
     const uint8_t* const la = lds[buf];
-    const uint8_t* const lb = la + kABytes;
+    const uint8_t* const lw = la + kAt;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      // lane (row, half) multiplies block 2 s + half of its row
+    for (int s = 0; s < C::kKS; ++s) {
       i32x8_t bf[TN];
       int bs[TN];
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        bf[j] = mx_operand(frag4(lb, (wn * TN + j) * 32 + r32, s));
-        bs[j] = (int)(b[j] >> (8 * (2 * s + half)));
+        const int row = (wn + j) * 32 + r32;
+        bf[j] = mx_operand(TW::fragment(lw, row, s, half));
+        bs[j] = TW::scale(la + kWsAt, row, s, half, h);
       }
-      if constexpr (PIECES == 1) {
-        const bool live = 4 * kt + 2 * s + half < nblk;
+      if constexpr (!C::kSplit) {
+        const bool live = 4 * h + 2 * s + half < nblk;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          u32x4_t v = frag4(la, (wm * TM + i) * 32 + r32, s);
+          const int row = (wm + i) * 32 + r32;
+          u32x4_t v = TA::fragment(la, row, s, half);
           v = live ? v : u32x4_t{0u, 0u, 0u, 0u};
-          const int as = (int)(a[i] >> (8 * (2 * s + half)));
-          const i32x8_t af = mx_operand(v);
+          const int as = TA::scale(la + kAsAt, row, s, half, h);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(af, bf[j], acc[i][j], kMfmaFp4, kMfmaFp4, 0, as, 0, bs[j]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(v), bf[j], acc[i][j], kMfmaFp4,
+                                                                        kMfmaFp4, 0, as, 0, bs[j]);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const uint8_t* const fr = la + ((wm * TM + i) * 2 + s) * kMxFragBytes;
-          const int as = (int)a[2 * i + s];
+          const uint8_t* const fr = la + (wm + i) * kMxFragBytes;
+          const int as = (int)reinterpret_cast<const uint32_t*>(la + kAsAt)[(wm + i) * 64 + lane];
           auto piece = [&](int p) {
             return mx_operand(*reinterpret_cast<const u32x4_t*>(fr + p * kMxPieceBytes + 16 * lane),
                               *reinterpret_cast<const u32x2_t*>(fr + p * kMxPieceBytes + 1024 + 8 * lane));
@@ -152,51 +292,65 @@ __global__ __launch_bounds__(kThreads) void mxfp4_gemm_kernel(const uint8_t* __r
         }
       }
     }
-  };
-
-  issue(0, 0);
-  issue_scales(0, sa[0], sb[0]);
-  __syncthreads();
-  int kt = 0;
-  for (; kt + 1 < ktiles; kt += 2) {
-    issue(kt + 1, 1);
-    issue_scales(kt + 1, sa[1], sb[1]);
-    compute(kt, 0, sa[0], sb[0]);
-    __syncthreads();
-    if (kt + 2 < ktiles) {
-      issue(kt + 2, 0);
-      issue_scales(kt + 2, sa[0], sb[0]);
-    }
-    compute(kt + 1, 1, sa[1], sb[1]);
-    __syncthreads();
+    buf = buf + 1 == C::kStages ? 0 : buf + 1;
   }
-  if (kt < ktiles) compute(kt, 0, sa[0], sb[0]);
+  wait_loads<0>();  // none may land in LDS that is another workgroup's by then
 
   // D: lane holds column r32, rows 8 (i / 4) + 4 half + i % 4.
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = n0 + (wn * TN + j) * 32 + r32;
+      const int n = n0 + (wn + j) * 32 + r32;
       if (n < N) {
+        uint16_t* const y = Y + (int64_t)m0 * N + n;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int m = m0 + (wm * TM + i) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-          if (m < M) Y[(int64_t)m * N + n] = YT::from_f32(acc[i][j][e]);
+          const int m = (wm + i) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+          if (m0 + m < M) y[(int64_t)m * N] = YT::from_f32(acc[i][j][e]);
         }
       }
     }
 }
 
+int64_t padded(int64_t rows) { return (rows + kScalePad - 1) / kScalePad * kScalePad; }
+size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)padded(rows) * (size_t)((K + 127) / 128) * 4; }
+
+// The scale dwords of W and, where it has rows, of A.
+hipError_t launch_scales(const void* Ws, int64_t N, void* wout, const void* As, int64_t M, void* aout, int64_t K,
+                         hipStream_t stream) {
+  const int64_t groups = (K + 511) / 512;
+  const int64_t wblocks = padded(N) * groups / kThreads, ablocks = M ? padded(M) * groups / kThreads : 0;
+  const ScaleJob w{static_cast<const uint8_t*>(Ws), static_cast<uint32_t*>(wout), (int)N, (int)padded(N)};
+  const ScaleJob a{static_cast<const uint8_t*>(As), static_cast<uint32_t*>(aout), (int)M, (int)padded(M)};
+  mxfp4_scales_kernel<<<(unsigned)(wblocks + ablocks), kThreads, 0, stream>>>(w, a, (int)(K / kMxBlock), (int)wblocks);
+  return hipGetLastError();
+}
+
+template <class YT, int PIECES, int TM, int TN>
+hipError_t launch_tiles(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
+                        void* Y, hipStream_t stream) {
+  const int64_t mt = (M + 64 * TM - 1) / (64 * TM), nt = (N + 64 * TN - 1) / (64 * TN);
+  const int64_t tiles = mt * nt;
+  const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds);
+  mxfp4_gemm_kernel<YT, PIECES, TM, TN><<<grid, kThreads, 0, stream>>>(
+      static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
+      static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)padded(M), (int)padded(N), (int)(K / kMxBlock), (int)mt,
+      (int)tiles, static_cast<uint16_t*>(Y));
+  return hipGetLastError();
+}
+
+// The large tile where it fills the chip, the 64 x 64 one where even 128 x 128
+// would leave much of it idle.
 template <class YT, int PIECES>
 hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                   void* Y, hipStream_t stream) {
-  constexpr int TM = 2, TN = 2;
-  const dim3 grid((unsigned)((M + 64 * TM - 1) / (64 * TM)), (unsigned)((N + 64 * TN - 1) / (64 * TN)));
-  mxfp4_gemm_kernel<YT, PIECES, TM, TN><<<grid, kThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
-      static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)K, static_cast<uint16_t*>(Y));
-  return hipGetLastError();
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  constexpr bool kSplit = PIECES == kMxPieces;
+  if (tiles(kSplit ? 128 : 256, kSplit ? 256 : 128) >= 384)
+    return launch_tiles<YT, PIECES, kSplit ? 2 : 4, kSplit ? 4 : 2>(A, As, W, Ws, M, N, K, Y, stream);
+  if (tiles(128, 128) >= 192) return launch_tiles<YT, PIECES, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
+  return launch_tiles<YT, PIECES, 1, 1>(A, As, W, Ws, M, N, K, Y, stream);
 }
 
 constexpr int64_t kSkinnyRows = 64;     // up to here the weight-streaming kernel, 16-bit activations
@@ -205,39 +359,46 @@ bool skinny(int64_t M, int64_t K, int64_t rows) { return M <= rows && K >= 128; 
 constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
 
 int64_t split_row_groups(int64_t M) { return (M + kRowPad - 1) / kRowPad * (kRowPad / 32); }
-int64_t split_ksteps(int64_t K) { return (K + kBK - 1) / kBK * 2; }
+int64_t split_ksteps(int64_t K) { return (K + 127) / 128 * 2; }
 
 }  // namespace
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return 0;
-  if (skinny(M, K, kSkinnyRows)) return (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * (kMxFragBytes + kMxFragScaleBytes);
-  return (size_t)(split_row_groups(M) * split_ksteps(K)) * (kMxFragBytes + kMxFragScaleBytes);
+  if (skinny(M, K, kSkinnyRows))
+    return (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * (kMxFragBytes + kMxFragScaleBytes);
+  return (size_t)(split_row_groups(M) * split_ksteps(K)) * (kMxFragBytes + kMxFragScaleBytes) + scale_bytes(N, K);
 }
 
 hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
                              int64_t K, void* Y, void* workspace, hipStream_t stream) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return launch_mxfp4_gemv(X, xdtype, codes, scales, N, K, Y, stream);
   uint8_t* const pieces = static_cast<uint8_t*>(workspace);
-  if (skinny(M, K, kSkinnyRows)) {
-    const int64_t steps = (K + 511) / 512 * 4, groups = (M + 15) / 16;
-    uint8_t* const ps = pieces + groups * steps * kMxFragBytes;
-    const hipError_t e = launch_mxfp4_split(X, xdtype, M, K, 16, groups, steps, pieces, ps, stream);
-    if (e != hipSuccess) return e;
-    return launch_mxfp4_skinny(pieces, ps, codes, scales, M, N, K, xdtype, Y, stream);
-  }
-  const int64_t rg = split_row_groups(M), ks = split_ksteps(K);
+  const bool few = skinny(M, K, kSkinnyRows);
+  const int64_t rg = few ? (M + 15) / 16 : split_row_groups(M), ks = few ? (K + 511) / 512 * 4 : split_ksteps(K);
   uint8_t* const ps = pieces + rg * ks * kMxFragBytes;
-  const hipError_t e = launch_mxfp4_split(X, xdtype, M, K, 32, rg, ks, pieces, ps, stream);
+  hipError_t e = launch_mxfp4_split(X, xdtype, M, K, few ? 16 : 32, rg, ks, pieces, ps, stream);
   if (e != hipSuccess) return e;
-  return xdtype == 0 ? launch<F16, kMxPieces>(pieces, ps, codes, scales, M, N, K, Y, stream)
-                     : launch<BF16, kMxPieces>(pieces, ps, codes, scales, M, N, K, Y, stream);
+  if (few) return launch_mxfp4_skinny(pieces, ps, codes, scales, M, N, K, xdtype, Y, stream);
+  uint8_t* const ws = ps + rg * ks * kMxFragScaleBytes;
+  e = launch_scales(scales, N, ws, nullptr, 0, nullptr, K, stream);
+  if (e != hipSuccess) return e;
+  return xdtype == 0 ? launch<F16, kMxPieces>(pieces, ps, codes, ws, M, N, K, Y, stream)
+                     : launch<BF16, kMxPieces>(pieces, ps, codes, ws, M, N, K, Y, stream);
+}
+
+size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return skinny(M, K, kSkinnyRowsMx) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
 }
 
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
-                                int64_t K, int ydtype, void* Y, hipStream_t stream) {
+                                int64_t K, int ydtype, void* Y, void* workspace, hipStream_t stream) {
   if (skinny(M, K, kSkinnyRowsMx)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
-  return ydtype == 0 ? launch<F16, 1>(A, As, W, Ws, M, N, K, Y, stream) : launch<BF16, 1>(A, As, W, Ws, M, N, K, Y, stream);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  uint8_t* const as = ws + scale_bytes(N, K);
+  const hipError_t e = launch_scales(Ws, N, ws, As, M, as, K, stream);
+  if (e != hipSuccess) return e;
+  return ydtype == 0 ? launch<F16, 1>(A, as, W, ws, M, N, K, Y, stream) : launch<BF16, 1>(A, as, W, ws, M, N, K, Y, stream);
 }
 
 }  // namespace woq

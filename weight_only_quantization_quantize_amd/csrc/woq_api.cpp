@@ -162,12 +162,12 @@ woq_status check_workspace(const void* workspace, size_t workspace_bytes, size_t
   return WOQ_OK;
 }
 
-// The tile grid of a product: 2^16 - 1 tiles of 64 columns, and activations
-// whose fragments a 32-bit index counts.
+// A product whose tiles and activation fragments 32-bit indexes count.
 woq_status check_mxfp4_gemm(int64_t M, int64_t N, int64_t K) {
   WOQ_TRY(check_mxfp4_shape(M, K, "M"));
   WOQ_TRY(check_mxfp4_shape(N, K, "N"));
-  if (N > 65535 * (int64_t)64 || (M + 255) / 32 * (K / 64 + 2) > INT32_MAX)
+  if (N > (1 << 26) || (M + 63) / 64 * ((N + 63) / 64) > INT32_MAX - 8 || (M + 255) / 32 * (K / 64 + 16) > INT32_MAX ||
+      K > (1 << 23))
     return fail(WOQ_ERR_UNSUPPORTED, "product too large for this library (M=%lld, N=%lld, K=%lld)", (long long)M,
                 (long long)N, (long long)K);
   return WOQ_OK;
@@ -431,14 +431,21 @@ woq_status woq_mxfp4_gemm(const void* X, int32_t xdtype, const void* codes, cons
   WOQ_GUARD_END
 }
 
+size_t woq_mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_mxfp4_gemm(M, N, K) != WOQ_OK) return 0;
+  return woq::mxfp4_gemm_mx_workspace_bytes(M, N, K);
+}
+
 woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const void* codes, const void* scales,
-                             int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream) {
+                             int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   WOQ_GUARD_BEGIN
   WOQ_TRY(check_mxfp4_gemm(M, N, K));
   WOQ_TRY(check_mxfp4_arrays(a_codes, a_scales, "activation"));
   WOQ_TRY(check_mxfp4_arrays(codes, scales, "weight"));
   WOQ_TRY(check_activations(a_codes, ydtype, Y));
-  return from_hip(woq::launch_mxfp4_gemm_mx(a_codes, a_scales, codes, scales, M, N, K, ydtype, Y,
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_gemm_mx_workspace_bytes(M, N, K)));
+  return from_hip(woq::launch_mxfp4_gemm_mx(a_codes, a_scales, codes, scales, M, N, K, ydtype, Y, workspace,
                                             static_cast<hipStream_t>(stream)),
                   "mxfp4_gemm_mx launch");
   WOQ_GUARD_END

@@ -493,8 +493,10 @@ def mxfp4_gemm_mx(
         _check_out(out, (M, N), dtype, "out")
     Y = out if out is not None else torch.empty((M, N), dtype=dtype, device=a_codes.device)
     _require_gpu(a_codes, a_scales, codes, scales, Y)
+    nbytes = int(_lib.call("woq_mxfp4_gemm_mx_workspace_bytes", M, N, K))
+    ws = _mx_workspace(a_codes.device, nbytes)
     _launch("woq_mxfp4_gemm_mx", a_codes.device, a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(),
-            scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr())
+            scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr(), _ptr(ws), nbytes)
     return Y
 
 

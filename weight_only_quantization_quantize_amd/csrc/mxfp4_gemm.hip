@@ -108,6 +108,7 @@ struct Tile4 {
   static constexpr int kUnits = kBytes / 1024;
   static constexpr int kScaleUnits = ROWS / 64;
   static constexpr int kScaleBytes = ROWS * 4;
+  static_assert(kScalePad % ROWS == 0, "a tile's scale loads stay inside the padded array");
   const uint8_t* codes;
   const uint8_t* scales;
   uint32_t scale_step;  // bytes between K tiles of the scale dwords
@@ -266,8 +267,8 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
           const int as = TA::scale(la + kAsAt, row, s, half, h);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(v), bf[j], acc[i][j], kMfmaFp4,
-                                                                        kMfmaFp4, 0, as, 0, bs[j]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], mx_operand(v), acc[i][j], kMfmaFp4,
+                                                                        kMfmaFp4, 0, bs[j], 0, as);
         }
       } else {
 #pragma unroll
@@ -282,35 +283,57 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
           const i32x8_t p2 = piece(2), p1 = piece(1), p0 = piece(0);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p2, bf[j], acc[i][j], kMfmaFp6, kMfmaFp4, 2, as, 0, bs[j]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p2, acc[i][j], kMfmaFp4, kMfmaFp6, 0, bs[j], 2, as);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p1, bf[j], acc[i][j], kMfmaFp6, kMfmaFp4, 1, as, 0, bs[j]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p1, acc[i][j], kMfmaFp4, kMfmaFp6, 0, bs[j], 1, as);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p0, bf[j], acc[i][j], kMfmaFp6, kMfmaFp4, 0, as, 0, bs[j]);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p0, acc[i][j], kMfmaFp4, kMfmaFp6, 0, bs[j], 0, as);
         }
       }
     }
     buf = buf + 1 == C::kStages ? 0 : buf + 1;
   }
   wait_loads<0>();  // none may land in LDS that is another workgroup's by then
+  __syncthreads();  // and nobody reads operands any more
 
-  // D: lane holds column r32, rows 8 (i / 4) + 4 half + i % 4.
+  // D: lane holds row r32 of Y and columns 8 (e / 4) + 4 half + e % 4 (W is the
+  // instruction's first operand for that).  Each wave turns 32 rows at a time
+  // through LDS of its own, so that Y is written in whole rows of the wave's
+  // columns, 16 bytes a lane.
+  constexpr int kPitch = 64 * TN + 16, kChunks = 4 * TN;
+  static_assert(kWaves * 32 * kPitch <= C::kStages * C::kStage, "the turn fits the stages' place");
+  uint8_t* const turn = &lds[0][0] + wave * 32 * kPitch;
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = n0 + (wn + j) * 32 + r32;
-      if (n < N) {
-        uint16_t* const y = Y + (int64_t)m0 * N + n;
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int m = (wm + i) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-          if (m0 + m < M) y[(int64_t)m * N] = YT::from_f32(acc[i][j][e]);
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t lo = (uint32_t)YT::from_f32(acc[i][j][4 * g]) | (uint32_t)YT::from_f32(acc[i][j][4 * g + 1]) << 16;
+        const uint32_t hi = (uint32_t)YT::from_f32(acc[i][j][4 * g + 2]) | (uint32_t)YT::from_f32(acc[i][j][4 * g + 3]) << 16;
+        *reinterpret_cast<u32x2_t*>(turn + r32 * kPitch + 64 * j + 16 * g + 8 * half) = u32x2_t{lo, hi};
+      }
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 32 * kChunks / 64; ++q) {
+      const int row = (64 * q + lane) / kChunks, ch = (64 * q + lane) % kChunks;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(turn + row * kPitch + 16 * ch);
+      const int m = m0 + (wm + i) * 32 + row, n = n0 + wn * 32 + 8 * ch;
+      if (m < M && n < N) {
+        uint16_t* const y = Y + (int64_t)m * N + n;
+        if (n + 8 <= N) {
+          __builtin_memcpy(y, &v, 16);  // of any alignment: N may be odd
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < N) y[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
         }
       }
     }
+    asm volatile("" ::: "memory");
+  }
 }
 
 int64_t padded(int64_t rows) { return (rows + kScalePad - 1) / kScalePad * kScalePad; }

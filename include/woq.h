@@ -334,7 +334,8 @@ woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const vo
                              int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* workspace,
                              size_t workspace_bytes, void* stream);
 
-/* A mixture-of-experts layer on a few tokens (T <= 64, E <= 512):
+/* A mixture-of-experts layer on a few tokens (T <= 64, E <= 512,
+ * top_k <= 64):
  *   logits[t, e] = sum_k X[t, k] router[e, k]   (fp32)
  *   S(t)   = the top_k experts of t by descending logit, the lower index first
  *            among equals (a NaN comes last)
@@ -347,7 +348,7 @@ woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const vo
  * X and p h are split into 6-bit pieces as in woq_mxfp4_gemm; sums over k and
  * i, and the sum over experts, are fp32, Y is rounded once.  No atomics: the
  * same inputs give the same bits.  workspace as above. */
-size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E);
+size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k);
 woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, const void* up_codes,
                          const void* up_scales, const void* down_codes, const void* down_scales, int64_t T, int64_t H,
                          int64_t I, int64_t E, int32_t top_k, void* Y, void* workspace, size_t workspace_bytes,

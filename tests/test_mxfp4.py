@@ -155,7 +155,7 @@ def test_gemm_mx_refuses():
 @pytest.mark.parametrize("case, needle", [
     ("tokens", "1 to 64 tokens"), ("no_tokens", "1 to 64 tokens"), ("router_shape", "router must be"),
     ("router_dtype", "router must be"), ("x_cols", "X must be"), ("down", "up must be"), ("odd_up", "up must be"),
-    ("top_k_0", "top_k"), ("top_k_5", "top_k"), ("experts", "512 experts"), ("grad", "no gradient"),
+    ("top_k_0", "top_k"), ("top_k_5", "top_k"), ("experts", "512 experts"), ("top_k_65", "top_k of up to 64"), ("grad", "no gradient"),
 ])
 def test_moe_refuses(case, needle):
     a = _moe_args()
@@ -180,6 +180,10 @@ def test_moe_refuses(case, needle):
     elif case == "experts":
         for j in range(1, 6):
             a[j] = a[j][:1].expand(513, *a[j].shape[1:])
+    elif case == "top_k_65":
+        for j in range(1, 6):
+            a[j] = a[j][:1].expand(100, *a[j].shape[1:])
+        a[6] = 65
     elif case == "grad":
         a[0].requires_grad_()
     with pytest.raises(ValueError, match=needle):
@@ -236,14 +240,15 @@ def test_abi_workspace_queries():
     assert lib.woq_mxfp4_gemm_workspace_bytes(1, 64, 16416) > 0        # but past the GEMV's K
     for bad in ((0, 64, 64), (4, 0, 64), (4, 64, 63), (4, 64, 0)):
         assert lib.woq_mxfp4_gemm_workspace_bytes(*bad) == 0
-    assert lib.woq_mxfp4_moe_workspace_bytes(1, 64, 32, 4) > 0
-    for bad in ((0, 64, 32, 4), (65, 64, 32, 4), (1, 48, 32, 4), (1, 64, 31, 4), (1, 64, 32, 0), (1, 64, 32, 513)):
+    assert lib.woq_mxfp4_moe_workspace_bytes(1, 64, 32, 4, 2) > 0
+    for bad in ((0, 64, 32, 4, 2), (65, 64, 32, 4, 2), (1, 48, 32, 4, 2), (1, 64, 31, 4, 2), (1, 64, 32, 0, 2),
+                (1, 64, 32, 513, 2), (1, 64, 32, 4, 0), (1, 64, 32, 4, 5), (1, 64, 32, 100, 65)):
         assert lib.woq_mxfp4_moe_workspace_bytes(*bad) == 0
 
 
 def test_abi_moe_refuses():
     lib = _lib.load()
-    need = lib.woq_mxfp4_moe_workspace_bytes(3, 64, 32, 4)
+    need = lib.woq_mxfp4_moe_workspace_bytes(3, 64, 32, 4, 2)
     good = [FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, 3, 64, 32, 4, 2, FAKE, FAKE, need, None]
     _refused("woq_mxfp4_moe", good,
              [(0, None, INVALID), (1, 2, INVALID), (2, None, INVALID), (2, FAKE + 8, INVALID), (3, None, INVALID),

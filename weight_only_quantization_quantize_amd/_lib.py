@@ -57,7 +57,7 @@ SIGNATURES = {
     "woq_mxfp4_gemm": (_i32, [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
     "woq_mxfp4_gemm_mx_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "woq_mxfp4_gemm_mx": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
-    "woq_mxfp4_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "woq_mxfp4_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i32]),
     "woq_mxfp4_moe": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     "woq_probe_stream_read": (_i32, [_vp, _sz, _i32, _i32, _i32, _vp, _i32, _vp]),
     "woq_probe_empty": (_i32, [_i32, _i32, _vp]),

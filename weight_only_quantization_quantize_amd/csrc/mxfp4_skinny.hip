@@ -14,18 +14,9 @@
 // of their own that read the same weights at the same time from the same L2 (a
 // column group's lie a multiple of 8 apart in dispatch order).
 //
-// Loads.  A load of a wave takes 4 rows x 256 contiguous bytes (16 blocks), as
-// long runs as the format has; loads of 16 rows x 64 bytes straight into the
-// matrix operands reached 2.2 TB/s where these reach what a copy does.  The
-// codes then turn in a per-wave LDS buffer, 16 rows x 16 blocks, block c of row
-// r at position c ^ r, so that neither side meets a bank conflict.  The next
-// tile's codes are loaded as soon as this one's are in LDS.
-//
-// K order.  At step s lane (r, q) (r = lane % 16, q = lane / 16) takes block
-// 4 q + s of the super-step, so that its four scale bytes are one dword and the
-// instruction's own byte select picks the step's.
-#include <type_traits>
-
+// Loads.  Units of 16 rows by 512 K in runs of 256 bytes (mxfp4_stream.h): loads
+// of 16 rows x 64 bytes straight into the matrix operands reached 2.2 TB/s.  The
+// next unit is loaded as soon as this one is in LDS.
 #include "mxfp4_stream.h"
 #include "woq_internal.h"
 
@@ -34,8 +25,6 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 constexpr int kMaxThreads = kMaxWaves * 64;
-constexpr int kSuper = 16;          // blocks per super-step
-constexpr int kStageBytes = 16 * 256 + 256;  // codes, then a scale dword per lane
 constexpr int kTargetGroups = 256;  // workgroups: one per compute unit
 
 // One super-step of a chunk of 16 rows of activations.
@@ -55,7 +44,7 @@ template <class YT, int PIECES, int TC, bool RESIDENT>
 __global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ W,
     const uint8_t* __restrict__ Ws, int M, int N, int nblk, int team, int supers, uint16_t* __restrict__ Y) {
-  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kMaxWaves][kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kMaxWaves][kUnitStage];
   __shared__ float4_t part[2][kMaxWaves][TC][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -76,28 +65,10 @@ __global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
     As += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragScaleBytes;
   }
 
-  u32x4_t c[4];
-  uint32_t cs;
-  // Blocks past the row's end are the last one's: the activations are zeros
-  // there.  Scale bytes come as the dword that holds them inside the row.
+  MxUnit u;
+  auto left = [&](int tile) { return (int64_t)(N - tile * 16) * nblk; };  // scale bytes from the tile on
   auto load_weights = [&](int tile, int S) {
-    const uint8_t* const wt = W + (int64_t)tile * 16 * nblk * 16;
-    const uint8_t* const wst = Ws + (int64_t)tile * 16 * nblk;
-    const int rows = N - tile * 16 - 1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int lr = 4 * j + q, n = lr < rows ? lr : rows;
-      int b = kSuper * S + (r ^ lr);
-      b = b < nblk ? b : nblk - 1;
-      c[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wt + (uint32_t)(n * nblk + b) * 16u));
-    }
-    const int n = r < rows ? r : rows, b = kSuper * S + 4 * q;
-    const int bc = b < nblk - 4 ? b : nblk - 4;
-    __builtin_memcpy(&cs, wst + (uint32_t)(n * nblk + bc), 4);
-  };
-  auto aligned_scales = [&](uint32_t v, int S) {
-    const int b = kSuper * S + 4 * q;
-    return b < nblk - 4 ? v : v >> (8 * ((b - (nblk - 4)) & 3));
+    mx_load_unit(u, W + (int64_t)tile * 16 * nblk * 16, Ws + (int64_t)tile * 16 * nblk, N - tile * 16 - 1, left(tile), nblk, S, lane);
   };
   Acts<PIECES> act[TC];
   auto load_acts = [&](int S) {
@@ -113,14 +84,14 @@ __global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
           const u32x4_t v = reinterpret_cast<const u32x4_t*>(A)[(uint32_t)(m * nblk + (b < nblk ? b : nblk - 1))];
           act[t].v[s] = b < nblk ? v : u32x4_t{0u, 0u, 0u, 0u};
         }
-        uint32_t v;
-        __builtin_memcpy(&v, As + (uint32_t)(m * nblk + (b0 < nblk - 4 ? b0 : nblk - 4)), 4);
-        act[t].s = aligned_scales(v, S);
+        const int from = b0 < nblk - 4 ? b0 : nblk - 4;  // a dword inside the row (K >= 128)
+        __builtin_memcpy(&act[t].s, As + (uint32_t)(m * nblk + from), 4);
+        act[t].s >>= 8 * ((b0 - from) & 3);
       } else {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const int64_t f = ((int64_t)t * supers + S) * 4 + s;
-          mx_load_activations(act[t].a[s], A + f * kMxFragBytes, reinterpret_cast<const uint32_t*>(As) + f * 64, lane);
+          mx_load_activations(act[t].a[s], A + f * kMxFragBytes, As + f * kMxFragScaleBytes, mx_place(0, lane));
         }
       }
     }
@@ -137,9 +108,7 @@ __global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
   float4_t acc[TC] = {};
   for (int i = 0, it = 0, k = 0; i < turns * per_turn; ++i) {
     const int S = RESIDENT ? tw : tw + k * team;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(stage + 1024 * j + 16 * lane) = c[j];
-    *reinterpret_cast<uint32_t*>(stage + 4096 + 4 * lane) = aligned_scales(cs, S);
+    mx_stage_unit(u, stage, N - tile * 16 - 1, left(tile), nblk, S, lane);
     const bool wraps = RESIDENT || k + 1 == per_turn;
     const int next = wraps ? (tile + step < tiles ? tile + step : tiles - 1) : tile;
     if constexpr (!RESIDENT) load_acts(S < supers ? S : supers - 1);
@@ -147,29 +116,20 @@ __global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
       const int Sn = RESIDENT || wraps ? tw : S + team;
       load_weights(next, Sn < supers ? Sn : supers - 1);
     }
-    const int scale = (int)*reinterpret_cast<const uint32_t*>(stage + 4096 + 4 * lane);
-    auto at_step = [&](auto sel) {
-      constexpr int s = decltype(sel)::value;
-      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(stage + 256 * r + 16 * ((4 * q + s) ^ r));
-      const i32x8_t wf = mx_operand(w);
-#pragma unroll
-      for (int t = 0; t < TC; ++t) {
-        if constexpr (PIECES == 1) {
-          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(act[t].v[s]), wf, acc[t], kMfmaFp4,
-                                                                    kMfmaFp4, s, (int)act[t].s, s, scale);
-        } else {
-          const MxActivations& a = act[t].a[s];
-          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.p2, wf, acc[t], kMfmaFp6, kMfmaFp4, 2, a.s, s, scale);
-          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.p1, wf, acc[t], kMfmaFp6, kMfmaFp4, 1, a.s, s, scale);
-          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.p0, wf, acc[t], kMfmaFp6, kMfmaFp4, 0, a.s, s, scale);
-        }
-      }
-    };
+    const int scale = mx_staged_scale(stage, lane);
     if (RESIDENT || S < supers) {
-      at_step(std::integral_constant<int, 0>{});
-      at_step(std::integral_constant<int, 1>{});
-      at_step(std::integral_constant<int, 2>{});
-      at_step(std::integral_constant<int, 3>{});
+      mx_each_step([&](auto sel) {
+        constexpr int s = decltype(sel)::value;
+        const i32x8_t w = mx_staged_weights(stage, s, lane);
+#pragma unroll
+        for (int t = 0; t < TC; ++t) {
+          if constexpr (PIECES == 1)
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(act[t].v[s]), w, acc[t], kMfmaFp4,
+                                                                      kMfmaFp4, s, (int)act[t].s, s, scale);
+          else
+            mx_multiply<s>(acc[t], act[t].a[s], w, scale);
+        }
+      });
     }
     ++k;
     if (!wraps) continue;

@@ -178,9 +178,10 @@ woq_status check_mxfp4_moe(int64_t T, int64_t H, int64_t I, int64_t E, int32_t t
   WOQ_TRY(check_mxfp4_shape(E, I, "E"));
   if (top_k < 1 || top_k > E)
     return fail(WOQ_ERR_INVALID_ARGUMENT, "top_k must be in [1, E] (got %d of %lld)", top_k, (long long)E);
-  if (T > woq::mxfp4_moe_max_tokens() || E > woq::mxfp4_moe_max_experts())
-    return fail(WOQ_ERR_UNSUPPORTED, "mxfp4_moe takes up to %d tokens and %d experts (got %lld, %lld)",
-                woq::mxfp4_moe_max_tokens(), woq::mxfp4_moe_max_experts(), (long long)T, (long long)E);
+  if (T > woq::mxfp4_moe_max_tokens() || E > woq::mxfp4_moe_max_experts() || top_k > woq::mxfp4_moe_max_top_k())
+    return fail(WOQ_ERR_UNSUPPORTED, "mxfp4_moe takes up to %d tokens, %d experts and a top_k of %d (got %lld, %lld, %d)",
+                woq::mxfp4_moe_max_tokens(), woq::mxfp4_moe_max_experts(), woq::mxfp4_moe_max_top_k(), (long long)T,
+                (long long)E, top_k);
   if (H > (1 << 20) || I > (1 << 20))
     return fail(WOQ_ERR_UNSUPPORTED, "layer too large for this library (H=%lld, I=%lld)", (long long)H, (long long)I);
   return WOQ_OK;
@@ -451,9 +452,9 @@ woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const vo
   WOQ_GUARD_END
 }
 
-size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E) {
-  if (check_mxfp4_moe(T, H, I, E, 1) != WOQ_OK) return 0;
-  return woq::mxfp4_moe_workspace_bytes(T, H, I, E);
+size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k) {
+  if (check_mxfp4_moe(T, H, I, E, top_k) != WOQ_OK) return 0;
+  return woq::mxfp4_moe_workspace_bytes(T, H, I, E, top_k);
 }
 
 woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, const void* up_codes,
@@ -467,7 +468,7 @@ woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, cons
     return fail(WOQ_ERR_INVALID_ARGUMENT, "router must be non-NULL and 16-byte aligned");
   WOQ_TRY(check_mxfp4_arrays(up_codes, up_scales, "up"));
   WOQ_TRY(check_mxfp4_arrays(down_codes, down_scales, "down"));
-  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_moe_workspace_bytes(T, H, I, E)));
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_moe_workspace_bytes(T, H, I, E, top_k)));
   return from_hip(woq::launch_mxfp4_moe(X, xdtype, router, up_codes, up_scales, down_codes, down_scales, T, H, I, E,
                                         top_k, Y, workspace, static_cast<hipStream_t>(stream)),
                   "mxfp4_moe launch");

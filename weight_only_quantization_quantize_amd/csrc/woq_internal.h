@@ -161,7 +161,8 @@ hipError_t launch_mxfp4_skinny_mx(const void* A, const void* As, const void* cod
 // A mixture-of-experts layer on a few tokens.
 int mxfp4_moe_max_tokens();
 int mxfp4_moe_max_experts();
-size_t mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E);
+int mxfp4_moe_max_top_k();
+size_t mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
 hipError_t launch_mxfp4_moe(const void* X, int xdtype, const void* router, const void* up_codes,
                             const void* up_scales, const void* down_codes, const void* down_scales, int64_t T,
                             int64_t H, int64_t I, int64_t E, int top_k, void* Y, void* workspace, hipStream_t stream);

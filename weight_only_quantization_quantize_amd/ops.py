@@ -526,9 +526,10 @@ def mxfp4_moe(
     if not 1 <= top_k <= E:
         raise ValueError(f"top_k must be in [1, {E}] (got {top_k})")
     T = X.shape[0]
-    nbytes = int(_lib.call("woq_mxfp4_moe_workspace_bytes", T, H, I, E))
+    nbytes = int(_lib.call("woq_mxfp4_moe_workspace_bytes", T, H, I, E, top_k))
     if nbytes == 0:
-        raise ValueError(f"mxfp4_moe takes 1 to 64 tokens and up to 512 experts (got T={T}, H={H}, I={I}, E={E})")
+        raise ValueError(f"mxfp4_moe takes 1 to 64 tokens, up to 512 experts and a top_k of up to 64 (got T={T}, H={H}, "
+                         f"I={I}, E={E}, top_k={top_k})")
     _no_grad(X, router)
     if out is not None:
         _check_out(out, (T, H), X.dtype, "out")

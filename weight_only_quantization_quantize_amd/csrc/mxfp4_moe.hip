@@ -11,21 +11,19 @@
 // units (mxfp4_stream.h); each further 16 tokens take a turn of their own, out of
 // L2.  (All chunks in one turn needs 64 sums a lane more and spilled.)
 //
-// Three launches:
-//   route  logits, one workgroup per expert and 8 tokens; x split into pieces
-//   up     one workgroup per (chosen expert, 32 columns of h).  Each works out
-//          the choice from the logits itself, which takes less than a launch
-//          would: where the tokens choose fewer experts than there are
-//          (T top_k < E), waves choose for a token each and the workgroup takes
-//          the slot-th chosen expert; otherwise a slot is an expert and only its
-//          rank among the logits is counted, a token a lane.  Gate and up rows,
-//          then w silu(g) u with w = exp(logit - max), split into pieces again
-//          (14 bits of a block's largest magnitude), one row per token of the
-//          expert.  The weight is folded in here, where the values are still
-//          fp32, so that the next product adds over experts by itself.
-//   down   one workgroup per 16 columns of y, over all slots: each wave adds its
-//          products into a sum per token in LDS of its own, the waves' sums are
-//          added in a fixed order (no atomics) and divided by the sum of w.
+// Four launches:
+//   route   logits, one workgroup per expert and 8 tokens; x split into pieces
+//   choose  one workgroup: the tokens' experts and shares, and the list of turns
+//           (an expert and up to 16 of its tokens, in ascending order)
+//   up      one workgroup per (turn, 32 columns of h): gate and up rows, then
+//           p silu(g) u, split into pieces again (14 bits of a block's largest
+//           magnitude).  The share is folded in here, where the values are still
+//           fp32, so that the next product adds over experts by itself.
+//   down    one workgroup per 16 columns of y, over all turns: each wave adds its
+//           products into a sum per token in LDS of its own, and the waves' sums
+//           are added in a fixed order (no atomics).
+// Working the choice out in every workgroup of the up launch instead of in a
+// launch of its own took 4 us there for one token and 15 for five.
 #include "mxfp4_stream.h"
 #include "woq_internal.h"
 
@@ -36,17 +34,22 @@ constexpr int kChunk = 16;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 64;
-constexpr int kMaxTurns = 4 * kMaxExperts;
-constexpr int kRouteThreads = 256;
+constexpr int kMaxTurns = kMaxExperts + kMaxTokens * kMaxTopK / 16;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteTokens = 8;   // tokens per workgroup of the logits
-constexpr int kUpWaves = 4;
+constexpr int kChooseWaves = 16;
+constexpr int kUpWaves = 8;         // at most
 constexpr int kDownWaves = 8;
 
-// What the up launch leaves for the down launch about a slot.
-struct Slot {
-  int expert, count;          // its tokens
-  float w[kMaxTokens];        // their weights, by the order of `token`
-  uint8_t token[kMaxTokens];  // ascending
+// An expert and up to 16 of its tokens.
+struct Turn {
+  int expert, count;
+  float share[kChunk];
+  uint8_t token[kChunk];
+};
+struct Plan {
+  int turns;
+  int pad[3];
 };
 
 // A logit's order as an unsigned number; the zeros are equal and a NaN comes
@@ -55,6 +58,9 @@ __device__ inline uint32_t order_key(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
   if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ inline float key_value(uint32_t k) {
+  return __builtin_bit_cast(float, k == 0 ? 0x7FC00000u : ((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k));
 }
 
 __device__ inline uint32_t wave_max(uint32_t v) {
@@ -71,9 +77,9 @@ __device__ inline uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// logits [E][64].  Workgroups [0, groups E) compute logits, the rest split x
+// logits [64][E].  Workgroups [0, groups E) compute logits, the rest split x
 // (fragments of 16 rows, super-step order).
-template <class XT>
+template <class XT, int TOKENS>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const uint16_t* __restrict__ X,
                                                                   const uint16_t* __restrict__ router, int T, int H,
                                                                   int E, int groups, float* __restrict__ logits,
@@ -90,18 +96,18 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const uint16_t
     mx_store_pieces(mx_split(v), xp + f * kMxFragBytes, xs + f * 64, (b % kSuper / 4) * kChunk + t % kChunk);
     return;
   }
-  __shared__ float part[kRouteThreads / 64][kRouteTokens];
-  const int e = (int)blockIdx.x / groups, t0 = (int)blockIdx.x % groups * kRouteTokens;
-  const int n = T - t0 < kRouteTokens ? T - t0 : kRouteTokens;
-  float a[kRouteTokens] = {};
+  __shared__ float part[kRouteThreads / 64][TOKENS];
+  const int e = (int)blockIdx.x / groups, t0 = (int)blockIdx.x % groups * TOKENS;
+  const int n = T - t0 < TOKENS ? T - t0 : TOKENS;
+  float a[TOKENS] = {};
   for (int k = (int)threadIdx.x * 8; k < H; k += kRouteThreads * 8) {
     const u32x4_t w = *reinterpret_cast<const u32x4_t*>(router + (int64_t)e * H + k);
-    u32x4_t v[kRouteTokens];
+    u32x4_t v[TOKENS];
 #pragma unroll
-    for (int t = 0; t < kRouteTokens; ++t)
+    for (int t = 0; t < TOKENS; ++t)
       v[t] = *reinterpret_cast<const u32x4_t*>(X + (int64_t)(t0 + (t < n ? t : n - 1)) * H + k);
 #pragma unroll
-    for (int t = 0; t < kRouteTokens; ++t)
+    for (int t = 0; t < TOKENS; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         a[t] = fmaf(XT::to_f32((uint16_t)(v[t][j] & 0xFFFFu)), XT::to_f32((uint16_t)(w[j] & 0xFFFFu)), a[t]);
@@ -109,7 +115,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const uint16_t
       }
   }
 #pragma unroll
-  for (int t = 0; t < kRouteTokens; ++t) {
+  for (int t = 0; t < TOKENS; ++t) {
     const float s = team_sum(a[t], 64);
     if (lane == 0) part[wave][t] = s;
   }
@@ -118,294 +124,254 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const uint16_t
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kRouteThreads / 64; ++w) s += part[w][threadIdx.x];
-    logits[e * kMaxTokens + t0 + threadIdx.x] = s;
+    logits[(t0 + (int)threadIdx.x) * E + e] = s;
   }
 }
 
-// Workgroup (i, slot): columns [32 i, 32 i + 32) of h for the slot's expert.
-__global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(const uint8_t* __restrict__ xp,
-                                                                  const uint32_t* __restrict__ xs,
+// One workgroup.  logits [T][E] -> the plan and its turns.
+// NJ: lanes' experts, 64 NJ >= E.
+template <int NJ>
+__global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const float* __restrict__ logits, int T, int E,
+                                                                       int top_k, Plan* __restrict__ plan,
+                                                                       Turn* __restrict__ turns) {
+  __shared__ uint16_t ids[kMaxTokens * kMaxTopK];      // [token][choice]
+  __shared__ float shares[kMaxTokens * kMaxTopK];
+  __shared__ unsigned long long tokens[kMaxExperts];   // of an expert
+  __shared__ uint16_t base[kMaxExperts];               // its first turn
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int e = threadIdx.x; e < E; e += kChooseWaves * 64) tokens[e] = 0;
+  __syncthreads();
+  constexpr int kTokens = kMaxTokens / kChooseWaves;  // of a wave, at most
+  float logit[kTokens][NJ];                           // of expert 64 j + lane
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int t = wave + kChooseWaves * i, e = 64 * j + lane;
+      logit[i][j] = t < T && e < E ? logits[t * E + e] : 0.0f;
+    }
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const int t = wave + kChooseWaves * i;
+    if (t >= T) break;
+    uint32_t key[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = 64 * j + lane < E ? order_key(logit[i][j]) : 0u;
+    uint32_t taken = 0;  // bit j: expert 64 j + lane
+    for (int c = 0; c < top_k; ++c) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (!(taken >> j & 1) && key[j] > m) m = key[j];
+      m = wave_max(m);
+      int id = -1;  // the lowest index of that key
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (id < 0) {
+          const uint64_t b = __ballot(!(taken >> j & 1) && key[j] == m && 64 * j + lane < E);
+          if (b) id = 64 * j + __builtin_ctzll(b);
+        }
+      if (lane == (id & 63)) taken |= 1u << (id >> 6);
+      if (lane == 0) {
+        ids[t * top_k + c] = (uint16_t)id;
+        shares[t * top_k + c] = key_value(m);
+        atomicOr(&tokens[id], 1ull << t);
+      }
+    }
+    // softmax over the choices, one a lane
+    const float w = lane < top_k ? expf(shares[t * top_k + lane] - shares[t * top_k]) : 0.0f;
+    const float sum = team_sum(w, 64);
+    if (lane < top_k) shares[t * top_k + lane] = w / sum;
+  }
+  __syncthreads();
+  if (wave == 0) {  // turns before each expert's
+    int at = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane;
+      const int n = e < E ? (__popcll(tokens[e]) + kChunk - 1) / kChunk : 0;
+      int upto = n;
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += o;
+      }
+      if (e < E) base[e] = (uint16_t)(at + upto - n);
+      at += __shfl(upto, 63, 64);
+    }
+    if (lane == 0) plan->turns = at;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kChooseWaves * 64) {
+    const int n = __popcll(tokens[e]);
+    for (int c = 0; c * kChunk < n; ++c) {
+      Turn& r = turns[base[e] + c];
+      r.expert = e;
+      r.count = n - c * kChunk < kChunk ? n - c * kChunk : kChunk;
+    }
+  }
+  for (int i = threadIdx.x; i < T * top_k; i += kChooseWaves * 64) {
+    const int t = i / top_k, e = ids[i];
+    const int row = __popcll(tokens[e] & ((1ull << t) - 1));
+    Turn& r = turns[base[e] + row / kChunk];
+    r.share[row % kChunk] = shares[i];
+    r.token[row % kChunk] = (uint8_t)t;
+  }
+}
+
+// Workgroup (i, turn): columns [32 i, 32 i + 32) of h for the turn's tokens.
+__global__ __launch_bounds__(kUpWaves * 64, 3) void moe_up_kernel(const uint8_t* __restrict__ xp,
+                                                                  const uint8_t* __restrict__ xs,
                                                                   const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales,
-                                                                  const float* __restrict__ logits, int T, int H,
-                                                                  int I, int E, int top_k, int by_token, int chunks,
-                                                                  Slot* __restrict__ slots, uint8_t* __restrict__ hp,
-                                                                  uint32_t* __restrict__ hs) {
-  constexpr int NT = 4;  // 2 tiles of gate rows, 2 of up rows
-  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kUpWaves][NT][kUnitStage];
+                                                                  const Plan* __restrict__ plan,
+                                                                  const Turn* __restrict__ turns, int H, int I, int E,
+                                                                  uint8_t* __restrict__ hp, uint32_t* __restrict__ hs) {
+  constexpr int NT = 4;  // gate rows, up rows, gate rows, up rows
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kUpWaves][kUnitStage];
   __shared__ float hbuf[kChunk][kMxBlock + 1];
-  __shared__ uint64_t words[kMaxExperts / 64];            // chosen experts, by token
-  __shared__ uint16_t ids[kMaxExperts];                   // [token][choice]: T top_k < E of them
-  __shared__ float weight[kMaxTokens];
-  __shared__ int ranks[kUpWaves][kMaxTokens];
-  __shared__ uint32_t tops[kUpWaves][kMaxTokens];
-  __shared__ uint8_t token[kMaxTokens];
-  __shared__ uint64_t chosen_by;
-  static_assert(kUpWaves * NT * 1024 <= (int)sizeof(stage_all), "the partial sums fit the stages' place");
+  static_assert(NT * 1024 <= kUnitStage, "a wave's partial sums fit its stage's place");
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = blockIdx.y, i0 = (int)blockIdx.x * kMxBlock;
-
-  // The slot's expert, the tokens that chose it and their weights.
-  int e = slot;
-  if (by_token) {
-    if (threadIdx.x < kMaxExperts / 64) words[threadIdx.x] = 0;
-    __syncthreads();
-    for (int t = wave; t < T; t += kUpWaves) {
-      uint32_t key[kMaxExperts / 64];
-#pragma unroll
-      for (int j = 0; j < kMaxExperts / 64; ++j)
-        if (64 * j < E) key[j] = 64 * j + lane < E ? order_key(logits[(64 * j + lane) * kMaxTokens + t]) : 0u;
-      uint32_t taken = 0;  // bit j: expert 64 j + lane
-      for (int c = 0; c < top_k; ++c) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < kMaxExperts / 64; ++j)
-          if (64 * j < E && !(taken >> j & 1) && key[j] > m) m = key[j];
-        m = wave_max(m);
-        int id = -1;  // the lowest index of that key
-#pragma unroll
-        for (int j = 0; j < kMaxExperts / 64; ++j) {
-          if (64 * j < E && id < 0) {
-            const uint64_t b = __ballot(!(taken >> j & 1) && key[j] == m && 64 * j + lane < E);
-            if (b) id = 64 * j + __builtin_ctzll(b);
-          }
-        }
-        if (lane == (id & 63)) taken |= 1u << (id >> 6);
-        if (lane == 0) {
-          ids[t * top_k + c] = (uint16_t)id;
-          atomicOr(reinterpret_cast<unsigned long long*>(&words[id >> 6]), 1ull << (id & 63));
-        }
-      }
-    }
-    __syncthreads();
-    int left = slot;
-    e = -1;
-    for (int j = 0; j < kMaxExperts / 64 && e < 0; ++j) {
-      uint64_t w = words[j];
-      const int n = __popcll(w);
-      if (left >= n) {
-        left -= n;
-      } else {
-        for (; left > 0; --left) w &= w - 1;
-        e = 64 * j + __builtin_ctzll(w);
-      }
-    }
-    e = __builtin_amdgcn_readfirstlane(e);
-    if (wave == 0) {
-      bool mine = false;
-      float w = 0.0f;
-      if (lane < T && e >= 0) {
-        for (int c = 0; c < top_k; ++c) mine |= ids[lane * top_k + c] == e;
-        w = expf(logits[e * kMaxTokens + lane] - logits[(int)ids[lane * top_k] * kMaxTokens + lane]);
-      }
-      const uint64_t b = __ballot(mine);
-      weight[lane] = mine ? w : 0.0f;
-      if (lane == 0) chosen_by = b;
-    }
-  } else {
-    // rank of e among the logits of token `lane`, a share of the experts a wave
-    const float own = lane < T ? logits[e * kMaxTokens + lane] : 0.0f;
-    const uint32_t key = order_key(own);
-    int rank = 0;
-    uint32_t top = 0;
-    float top_logit = 0.0f;
-    for (int j = wave; j < E; j += kUpWaves) {
-      const uint32_t k = order_key(lane < T ? logits[j * kMaxTokens + lane] : 0.0f);
-      rank += (k > key || (k == key && j < e)) ? 1 : 0;
-      top = k > top ? k : top;
-    }
-    ranks[wave][lane] = rank;
-    tops[wave][lane] = top;
-    __syncthreads();
-    if (wave == 0) {
-      for (int w = 1; w < kUpWaves; ++w) {
-        rank += ranks[w][lane];
-        top = tops[w][lane] > top ? tops[w][lane] : top;
-      }
-      // the logit of that key (all NaN: key 0, and the weight is a NaN)
-      top_logit = __builtin_bit_cast(float, top == 0 ? 0x7FC00000u : ((top & 0x80000000u) ? top & 0x7FFFFFFFu : ~top));
-      const bool mine = lane < T && rank < top_k;
-      const uint64_t b = __ballot(mine);
-      weight[lane] = mine ? expf(own - top_logit) : 0.0f;
-      if (lane == 0) chosen_by = b;
-    }
-  }
-  __syncthreads();
-  const uint64_t mask = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(chosen_by >> 32)) << 32 |
-                        (uint32_t)__builtin_amdgcn_readfirstlane((int)chosen_by);
-  const int count = __popcll(mask);
-  if (wave == 0 && (mask >> lane & 1)) token[__popcll(mask & ((1ull << lane) - 1))] = (uint8_t)lane;
-  __syncthreads();
-  if (blockIdx.x == 0 && wave == 0) {
-    Slot& s = slots[slot];
-    if (lane == 0) {
-      s.expert = e;
-      s.count = count;
-    }
-    if (lane < count) {
-      s.token[lane] = token[lane];
-      s.w[lane] = weight[token[lane]];
-    }
-  }
-  if (count == 0) return;
+  const int turn = blockIdx.y, i0 = (int)blockIdx.x * kMxBlock;
+  if (turn >= plan->turns) return;
+  const Turn& rec = turns[turn];
+  const int e = rec.expert, count = rec.count;
 
   const int nblk = H / kMxBlock, supers = (H + 511) / 512, hsupers = (I + 511) / 512;
   const int64_t rows_left = (int64_t)E * 2 * I - ((int64_t)e * 2 * I + i0);
   const uint8_t* const wcodes = codes + ((int64_t)e * 2 * I + i0) * nblk * 16;
   const uint8_t* const wscales = scales + ((int64_t)e * 2 * I + i0) * nblk;
-  auto tile_row = [&](int j) { return (j >= 2 ? I : 0) + (j & 1) * 16; };
-  MxUnit u[NT];
-  auto load = [&](int S) {
+  const int waves = blockDim.x >> 6;  // wave w takes super-steps w, w + waves, ...
+  uint8_t* const stage = stage_all[wave];
+  // tiles in the order gate, up, gate, up; two units in flight, loaded in order;
+  // past the end a line or two of the first rows is loaded in their place
+  MxUnit u[2];
+  auto row_of = [&](int j) { return (j & 1 ? I : 0) + (j >> 1) * 16; };
+  auto ahead = [&](int j, int S_) {
+    const bool more = S_ < supers;
+    const int S = more ? S_ : 0;
+    const int64_t row = more ? row_of(j) : 0;
+    __builtin_amdgcn_sched_barrier(0);
+    mx_load_unit(u[j & 1], wcodes + row * nblk * 16, wscales + row * nblk, 15, (rows_left - row) * nblk, more ? nblk : 1, S, lane);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  float4_t acc[NT] = {};
+  int S = wave;
+  // rows past the turn's last token repeat it
+  const int t = rec.token[(lane & 15) < count ? lane & 15 : count - 1];
+  const MxPlace place = mx_place(t / kChunk * supers * 4, (lane & 48) + t % kChunk);
+  ahead(0, S);
+  ahead(1, S);
+  for (; S < supers; S += waves) {
+    MxActivations a[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      mx_load_activations(a[s], xp + (int64_t)(S * 4 + s) * kMxFragBytes, xs + (int64_t)(S * 4 + s) * kMxFragScaleBytes, place);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int64_t row = tile_row(j);
-      mx_load_unit(u[j], wcodes + row * nblk * 16, wscales + row * nblk, 15, (rows_left - row) * nblk, nblk, S, lane);
-    }
-  };
-  float* const part = reinterpret_cast<float*>(&stage_all[0][0][0]);  // [wave][tile][lane][4]
-  // an expert with more than 16 tokens takes another turn over its weights, out of L2
-  for (int c = 0; c * kChunk < count; ++c) {
-    const int own = c * kChunk + (lane & 15), t = token[own < count ? own : count - 1];
-    const MxPlace place = mx_place(t / kChunk * supers * 4, (lane & 48) + t % kChunk);
-    float4_t acc[NT] = {};
-    int S = wave;
-    if (S < supers) load(S);
-    for (; S < supers; S += kUpWaves) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        mx_stage_unit(u[j], stage_all[wave][j], 15, (rows_left - tile_row(j)) * nblk, nblk, S, lane);
-      if (S + kUpWaves < supers) load(S + kUpWaves);
-      int sc[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) sc[j] = mx_staged_scale(stage_all[wave][j], lane);
+      mx_stage_unit(u[j & 1], stage, 15, (rows_left - row_of(j)) * nblk, nblk, S, lane);
+      ahead((j + 2) & 3, j < 2 ? S : S + waves);
+      const int sc = mx_staged_scale(stage, lane);
       mx_each_step([&](auto sel) {
         constexpr int s = decltype(sel)::value;
-        MxActivations a;
-        const int64_t f = S * 4 + s;
-        mx_load_activations(a, xp + f * kMxFragBytes, reinterpret_cast<const uint8_t*>(xs) + f * kMxFragScaleBytes, place);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mx_multiply<s>(acc[j], a, mx_staged_weights(stage_all[wave][j], s, lane), sc[j]);
+        mx_multiply<s>(acc[j], a[s], mx_staged_weights(stage, s, lane), sc);
       });
     }
-    __syncthreads();
+  }
+  // the waves' partial sums meet in the stages' place, [tile][lane][4] a wave
 #pragma unroll
-    for (int j = 0; j < NT; ++j) *reinterpret_cast<float4_t*>(part + ((wave * NT + j) * 64 + lane) * 4) = acc[j];
-    __syncthreads();
-    // two elements of the 16 x 32 block of h a thread
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      const int tm = (int)(threadIdx.x >> 5) + 8 * o, tn = threadIdx.x & 31;
-      const int sl = (tm >> 2) * 16 + (tn & 15);
-      float g = 0.0f, v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kUpWaves; ++w) {
-        g += part[((w * NT + (tn >> 4)) * 64 + sl) * 4 + (tm & 3)];
-        v += part[((w * NT + 2 + (tn >> 4)) * 64 + sl) * 4 + (tm & 3)];
-      }
-      const int row = c * kChunk + tm;
-      hbuf[tm][tn] = row < count ? weight[token[row]] * (g / (1.0f + expf(-g))) * v : 0.0f;
+  for (int j = 0; j < NT; ++j) *reinterpret_cast<float4_t*>(stage + (j * 64 + lane) * 16) = acc[j];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kChunk * kMxBlock; o += (int)blockDim.x) {
+    const int tm = o >> 5, tn = o & 31;
+    const int sl = (tm >> 2) * 16 + (tn & 15);
+    float g = 0.0f, v = 0.0f;
+    for (int w = 0; w < waves; ++w) {
+      const float* const part = reinterpret_cast<const float*>(stage_all[w]);
+      g += part[((tn >> 4) * 128 + sl) * 4 + (tm & 3)];
+      v += part[((tn >> 4) * 128 + 64 + sl) * 4 + (tm & 3)];
     }
-    __syncthreads();
-    // 16 threads split a row's block each; behind the last block of h the rest
-    // of its super-step is zeros
-    const int blk = i0 / kMxBlock, last = blk == I / kMxBlock - 1 ? kSuper * hsupers - blk : 1;
-    if ((int)threadIdx.x < kChunk * last) {
-      const int m = threadIdx.x & 15, b = blk + (int)(threadIdx.x >> 4);
-      float v[kMxBlock];
+    hbuf[tm][tn] = tm < count ? rec.share[tm] * (g / (1.0f + expf(-g))) * v : 0.0f;
+  }
+  __syncthreads();
+  // 16 threads split a row's block each; behind the last block of h the rest of
+  // its super-step is zeros
+  const int blk = i0 / kMxBlock, last = blk == I / kMxBlock - 1 ? kSuper * hsupers - blk : 1;
+  for (int o = threadIdx.x; o < kChunk * last; o += (int)blockDim.x) {
+    const int m = o & 15, b = blk + (o >> 4);
+    float v[kMxBlock];
 #pragma unroll
-      for (int k = 0; k < kMxBlock; ++k) v[k] = b == blk ? hbuf[m][k] : 0.0f;
-      const int64_t f = (((int64_t)slot * chunks + c) * hsupers + b / kSuper) * 4 + b % 4;
-      mx_store_pieces(mx_split(v), hp + f * kMxFragBytes, hs + f * 64, (b % kSuper / 4) * kChunk + m);
-    }
+    for (int k = 0; k < kMxBlock; ++k) v[k] = b == blk ? hbuf[m][k] : 0.0f;
+    const int64_t f = ((int64_t)turn * hsupers + b / kSuper) * 4 + b % 4;
+    mx_store_pieces(mx_split(v), hp + f * kMxFragBytes, hs + f * 64, (b % kSuper / 4) * kChunk + m);
   }
 }
 
 // Workgroup: columns [16 b, 16 b + 16) of y for all tokens.
 template <class YT, int TC>
 __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(const uint8_t* __restrict__ hp,
-                                                                   const uint32_t* __restrict__ hs,
+                                                                   const uint8_t* __restrict__ hs,
                                                                    const uint8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales,
-                                                                   const Slot* __restrict__ slots, int nslots, int T,
-                                                                   int H, int I, int E, uint16_t* __restrict__ Y) {
-  constexpr int kRows = TC * kChunk, chunks = TC;
+                                                                   const Plan* __restrict__ plan,
+                                                                   const Turn* __restrict__ turns, int T, int H, int I,
+                                                                   int E, uint16_t* __restrict__ Y) {
+  constexpr int kRows = TC * kChunk;
   __shared__ __attribute__((aligned(16))) uint8_t stage_all[kDownWaves][kUnitStage];
   __shared__ float sums[kDownWaves][kRows][kChunk + 1];
-  __shared__ float total[kRows];
-  __shared__ uint16_t list[kMaxExperts], experts[kMaxExperts], counts[kMaxExperts];
-  __shared__ uint16_t turn[kMaxTurns];  // (place in the list) * 4 + chunk
-  __shared__ int live, turns;
+  __shared__ uint32_t table[kMaxTurns];  // expert + count << 16
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (wave == 0) {  // the slots that have tokens
-    int n = 0;
-    for (int s0 = 0; s0 < nslots; s0 += 64) {
-      const int c = s0 + lane < nslots ? slots[s0 + lane].count : 0;
-      const uint64_t b = __ballot(c > 0);
-      if (c > 0) {
-        const int at = n + __popcll(b & ((1ull << lane) - 1));
-        list[at] = (uint16_t)(s0 + lane);
-        experts[at] = (uint16_t)slots[s0 + lane].expert;
-        counts[at] = (uint16_t)c;
-      }
-      n += __popcll(b);
-    }
-    if (lane == 0) live = n;
-    // a slot's chunks of 16 tokens, one turn each
-    int at = 0;
-    for (int k0 = 0; k0 < n; k0 += 64) {
-      const int k = k0 + lane, c = k < n ? (counts[k] + kChunk - 1) / kChunk : 0;
-      int before = c;  // inclusive sum over the lanes
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(before, off, 64);
-        if (lane >= off) before += o;
-      }
-      for (int i = 0; i < c; ++i) turn[at + before - c + i] = (uint16_t)(4 * k + i);
-      at += __shfl(before, 63, 64);
-    }
-    if (lane == 0) turns = at;
-  }
-  for (int o = threadIdx.x; o < kDownWaves * kRows * (kChunk + 1); o += kDownWaves * 64) (&sums[0][0][0])[o] = 0.0f;
-  __syncthreads();
   const int nblk = I / kMxBlock, supers = (I + 511) / 512;
-  const int slots_live = __builtin_amdgcn_readfirstlane(live);
-  const int units = __builtin_amdgcn_readfirstlane(turns) * supers;
+  const int nturns = plan->turns, units = nturns * supers;
   const int n0 = (int)blockIdx.x * 16;
   uint8_t* const stage = stage_all[wave];
+  for (int k = threadIdx.x; k < nturns; k += kDownWaves * 64) table[k] = (uint32_t)turns[k].expert | (uint32_t)turns[k].count << 16;
+  for (int o = lane; o < kRows * (kChunk + 1); o += 64) (&sums[wave][0][0])[o] = 0.0f;
+  __syncthreads();
   // the wave's run of units: a turn's super-steps follow one another
   const int u0 = (int)((int64_t)units * wave / kDownWaves), u1 = (int)((int64_t)units * (wave + 1) / kDownWaves);
-  auto load = [&](MxUnit& u, int i) {
-    const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(experts[turn[i / supers] >> 2]) * H + n0;
-    mx_load_unit(u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, i % supers, lane);
+  struct Work {
+    MxUnit u;
+    MxActivations a[4];
+    uint32_t token;  // of rows 4 q .. 4 q + 3
+  };
+  auto load = [&](Work& w, int i) {
+    const int k = i / supers, S = i % supers;
+    const uint32_t rec = (uint32_t)__builtin_amdgcn_readfirstlane((int)table[k]);
+    const int64_t row = (int64_t)(rec & 0xFFFFu) * H + n0;
+    mx_load_unit(w.u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, S, lane);
+    // rows past the turn's tokens are left as they are: their sums are not taken
+    if ((lane & 15) < (int)(rec >> 16)) {
+      const MxPlace place = mx_place(0, lane);
+      const int64_t f = ((int64_t)k * supers + S) * 4;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mx_load_activations(w.a[s], hp + (f + s) * kMxFragBytes, hs + (f + s) * kMxFragScaleBytes, place);
+    }
+    w.token = reinterpret_cast<const uint32_t*>(turns[k].token)[lane >> 4];
   };
   float4_t acc = {};
-  auto work = [&](const MxUnit& u, int i) {
-    const int k4 = __builtin_amdgcn_readfirstlane(turn[i / supers]), k = k4 >> 2, c = k4 & 3, S = i % supers;
-    const int sl = __builtin_amdgcn_readfirstlane(list[k]), count = __builtin_amdgcn_readfirstlane(counts[k]);
-    const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(experts[k]) * H + n0;
-    mx_stage_unit(u, stage, 15, ((int64_t)E * H - row) * nblk, nblk, S, lane);
+  auto work = [&](const Work& w, int i) {
+    const int k = i / supers, S = i % supers;
+    const uint32_t rec = (uint32_t)__builtin_amdgcn_readfirstlane((int)table[k]);
+    const int64_t row = (int64_t)(rec & 0xFFFFu) * H + n0;
+    mx_stage_unit(w.u, stage, 15, ((int64_t)E * H - row) * nblk, nblk, S, lane);
     const int sc = mx_staged_scale(stage, lane);
-    const int left = count - c * kChunk;  // rows past the last repeat it: their sums are not taken
-    const MxPlace place = mx_place(0, (lane & 48) + ((lane & 15) < left ? lane & 15 : left - 1));
     mx_each_step([&](auto sel) {
       constexpr int s = decltype(sel)::value;
-      MxActivations a;
-      const int64_t f = (((int64_t)sl * chunks + c) * supers + S) * 4 + s;
-      mx_load_activations(a, hp + f * kMxFragBytes, reinterpret_cast<const uint8_t*>(hs) + f * kMxFragScaleBytes, place);
-      mx_multiply<s>(acc, a, mx_staged_weights(stage, s, lane), sc);
+      mx_multiply<s>(acc, w.a[s], mx_staged_weights(stage, s, lane), sc);
     });
     if (S == supers - 1 || i + 1 == u1) {  // the wave is through with the turn
+      const int count = (int)(rec >> 16);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 4 * (lane >> 4) + e;
-        if (r < left) sums[wave][slots[sl].token[c * kChunk + r]][lane & 15] += acc[e];
-      }
+      for (int e = 0; e < 4; ++e)
+        if (4 * (lane >> 4) + e < count) sums[wave][w.token >> (8 * e) & 63u][lane & 15] += acc[e];
       acc = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
   };
-  MxUnit a, b;
+  Work a = {}, b = {};
   if (u0 < u1) load(a, u0);
   if (u0 + 1 < u1) load(b, u0 + 1);
   for (int i = u0; i < u1; i += 2) {
@@ -414,39 +380,31 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(const uint8_t
     if (i + 1 < u1) work(b, i + 1);
     if (i + 3 < u1) load(b, i + 3);
   }
-  // the sum of a token's weights, slots in order
-  if ((int)threadIdx.x < kRows) total[threadIdx.x] = 0.0f;
-  __syncthreads();
-  if (wave == 0) {
-    for (int k = 0; k < slots_live; ++k) {
-      const Slot& s = slots[list[k]];
-      if (lane < s.count) total[s.token[lane]] += s.w[lane];
-    }
-  }
   __syncthreads();
   for (int o = threadIdx.x; o < T * kChunk; o += kDownWaves * 64) {
     const int t = o / kChunk, n = o % kChunk;
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kDownWaves; ++w) v += sums[w][t][n];
-    Y[(int64_t)t * H + n0 + n] = YT::from_f32(v / total[t]);
+    Y[(int64_t)t * H + n0 + n] = YT::from_f32(v);
   }
 }
 
 struct Layout {
-  int64_t chunks, slots, xfrags, hfrags;
-  size_t logits, records, xp, xs, hp, hs, bytes;
+  int64_t turns, xfrags, hfrags;
+  size_t logits, plan, records, xp, xs, hp, hs, bytes;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Layout layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
   Layout l;
-  l.chunks = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
-  l.slots = T * top_k < E ? T * top_k : E;
-  l.xfrags = l.chunks * ((H + 511) / 512 * 4);
-  l.hfrags = l.slots * l.chunks * ((I + 511) / 512 * 4);
+  // a turn for each chosen expert and one for each further 16 tokens of it
+  l.turns = (T * top_k < E ? T * top_k : E) + T * top_k / kChunk;
+  l.xfrags = (T + kChunk - 1) / kChunk * ((H + 511) / 512 * 4);
+  l.hfrags = l.turns * ((I + 511) / 512 * 4);
   l.logits = 0;
-  l.records = l.logits + (size_t)E * kMaxTokens * 4;
-  l.xp = up256(l.records + (size_t)l.slots * sizeof(Slot));
+  l.plan = up256((size_t)E * T * 4);
+  l.records = l.plan + 256;
+  l.xp = up256(l.records + (size_t)l.turns * sizeof(Turn));
   l.xs = l.xp + (size_t)l.xfrags * kMxFragBytes;
   l.hp = l.xs + (size_t)l.xfrags * kMxFragScaleBytes;
   l.hs = l.hp + (size_t)l.hfrags * kMxFragBytes;
@@ -459,21 +417,36 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
                   const uint8_t* down_codes, const uint8_t* down_scales, int T, int H, int I, int E, int top_k,
                   uint16_t* Y, uint8_t* ws, const Layout& l, hipStream_t stream) {
   float* const logits = reinterpret_cast<float*>(ws + l.logits);
-  Slot* const slots = reinterpret_cast<Slot*>(ws + l.records);
-  uint32_t* const xs = reinterpret_cast<uint32_t*>(ws + l.xs);
-  uint32_t* const hs = reinterpret_cast<uint32_t*>(ws + l.hs);
-  const int groups = (T + kRouteTokens - 1) / kRouteTokens;
+  Plan* const plan = reinterpret_cast<Plan*>(ws + l.plan);
+  Turn* const turns = reinterpret_cast<Turn*>(ws + l.records);
+  uint8_t* const xs = ws + l.xs;
+  uint8_t* const hs = ws + l.hs;
+  const int tokens = T == 1 ? 1 : kRouteTokens;
+  const int groups = (T + tokens - 1) / tokens;
   const int blocks = T * kSuper * ((H + 511) / 512);
-  moe_route_kernel<XT><<<(unsigned)(groups * E + (blocks + kRouteThreads - 1) / kRouteThreads), kRouteThreads, 0, stream>>>(
-      X, router, T, H, E, groups, logits, ws + l.xp, xs);
+  const unsigned grid = (unsigned)(groups * E + (blocks + kRouteThreads - 1) / kRouteThreads);
+  if (T == 1)
+    moe_route_kernel<XT, 1><<<grid, kRouteThreads, 0, stream>>>(X, router, T, H, E, groups, logits, ws + l.xp,
+                                                                reinterpret_cast<uint32_t*>(xs));
+  else
+    moe_route_kernel<XT, kRouteTokens><<<grid, kRouteThreads, 0, stream>>>(X, router, T, H, E, groups, logits, ws + l.xp,
+                                                                           reinterpret_cast<uint32_t*>(xs));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  moe_up_kernel<<<dim3((unsigned)(I / kMxBlock), (unsigned)l.slots), kUpWaves * 64, 0, stream>>>(
-      ws + l.xp, xs, up_codes, up_scales, logits, T, H, I, E, top_k, T * top_k < E ? 1 : 0, TC, slots, ws + l.hp, hs);
+  if (E <= 64)
+    moe_choose_kernel<1><<<1, kChooseWaves * 64, 0, stream>>>(logits, T, E, top_k, plan, turns);
+  else
+    moe_choose_kernel<kMaxExperts / 64><<<1, kChooseWaves * 64, 0, stream>>>(logits, T, E, top_k, plan, turns);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // a wave for every super-step of a row, up to 8: all loads of a row tile start at once
+  const int supers = (H + 511) / 512, waves = supers < kUpWaves ? supers : kUpWaves;
+  moe_up_kernel<<<dim3((unsigned)(I / kMxBlock), (unsigned)l.turns), (unsigned)(waves * 64), 0, stream>>>(
+      ws + l.xp, xs, up_codes, up_scales, plan, turns, H, I, E, ws + l.hp, reinterpret_cast<uint32_t*>(hs));
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   moe_down_kernel<XT, TC><<<(unsigned)(H / 16), kDownWaves * 64, 0, stream>>>(ws + l.hp, hs, down_codes, down_scales,
-                                                                             slots, (int)l.slots, T, H, I, E, Y);
+                                                                             plan, turns, T, H, I, E, Y);
   return hipGetLastError();
 }
 
@@ -499,9 +472,9 @@ hipError_t launch_mxfp4_moe(const void* X, int xdtype, const void* router, const
         static_cast<uint8_t*>(workspace), l, stream);
   };
   auto chunks = [&](auto tag) {
-    return l.chunks == 1   ? run(tag, std::integral_constant<int, 1>{})
-           : l.chunks == 2 ? run(tag, std::integral_constant<int, 2>{})
-                           : run(tag, std::integral_constant<int, 4>{});
+    return T <= 16   ? run(tag, std::integral_constant<int, 1>{})
+           : T <= 32 ? run(tag, std::integral_constant<int, 2>{})
+                     : run(tag, std::integral_constant<int, 4>{});
   };
   return xdtype == 0 ? chunks(F16{}) : chunks(BF16{});
 }

@@ -68,7 +68,7 @@ __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-// Scale bytes [rows, nblk] -> dwords [ceil(nblk / 4)][rows_pad], 127 in the
+// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 127 in the
 // place of rows and blocks that are not there.
 struct ScaleJob {
   const uint8_t* scales;
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_scales_kernel(ScaleJob w, Scal
   const bool first = (int)blockIdx.x < wblocks;
   const ScaleJob j = first ? w : a;
   const int64_t i = (int64_t)((int)blockIdx.x - (first ? 0 : wblocks)) * kThreads + threadIdx.x;
-  const int ktiles = (nblk + 3) >> 2;
+  const int ktiles = (nblk + 7) / 8 * 2;
   // a thread takes 16 blocks of a row, a wave 64 rows: the writes are contiguous
   const int row = (int)(i % j.rows_pad), g = (int)(i / j.rows_pad);
   if (4 * g >= ktiles) return;
@@ -99,22 +99,23 @@ __global__ __launch_bounds__(kThreads) void mxfp4_scales_kernel(ScaleJob w, Scal
     if (4 * g + q < ktiles) j.out[(int64_t)(4 * g + q) * j.rows_pad + row] = v[q];
 }
 
-// A 4-bit operand: ROWS rows, stages of 64 KS.  One load of a wave takes 16
-// rows (KS = 2) or 32 (KS = 1).
+// A 4-bit operand: ROWS rows, stages of 64 KS (KS 1, 2 or 4).  One load of a wave
+// takes 32 / KS rows.
 template <int ROWS, int KS>
 struct Tile4 {
   static constexpr int kRowBytes = 32 * KS;
   static constexpr int kBytes = ROWS * kRowBytes;
   static constexpr int kUnits = kBytes / 1024;
-  static constexpr int kScaleUnits = ROWS / 64;
-  static constexpr int kScaleBytes = ROWS * 4;
+  static constexpr int kDwords = KS == 4 ? 2 : 1;  // scale dwords of a row's stage, [dword][row]
+  static constexpr int kScaleUnits = ROWS / 64 * kDwords;
+  static constexpr int kScaleBytes = ROWS * 4 * kDwords;
   static_assert(kScalePad % ROWS == 0, "a tile's scale loads stay inside the padded array");
   const uint8_t* codes;
   const uint8_t* scales;
   uint32_t scale_step;  // bytes between K tiles of the scale dwords
   int nblk, last, chunk;
 
-  __device__ static int swizzle(int row) { return KS == 2 ? (row >> 2) & 3 : (row >> 3) & 1; }
+  __device__ static int swizzle(int row) { return KS == 4 ? (row >> 1) & 7 : (KS == 2 ? (row >> 2) & 3 : (row >> 3) & 1); }
   __device__ void start(const uint8_t* codes_, const uint8_t* scales_, int row0, int rows, int rows_pad, int nblk_, int) {
     nblk = nblk_;
     codes = codes_ + (int64_t)row0 * nblk * 16;
@@ -128,13 +129,15 @@ struct Tile4 {
     const int lane = threadIdx.x & 63;
     int r = unit * (32 / KS) + lane / (2 * KS);
     r = r < last ? r : last;
-    int b = 2 * KS * h + chunk;
+    // (KS = 4: a load's 8 rows take every other half of the swizzle)
+    int b = 2 * KS * h + (KS == 4 ? chunk ^ ((unit & 1) << 2) : chunk);
     b = b < nblk ? b : nblk - 1;  // past the row's end: its last block, A is zeros there
     load_lds16(codes, (uint32_t)(r * nblk + b) * 16u, to + 1024u * (uint32_t)unit);
   }
   __device__ void load_scales(int unit, int h, uint32_t to) const {
-    const int kt = KS == 2 ? h : h >> 1;
-    load_lds4(scales + (int64_t)kt * scale_step, 256u * (uint32_t)unit + 4u * (threadIdx.x & 63), to + 256u * (uint32_t)unit);
+    const int kt = KS == 1 ? h >> 1 : kDwords * h + unit / (ROWS / 64);
+    const uint32_t rows = 256u * (uint32_t)(unit % (ROWS / 64));
+    load_lds4(scales + (int64_t)kt * scale_step, rows + 4u * (threadIdx.x & 63), to + 256u * (uint32_t)unit);
   }
   // lane (row, half) multiplies block 2 s + half of its row's stage
   __device__ static u32x4_t fragment(const uint8_t* lds, int row, int s, int half) {
@@ -142,18 +145,18 @@ struct Tile4 {
     return *reinterpret_cast<const u32x4_t*>(lds + row * kRowBytes + c * 16);
   }
   __device__ static int scale(const uint8_t* lds, int row, int s, int half, int h) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(lds + 4 * row);
-    return (int)(v >> (8 * (2 * (KS == 2 ? s : h & 1) + half)));
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(lds + 4 * (ROWS * (KS == 4 ? s >> 1 : 0) + row));
+    return (int)(v >> (8 * (2 * (KS == 1 ? h & 1 : s & 1) + half)));
   }
 };
 
-// Split activations: stages of one fragment (64 of K) of each 32 rows.
-template <int ROWS>
+// Split activations: stages of KS fragments (64 of K each) of each 32 rows.
+template <int ROWS, int KS>
 struct TileSplit {
-  static constexpr int kBytes = ROWS / 32 * kMxFragBytes;
+  static constexpr int kBytes = ROWS / 32 * KS * kMxFragBytes;
   static constexpr int kUnits = kBytes / 1024;
-  static constexpr int kScaleUnits = ROWS / 32;
-  static constexpr int kScaleBytes = ROWS * 8;
+  static constexpr int kScaleUnits = ROWS / 32 * KS;
+  static constexpr int kScaleBytes = ROWS * 8 * KS;
   static_assert(kBytes % 1024 == 0, "whole loads");
   const uint8_t* pieces;
   const uint8_t* scales;
@@ -166,25 +169,30 @@ struct TileSplit {
   }
   __device__ void load(int unit, int h, uint32_t to) const {
     const uint32_t o = 1024u * (uint32_t)unit + 16u * (threadIdx.x & 63);
-    const uint32_t rg = o / kMxFragBytes, in = o % kMxFragBytes;
-    load_lds16(pieces + (int64_t)h * kMxFragBytes, rg * ksteps * kMxFragBytes + in, to + 1024u * (uint32_t)unit);
+    const uint32_t rg = o / (KS * kMxFragBytes), in = o % (KS * kMxFragBytes);
+    load_lds16(pieces + (int64_t)h * KS * kMxFragBytes, rg * ksteps * kMxFragBytes + in, to + 1024u * (uint32_t)unit);
   }
   __device__ void load_scales(int unit, int h, uint32_t to) const {
-    load_lds4(scales + (int64_t)h * kMxFragScaleBytes, (uint32_t)unit * ksteps * kMxFragScaleBytes + 4u * (threadIdx.x & 63),
+    const uint32_t rg = (uint32_t)unit / KS, in = (uint32_t)unit % KS;
+    load_lds4(scales + ((int64_t)h * KS + in) * kMxFragScaleBytes, rg * ksteps * kMxFragScaleBytes + 4u * (threadIdx.x & 63),
               to + 256u * (uint32_t)unit);
   }
 };
 
-template <int PIECES, int TM, int TN>
+template <int PIECES, int TM, int TN, int KS, int KG>
 struct Config {
   static constexpr bool kSplit = PIECES == kMxPieces;
-  static constexpr int kKS = kSplit ? 1 : 2;
+  static constexpr int kKS = KS;
   static constexpr int BM = 64 * TM, BN = 64 * TN;
-  using TA = std::conditional_t<kSplit, TileSplit<BM>, Tile4<BM, kKS>>;
+  using TA = std::conditional_t<kSplit, TileSplit<BM, KS>, Tile4<BM, KS>>;
   using TW = Tile4<BN, kKS>;
   static constexpr int kStage = TA::kBytes + TW::kBytes + TA::kScaleBytes + TW::kScaleBytes;
-  // as many stages as leave room for a second workgroup, at most 4
-  static constexpr int kFit = 80 * 1024 / kStage;
+  // as many stages as leave room for a second workgroup (or fill the LDS, where
+  // there are four K groups), at most 4
+#ifndef FIT
+#define FIT (KG * kStage * 2 > 80 * 1024 ? 160 : 80)
+#endif
+  static constexpr int kFit = FIT * 1024 / (KG * kStage);
   static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
   static constexpr int per_wave(int units) { return (units + kWaves - 1) / kWaves; }
   static constexpr int kALoads = per_wave(TA::kUnits), kWLoads = per_wave(TW::kUnits);
@@ -192,28 +200,33 @@ struct Config {
   static constexpr int kLoads = kALoads + kWLoads + kAScaleLoads + kWScaleLoads;
 };
 
-template <class YT, int PIECES, int TM, int TN>
-__global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
+template <class YT, int PIECES, int TM, int TN, int KS, int KG>
+__global__ __launch_bounds__(kThreads * KG, KG == 4 ? 4 : 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
                                                                  const uint8_t* __restrict__ As,
                                                                  const uint8_t* __restrict__ W,
                                                                  const uint8_t* __restrict__ Ws, int M, int N,
                                                                  int m_pad, int n_pad, int nblk, int mtiles, int tiles,
                                                                  uint16_t* __restrict__ Y) {
-  using C = Config<PIECES, TM, TN>;
+  using C = Config<PIECES, TM, TN, KS, KG>;
   using TA = typename C::TA;
   using TW = typename C::TW;
   constexpr int kAt = TA::kBytes, kAsAt = kAt + TW::kBytes, kWsAt = kAsAt + TA::kScaleBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kStages][C::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KG][C::kStages][C::kStage];
 
   const int per = (tiles + kXcds - 1) / kXcds;
   const int tile = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
   if (tile >= tiles) return;
   const int m0 = tile % mtiles * C::BM, n0 = tile / mtiles * C::BN;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = wave_all % kWaves, group = wave_all / kWaves;
   const int wm = (wave & 1) * TM, wn = (wave >> 1) * TN;  // in units of 32 rows
   const int half = lane >> 5, r32 = lane & 31;
-  const int turns = (nblk + 2 * C::kKS - 1) / (2 * C::kKS);
+  // K group `group` takes the stages [h0, h1); all groups make the same number of turns
+  const int stages = (nblk + 2 * C::kKS - 1) / (2 * C::kKS);
+  const int turns = (stages + KG - 1) / KG;
+  const int h0 = group * turns, h1 = h0 + turns < stages ? h0 + turns : stages;
+  uint8_t(*const lds)[C::kStage] = lds_all[group];
 
   TA ta;
   TW tw;
@@ -222,7 +235,7 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
   // every wave starts the same number of loads a stage: past an operand's units
   // the last one is loaded again, past the last stage that stage
   auto issue = [&](int h_, int buf) {
-    const int h = h_ < turns ? h_ : turns - 1;
+    const int h = h_ < stages ? h_ : stages - 1;
     const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_address(lds[0])) + (uint32_t)(buf * C::kStage);
     auto unit = [&](int j, int units) {
       const int u = wave + kWaves * j;
@@ -239,14 +252,16 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
   };
 
   float16_t acc[TM][TN] = {};
-  for (int st = 0; st + 1 < C::kStages; ++st) issue(st, st);
+  for (int st = 0; st + 1 < C::kStages; ++st) issue(h0 + st, st);
   int buf = 0;
-  for (int h = 0; h < turns; ++h) {
+  for (int h = h0; h < h0 + turns; ++h) {
     wait_loads<(C::kStages - 2) * C::kLoads>();
     __builtin_amdgcn_s_barrier();
     issue(h + C::kStages - 1, buf == 0 ? C::kStages - 1 : buf - 1);
     const uint8_t* const la = lds[buf];
     const uint8_t* const lw = la + kAt;
+    buf = buf + 1 == C::kStages ? 0 : buf + 1;
+    if (KG > 1 && h >= h1) continue;
 #pragma unroll
     for (int s = 0; s < C::kKS; ++s) {
       i32x8_t bf[TN];
@@ -258,7 +273,7 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
         bs[j] = TW::scale(la + kWsAt, row, s, half, h);
       }
       if constexpr (!C::kSplit) {
-        const bool live = 4 * h + 2 * s + half < nblk;
+        const bool live = 2 * KS * h + 2 * s + half < nblk;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
           const int row = (wm + i) * 32 + r32;
@@ -273,8 +288,8 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
       } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const uint8_t* const fr = la + (wm + i) * kMxFragBytes;
-          const int as = (int)reinterpret_cast<const uint32_t*>(la + kAsAt)[(wm + i) * 64 + lane];
+          const uint8_t* const fr = la + ((wm + i) * KS + s) * kMxFragBytes;
+          const int as = (int)reinterpret_cast<const uint32_t*>(la + kAsAt)[((wm + i) * KS + s) * 64 + lane];
           auto piece = [&](int p) {
             return mx_operand(*reinterpret_cast<const u32x4_t*>(fr + p * kMxPieceBytes + 16 * lane),
                               *reinterpret_cast<const u32x2_t*>(fr + p * kMxPieceBytes + 1024 + 8 * lane));
@@ -293,10 +308,30 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
         }
       }
     }
-    buf = buf + 1 == C::kStages ? 0 : buf + 1;
   }
   wait_loads<0>();  // none may land in LDS that is another workgroup's by then
   __syncthreads();  // and nobody reads operands any more
+
+  if constexpr (KG > 1) {
+    // the groups' sums meet in LDS, [wave][tile][lane], added in order
+    static_assert(TM * TN * kWaves * 4096 <= C::kStages * C::kStage, "a group's sums fit its stages' place");
+    float16_t* const mine = reinterpret_cast<float16_t*>(&lds[0][0]) + wave * TM * TN * 64 + lane;
+    if (group)
+#pragma unroll
+      for (int i = 0; i < TM * TN; ++i) mine[i * 64] = acc[i / TN][i % TN];
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int g = 1; g < KG; ++g) {
+      const float16_t* const other = reinterpret_cast<const float16_t*>(&lds_all[g][0][0]) + wave * TM * TN * 64 + lane;
+#pragma unroll
+      for (int i = 0; i < TM * TN; ++i) {
+        const float16_t v = other[i * 64];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i / TN][i % TN][e] += v[e];
+      }
+    }
+  }
 
   // D: lane holds row r32 of Y and columns 8 (e / 4) + 4 half + e % 4 (W is the
   // instruction's first operand for that).  Each wave turns 32 rows at a time
@@ -337,7 +372,7 @@ __global__ __launch_bounds__(kThreads, 2) void mxfp4_gemm_kernel(const uint8_t* 
 }
 
 int64_t padded(int64_t rows) { return (rows + kScalePad - 1) / kScalePad * kScalePad; }
-size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)padded(rows) * (size_t)((K + 127) / 128) * 4; }
+size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)padded(rows) * (size_t)((K + 255) / 256 * 2) * 4; }
 
 // The scale dwords of W and, where it has rows, of A.
 hipError_t launch_scales(const void* Ws, int64_t N, void* wout, const void* As, int64_t M, void* aout, int64_t K,
@@ -350,30 +385,32 @@ hipError_t launch_scales(const void* Ws, int64_t N, void* wout, const void* As, 
   return hipGetLastError();
 }
 
-template <class YT, int PIECES, int TM, int TN>
+template <class YT, int PIECES, int TM, int TN, int KS, int KG>
 hipError_t launch_tiles(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                         void* Y, hipStream_t stream) {
   const int64_t mt = (M + 64 * TM - 1) / (64 * TM), nt = (N + 64 * TN - 1) / (64 * TN);
   const int64_t tiles = mt * nt;
   const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds);
-  mxfp4_gemm_kernel<YT, PIECES, TM, TN><<<grid, kThreads, 0, stream>>>(
+  mxfp4_gemm_kernel<YT, PIECES, TM, TN, KS, KG><<<grid, kThreads * KG, 0, stream>>>(
       static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
       static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)padded(M), (int)padded(N), (int)(K / kMxBlock), (int)mt,
       (int)tiles, static_cast<uint16_t*>(Y));
   return hipGetLastError();
 }
 
-// The large tile where it fills the chip, the 64 x 64 one where even 128 x 128
-// would leave much of it idle.
+// The large tile where it fills the chip; below that 128 x 128; and where even
+// those would leave much of it idle 64 x 64, with K split between groups of four
+// waves where a compute unit would have one workgroup or less.
 template <class YT, int PIECES>
 hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                   void* Y, hipStream_t stream) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   constexpr bool kSplit = PIECES == kMxPieces;
+  constexpr int kKS = kSplit ? 1 : 2;
   if (tiles(kSplit ? 128 : 256, kSplit ? 256 : 128) >= 384)
-    return launch_tiles<YT, PIECES, kSplit ? 2 : 4, kSplit ? 4 : 2>(A, As, W, Ws, M, N, K, Y, stream);
-  if (tiles(128, 128) >= 192) return launch_tiles<YT, PIECES, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
-  return launch_tiles<YT, PIECES, 1, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    return launch_tiles<YT, PIECES, kSplit ? 2 : 4, kSplit ? 4 : 2, kKS, 1>(A, As, W, Ws, M, N, K, Y, stream);
+  if (tiles(128, 128) >= 192) return launch_tiles<YT, PIECES, 2, 2, kKS, 1>(A, As, W, Ws, M, N, K, Y, stream);
+  return launch_tiles<YT, PIECES, 1, 1, 2 * kKS, 2>(A, As, W, Ws, M, N, K, Y, stream);
 }
 
 constexpr int64_t kSkinnyRows = 64;     // up to here the weight-streaming kernel, 16-bit activations

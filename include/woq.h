@@ -328,7 +328,7 @@ woq_status woq_mxfp4_gemm(const void* X, int32_t xdtype, const void* codes, cons
 
 /* Y[m, n] = sum_k a[m, k] w[n, k] for microscaled a [M, K] and w [N, K]; exact
  * products, fp32 sums, Y [M, N] of ydtype (WOQ_F16 or WOQ_BF16) rounded once.
- * workspace as above (M > 64: the scales in tile order). */
+ * workspace as above (beyond a few rows: the scales in tile order). */
 size_t woq_mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K);
 woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const void* codes, const void* scales,
                              int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* workspace,

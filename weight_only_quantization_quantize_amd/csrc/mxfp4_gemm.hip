@@ -6,26 +6,34 @@
 // all of it inside v_mfma_scale_f32_32x32x64_f8f6f4: no element is decoded,
 // the products are exact and the sums are the matrix unit's fp32.
 //
-// Tile.  2 x 2 waves compute 64 TM x 64 TN of Y, a wave 32 TM x 32 TN.  Large
-// products take 256 x 128 (4-bit A) and 128 x 256 (three pieces: A is the
-// heavier operand, 2.25 bytes an element against 17/32, so it gets the shorter
-// side); two such workgroups share a compute unit, which hides the one's
-// barriers, prologue and stores behind the other's matrix instructions.
+// Tile.  A group of 2 x WN waves computes 64 TM x 32 WN TN of Y, a wave 32 TM x
+// 32 TN; KG groups of a workgroup share a tile's K and add their sums through
+// LDS at the end.  `launch` chooses: where there is work for all compute units
+// the matrix instructions bound the product and the largest tile wins (with three
+// pieces A is the heavier operand, 2.25 bytes an element against 17 / 32, and gets
+// the shorter side; two workgroups of that tile share a compute unit, which hides
+// the one's barriers, prologue and stores behind the other's instructions).
+// Below that the number of stages in flight counts: small tiles, K split.
+// 2048 x 11008 x 4096 takes 156 us with split activations (3 x 185 G multiply-adds,
+// 3.5 P flop/s as the matrix unit counts them, of the 6.3 P that it reaches on
+// registers alone) and 62 us with 4-bit ones (3.0 of 6.7).
 //
-// Pipeline.  K goes in stages of 64 KS (128; 64 for split activations), STAGES
-// of them in LDS, filled by direct loads (global_load_lds: no registers, no
-// instructions to write LDS).  At the top of a turn a wave waits until its own
-// loads of this stage are done, meets the others at the barrier, which also
-// says that everybody is through with the previous stage, starts the loads of
-// the stage STAGES - 1 ahead into that one's place, and multiplies.  The loads
-// are written out in assembly because the compiler would wait for all of them
-// before every read of LDS; their counter is waited for by hand, and there is
-// no other vector memory access inside the loop.
+// Pipeline.  K goes in stages of 64 KS, kStages of them in LDS, filled by direct
+// loads (global_load_lds: no registers, no instructions to write LDS).  At the top
+// of a turn a wave waits until its own loads of this stage are done, meets the
+// others at the barrier, which also says that everybody is through with the
+// previous stage, starts the loads of the stage kStages - 1 ahead into that one's
+// place, and multiplies.  The loads are written out in assembly because the
+// compiler would wait for all of them before every read of LDS; their counter is
+// waited for by hand, and there is no other vector memory access inside the loop.
+// Longer stages mean fewer barriers: 256 of K for 4-bit operands took 333 x 1001 x
+// 5152 from 15 to 11 us, 64 of K left the large three-piece tile two workgroups a
+// compute unit (152 against 171 us with 128).
 //
-// Scales.  The 4-bit operands' scale bytes lie K/32 bytes apart from row to row
-// at any alignment, which direct loads cannot gather; a pass before the product
-// (mxfp4_scales_kernel) turns them into one dword per row and 128 of K, rows
-// contiguous, with 127 past the row's end.
+// Scales.  The 4-bit operands' scale bytes lie K / 32 bytes apart from row to row
+// at any alignment, which direct loads cannot gather; turn_scales
+// (mxfp4_quantize.hip; in the split's launch where there is one) makes them one
+// dword per row and 128 of K, rows contiguous, with 127 past the row's end.
 //
 // LDS layout of a 4-bit operand: a row's 32 KS bytes of a stage are chunks of
 // one block each, chunk c at position c ^ swizzle(row), so that 16 rows read at
@@ -43,9 +51,7 @@ namespace woq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kXcds = 8;
-constexpr int kScalePad = 256;  // rows of a scale array are padded to the largest tile's and a workgroup's
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -68,37 +74,6 @@ __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 127 in the
-// place of rows and blocks that are not there.
-struct ScaleJob {
-  const uint8_t* scales;
-  uint32_t* out;
-  int rows, rows_pad;
-};
-__global__ __launch_bounds__(kThreads) void mxfp4_scales_kernel(ScaleJob w, ScaleJob a, int nblk, int wblocks) {
-  const bool first = (int)blockIdx.x < wblocks;
-  const ScaleJob j = first ? w : a;
-  const int64_t i = (int64_t)((int)blockIdx.x - (first ? 0 : wblocks)) * kThreads + threadIdx.x;
-  const int ktiles = (nblk + 7) / 8 * 2;
-  // a thread takes 16 blocks of a row, a wave 64 rows: the writes are contiguous
-  const int row = (int)(i % j.rows_pad), g = (int)(i / j.rows_pad);
-  if (4 * g >= ktiles) return;
-  u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
-  if (row < j.rows) {
-    const uint8_t* const p = j.scales + (int64_t)row * nblk + 16 * g;
-    if (16 * g + 16 <= nblk) {
-      __builtin_memcpy(&v, p, 16);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (16 * g + q < nblk) v[q / 4] = (v[q / 4] & ~(0xFFu << (8 * (q % 4)))) | ((uint32_t)p[q] << (8 * (q % 4)));
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (4 * g + q < ktiles) j.out[(int64_t)(4 * g + q) * j.rows_pad + row] = v[q];
-}
-
 // A 4-bit operand: ROWS rows, stages of 64 KS (KS 1, 2 or 4).  One load of a wave
 // takes 32 / KS rows.
 template <int ROWS, int KS>
@@ -109,7 +84,7 @@ struct Tile4 {
   static constexpr int kDwords = KS == 4 ? 2 : 1;  // scale dwords of a row's stage, [dword][row]
   static constexpr int kScaleUnits = ROWS / 64 * kDwords;
   static constexpr int kScaleBytes = ROWS * 4 * kDwords;
-  static_assert(kScalePad % ROWS == 0, "a tile's scale loads stay inside the padded array");
+  static_assert(kMxScaleRowPad % ROWS == 0, "a tile's scale loads stay inside the padded array");
   const uint8_t* codes;
   const uint8_t* scales;
   uint32_t scale_step;  // bytes between K tiles of the scale dwords
@@ -179,20 +154,19 @@ struct TileSplit {
   }
 };
 
-template <int PIECES, int TM, int TN, int KS, int KG>
+template <int PIECES, int TM, int TN, int WN, int KS, int KG>
 struct Config {
+  static constexpr int kWaves = 2 * WN, kThreads = 64 * kWaves * KG;
   static constexpr bool kSplit = PIECES == kMxPieces;
   static constexpr int kKS = KS;
-  static constexpr int BM = 64 * TM, BN = 64 * TN;
+  static constexpr int BM = 64 * TM, BN = 32 * WN * TN;
   using TA = std::conditional_t<kSplit, TileSplit<BM, KS>, Tile4<BM, KS>>;
   using TW = Tile4<BN, kKS>;
   static constexpr int kStage = TA::kBytes + TW::kBytes + TA::kScaleBytes + TW::kScaleBytes;
-  // as many stages as leave room for a second workgroup (or fill the LDS, where
-  // there are four K groups), at most 4
-#ifndef FIT
-#define FIT (KG * kStage * 2 > 80 * 1024 ? 160 : 80)
-#endif
-  static constexpr int kFit = FIT * 1024 / (KG * kStage);
+  // as many stages as leave room for a second workgroup, or, where that would be
+  // fewer than two, as fill the LDS; at most 4
+  static constexpr int kRoom = (KG * kStage * 2 > 80 * 1024 ? 160 : 80) * 1024;
+  static constexpr int kFit = kRoom / (KG * kStage);
   static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
   static constexpr int per_wave(int units) { return (units + kWaves - 1) / kWaves; }
   static constexpr int kALoads = per_wave(TA::kUnits), kWLoads = per_wave(TW::kUnits);
@@ -200,14 +174,15 @@ struct Config {
   static constexpr int kLoads = kALoads + kWLoads + kAScaleLoads + kWScaleLoads;
 };
 
-template <class YT, int PIECES, int TM, int TN, int KS, int KG>
-__global__ __launch_bounds__(kThreads * KG, KG == 4 ? 4 : 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
+template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG>
+__global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
                                                                  const uint8_t* __restrict__ As,
                                                                  const uint8_t* __restrict__ W,
                                                                  const uint8_t* __restrict__ Ws, int M, int N,
                                                                  int m_pad, int n_pad, int nblk, int mtiles, int tiles,
                                                                  uint16_t* __restrict__ Y) {
-  using C = Config<PIECES, TM, TN, KS, KG>;
+  using C = Config<PIECES, TM, TN, WN, KS, KG>;
+  constexpr int kWaves = C::kWaves;
   using TA = typename C::TA;
   using TW = typename C::TW;
   constexpr int kAt = TA::kBytes, kAsAt = kAt + TW::kBytes, kWsAt = kAsAt + TA::kScaleBytes;
@@ -371,51 +346,66 @@ __global__ __launch_bounds__(kThreads * KG, KG == 4 ? 4 : 2) void mxfp4_gemm_ker
   }
 }
 
-int64_t padded(int64_t rows) { return (rows + kScalePad - 1) / kScalePad * kScalePad; }
-size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)padded(rows) * (size_t)((K + 255) / 256 * 2) * 4; }
+size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)mxfp4_scale_rows(rows) * (size_t)((K + 255) / 256 * 2) * 4; }
 
-// The scale dwords of W and, where it has rows, of A.
-hipError_t launch_scales(const void* Ws, int64_t N, void* wout, const void* As, int64_t M, void* aout, int64_t K,
-                         hipStream_t stream) {
-  const int64_t groups = (K + 511) / 512;
-  const int64_t wblocks = padded(N) * groups / kThreads, ablocks = M ? padded(M) * groups / kThreads : 0;
-  const ScaleJob w{static_cast<const uint8_t*>(Ws), static_cast<uint32_t*>(wout), (int)N, (int)padded(N)};
-  const ScaleJob a{static_cast<const uint8_t*>(As), static_cast<uint32_t*>(aout), (int)M, (int)padded(M)};
-  mxfp4_scales_kernel<<<(unsigned)(wblocks + ablocks), kThreads, 0, stream>>>(w, a, (int)(K / kMxBlock), (int)wblocks);
-  return hipGetLastError();
-}
-
-template <class YT, int PIECES, int TM, int TN, int KS, int KG>
+template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG>
 hipError_t launch_tiles(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                         void* Y, hipStream_t stream) {
-  const int64_t mt = (M + 64 * TM - 1) / (64 * TM), nt = (N + 64 * TN - 1) / (64 * TN);
+  using C = Config<PIECES, TM, TN, WN, KS, KG>;
+  const int64_t mt = (M + C::BM - 1) / C::BM, nt = (N + C::BN - 1) / C::BN;
   const int64_t tiles = mt * nt;
   const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds);
-  mxfp4_gemm_kernel<YT, PIECES, TM, TN, KS, KG><<<grid, kThreads * KG, 0, stream>>>(
+  mxfp4_gemm_kernel<YT, PIECES, TM, TN, WN, KS, KG><<<grid, C::kThreads, 0, stream>>>(
       static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
-      static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)padded(M), (int)padded(N), (int)(K / kMxBlock), (int)mt,
+      static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)mxfp4_scale_rows(M), (int)mxfp4_scale_rows(N), (int)(K / kMxBlock), (int)mt,
       (int)tiles, static_cast<uint16_t*>(Y));
   return hipGetLastError();
 }
 
-// The large tile where it fills the chip; below that 128 x 128; and where even
-// those would leave much of it idle 64 x 64, with K split between groups of four
-// waves where a compute unit would have one workgroup or less.
+// The tile with the smallest time by a model of what was measured at K = 4096 (all
+// grow with K alike), in us for n = ceil(tiles / 256) tiles a compute unit:
+//   4-bit A:      256 x 256 36 n          (2048 x 8192: 40;  1024 x 28672, K / 2: 70)
+//                 128 x 128 6 + 10 n      (n = 1: 14 .. 17, 2: 22 .. 24, 4: 45, 6: 63 .. 68)
+//                 64 x 64   3 + 4.5 n     (n = 1: 8, 2: 10, 4: 18 .. 21, 8: 34 .. 40)
+//   three pieces: 128 x 256 9 + 49 n      (n = 1: 59 .. 61, 2: 107, 3: 152)
+//                 64 x 256  1 + 28 n      (n = 1: 27 .. 34, 2: 56 .. 59, 4: 116)
+//                 64 x 128  19.5 n        (n = 1: 18 .. 21, 2: 37 .. 41, 4: 75)
+//                 64 x 64   14 n          (n = 1: 15, 2: 27, 4: 52 .. 59)
+// The small ones split K between two groups of waves.
 template <class YT, int PIECES>
 hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                   void* Y, hipStream_t stream) {
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  constexpr bool kSplit = PIECES == kMxPieces;
-  constexpr int kKS = kSplit ? 1 : 2;
-  if (tiles(kSplit ? 128 : 256, kSplit ? 256 : 128) >= 384)
-    return launch_tiles<YT, PIECES, kSplit ? 2 : 4, kSplit ? 4 : 2, kKS, 1>(A, As, W, Ws, M, N, K, Y, stream);
-  if (tiles(128, 128) >= 192) return launch_tiles<YT, PIECES, 2, 2, kKS, 1>(A, As, W, Ws, M, N, K, Y, stream);
-  return launch_tiles<YT, PIECES, 1, 1, 2 * kKS, 2>(A, As, W, Ws, M, N, K, Y, stream);
+  auto per_cu = [&](int64_t bm, int64_t bn) { return (double)(((M + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256); };
+  if constexpr (PIECES == 1) {
+    const double large = 36.0 * per_cu(256, 256), mid = 6.0 + 10.0 * per_cu(128, 128), small = 3.0 + 4.5 * per_cu(64, 64);
+    if (large <= mid && large <= small) return launch_tiles<YT, 1, 4, 2, 4, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    if (mid <= small) return launch_tiles<YT, 1, 2, 2, 2, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    return launch_tiles<YT, 1, 1, 1, 2, 4, 2>(A, As, W, Ws, M, N, K, Y, stream);
+  } else {
+    const double large = 9.0 + 49.0 * per_cu(128, 256), wide = 1.0 + 28.0 * per_cu(64, 256), mid = 19.5 * per_cu(64, 128),
+                 small = 14.0 * per_cu(64, 64);
+    if (large <= wide && large <= mid && large <= small)
+      return launch_tiles<YT, kMxPieces, 2, 4, 2, 1, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    if (wide <= mid && wide <= small) return launch_tiles<YT, kMxPieces, 1, 2, 4, 2, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    if (mid <= small) return launch_tiles<YT, kMxPieces, 1, 2, 2, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
+    return launch_tiles<YT, kMxPieces, 1, 1, 2, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
+  }
 }
 
-constexpr int64_t kSkinnyRows = 64;     // up to here the weight-streaming kernel, 16-bit activations
-constexpr int64_t kSkinnyRowsMx = 64;   // and microscaled ones
-bool skinny(int64_t M, int64_t K, int64_t rows) { return M <= rows && K >= 128; }
+// Few rows (and K >= 128) go to the weight-streaming kernel, which reads the
+// weights once per 16 rows of split activations, once per 32 rows of 4-bit ones,
+// and needs no pass over the scales.  Whole products, us, streaming / tiles:
+//   split, 16 rows   4096 x 4096 10 / 18, 28672 x 8192 39 / 52
+//          32 rows   4096 x 4096 12 / 18, 8192 x 8192 24 / 30, 4096 x 11008 28 / 39,
+//                    16384 x 4096 21 / 20, 28672 x 8192 55 / 52
+//          64 rows   4096 x 4096 16 / 18, 8192 x 8192 33 / 30, 4096 x 11008 46 / 39
+//   4-bit, 32 rows   4096 x 4096 6 / 10, 28672 x 8192 29 / 35, 4096 x 11008 14 / 20
+//          64 rows   4096 x 4096 7 / 10, 8192 x 8192 17 / 17, 4096 x 11008 23 / 20,
+//                    28672 x 8192 40 / 37
+bool skinny(int64_t M, int64_t N, int64_t K) { return K >= 128 && (M <= 16 || (M <= 32 && N < 16384)); }
+bool skinny_mx(int64_t M, int64_t N, int64_t K) {
+  return K >= 128 && (M <= 32 || (M <= 64 && N <= 8192 && K <= 8192));
+}
 constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
 
 int64_t split_row_groups(int64_t M) { return (M + kRowPad - 1) / kRowPad * (kRowPad / 32); }
@@ -425,7 +415,7 @@ int64_t split_ksteps(int64_t K) { return (K + 127) / 128 * 2; }
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return 0;
-  if (skinny(M, K, kSkinnyRows))
+  if (skinny(M, N, K))
     return (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * (kMxFragBytes + kMxFragScaleBytes);
   return (size_t)(split_row_groups(M) * split_ksteps(K)) * (kMxFragBytes + kMxFragScaleBytes) + scale_bytes(N, K);
 }
@@ -434,29 +424,27 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
                              int64_t K, void* Y, void* workspace, hipStream_t stream) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return launch_mxfp4_gemv(X, xdtype, codes, scales, N, K, Y, stream);
   uint8_t* const pieces = static_cast<uint8_t*>(workspace);
-  const bool few = skinny(M, K, kSkinnyRows);
+  const bool few = skinny(M, N, K);
   const int64_t rg = few ? (M + 15) / 16 : split_row_groups(M), ks = few ? (K + 511) / 512 * 4 : split_ksteps(K);
   uint8_t* const ps = pieces + rg * ks * kMxFragBytes;
-  hipError_t e = launch_mxfp4_split(X, xdtype, M, K, few ? 16 : 32, rg, ks, pieces, ps, stream);
+  uint8_t* const ws = ps + rg * ks * kMxFragScaleBytes;
+  const hipError_t e = launch_mxfp4_split(X, xdtype, M, K, few ? 16 : 32, rg, ks, pieces, ps, few ? nullptr : scales, N, ws, stream);
   if (e != hipSuccess) return e;
   if (few) return launch_mxfp4_skinny(pieces, ps, codes, scales, M, N, K, xdtype, Y, stream);
-  uint8_t* const ws = ps + rg * ks * kMxFragScaleBytes;
-  e = launch_scales(scales, N, ws, nullptr, 0, nullptr, K, stream);
-  if (e != hipSuccess) return e;
   return xdtype == 0 ? launch<F16, kMxPieces>(pieces, ps, codes, ws, M, N, K, Y, stream)
                      : launch<BF16, kMxPieces>(pieces, ps, codes, ws, M, N, K, Y, stream);
 }
 
 size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return skinny(M, K, kSkinnyRowsMx) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
+  return skinny_mx(M, N, K) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
 }
 
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, void* workspace, hipStream_t stream) {
-  if (skinny(M, K, kSkinnyRowsMx)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
+  if (skinny_mx(M, N, K)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   uint8_t* const as = ws + scale_bytes(N, K);
-  const hipError_t e = launch_scales(Ws, N, ws, As, M, as, K, stream);
+  const hipError_t e = launch_mxfp4_scales(Ws, N, ws, As, M, as, K, stream);
   if (e != hipSuccess) return e;
   return ydtype == 0 ? launch<F16, 1>(A, as, W, ws, M, N, K, Y, stream) : launch<BF16, 1>(A, as, W, ws, M, N, K, Y, stream);
 }

@@ -107,12 +107,52 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32
   }
 }
 
+// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 127 in the
+// place of rows and blocks that are not there.
+struct ScaleJob {
+  const uint8_t* scales;
+  uint32_t* out;
+  int rows, rows_pad;
+};
+// Workgroup `block` of a job's.
+__device__ inline void turn_scales(const ScaleJob& j, int nblk, int block) {
+  const int64_t i = (int64_t)block * kThreads + threadIdx.x;
+  const int ktiles = (nblk + 7) / 8 * 2;
+  // a thread takes 16 blocks of a row, a wave 64 rows: the writes are contiguous
+  const int row = (int)(i % j.rows_pad), g = (int)(i / j.rows_pad);
+  if (4 * g >= ktiles) return;
+  u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  if (row < j.rows) {
+    const uint8_t* const p = j.scales + (int64_t)row * nblk + 16 * g;
+    if (16 * g + 16 <= nblk) {
+      __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (16 * g + q < nblk) v[q / 4] = (v[q / 4] & ~(0xFFu << (8 * (q % 4)))) | ((uint32_t)p[q] << (8 * (q % 4)));
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (4 * g + q < ktiles) j.out[(int64_t)(4 * g + q) * j.rows_pad + row] = v[q];
+}
+
+__global__ __launch_bounds__(kThreads) void mxfp4_scales_kernel(ScaleJob w, ScaleJob a, int nblk, int wblocks) {
+  const bool first = (int)blockIdx.x < wblocks;
+  turn_scales(first ? w : a, nblk, (int)blockIdx.x - (first ? 0 : wblocks));
+}
+
+// Workgroups [0, split) split X, the rest turn W's scales.
 // One wave per fragment of R rows x 2048 / R elements (layout in
 // mxfp4_device.h).
 template <class XT, int R>
 __global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* __restrict__ X, int M, int K,
                                                                int ksteps, int frags, uint8_t* __restrict__ pieces,
-                                                               uint32_t* __restrict__ scales) {
+                                                               uint32_t* __restrict__ scales, ScaleJob w, int split) {
+  if ((int)blockIdx.x >= split) {
+    turn_scales(w, K / kMxBlock, (int)blockIdx.x - split);
+    return;
+  }
   const int f = (int)blockIdx.x * (kThreads / 64) + (int)(threadIdx.x >> 6);
   if (f >= frags) return;
   const int lane = threadIdx.x & 63;
@@ -124,6 +164,13 @@ __global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* _
   if (row < M && k < K) mx_load_block<XT>(X + (int64_t)row * K + k, v);
   const MxPieces s = mx_split(v);
   mx_store_pieces(s, pieces + (int64_t)f * kMxFragBytes, scales + (int64_t)f * 64, lane);
+}
+
+// Workgroups of a scale job, one row and 512 of K a thread.
+static_assert(kMxScaleRowPad % kThreads == 0, "a workgroup's rows are whole");
+int64_t scale_blocks(int64_t rows, int64_t K) { return mxfp4_scale_rows(rows) * ((K + 511) / 512) / kThreads; }
+ScaleJob scale_job(const void* scales, int64_t rows, void* out) {
+  return ScaleJob{static_cast<const uint8_t*>(scales), static_cast<uint32_t*>(out), (int)rows, (int)mxfp4_scale_rows(rows)};
 }
 
 unsigned grid_for(int64_t units) {
@@ -160,24 +207,27 @@ hipError_t launch_mxfp4_dequantize(const void* codes, const void* scales, int64_
   return hipGetLastError();
 }
 
+hipError_t launch_mxfp4_scales(const void* Ws, int64_t N, void* wout, const void* As, int64_t M, void* aout, int64_t K,
+                               hipStream_t stream) {
+  const int64_t wblocks = scale_blocks(N, K), ablocks = scale_blocks(M, K);
+  mxfp4_scales_kernel<<<(unsigned)(wblocks + ablocks), kThreads, 0, stream>>>(
+      scale_job(Ws, N, wout), scale_job(As, M, aout), (int)(K / kMxBlock), (int)wblocks);
+  return hipGetLastError();
+}
+
 hipError_t launch_mxfp4_split(const void* X, int xdtype, int64_t M, int64_t K, int R, int64_t row_groups,
-                              int64_t ksteps, void* pieces, void* scales, hipStream_t stream) {
+                              int64_t ksteps, void* pieces, void* scales, const void* Ws, int64_t N, void* wout,
+                              hipStream_t stream) {
   const int frags = (int)(row_groups * ksteps);
-  const unsigned grid = (unsigned)((frags + kThreads / 64 - 1) / (kThreads / 64));
+  const int split = (frags + kThreads / 64 - 1) / (kThreads / 64);
+  const unsigned grid = (unsigned)(split + (Ws ? scale_blocks(N, K) : 0));
+  const ScaleJob w = scale_job(Ws, N, wout);
   const auto* xp = static_cast<const uint16_t*>(X);
   auto* pp = static_cast<uint8_t*>(pieces);
   auto* sp = static_cast<uint32_t*>(scales);
-  if (R == 32) {
-    if (xdtype == 0)
-      mxfp4_split_kernel<F16, 32><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
-    else
-      mxfp4_split_kernel<BF16, 32><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
-  } else {
-    if (xdtype == 0)
-      mxfp4_split_kernel<F16, 16><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
-    else
-      mxfp4_split_kernel<BF16, 16><<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp);
-  }
+  auto* const f = R == 32 ? (xdtype == 0 ? mxfp4_split_kernel<F16, 32> : mxfp4_split_kernel<BF16, 32>)
+                          : (xdtype == 0 ? mxfp4_split_kernel<F16, 16> : mxfp4_split_kernel<BF16, 16>);
+  f<<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp, w, split);
   return hipGetLastError();
 }
 

@@ -140,7 +140,15 @@ hipError_t launch_mxfp4_dequantize(const void* codes, const void* scales, int64_
 // Splits 16-bit X [M, K] into 6-bit pieces, fragment-major: row_groups groups
 // of R rows (32 or 16) by ksteps steps of 2048 / R elements.
 hipError_t launch_mxfp4_split(const void* X, int xdtype, int64_t M, int64_t K, int R, int64_t row_groups,
-                              int64_t ksteps, void* pieces, void* scales, hipStream_t stream);
+                              int64_t ksteps, void* pieces, void* scales, const void* Ws, int64_t N, void* wout,
+                              hipStream_t stream);
+// Scale bytes [rows, K / 32] in the tile kernels' order: one dword per row and
+// 128 of K, [K tile][mxfp4_scale_rows(rows)]; launch_mxfp4_split does W's beside
+// the split where Ws is given.
+constexpr int kMxScaleRowPad = 256;
+inline int64_t mxfp4_scale_rows(int64_t rows) { return (rows + kMxScaleRowPad - 1) / kMxScaleRowPad * kMxScaleRowPad; }
+hipError_t launch_mxfp4_scales(const void* Ws, int64_t N, void* wout, const void* As, int64_t M, void* aout, int64_t K,
+                               hipStream_t stream);
 // One row of activations, K <= mxfp4_gemv_max_k().
 int64_t mxfp4_gemv_max_k();
 hipError_t launch_mxfp4_gemv(const void* x, int xdtype, const void* codes, const void* scales, int64_t N, int64_t K,

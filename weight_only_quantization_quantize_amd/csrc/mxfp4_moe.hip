@@ -11,19 +11,26 @@
 // units (mxfp4_stream.h); each further 16 tokens take a turn of their own, out of
 // L2.  (All chunks in one turn needs 64 sums a lane more and spilled.)
 //
-// Four launches:
-//   route   logits, one workgroup per expert and 8 tokens; x split into pieces
-//   choose  one workgroup: the tokens' experts and shares, and the list of turns
-//           (an expert and up to 16 of its tokens, in ascending order)
-//   up      one workgroup per (turn, 32 columns of h): gate and up rows, then
-//           p silu(g) u, split into pieces again (14 bits of a block's largest
-//           magnitude).  The share is folded in here, where the values are still
-//           fp32, so that the next product adds over experts by itself.
-//   down    one workgroup per 16 columns of y, over all turns: each wave adds its
-//           products into a sum per token in LDS of its own, and the waves' sums
-//           are added in a fixed order (no atomics).
-// Working the choice out in every workgroup of the up launch instead of in a
-// launch of its own took 4 us there for one token and 15 for five.
+// Launches:
+//   route    logits, one workgroup per expert and 8 tokens; x split into pieces
+//   choose   one workgroup: the tokens' experts and shares, and the list of turns
+//            (an expert and up to 16 of its tokens, in ascending order)
+//   up       32 columns of h a time: gate and up rows, then p silu(g) u, split into
+//            pieces again (14 bits of a block's largest magnitude).  The share is
+//            folded in here, where the values are still fp32.
+//   down     64 columns of a turn's products a time
+//   combine  y from its experts' products, added in the order of choice (no atomics)
+// One token needs no list: up and down work the choices out from the logits, and
+// down adds over the experts itself.
+//
+// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 105 us, of which up 63
+// (285 MB of weights, 4.5 TB/s) and down 31 (142 MB, 4.6 TB/s); one token 24 us,
+// up 13, down 8.5, logits 5.  A workgroup per 32 columns and turn (up) and per 16
+// columns of y over all turns (down) took 86 and 51: they read the activations again
+// for every 64 (16) weight rows, and a workgroup's first loads had nothing before
+// them to hide behind.
+#include <cstddef>
+
 #include "mxfp4_stream.h"
 #include "woq_internal.h"
 
@@ -34,12 +41,10 @@ constexpr int kChunk = 16;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 64;
-constexpr int kMaxTurns = kMaxExperts + kMaxTokens * kMaxTopK / 16;
 constexpr int kRouteThreads = 512;
 constexpr int kRouteTokens = 8;   // tokens per workgroup of the logits
 constexpr int kChooseWaves = 16;
-constexpr int kUpWaves = 8;         // at most
-constexpr int kDownWaves = 8;
+constexpr int kExpertWaves = 8;     // at most
 
 // An expert and up to 16 of its tokens.
 struct Turn {
@@ -128,12 +133,57 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const uint16_t
   }
 }
 
-// One workgroup.  logits [T][E] -> the plan and its turns.
+// A token's choices, one a lane: the wave works them out from its logits, lane
+// holding those of the experts 64 j + lane.
+struct Choice {
+  int expert;
+  float share;
+};
+template <int NJ>
+__device__ inline Choice choose(const float (&logit)[NJ], int E, int top_k, int lane) {
+  uint32_t key[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) key[j] = 64 * j + lane < E ? order_key(logit[j]) : 0u;
+  uint32_t taken = 0;  // bit j: expert 64 j + lane
+  int expert = 0;
+  uint32_t chosen = 0, first = 0;
+  for (int c = 0; c < top_k; ++c) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (!(taken >> j & 1) && key[j] > m) m = key[j];
+    m = wave_max(m);
+    int id = -1;  // the lowest index of that key
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (id < 0) {
+        const uint64_t b = __ballot(!(taken >> j & 1) && key[j] == m && 64 * j + lane < E);
+        if (b) id = 64 * j + __builtin_ctzll(b);
+      }
+    if (lane == (id & 63)) taken |= 1u << (id >> 6);
+    if (c == 0) first = m;
+    if (lane == c) {
+      expert = id;
+      chosen = m;
+    }
+  }
+  const float w = lane < top_k ? expf(key_value(chosen) - key_value(first)) : 0.0f;
+  return Choice{expert, w / team_sum(w, 64)};
+}
+template <int NJ>
+__device__ inline void load_logits(float (&logit)[NJ], const float* __restrict__ logits, int E, int lane) {
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) logit[j] = 64 * j + lane < E ? logits[64 * j + lane] : 0.0f;
+}
+
+// One workgroup.  logits [T][E] -> the plan, its turns, and the row of the turns'
+// products for each token's choices.
 // NJ: lanes' experts, 64 NJ >= E.
 template <int NJ>
 __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const float* __restrict__ logits, int T, int E,
                                                                        int top_k, Plan* __restrict__ plan,
-                                                                       Turn* __restrict__ turns) {
+                                                                       Turn* __restrict__ turns,
+                                                                       int* __restrict__ where) {
   __shared__ uint16_t ids[kMaxTokens * kMaxTopK];      // [token][choice]
   __shared__ float shares[kMaxTokens * kMaxTopK];
   __shared__ unsigned long long tokens[kMaxExperts];   // of an expert
@@ -143,46 +193,22 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const flo
   for (int e = threadIdx.x; e < E; e += kChooseWaves * 64) tokens[e] = 0;
   __syncthreads();
   constexpr int kTokens = kMaxTokens / kChooseWaves;  // of a wave, at most
-  float logit[kTokens][NJ];                           // of expert 64 j + lane
+  float logit[kTokens][NJ];
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int t = wave + kChooseWaves * i, e = 64 * j + lane;
-      logit[i][j] = t < T && e < E ? logits[t * E + e] : 0.0f;
-    }
+  for (int i = 0; i < kTokens; ++i) {
+    const int t = wave + kChooseWaves * i;
+    load_logits(logit[i], logits + (int64_t)(t < T ? t : 0) * E, E, lane);
+  }
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     const int t = wave + kChooseWaves * i;
     if (t >= T) break;
-    uint32_t key[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = 64 * j + lane < E ? order_key(logit[i][j]) : 0u;
-    uint32_t taken = 0;  // bit j: expert 64 j + lane
-    for (int c = 0; c < top_k; ++c) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (!(taken >> j & 1) && key[j] > m) m = key[j];
-      m = wave_max(m);
-      int id = -1;  // the lowest index of that key
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (id < 0) {
-          const uint64_t b = __ballot(!(taken >> j & 1) && key[j] == m && 64 * j + lane < E);
-          if (b) id = 64 * j + __builtin_ctzll(b);
-        }
-      if (lane == (id & 63)) taken |= 1u << (id >> 6);
-      if (lane == 0) {
-        ids[t * top_k + c] = (uint16_t)id;
-        shares[t * top_k + c] = key_value(m);
-        atomicOr(&tokens[id], 1ull << t);
-      }
+    const Choice c = choose(logit[i], E, top_k, lane);
+    if (lane < top_k) {
+      ids[t * top_k + lane] = (uint16_t)c.expert;
+      shares[t * top_k + lane] = c.share;
+      atomicOr(&tokens[c.expert], 1ull << t);
     }
-    // softmax over the choices, one a lane
-    const float w = lane < top_k ? expf(shares[t * top_k + lane] - shares[t * top_k]) : 0.0f;
-    const float sum = team_sum(w, 64);
-    if (lane < top_k) shares[t * top_k + lane] = w / sum;
   }
   __syncthreads();
   if (wave == 0) {  // turns before each expert's
@@ -215,184 +241,249 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const flo
     Turn& r = turns[base[e] + row / kChunk];
     r.share[row % kChunk] = shares[i];
     r.token[row % kChunk] = (uint8_t)t;
+    where[i] = (int)base[e] * kChunk + row;
   }
 }
 
-// Workgroup (i, turn): columns [32 i, 32 i + 32) of h for the turn's tokens.
-__global__ __launch_bounds__(kUpWaves * 64, 3) void moe_up_kernel(const uint8_t* __restrict__ xp,
-                                                                  const uint8_t* __restrict__ xs,
-                                                                  const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales,
-                                                                  const Plan* __restrict__ plan,
-                                                                  const Turn* __restrict__ turns, int H, int I, int E,
-                                                                  uint8_t* __restrict__ hp, uint32_t* __restrict__ hs) {
-  constexpr int NT = 4;  // gate rows, up rows, gate rows, up rows
-  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kUpWaves][kUnitStage];
-  __shared__ float hbuf[kChunk][kMxBlock + 1];
-  static_assert(NT * 1024 <= kUnitStage, "a wave's partial sums fit its stage's place");
+// The experts' products.  Item: a turn and 64 weight rows of its expert: UP, 32
+// gate rows and their 32 up rows, which make 32 columns of h; else 64 rows of
+// down, 64 columns of y.  A workgroup takes a run of items, K split between its
+// waves (wave w: super-steps w, w + waves, ...).  The activations stay in
+// registers while the turn does not change, and the next item's weights are on
+// their way while an item's sums meet in LDS.
+// NJ > 0: one token; every wave works its choices out from the logits, and turn k
+// is choice k.
+template <bool UP, int WAVES, int NJ>
+__global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
+    const uint8_t* __restrict__ xp, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ codes,
+    const uint8_t* __restrict__ scales, const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan,
+    const Turn* __restrict__ turns, int K, int rows, int E, int groups, uint8_t* __restrict__ hp,
+    uint32_t* __restrict__ hs, float* __restrict__ products) {
+  constexpr int NT = 4;  // tiles of 16 rows; UP: gate rows, up rows, gate rows, up rows
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[WAVES][kUnitStage];
+  __shared__ float4_t parts[2][WAVES][NT][64];  // alternating: one barrier an item
+  __shared__ float hbuf[kChunk + 1][kMxBlock + 1];  // the last row: zeros
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int turn = blockIdx.y, i0 = (int)blockIdx.x * kMxBlock;
-  if (turn >= plan->turns) return;
-  const Turn& rec = turns[turn];
-  const int e = rec.expert, count = rec.count;
-
-  const int nblk = H / kMxBlock, supers = (H + 511) / 512, hsupers = (I + 511) / 512;
-  const int64_t rows_left = (int64_t)E * 2 * I - ((int64_t)e * 2 * I + i0);
-  const uint8_t* const wcodes = codes + ((int64_t)e * 2 * I + i0) * nblk * 16;
-  const uint8_t* const wscales = scales + ((int64_t)e * 2 * I + i0) * nblk;
-  const int waves = blockDim.x >> 6;  // wave w takes super-steps w, w + waves, ...
+  const int waves = blockDim.x >> 6;
+  const int nblk = K / kMxBlock, supers = (K + 511) / 512;
+  __shared__ Choice choices[NJ > 0 ? WAVES : 1][NJ > 0 ? kMaxTopK : 1];
+  if constexpr (NJ > 0) {
+    float logit[NJ];
+    load_logits(logit, logits, E, lane);
+    choices[wave][lane] = choose(logit, E, top_k, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  const int64_t items = (int64_t)(NJ > 0 ? top_k : plan->turns) * groups;
+  const int i0 = (int)(items * blockIdx.x / gridDim.x), i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+  if (i0 >= i1) return;
   uint8_t* const stage = stage_all[wave];
-  // tiles in the order gate, up, gate, up; two units in flight, loaded in order;
-  // past the end a line or two of the first rows is loaded in their place
-  MxUnit u[2];
-  auto row_of = [&](int j) { return (j & 1 ? I : 0) + (j >> 1) * 16; };
-  auto ahead = [&](int j, int S_) {
-    const bool more = S_ < supers;
-    const int S = more ? S_ : 0;
-    const int64_t row = more ? row_of(j) : 0;
+  const int64_t all = (int64_t)E * rows;
+  auto first_row = [&](int item) {
+    const int k = item / groups;
+    const int e = NJ > 0 ? __builtin_amdgcn_readfirstlane(choices[wave][k].expert) : turns[k].expert;
+    return (int64_t)e * rows + item % groups * (UP ? 32 : 64);
+  };
+  // a turn's record, a dword a lane; on its way before the weights of its first item
+  static_assert(sizeof(Turn) == 4 * 22 && offsetof(Turn, share) == 8 && offsetof(Turn, token) == 72, "read as dwords");
+  auto record = [&](int k) { return reinterpret_cast<const uint32_t*>(turns + k)[lane < 22 ? lane : 21]; };
+  // rows past the expert's last (its columns are a multiple of 32) repeat the first tile
+  auto tile_row = [&](int j, int item) {
+    return UP ? (j & 1) * (rows / 2) + (j >> 1) * 16 : (item % groups * 64 + 16 * j < rows ? 16 * j : 0);
+  };
+
+  // the wave's next step, whose units are loaded as the current one's are used;
+  // past the end a line or two of the last one is loaded in their place
+  int item_n = i0, S_n = wave;
+  uint32_t rec_n = NJ > 0 ? 0u : record(i0 / groups);
+  int64_t row_n = first_row(i0);
+  MxUnit u[NT];
+  auto ahead = [&](int j) {
+    const bool more = item_n < i1;
+    const int64_t row = row_n + tile_row(j, more ? item_n : i1 - 1);
     __builtin_amdgcn_sched_barrier(0);
-    mx_load_unit(u[j & 1], wcodes + row * nblk * 16, wscales + row * nblk, 15, (rows_left - row) * nblk, more ? nblk : 1, S, lane);
+    mx_load_unit(u[j], codes + row * nblk * 16, scales + row * nblk, 15, (all - row) * nblk, more ? nblk : 1, more ? S_n : 0, lane);
     __builtin_amdgcn_sched_barrier(0);
   };
-  float4_t acc[NT] = {};
-  int S = wave;
-  // rows past the turn's last token repeat it
-  const int t = rec.token[(lane & 15) < count ? lane & 15 : count - 1];
-  const MxPlace place = mx_place(t / kChunk * supers * 4, (lane & 48) + t % kChunk);
-  ahead(0, S);
-  ahead(1, S);
-  for (; S < supers; S += waves) {
-    MxActivations a[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      mx_load_activations(a[s], xp + (int64_t)(S * 4 + s) * kMxFragBytes, xs + (int64_t)(S * 4 + s) * kMxFragScaleBytes, place);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      mx_stage_unit(u[j & 1], stage, 15, (rows_left - row_of(j)) * nblk, nblk, S, lane);
-      ahead((j + 2) & 3, j < 2 ? S : S + waves);
-      const int sc = mx_staged_scale(stage, lane);
-      mx_each_step([&](auto sel) {
-        constexpr int s = decltype(sel)::value;
-        mx_multiply<s>(acc[j], a[s], mx_staged_weights(stage, s, lane), sc);
-      });
+  for (int j = 0; j < NT; ++j) ahead(j);
+
+  if (threadIdx.x < kMxBlock) hbuf[kChunk][threadIdx.x] = 0.0f;
+  MxActivations a[4];
+  int turn = -1, count = 0, token = 0;
+  float share = 0.0f;  // of row lane % 16; rows past the turn's last token repeat it
+  for (int item = i0; item < i1; ++item) {
+    const int k = item / groups, group = item % groups;
+    const bool changed = k != turn;
+    if (changed) {
+      turn = k;
+      if constexpr (NJ > 0) {
+        count = 1;
+        share = choices[wave][k].share;
+      } else {
+        count = __builtin_amdgcn_readlane((int)rec_n, 1);
+        const int m = (lane & 15) < count ? lane & 15 : count - 1;
+        share = __builtin_bit_cast(float, __shfl((int)rec_n, 2 + m, 64));
+        token = UP ? __shfl((int)rec_n, 18 + m / 4, 64) >> (8 * (m & 3)) & 0xFF : m;
+      }
     }
-  }
-  // the waves' partial sums meet in the stages' place, [tile][lane][4] a wave
+    float4_t acc[NT] = {};
+    const int64_t row0 = row_n;
+    for (int S = wave; S < supers; S += waves) {
+      if (changed || supers > waves) {
+        const MxPlace place = mx_place(UP ? token / kChunk * supers * 4 : 0, (lane & 48) + token % kChunk);
+        const int64_t f = ((int64_t)(UP ? 0 : k) * supers + S) * 4;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) *reinterpret_cast<float4_t*>(stage + (j * 64 + lane) * 16) = acc[j];
-  __syncthreads();
-  for (int o = threadIdx.x; o < kChunk * kMxBlock; o += (int)blockDim.x) {
-    const int tm = o >> 5, tn = o & 31;
-    const int sl = (tm >> 2) * 16 + (tn & 15);
-    float g = 0.0f, v = 0.0f;
-    for (int w = 0; w < waves; ++w) {
-      const float* const part = reinterpret_cast<const float*>(stage_all[w]);
-      g += part[((tn >> 4) * 128 + sl) * 4 + (tm & 3)];
-      v += part[((tn >> 4) * 128 + 64 + sl) * 4 + (tm & 3)];
+        for (int s = 0; s < 4; ++s)
+          mx_load_activations(a[s], xp + (f + s) * kMxFragBytes, xs + (f + s) * kMxFragScaleBytes, place);
+      }
+      S_n = S + waves;
+      if (S_n >= supers) {
+        S_n = wave;
+        if (++item_n < i1) {
+          if (NJ == 0 && item_n / groups != k) rec_n = record(item_n / groups);
+          row_n = first_row(item_n);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mx_stage_unit(u[j], stage, 15, (all - (row0 + tile_row(j, item))) * nblk, nblk, S, lane);
+        ahead(j);
+        const int sc = mx_staged_scale(stage, lane);
+        mx_each_step([&](auto sel) {
+          constexpr int s = decltype(sel)::value;
+          mx_multiply<s>(acc[j], a[s], mx_staged_weights(stage, s, lane), sc);
+        });
+      }
     }
-    hbuf[tm][tn] = tm < count ? rec.share[tm] * (g / (1.0f + expf(-g))) * v : 0.0f;
-  }
-  __syncthreads();
-  // 16 threads split a row's block each; behind the last block of h the rest of
-  // its super-step is zeros
-  const int blk = i0 / kMxBlock, last = blk == I / kMxBlock - 1 ? kSuper * hsupers - blk : 1;
-  for (int o = threadIdx.x; o < kChunk * last; o += (int)blockDim.x) {
-    const int m = o & 15, b = blk + (o >> 4);
-    float v[kMxBlock];
+    float4_t(*const part)[NT][64] = parts[(item - i0) & 1];
 #pragma unroll
-    for (int k = 0; k < kMxBlock; ++k) v[k] = b == blk ? hbuf[m][k] : 0.0f;
-    const int64_t f = ((int64_t)turn * hsupers + b / kSuper) * 4 + b % 4;
-    mx_store_pieces(mx_split(v), hp + f * kMxFragBytes, hs + f * 64, (b % kSuper / 4) * kChunk + m);
+    for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
+    __syncthreads();
+    // value (row m, tile j, column c) of a wave: part[w][j][(m / 4) 16 + c][m % 4]
+    auto sum = [&](int m, int j, int c) {
+      float v = 0.0f;
+      for (int w = 0; w < waves; ++w) v += part[w][j][(m >> 2) * 16 + c][m & 3];
+      return v;
+    };
+    if constexpr (UP) {
+      // wave w takes the rows 2 w, 2 w + 1, + 2 waves, ...
+      for (int m0 = 2 * wave; m0 < count; m0 += 2 * waves) {
+        const int m = m0 + (lane >> 5), c = lane & 31;
+        if (m < count) {
+          const float g = sum(m, (c >> 4) * 2, c & 15), v = sum(m, (c >> 4) * 2 + 1, c & 15);
+          hbuf[m][c] = g / (1.0f + expf(-g)) * v;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // a lane splits a row's block; behind the last block of h the rest of its
+      // super-step is zeros
+      const int m = lane & 15, hsupers = (groups + kSuper - 1) / kSuper;
+      const int end = group == groups - 1 ? kSuper * hsupers : group + 1;
+      if (m < count && (m >> 1) % waves == wave) {
+        for (int b = group + (lane >> 4); b < end; b += 4) {
+          const float* const row = hbuf[b == group ? m : kChunk];
+          const float scale = b == group ? share : 0.0f;
+          float v[kMxBlock];
+#pragma unroll
+          for (int c = 0; c < kMxBlock; ++c) v[c] = scale * row[c];
+          const int64_t f = ((int64_t)k * hsupers + b / kSuper) * 4 + b % 4;
+          mx_store_pieces(mx_split(v), hp + f * kMxFragBytes, hs + f * 64, (b % kSuper / 4) * kChunk + m);
+        }
+      }
+    } else {
+      const int n = group * 64 + lane;
+      for (int m = wave; m < count; m += waves)
+        if (n < rows) products[((int64_t)k * kChunk + m) * rows + n] = sum(m, lane >> 4, lane & 15);
+    }
   }
 }
 
-// Workgroup: columns [16 b, 16 b + 16) of y for all tokens.
-template <class YT, int TC>
-__global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(const uint8_t* __restrict__ hp,
-                                                                   const uint8_t* __restrict__ hs,
-                                                                   const uint8_t* __restrict__ codes,
-                                                                   const uint8_t* __restrict__ scales,
-                                                                   const Plan* __restrict__ plan,
-                                                                   const Turn* __restrict__ turns, int T, int H, int I,
-                                                                   int E, uint16_t* __restrict__ Y) {
-  constexpr int kRows = TC * kChunk;
-  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kDownWaves][kUnitStage];
-  __shared__ float sums[kDownWaves][kRows][kChunk + 1];
-  __shared__ uint32_t table[kMaxTurns];  // expert + count << 16
+// One token: columns [16 b, 16 b + 16) of y, over all turns' super-steps, which
+// the waves share out; their sums are added in order.  (As items of the general
+// form and a launch for the sum over experts they took 14 us for 4 experts of
+// 4096 x 2048, this takes 8.5.)
+template <class YT, int NJ>
+__global__ __launch_bounds__(kExpertWaves * 64) void moe_one_down_kernel(const uint8_t* __restrict__ hp,
+                                                                         const uint8_t* __restrict__ hs,
+                                                                         const uint8_t* __restrict__ codes,
+                                                                         const uint8_t* __restrict__ scales,
+                                                                         const float* __restrict__ logits, int top_k,
+                                                                         int H, int I, int E, uint16_t* __restrict__ Y) {
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kExpertWaves][kUnitStage];
+  __shared__ float sums[kExpertWaves][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nblk = I / kMxBlock, supers = (I + 511) / 512;
-  const int nturns = plan->turns, units = nturns * supers;
+  const int nblk = I / kMxBlock, supers = (I + 511) / 512, units = top_k * supers;
   const int n0 = (int)blockIdx.x * 16;
   uint8_t* const stage = stage_all[wave];
-  for (int k = threadIdx.x; k < nturns; k += kDownWaves * 64) table[k] = (uint32_t)turns[k].expert | (uint32_t)turns[k].count << 16;
-  for (int o = lane; o < kRows * (kChunk + 1); o += 64) (&sums[wave][0][0])[o] = 0.0f;
-  __syncthreads();
-  // the wave's run of units: a turn's super-steps follow one another
-  const int u0 = (int)((int64_t)units * wave / kDownWaves), u1 = (int)((int64_t)units * (wave + 1) / kDownWaves);
+  float logit[NJ];
+  load_logits(logit, logits, E, lane);
+  const Choice choice = choose(logit, E, top_k, lane);
   struct Work {
     MxUnit u;
     MxActivations a[4];
-    uint32_t token;  // of rows 4 q .. 4 q + 3
   };
+  auto row_of = [&](int i) { return (int64_t)__builtin_amdgcn_readlane(choice.expert, i / supers) * H + n0; };
+  const MxPlace place = mx_place(0, lane & 48);  // every row is the token's
   auto load = [&](Work& w, int i) {
-    const int k = i / supers, S = i % supers;
-    const uint32_t rec = (uint32_t)__builtin_amdgcn_readfirstlane((int)table[k]);
-    const int64_t row = (int64_t)(rec & 0xFFFFu) * H + n0;
-    mx_load_unit(w.u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, S, lane);
-    // rows past the turn's tokens are left as they are: their sums are not taken
-    if ((lane & 15) < (int)(rec >> 16)) {
-      const MxPlace place = mx_place(0, lane);
-      const int64_t f = ((int64_t)k * supers + S) * 4;
+    const int64_t row = row_of(i);
+    mx_load_unit(w.u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, i % supers, lane);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        mx_load_activations(w.a[s], hp + (f + s) * kMxFragBytes, hs + (f + s) * kMxFragScaleBytes, place);
-    }
-    w.token = reinterpret_cast<const uint32_t*>(turns[k].token)[lane >> 4];
+    for (int s = 0; s < 4; ++s)
+      mx_load_activations(w.a[s], hp + ((int64_t)i * 4 + s) * kMxFragBytes, hs + ((int64_t)i * 4 + s) * kMxFragScaleBytes, place);
   };
   float4_t acc = {};
   auto work = [&](const Work& w, int i) {
-    const int k = i / supers, S = i % supers;
-    const uint32_t rec = (uint32_t)__builtin_amdgcn_readfirstlane((int)table[k]);
-    const int64_t row = (int64_t)(rec & 0xFFFFu) * H + n0;
-    mx_stage_unit(w.u, stage, 15, ((int64_t)E * H - row) * nblk, nblk, S, lane);
+    mx_stage_unit(w.u, stage, 15, ((int64_t)E * H - row_of(i)) * nblk, nblk, i % supers, lane);
     const int sc = mx_staged_scale(stage, lane);
     mx_each_step([&](auto sel) {
       constexpr int s = decltype(sel)::value;
       mx_multiply<s>(acc, w.a[s], mx_staged_weights(stage, s, lane), sc);
     });
-    if (S == supers - 1 || i + 1 == u1) {  // the wave is through with the turn
-      const int count = (int)(rec >> 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * (lane >> 4) + e < count) sums[wave][w.token >> (8 * e) & 63u][lane & 15] += acc[e];
-      acc = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
   };
-  Work a = {}, b = {};
-  if (u0 < u1) load(a, u0);
-  if (u0 + 1 < u1) load(b, u0 + 1);
-  for (int i = u0; i < u1; i += 2) {
+  // two units at a time; an odd last one is loaded twice and multiplied once
+  constexpr int W = kExpertWaves;
+  for (int i = wave; i < units; i += 2 * W) {
+    const bool two = i + W < units;
+    Work a, b;
+    load(a, i);
+    load(b, two ? i + W : i);
+    __builtin_amdgcn_sched_barrier(0);  // all loads start before the first product
     work(a, i);
-    if (i + 2 < u1) load(a, i + 2);
-    if (i + 1 < u1) work(b, i + 1);
-    if (i + 3 < u1) load(b, i + 3);
+    if (two) work(b, i + W);
   }
+  if (lane < 16) sums[wave][lane] = acc[0];
   __syncthreads();
-  for (int o = threadIdx.x; o < T * kChunk; o += kDownWaves * 64) {
-    const int t = o / kChunk, n = o % kChunk;
+  if (threadIdx.x < 16) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) v += sums[w][t][n];
-    Y[(int64_t)t * H + n0 + n] = YT::from_f32(v);
+    for (int w = 0; w < W; ++w) v += sums[w][threadIdx.x];
+    Y[n0 + threadIdx.x] = YT::from_f32(v);
   }
+}
+
+// y[t] = the sum of its experts' rows of `products`, in the order of choice.
+template <class YT>
+__global__ __launch_bounds__(64) void moe_combine_kernel(const float* __restrict__ products, const int* __restrict__ where,
+                                                         int H, int top_k, uint16_t* __restrict__ Y) {
+  const int n = ((int)blockIdx.x * 64 + (int)threadIdx.x) * 4, t = blockIdx.y;
+  if (n >= H) return;
+  float4_t v = {};
+  for (int c = 0; c < top_k; ++c) {
+    const float4_t p = *reinterpret_cast<const float4_t*>(products + (int64_t)where[t * top_k + c] * H + n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += p[e];
+  }
+  const uint32_t lo = (uint32_t)YT::from_f32(v[0]) | (uint32_t)YT::from_f32(v[1]) << 16;
+  const uint32_t hi = (uint32_t)YT::from_f32(v[2]) | (uint32_t)YT::from_f32(v[3]) << 16;
+  *reinterpret_cast<u32x2_t*>(Y + (int64_t)t * H + n) = u32x2_t{lo, hi};
 }
 
 struct Layout {
   int64_t turns, xfrags, hfrags;
-  size_t logits, plan, records, xp, xs, hp, hs, bytes;
+  size_t logits, plan, records, where, xp, xs, hp, hs, products, bytes;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Layout layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
@@ -404,21 +495,25 @@ Layout layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
   l.logits = 0;
   l.plan = up256((size_t)E * T * 4);
   l.records = l.plan + 256;
-  l.xp = up256(l.records + (size_t)l.turns * sizeof(Turn));
+  l.where = up256(l.records + (size_t)l.turns * sizeof(Turn));
+  l.xp = up256(l.where + (size_t)(T * top_k) * 4);
   l.xs = l.xp + (size_t)l.xfrags * kMxFragBytes;
   l.hp = l.xs + (size_t)l.xfrags * kMxFragScaleBytes;
   l.hs = l.hp + (size_t)l.hfrags * kMxFragBytes;
-  l.bytes = l.hs + (size_t)l.hfrags * kMxFragScaleBytes;
+  l.products = l.hs + (size_t)l.hfrags * kMxFragScaleBytes;
+  l.bytes = l.products + (size_t)(l.turns * kChunk * H) * 4;
   return l;
 }
 
-template <class XT, int TC>
+template <class XT>
 hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_codes, const uint8_t* up_scales,
                   const uint8_t* down_codes, const uint8_t* down_scales, int T, int H, int I, int E, int top_k,
                   uint16_t* Y, uint8_t* ws, const Layout& l, hipStream_t stream) {
   float* const logits = reinterpret_cast<float*>(ws + l.logits);
   Plan* const plan = reinterpret_cast<Plan*>(ws + l.plan);
   Turn* const turns = reinterpret_cast<Turn*>(ws + l.records);
+  int* const where = reinterpret_cast<int*>(ws + l.where);
+  float* const products = reinterpret_cast<float*>(ws + l.products);
   uint8_t* const xs = ws + l.xs;
   uint8_t* const hs = ws + l.hs;
   const int tokens = T == 1 ? 1 : kRouteTokens;
@@ -433,20 +528,39 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
                                                                            reinterpret_cast<uint32_t*>(xs));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (E <= 64)
-    moe_choose_kernel<1><<<1, kChooseWaves * 64, 0, stream>>>(logits, T, E, top_k, plan, turns);
-  else
-    moe_choose_kernel<kMaxExperts / 64><<<1, kChooseWaves * 64, 0, stream>>>(logits, T, E, top_k, plan, turns);
-  e = hipGetLastError();
+  constexpr int kLarge = kMaxExperts / 64;
+  if (T > 1) {
+    auto* const f = E <= 64 ? moe_choose_kernel<1> : moe_choose_kernel<kLarge>;
+    f<<<1, kChooseWaves * 64, 0, stream>>>(logits, T, E, top_k, plan, turns, where);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // a wave for every super-step of a row, up to 8; 8 waves fill a compute unit
+  auto experts = [&](auto up, auto nj, const uint8_t* acts, const uint8_t* act_scales, const uint8_t* codes,
+                     const uint8_t* scales, int K, int rows, int groups) {
+    constexpr bool kUp = decltype(up)::value;
+    constexpr int kNj = decltype(nj)::value;
+    const int supers = (K + 511) / 512, waves = supers < kExpertWaves ? supers : kExpertWaves;
+    auto* const f = waves > 4 ? moe_experts_kernel<kUp, kExpertWaves, kNj> : moe_experts_kernel<kUp, 4, kNj>;
+    f<<<256u * (unsigned)(kExpertWaves / waves), (unsigned)(waves * 64), 0, stream>>>(
+        acts, act_scales, codes, scales, logits, top_k, plan, turns, K, rows, E, groups, ws + l.hp,
+        reinterpret_cast<uint32_t*>(hs), products);
+    return hipGetLastError();
+  };
+  auto up = [&](auto nj) { return experts(std::true_type{}, nj, ws + l.xp, xs, up_codes, up_scales, H, 2 * I, I / kMxBlock); };
+  using Nj0 = std::integral_constant<int, 0>;
+  using Nj1 = std::integral_constant<int, 1>;
+  using NjN = std::integral_constant<int, kLarge>;
+  e = T > 1 ? up(Nj0{}) : (E <= 64 ? up(Nj1{}) : up(NjN{}));
   if (e != hipSuccess) return e;
-  // a wave for every super-step of a row, up to 8: all loads of a row tile start at once
-  const int supers = (H + 511) / 512, waves = supers < kUpWaves ? supers : kUpWaves;
-  moe_up_kernel<<<dim3((unsigned)(I / kMxBlock), (unsigned)l.turns), (unsigned)(waves * 64), 0, stream>>>(
-      ws + l.xp, xs, up_codes, up_scales, plan, turns, H, I, E, ws + l.hp, reinterpret_cast<uint32_t*>(hs));
-  e = hipGetLastError();
+  if (T == 1) {
+    auto* const f = E <= 64 ? moe_one_down_kernel<XT, 1> : moe_one_down_kernel<XT, kLarge>;
+    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(ws + l.hp, hs, down_codes, down_scales, logits, top_k, H, I, E, Y);
+    return hipGetLastError();
+  }
+  e = experts(std::false_type{}, Nj0{}, ws + l.hp, hs, down_codes, down_scales, I, H, (H + 63) / 64);
   if (e != hipSuccess) return e;
-  moe_down_kernel<XT, TC><<<(unsigned)(H / 16), kDownWaves * 64, 0, stream>>>(ws + l.hp, hs, down_codes, down_scales,
-                                                                             plan, turns, T, H, I, E, Y);
+  moe_combine_kernel<XT><<<dim3((unsigned)((H + 255) / 256), (unsigned)T), 64, 0, stream>>>(products, where, H, top_k, Y);
   return hipGetLastError();
 }
 
@@ -464,19 +578,14 @@ hipError_t launch_mxfp4_moe(const void* X, int xdtype, const void* router, const
                             const void* up_scales, const void* down_codes, const void* down_scales, int64_t T,
                             int64_t H, int64_t I, int64_t E, int top_k, void* Y, void* workspace, hipStream_t stream) {
   const Layout l = layout(T, H, I, E, top_k);
-  auto run = [&](auto tag, auto tc) {
-    return launch<decltype(tag), decltype(tc)::value>(
+  auto run = [&](auto tag) {
+    return launch<decltype(tag)>(
         static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(router), static_cast<const uint8_t*>(up_codes),
         static_cast<const uint8_t*>(up_scales), static_cast<const uint8_t*>(down_codes),
         static_cast<const uint8_t*>(down_scales), (int)T, (int)H, (int)I, (int)E, top_k, static_cast<uint16_t*>(Y),
         static_cast<uint8_t*>(workspace), l, stream);
   };
-  auto chunks = [&](auto tag) {
-    return T <= 16   ? run(tag, std::integral_constant<int, 1>{})
-           : T <= 32 ? run(tag, std::integral_constant<int, 2>{})
-                     : run(tag, std::integral_constant<int, 4>{});
-  };
-  return xdtype == 0 ? chunks(F16{}) : chunks(BF16{});
+  return xdtype == 0 ? run(F16{}) : run(BF16{});
 }
 
 }  // namespace woq

@@ -392,20 +392,17 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   }
 }
 
-// Few rows (and K >= 128) go to the weight-streaming kernel, which reads the
-// weights once per 16 rows of split activations, once per 32 rows of 4-bit ones,
-// and needs no pass over the scales.  Whole products, us, streaming / tiles:
-//   split, 16 rows   4096 x 4096 10 / 18, 28672 x 8192 39 / 52
-//          32 rows   4096 x 4096 12 / 18, 8192 x 8192 24 / 30, 4096 x 11008 28 / 39,
-//                    16384 x 4096 21 / 20, 28672 x 8192 55 / 52
-//          64 rows   4096 x 4096 16 / 18, 8192 x 8192 33 / 30, 4096 x 11008 46 / 39
-//   4-bit, 32 rows   4096 x 4096 6 / 10, 28672 x 8192 29 / 35, 4096 x 11008 14 / 20
-//          64 rows   4096 x 4096 7 / 10, 8192 x 8192 17 / 17, 4096 x 11008 23 / 20,
-//                    28672 x 8192 40 / 37
-bool skinny(int64_t M, int64_t N, int64_t K) { return K >= 128 && (M <= 16 || (M <= 32 && N < 16384)); }
-bool skinny_mx(int64_t M, int64_t N, int64_t K) {
-  return K >= 128 && (M <= 32 || (M <= 64 && N <= 8192 && K <= 8192));
-}
+// Few rows (and K >= 128) go to the weight-streaming kernels, which need no pass
+// over the scales.  Whole products, us, streaming / tiles:
+//   split, 32 rows   4096 x 4096 10 / 18, 8192 x 8192 20 / 30, 4096 x 11008 24 / 39,
+//                    16384 x 4096 17 / 19, 28672 x 8192 37 / 53
+//          64 rows   4096 x 4096 12 / 18, 8192 x 8192 26 / 30, 4096 x 11008 39 / 39,
+//                    16384 x 4096 24 / 20, 28672 x 8192 59 / 53
+//   4-bit, 32 rows   4096 x 4096 6 / 10, 28672 x 8192 26 / 35, 4096 x 11008 14 / 20
+//          64 rows   4096 x 4096 8 / 10, 8192 x 8192 17 / 17, 16384 x 4096 14 / 13,
+//                    28672 x 8192 31 / 37, 4096 x 11008 20 / 20
+bool skinny(int64_t M, int64_t N, int64_t K) { return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192 && N <= 8192)); }
+bool skinny_mx(int64_t M, int64_t K) { return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192)); }
 constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
 
 int64_t split_row_groups(int64_t M) { return (M + kRowPad - 1) / kRowPad * (kRowPad / 32); }
@@ -436,12 +433,12 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
 }
 
 size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return skinny_mx(M, N, K) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
+  return skinny_mx(M, K) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
 }
 
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, void* workspace, hipStream_t stream) {
-  if (skinny_mx(M, N, K)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
+  if (skinny_mx(M, K)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   uint8_t* const as = ws + scale_bytes(N, K);
   const hipError_t e = launch_mxfp4_scales(Ws, N, ws, As, M, as, K, stream);

@@ -293,17 +293,15 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
     return UP ? (j & 1) * (rows / 2) + (j >> 1) * 16 : (item % groups * 64 + 16 * j < rows ? 16 * j : 0);
   };
 
-  // the wave's next step, whose units are loaded as the current one's are used;
-  // past the end a line or two of the last one is loaded in their place
+  // the wave's next step, whose units are loaded as the current one's are used
   int item_n = i0, S_n = wave;
   uint32_t rec_n = NJ > 0 ? 0u : record(i0 / groups);
   int64_t row_n = first_row(i0);
   MxUnit u[NT];
   auto ahead = [&](int j) {
-    const bool more = item_n < i1;
-    const int64_t row = row_n + tile_row(j, more ? item_n : i1 - 1);
+    const int64_t row = row_n + tile_row(j, item_n);
     __builtin_amdgcn_sched_barrier(0);
-    mx_load_unit(u[j], codes + row * nblk * 16, scales + row * nblk, 15, (all - row) * nblk, more ? nblk : 1, more ? S_n : 0, lane);
+    mx_load_unit(u[j], codes + row * nblk * 16, scales + row * nblk, 15, (all - row) * nblk, nblk, S_n, lane);
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
@@ -346,21 +344,31 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
           row_n = first_row(item_n);
         }
       }
+      auto multiply = [&](auto more) {
+        int l = lane;
+        asm volatile("" : "+v"(l));  // LDS addresses are worked out each time: kept, they spill
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mx_stage_unit(u[j], stage, 15, (all - (row0 + tile_row(j, item))) * nblk, nblk, S, lane);
-        ahead(j);
-        const int sc = mx_staged_scale(stage, lane);
-        mx_each_step([&](auto sel) {
-          constexpr int s = decltype(sel)::value;
-          mx_multiply<s>(acc[j], a[s], mx_staged_weights(stage, s, lane), sc);
-        });
-      }
+        for (int j = 0; j < NT; ++j) {
+          mx_stage_unit(u[j], stage, 15, (all - (row0 + tile_row(j, item))) * nblk, nblk, S, l);
+          if constexpr (decltype(more)::value) ahead(j);
+          const int sc = mx_staged_scale(stage, l);
+          mx_each_step([&](auto sel) {
+            constexpr int s = decltype(sel)::value;
+            mx_multiply<s>(acc[j], a[s], mx_staged_weights(stage, s, l), sc);
+          });
+        }
+      };
+      if (item_n < i1)
+        multiply(std::true_type{});
+      else
+        multiply(std::false_type{});
     }
     float4_t(*const part)[NT][64] = parts[(item - i0) & 1];
 #pragma unroll
     for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
     __syncthreads();
+    int l = lane;
+    asm volatile("" : "+v"(l));  // as above
     // value (row m, tile j, column c) of a wave: part[w][j][(m / 4) 16 + c][m % 4]
     auto sum = [&](int m, int j, int c) {
       float v = 0.0f;
@@ -370,7 +378,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
     if constexpr (UP) {
       // wave w takes the rows 2 w, 2 w + 1, + 2 waves, ...
       for (int m0 = 2 * wave; m0 < count; m0 += 2 * waves) {
-        const int m = m0 + (lane >> 5), c = lane & 31;
+        const int m = m0 + (l >> 5), c = l & 31;
         if (m < count) {
           const float g = sum(m, (c >> 4) * 2, c & 15), v = sum(m, (c >> 4) * 2 + 1, c & 15);
           hbuf[m][c] = g / (1.0f + expf(-g)) * v;
@@ -379,10 +387,10 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       // a lane splits a row's block; behind the last block of h the rest of its
       // super-step is zeros
-      const int m = lane & 15, hsupers = (groups + kSuper - 1) / kSuper;
+      const int m = l & 15, hsupers = (groups + kSuper - 1) / kSuper;
       const int end = group == groups - 1 ? kSuper * hsupers : group + 1;
       if (m < count && (m >> 1) % waves == wave) {
-        for (int b = group + (lane >> 4); b < end; b += 4) {
+        for (int b = group + (l >> 4); b < end; b += 4) {
           const float* const row = hbuf[b == group ? m : kChunk];
           const float scale = b == group ? share : 0.0f;
           float v[kMxBlock];
@@ -393,9 +401,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
         }
       }
     } else {
-      const int n = group * 64 + lane;
+      const int n = group * 64 + l;
       for (int m = wave; m < count; m += waves)
-        if (n < rows) products[((int64_t)k * kChunk + m) * rows + n] = sum(m, lane >> 4, lane & 15);
+        if (n < rows) products[((int64_t)k * kChunk + m) * rows + n] = sum(m, l >> 4, l & 15);
     }
   }
 }

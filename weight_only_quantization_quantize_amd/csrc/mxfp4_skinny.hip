@@ -1,30 +1,29 @@
-// Products of a few rows of activations with microscaled weights (2 to 16 rows
-// of 16-bit activations, up to 64 rows of microscaled ones), bound by
-// streaming the weights:
+// Products of a few rows of activations (up to 64) with microscaled weights, bound
+// by streaming the weights:
 //   Y[m, n] = sum_b 2^(sA + sW - 254) sum_{k in block b} a[m, k] w[n, k].
 //
 // Work split.  K is cut into super-steps of 512 (four steps of
-// v_mfma_scale_f32_16x16x128).  A workgroup holds `slots` teams of `team` waves;
-// wave w of a team owns the super-steps w, w + team, ... and the team walks over
-// tiles of 16 columns of Y.  Up to K = 8192 a wave owns one super-step and its
-// activations stay in registers for the whole launch (RESIDENT); the only
-// traffic left is the weights'.  The team's partial sums of a tile meet in LDS
-// and are added in a fixed order.  More rows than the registers hold (16 of
-// three pieces, 32 of 4-bit activations) are cut into row groups, workgroups
-// of their own that read the same weights at the same time from the same L2 (a
-// column group's lie a multiple of 8 apart in dispatch order).
+// v_mfma_scale_f32_16x16x128).  A workgroup of 8 waves holds `slots` teams of `team`
+// waves; a wave owns one or two super-steps, whose activations stay in registers
+// for the whole launch, and the team walks over its run of tiles of 16 columns of
+// Y: the only traffic left is the weights'.  The team's partial sums of a tile meet
+// in LDS and are added in a fixed order.  More rows than the registers hold (16 of
+// split activations, 64 of 4-bit ones) are cut into row groups, workgroups of their
+// own that read the same weights at the same time from the same L2.
 //
 // Loads.  Units of 16 rows by 512 K in runs of 256 bytes (mxfp4_stream.h): loads
-// of 16 rows x 64 bytes straight into the matrix operands reached 2.2 TB/s.  The
-// next unit is loaded as soon as this one is in LDS.
+// of 16 rows x 64 bytes straight into the matrix operands reached 2.2 TB/s.  A wave
+// has up to four units on their way, 139 KB a compute unit; 16 waves with one each
+// had half of that and took 34 us for 16 rows of 28672 x 8192 (125 MB), where this
+// takes 26 (4.8 TB/s); 16 rows of 4-bit activations take 23.
 #include "mxfp4_stream.h"
 #include "woq_internal.h"
 
 namespace woq {
 namespace {
 
-constexpr int kMaxWaves = 16;
-constexpr int kMaxThreads = kMaxWaves * 64;
+constexpr int kWaves = 8;        // K <= 8192
+constexpr int kLongWaves = 16;   // longer rows
 constexpr int kTargetGroups = 256;  // workgroups: one per compute unit
 
 // One super-step of a chunk of 16 rows of activations.
@@ -40,20 +39,40 @@ struct Acts<kMxPieces> {
   MxActivations a[4];
 };
 
-template <class YT, int PIECES, int TC, bool RESIDENT>
-__global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ W,
-    const uint8_t* __restrict__ Ws, int M, int N, int nblk, int team, int supers, uint16_t* __restrict__ Y) {
-  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kMaxWaves][kUnitStage];
-  __shared__ float4_t part[2][kMaxWaves][TC][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slots = (int)(blockDim.x >> 6) / team;
-  const int slot = wave / team, tw = wave % team;
+// Chunk t's super-step S; A, As, M: the row group's.
+__device__ inline void load_acts(Acts<1>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t, int S,
+                                 int M, int nblk, int, int lane) {
   const int r = lane & 15, q = lane >> 4;
-  const int tiles = (N + 15) >> 4;
-  uint8_t* const stage = stage_all[wave];
-  // row group blockIdx.y: 16 TC rows
+  int m = 16 * t + r;
+  m = m < M ? m : M - 1;
+  const int b0 = kSuper * S + 4 * q;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int b = b0 + s;
+    const u32x4_t v = reinterpret_cast<const u32x4_t*>(A)[(uint32_t)(m * nblk + (b < nblk ? b : nblk - 1))];
+    act.v[s] = b < nblk ? v : u32x4_t{0u, 0u, 0u, 0u};
+  }
+  const int from = b0 < nblk - 4 ? b0 : nblk - 4;  // a dword inside the row (K >= 128)
+  __builtin_memcpy(&act.s, As + (uint32_t)(m * nblk + from), 4);
+  act.s >>= 8 * ((b0 - from) & 3);
+}
+__device__ inline void load_acts(Acts<kMxPieces>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t,
+                                 int S, int, int, int supers, int lane) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t f = ((int64_t)t * supers + S) * 4 + s;
+    mx_load_activations(act.a[s], A + f * kMxFragBytes, As + f * kMxFragScaleBytes, mx_place(0, lane));
+  }
+}
+template <int S>
+__device__ inline void multiply(float4_t& acc, const Acts<1>& act, i32x8_t w, int scale) {
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(act.v[S]), w, acc, kMfmaFp4, kMfmaFp4, S, (int)act.s, S, scale);
+}
+
+// What a row group's workgroups see of the operands.
+template <int PIECES, int TC>
+__device__ inline void enter_row_group(const uint8_t* __restrict__& A, const uint8_t* __restrict__& As, int& M,
+                                       uint16_t* __restrict__& Y, int N, int nblk, int supers) {
   const int m0 = (int)blockIdx.y * 16 * TC;
   M = M - m0 < 16 * TC ? M - m0 : 16 * TC;
   Y += (int64_t)m0 * N;
@@ -64,104 +83,210 @@ __global__ __launch_bounds__(kMaxThreads) void mxfp4_skinny_kernel(
     A += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragBytes;
     As += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragScaleBytes;
   }
+}
+
+// Rows 4 q .. 4 q + 3 of chunk t, column n of Y.
+template <class YT>
+__device__ inline void store(uint16_t* __restrict__ Y, int M, int N, int t, int n, int q, const float4_t& v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int m = 16 * t + 4 * q + e;
+    if (m < M && n < N) Y[(int64_t)m * N + n] = YT::from_f32(v[e]);
+  }
+}
+
+// K <= 8192.  A team's wave owns SU super-steps (tw, tw + team) whose activations
+// stay in registers; the team takes TI tiles at a time while the next ones' units
+// are on their way.
+template <class YT, int PIECES, int TC, int SU, int TI>
+__global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ W,
+    const uint8_t* __restrict__ Ws, int M, int N, int nblk, int team, int supers, uint16_t* __restrict__ Y) {
+  constexpr int NU = SU * TI;  // units a turn
+  constexpr bool kSpread = PIECES == kMxPieces && SU == 2;  // one super-step's third pieces go to LDS: the registers are full
+  constexpr int kBuffers = TI * TC > 4 ? 1 : 2;
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kWaves][kUnitStage];
+  __shared__ float4_t part[kBuffers][kWaves][TI * TC][64];
+  __shared__ u32x4_t third4[kSpread ? kWaves : 1][4][64];
+  __shared__ u32x2_t third2[kSpread ? kWaves : 1][4][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slots = (int)(blockDim.x >> 6) / team;
+  const int slot = wave / team, tw = wave % team;
+  uint8_t* const stage = stage_all[wave];
+  enter_row_group<PIECES, TC>(A, As, M, Y, N, nblk, supers);
+
+  // the team's run of tiles; all teams of the workgroup make as many turns
+  const int tiles = (N + 15) >> 4, teams = (int)gridDim.x * slots;
+  auto run = [&](int g) { return (int)((int64_t)tiles * g / teams); };
+  const int begin = run((int)blockIdx.x * slots + slot), end = run((int)blockIdx.x * slots + slot + 1);
+  int longest = 0;
+  for (int g = 0; g < slots; ++g) {
+    const int n = run((int)blockIdx.x * slots + g + 1) - run((int)blockIdx.x * slots + g);
+    longest = n > longest ? n : longest;
+  }
+
+  auto super_of = [&](int j) { return tw + j % SU * team; };
+  MxUnit u[NU];
+  auto ahead = [&](int j, int t0) {
+    const int tile = t0 + j / SU, S = super_of(j);
+    const bool live = tile < end && S < supers;  // else a line or two in its place
+    const int64_t row = live ? (int64_t)tile * 16 : 0;
+    __builtin_amdgcn_sched_barrier(0);
+    mx_load_unit(u[j], W + row * nblk * 16, Ws + row * nblk, (int)(N - row - 1), (N - row) * nblk, live ? nblk : 1, live ? S : 0, lane);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Acts<PIECES> act[TC][SU];
+#pragma unroll
+  for (int t = 0; t < TC; ++t)
+#pragma unroll
+    for (int i = 0; i < SU; ++i) {
+      load_acts(act[t][i], A, As, t, super_of(i) < supers ? super_of(i) : supers - 1, M, nblk, supers, lane);
+      if constexpr (kSpread) {
+        if (i == 1) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const i32x8_t p = act[t][i].a[s].p2;
+            third4[wave][s][lane] = u32x4_t{(uint32_t)p[0], (uint32_t)p[1], (uint32_t)p[2], (uint32_t)p[3]};
+            third2[wave][s][lane] = u32x2_t{(uint32_t)p[4], (uint32_t)p[5]};
+          }
+        }
+      }
+    }
+  // (before the activations instead: 4-bit products took 1 .. 1.5 us more)
+#pragma unroll
+  for (int j = 0; j < NU; ++j) ahead(j, begin);
+  float4_t acc[TI][TC];
+  auto take = [&](int t0, auto more) {
+    int l = lane;
+    asm volatile("" : "+v"(l));  // LDS addresses are worked out each turn: kept, they spill
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int tile = t0 + j / SU, S = super_of(j);
+      const int64_t row = (int64_t)tile * 16;
+      const bool live = tile < end && S < supers;
+      if (live) mx_stage_unit(u[j], stage, (int)(N - row - 1), (N - row) * nblk, nblk, S, l);
+      if constexpr (decltype(more)::value) ahead(j, t0 + TI);
+      if (live) {
+        const int scale = mx_staged_scale(stage, l);
+        mx_each_step([&](auto sel) {
+          constexpr int s = decltype(sel)::value;
+          const i32x8_t w = mx_staged_weights(stage, s, l);
+          if constexpr (PIECES == 1) {
+#pragma unroll
+            for (int t = 0; t < TC; ++t) multiply<s>(acc[j / SU][t], act[t][j % SU], w, scale);
+          } else {
+            static_assert(TC == 1);
+            MxActivations a = act[0][j % SU].a[s];
+            if (kSpread && j % SU == 1) a.p2 = mx_operand(third4[wave][s][l], third2[wave][s][l]);
+            mx_multiply<s>(acc[j / SU][0], a, w, scale);
+          }
+        });
+      }
+    }
+  };
+  const int turns = (longest + TI - 1) / TI;
+  for (int it = 0; it < turns; ++it) {
+    const int t0 = begin + it * TI;
+#pragma unroll
+    for (int i = 0; i < TI * TC; ++i) acc[i / TC][i % TC] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (it + 1 < turns)
+      take(t0, std::true_type{});
+    else
+      take(t0, std::false_type{});
+    float4_t(*const sums)[TI * TC][64] = part[kBuffers == 2 ? it & 1 : 0];
+#pragma unroll
+    for (int i = 0; i < TI * TC; ++i) sums[wave][i][lane] = acc[i / TC][i % TC];
+    __syncthreads();
+    // a wave adds the team's partials of a tile and chunk, in order, other waves each turn
+    int l = lane;
+    asm volatile("" : "+v"(l));
+#pragma unroll
+    for (int i = 0; i < TI * TC; ++i) {
+      const int tile = t0 + i / TC;
+      if (tile < end && tw == (it * TI * TC + i) % team) {
+        float4_t v = sums[slot * team][i][l];
+        for (int w = 1; w < team; ++w) {
+          const float4_t p = sums[slot * team + w][i][l];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += p[e];
+        }
+        store<YT>(Y, M, N, i % TC, tile * 16 + (l & 15), l >> 4, v);
+      }
+    }
+    if (kBuffers == 1) __syncthreads();
+  }
+}
+
+// Longer rows: wave w takes the super-steps w, w + 16, ... of a tile and loads the
+// activations of each; the next unit is on its way meanwhile.
+template <class YT, int PIECES, int TC>
+__global__ __launch_bounds__(kLongWaves * 64) void mxfp4_skinny_long_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ W,
+    const uint8_t* __restrict__ Ws, int M, int N, int nblk, int supers, uint16_t* __restrict__ Y) {
+  constexpr int team = kLongWaves;
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[team][kUnitStage];
+  __shared__ float4_t part[2][team][TC][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (N + 15) >> 4;
+  uint8_t* const stage = stage_all[wave];
+  enter_row_group<PIECES, TC>(A, As, M, Y, N, nblk, supers);
 
   MxUnit u;
   auto left = [&](int tile) { return (int64_t)(N - tile * 16) * nblk; };  // scale bytes from the tile on
   auto load_weights = [&](int tile, int S) {
     mx_load_unit(u, W + (int64_t)tile * 16 * nblk * 16, Ws + (int64_t)tile * 16 * nblk, N - tile * 16 - 1, left(tile), nblk, S, lane);
   };
-  Acts<PIECES> act[TC];
-  auto load_acts = [&](int S) {
+  // every wave makes the same number of turns; one without a super-step multiplies nothing
+  const int rounds = (supers + team - 1) / team;
+  int tile = blockIdx.x;
+  load_weights(tile, wave);
+  for (int it = 0; tile < tiles; ++it) {
+    const int next = tile + (int)gridDim.x;
+    float4_t acc[TC] = {};
+    for (int k = 0; k < rounds; ++k) {
+      const int S = wave + k * team;
+      mx_stage_unit(u, stage, N - tile * 16 - 1, left(tile), nblk, S, lane);
+      Acts<PIECES> act[TC];
 #pragma unroll
-    for (int t = 0; t < TC; ++t) {
-      if constexpr (PIECES == 1) {
-        int m = 16 * t + r;
-        m = m < M ? m : M - 1;
-        const int b0 = kSuper * S + 4 * q;
+      for (int t = 0; t < TC; ++t) load_acts(act[t], A, As, t, S < supers ? S : supers - 1, M, nblk, supers, lane);
+      const int Sn = k + 1 < rounds ? S + team : wave;
+      const int tn = k + 1 < rounds ? tile : next;
+      load_weights(tn < tiles ? tn : tile, Sn < supers ? Sn : supers - 1);
+      if (S < supers) {
+        const int scale = mx_staged_scale(stage, lane);
+        mx_each_step([&](auto sel) {
+          constexpr int s = decltype(sel)::value;
+          const i32x8_t w = mx_staged_weights(stage, s, lane);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int b = b0 + s;
-          const u32x4_t v = reinterpret_cast<const u32x4_t*>(A)[(uint32_t)(m * nblk + (b < nblk ? b : nblk - 1))];
-          act[t].v[s] = b < nblk ? v : u32x4_t{0u, 0u, 0u, 0u};
-        }
-        const int from = b0 < nblk - 4 ? b0 : nblk - 4;  // a dword inside the row (K >= 128)
-        __builtin_memcpy(&act[t].s, As + (uint32_t)(m * nblk + from), 4);
-        act[t].s >>= 8 * ((b0 - from) & 3);
-      } else {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int64_t f = ((int64_t)t * supers + S) * 4 + s;
-          mx_load_activations(act[t].a[s], A + f * kMxFragBytes, As + f * kMxFragScaleBytes, mx_place(0, lane));
-        }
+          for (int t = 0; t < TC; ++t) {
+            if constexpr (PIECES == 1)
+              multiply<s>(acc[t], act[t], w, scale);
+            else
+              mx_multiply<s>(acc[t], act[t].a[s], w, scale);
+          }
+        });
       }
     }
-  };
-
-  const int first = (int)blockIdx.x * slots + slot, step = (int)gridDim.x * slots;
-  if constexpr (RESIDENT) load_acts(tw);
-  int tile = first < tiles ? first : tiles - 1;  // teams past the last tile keep the barriers' company
-  load_weights(tile, tw);
-  // every team of the workgroup makes the same number of turns of the same
-  // number of super-steps; a wave without one (K short of it) multiplies zeros
-  const int turns = (tiles - (int)blockIdx.x * slots + step - 1) / step;
-  const int per_turn = RESIDENT ? 1 : (supers + team - 1) / team;
-  float4_t acc[TC] = {};
-  for (int i = 0, it = 0, k = 0; i < turns * per_turn; ++i) {
-    const int S = RESIDENT ? tw : tw + k * team;
-    mx_stage_unit(u, stage, N - tile * 16 - 1, left(tile), nblk, S, lane);
-    const bool wraps = RESIDENT || k + 1 == per_turn;
-    const int next = wraps ? (tile + step < tiles ? tile + step : tiles - 1) : tile;
-    if constexpr (!RESIDENT) load_acts(S < supers ? S : supers - 1);
-    if (i + 1 < turns * per_turn) {
-      const int Sn = RESIDENT || wraps ? tw : S + team;
-      load_weights(next, Sn < supers ? Sn : supers - 1);
-    }
-    const int scale = mx_staged_scale(stage, lane);
-    if (RESIDENT || S < supers) {
-      mx_each_step([&](auto sel) {
-        constexpr int s = decltype(sel)::value;
-        const i32x8_t w = mx_staged_weights(stage, s, lane);
-#pragma unroll
-        for (int t = 0; t < TC; ++t) {
-          if constexpr (PIECES == 1)
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(act[t].v[s]), w, acc[t], kMfmaFp4,
-                                                                      kMfmaFp4, s, (int)act[t].s, s, scale);
-          else
-            mx_multiply<s>(acc[t], act[t].a[s], w, scale);
-        }
-      });
-    }
-    ++k;
-    if (!wraps) continue;
     const int buf = it & 1;
 #pragma unroll
     for (int t = 0; t < TC; ++t) part[buf][wave][t][lane] = acc[t];
     __syncthreads();
-    // one wave a chunk adds the team's partials, another one each turn
-    const bool live = first + it * step < tiles;
+    // a wave a chunk adds the partials, other ones each turn
 #pragma unroll
     for (int t = 0; t < TC; ++t) {
-      if (live && tw == (it + t) % team) {
-        float4_t v = part[buf][slot * team][t][lane];
+      if (wave == (it + t) % team) {
+        float4_t v = part[buf][0][t][lane];
         for (int w = 1; w < team; ++w) {
-          const float4_t p = part[buf][slot * team + w][t][lane];
+          const float4_t p = part[buf][w][t][lane];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += p[e];
         }
-        if (tile * 16 + r < N) {
-          uint16_t* const yt = Y + (int64_t)tile * 16;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = 16 * t + 4 * q + e;
-            if (m < M) yt[(uint32_t)(m * N + r)] = YT::from_f32(v[e]);
-          }
-        }
+        store<YT>(Y, M, N, t, tile * 16 + (lane & 15), lane >> 4, v);
       }
-      acc[t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     tile = next;
-    ++it;
-    k = 0;
   }
 }
 
@@ -174,19 +299,40 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   const auto* wsp = static_cast<const uint8_t*>(Ws);
   auto* yp = static_cast<uint16_t*>(Y);
   const int tiles = (N + 15) / 16, supers = (nblk + kSuper - 1) / kSuper;
-  const int team = supers < kMaxWaves ? supers : kMaxWaves;
+  // workgroups a row group: a column group's lie a multiple of 8 apart in dispatch
+  // order, on one XCD (three row groups of 85 took 28 us where four of 64 take 26)
+  const int rgroups = (M + 16 * TC - 1) / (16 * TC);
+  const int target = kTargetGroups / (rgroups == 3 ? 4 : rgroups);
+  if constexpr (TC < 4) {  // more than 32 rows come with K <= 8192 only
+    if (supers > 2 * kWaves) {
+      const dim3 grid((unsigned)(tiles < target ? tiles : target), (unsigned)rgroups);
+      mxfp4_skinny_long_kernel<YT, PIECES, TC><<<grid, kLongWaves * 64, 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, supers, yp);
+      return hipGetLastError();
+    }
+  }
+  const bool two = supers > kWaves;
+  const int team = two ? (supers + 1) / 2 : supers;
   // short rows: several teams a workgroup, where there are tiles for them
-  int slots = kMaxWaves / team;
-  const int per = (tiles + kTargetGroups - 1) / kTargetGroups;
+  int slots = kWaves / team;
+  const int per = (tiles + target - 1) / target;
   slots = slots < per ? slots : per;
   const int groups = (tiles + slots - 1) / slots;
-  const int rgroups = (M + 16 * TC - 1) / (16 * TC), target = kTargetGroups / rgroups;
   const dim3 grid((unsigned)(groups < target ? groups : target), (unsigned)rgroups);
-  const unsigned threads = (unsigned)(slots * team * 64);
-  if (supers <= kMaxWaves)
-    mxfp4_skinny_kernel<YT, PIECES, TC, true><<<grid, threads, 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, team, supers, yp);
-  else
-    mxfp4_skinny_kernel<YT, PIECES, TC, false><<<grid, threads, 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, team, supers, yp);
+  // four units ahead, fewer where a team has fewer tiles (units that are not there
+  // cost their loads all the same: 4096 x 4096 takes 9.7 us with one, 11.2 with
+  // four) or where 64 rows leave no registers for them
+  const int most = (tiles + (int)grid.x * slots - 1) / ((int)grid.x * slots);
+  void (*f)(const uint8_t*, const uint8_t*, const uint8_t*, const uint8_t*, int, int, int, int, int, uint16_t*);
+  if (two) {
+    f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 1>;
+    if constexpr (TC < 4)
+      if (most > 1) f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 2>;
+  } else {
+    f = most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 2> : mxfp4_skinny_kernel<YT, PIECES, TC, 1, 1>;
+    if constexpr (TC < 4)
+      if (most > 2) f = mxfp4_skinny_kernel<YT, PIECES, TC, 1, 4>;
+  }
+  f<<<grid, (unsigned)(slots * team * 64), 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, team, supers, yp);
   return hipGetLastError();
 }
 
@@ -204,8 +350,13 @@ hipError_t launch_mxfp4_skinny(const void* pieces, const void* piece_scales, con
 hipError_t launch_mxfp4_skinny_mx(const void* A, const void* As, const void* codes, const void* scales, int64_t M,
                                   int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream) {
   const int nblk = (int)(K / kMxBlock);
-  auto* const f = M <= 16 ? (ydtype == 0 ? launch<F16, 1, 1> : launch<BF16, 1, 1>)
-                          : (ydtype == 0 ? launch<F16, 1, 2> : launch<BF16, 1, 2>);
+  // chunks of 16 rows a workgroup: all of them, so that the weights are read once,
+  // but for 64 rows of few columns, where a workgroup loads more activations than
+  // weights (8192 x 8192: 15.5 us in two row groups, 17 in one; 28672 x 8192: 34, 31)
+  const int chunks = M <= 16 ? 1 : (M <= 32 || (M > 48 && N <= 8192) ? 2 : 4);
+  auto* const f = chunks == 1   ? (ydtype == 0 ? launch<F16, 1, 1> : launch<BF16, 1, 1>)
+                  : chunks == 2 ? (ydtype == 0 ? launch<F16, 1, 2> : launch<BF16, 1, 2>)
+                                : (ydtype == 0 ? launch<F16, 1, 4> : launch<BF16, 1, 4>);
   return f(A, As, codes, scales, (int)M, (int)N, nblk, Y, stream);
 }
 

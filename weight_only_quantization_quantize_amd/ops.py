@@ -373,20 +373,22 @@ _MX_OUT = {torch.float16: _lib.WOQ_F16, torch.bfloat16: _lib.WOQ_BF16, torch.flo
 
 def _check_mxfp4(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int = 2) -> Tuple[int, ...]:
     """The matrix sizes of a microscaled set [..., M, K]."""
-    if codes.dtype != torch.uint8 or codes.dim() != dims or codes.shape[-1] < 16 or codes.shape[-1] % 16:
+    shape = codes.shape
+    if codes.dtype != torch.uint8 or len(shape) != dims or shape[-1] < 16 or shape[-1] % 16:
         raise ValueError(f"{name} codes must be {dims}-D uint8 with K/2 columns, K a positive multiple of 32 "
-                         f"(got {codes.dtype}, {tuple(codes.shape)})")
-    shape = tuple(codes.shape)
-    if scales.dtype != torch.uint8 or tuple(scales.shape) != shape[:-1] + (shape[-1] // 16,):
-        raise ValueError(f"{name} scales must be uint8 of shape {shape[:-1] + (shape[-1] // 16,)} "
+                         f"(got {codes.dtype}, {tuple(shape)})")
+    *rows, half = shape
+    if scales.dtype != torch.uint8 or scales.shape != (*rows, half // 16):
+        raise ValueError(f"{name} scales must be uint8 of shape {(*rows, half // 16)} "
                          f"(got {scales.dtype}, {tuple(scales.shape)})")
-    return shape[:-1] + (2 * shape[-1],)
+    return (*rows, 2 * half)
 
 
 def _no_grad(*ts: torch.Tensor) -> None:
     """These operators are for inference: a gradient asked of them is refused, not dropped."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in ts):
-        raise ValueError("the mxfp4 operators have no gradient (use torch.no_grad() or detach the input)")
+    for t in ts:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("the mxfp4 operators have no gradient (use torch.no_grad() or detach the input)")
 
 
 def _launch(name: str, device: torch.device, *args) -> None:
@@ -414,8 +416,8 @@ def mxfp4_quantize(
     M, K = x.shape
     _no_grad(x)
     if out is None:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty(M, K // 2, dtype=torch.uint8)
+        scales = codes.new_empty(M, K // 32)
     else:
         codes, scales = out
         _check_out(codes, (M, K // 2), torch.uint8, "out codes")
@@ -432,18 +434,18 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
         raise ValueError(f"dtype must be float32, bfloat16 or float16 (got {dtype})")
     if M < 1:
         raise ValueError("need at least one row")
-    out = torch.empty((M, K), dtype=dtype, device=codes.device)
+    out = codes.new_empty(M, K, dtype=dtype)
     _require_gpu(codes, scales, out)
     _launch("woq_mxfp4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), M, K, _MX_OUT[dtype],
             out.data_ptr())
     return out
 
 
-def _mx_workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
+def _mx_workspace(like: torch.Tensor, nbytes: int) -> Optional[torch.Tensor]:
     """A call's own scratch.  It comes from PyTorch's allocator each time: the
     allocator keeps it on this stream, and under graph capture in that graph's
     pool, so no two calls that may run at once share it."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def mxfp4_gemm(
@@ -462,10 +464,10 @@ def mxfp4_gemm(
     _no_grad(X)
     if out is not None:
         _check_out(out, (M, N), X.dtype, "out")
-    Y = out if out is not None else torch.empty((M, N), dtype=X.dtype, device=X.device)
+    Y = out if out is not None else X.new_empty(M, N)
     _require_gpu(X, codes, scales, Y)
     nbytes = int(_lib.call("woq_mxfp4_gemm_workspace_bytes", M, N, K))
-    ws = _mx_workspace(X.device, nbytes)
+    ws = _mx_workspace(X, nbytes)
     _launch("woq_mxfp4_gemm", X.device, X.data_ptr(), _DTYPE[X.dtype], codes.data_ptr(), scales.data_ptr(), M, N, K,
             Y.data_ptr(), _ptr(ws), nbytes)
     return Y
@@ -491,10 +493,10 @@ def mxfp4_gemm_mx(
         raise ValueError("need at least one row of activations and of weights")
     if out is not None:
         _check_out(out, (M, N), dtype, "out")
-    Y = out if out is not None else torch.empty((M, N), dtype=dtype, device=a_codes.device)
+    Y = out if out is not None else a_codes.new_empty(M, N, dtype=dtype)
     _require_gpu(a_codes, a_scales, codes, scales, Y)
     nbytes = int(_lib.call("woq_mxfp4_gemm_mx_workspace_bytes", M, N, K))
-    ws = _mx_workspace(a_codes.device, nbytes)
+    ws = _mx_workspace(a_codes, nbytes)
     _launch("woq_mxfp4_gemm_mx", a_codes.device, a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(),
             scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr(), _ptr(ws), nbytes)
     return Y
@@ -533,9 +535,9 @@ def mxfp4_moe(
     _no_grad(X, router)
     if out is not None:
         _check_out(out, (T, H), X.dtype, "out")
-    Y = out if out is not None else torch.empty((T, H), dtype=X.dtype, device=X.device)
+    Y = out if out is not None else X.new_empty(T, H)
     _require_gpu(X, router, up_codes, up_scales, down_codes, down_scales, Y)
-    ws = _mx_workspace(X.device, nbytes)
+    ws = _mx_workspace(X, nbytes)
     _launch("woq_mxfp4_moe", X.device, X.data_ptr(), _DTYPE[X.dtype], router.data_ptr(), up_codes.data_ptr(),
             up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k, Y.data_ptr(),
             _ptr(ws), nbytes)

@@ -26,9 +26,10 @@
 // place, and multiplies.  The loads are written out in assembly because the
 // compiler would wait for all of them before every read of LDS; their counter is
 // waited for by hand, and there is no other vector memory access inside the loop.
-// Longer stages mean fewer barriers: 256 of K for 4-bit operands took 333 x 1001 x
-// 5152 from 15 to 11 us, 64 of K left the large three-piece tile two workgroups a
-// compute unit (152 against 171 us with 128).
+// Longer stages mean fewer barriers: 256 of K for 4-bit operands and K split
+// between two groups of waves took 333 x 1001 x 5152 from 15 to 9 us; the large
+// three-piece tile keeps 64, which leave it two workgroups a compute unit (2048 x
+// 11008 x 4096: 154 us against 169 with 128).
 //
 // Scales.  The 4-bit operands' scale bytes lie K / 32 bytes apart from row to row
 // at any alignment, which direct loads cannot gather; turn_scales

@@ -7,6 +7,7 @@ library.  Nothing is computed here.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -410,20 +411,22 @@ def mxfp4_quantize(
 ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Quantize x [M, K] (fp16 or bf16; weights or activations) to microscaled
     4-bit floats -> (codes uint8 [M, K/2], scales uint8 [M, K/32])."""
-    if x.dtype not in _DTYPE or x.dim() != 2 or x.shape[1] < 32 or x.shape[1] % 32 or x.shape[0] < 1:
+    xdtype, shape = _DTYPE.get(x.dtype), x.shape
+    if xdtype is None or len(shape) != 2 or shape[1] < 32 or shape[1] % 32 or shape[0] < 1:
         raise ValueError(f"x must be fp16/bf16 [M, K] with M >= 1 and K a positive multiple of 32 "
-                         f"(got {x.dtype}, {tuple(x.shape)})")
-    M, K = x.shape
+                         f"(got {x.dtype}, {tuple(shape)})")
+    M, K = shape
     _no_grad(x)
     if out is None:
+        _require_gpu(x)
         codes = x.new_empty(M, K // 2, dtype=torch.uint8)
         scales = codes.new_empty(M, K // 32)
     else:
         codes, scales = out
         _check_out(codes, (M, K // 2), torch.uint8, "out codes")
         _check_out(scales, (M, K // 32), torch.uint8, "out scales")
-    _require_gpu(x, codes, scales)
-    _launch("woq_mxfp4_quantize", x.device, x.data_ptr(), _DTYPE[x.dtype], M, K, codes.data_ptr(), scales.data_ptr())
+        _require_gpu(x, codes, scales)
+    _launch("woq_mxfp4_quantize", x.device, x.data_ptr(), xdtype, M, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -434,11 +437,16 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dty
         raise ValueError(f"dtype must be float32, bfloat16 or float16 (got {dtype})")
     if M < 1:
         raise ValueError("need at least one row")
+    _require_gpu(codes, scales)
     out = codes.new_empty(M, K, dtype=dtype)
-    _require_gpu(codes, scales, out)
     _launch("woq_mxfp4_dequantize", codes.device, codes.data_ptr(), scales.data_ptr(), M, K, _MX_OUT[dtype],
             out.data_ptr())
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx_workspace_bytes(name: str, *sizes: int) -> int:
+    return int(_lib.call(name, *sizes))
 
 
 def _mx_workspace(like: torch.Tensor, nbytes: int) -> Optional[torch.Tensor]:
@@ -456,19 +464,20 @@ def mxfp4_gemm(
 ) -> torch.Tensor:
     """Y [M, N] = X @ w^T for X [M, K] (fp16 or bf16) and microscaled weights w [N, K]."""
     N, K = _check_mxfp4(codes, scales, "weight")
-    if X.dtype not in _DTYPE or X.dim() != 2 or X.shape[1] != K:
-        raise ValueError(f"X must be fp16/bf16 [M, {K}] (got {X.dtype}, {tuple(X.shape)})")
-    M = X.shape[0]
+    xdtype, shape = _DTYPE.get(X.dtype), X.shape
+    if xdtype is None or len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"X must be fp16/bf16 [M, {K}] (got {X.dtype}, {tuple(shape)})")
+    M = shape[0]
     if M < 1 or N < 1:
         raise ValueError("need at least one row of X and of the weights")
     _no_grad(X)
     if out is not None:
         _check_out(out, (M, N), X.dtype, "out")
+    _require_gpu(X, codes, scales, out)
     Y = out if out is not None else X.new_empty(M, N)
-    _require_gpu(X, codes, scales, Y)
-    nbytes = int(_lib.call("woq_mxfp4_gemm_workspace_bytes", M, N, K))
+    nbytes = _mx_workspace_bytes("woq_mxfp4_gemm_workspace_bytes", M, N, K)
     ws = _mx_workspace(X, nbytes)
-    _launch("woq_mxfp4_gemm", X.device, X.data_ptr(), _DTYPE[X.dtype], codes.data_ptr(), scales.data_ptr(), M, N, K,
+    _launch("woq_mxfp4_gemm", X.device, X.data_ptr(), xdtype, codes.data_ptr(), scales.data_ptr(), M, N, K,
             Y.data_ptr(), _ptr(ws), nbytes)
     return Y
 
@@ -493,9 +502,9 @@ def mxfp4_gemm_mx(
         raise ValueError("need at least one row of activations and of weights")
     if out is not None:
         _check_out(out, (M, N), dtype, "out")
+    _require_gpu(a_codes, a_scales, codes, scales, out)
     Y = out if out is not None else a_codes.new_empty(M, N, dtype=dtype)
-    _require_gpu(a_codes, a_scales, codes, scales, Y)
-    nbytes = int(_lib.call("woq_mxfp4_gemm_mx_workspace_bytes", M, N, K))
+    nbytes = _mx_workspace_bytes("woq_mxfp4_gemm_mx_workspace_bytes", M, N, K)
     ws = _mx_workspace(a_codes, nbytes)
     _launch("woq_mxfp4_gemm_mx", a_codes.device, a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(),
             scales.data_ptr(), M, N, K, _DTYPE[dtype], Y.data_ptr(), _ptr(ws), nbytes)
@@ -528,15 +537,15 @@ def mxfp4_moe(
     if not 1 <= top_k <= E:
         raise ValueError(f"top_k must be in [1, {E}] (got {top_k})")
     T = X.shape[0]
-    nbytes = int(_lib.call("woq_mxfp4_moe_workspace_bytes", T, H, I, E, top_k))
+    nbytes = _mx_workspace_bytes("woq_mxfp4_moe_workspace_bytes", T, H, I, E, top_k)
     if nbytes == 0:
         raise ValueError(f"mxfp4_moe takes 1 to 64 tokens, up to 512 experts and a top_k of up to 64 (got T={T}, H={H}, "
                          f"I={I}, E={E}, top_k={top_k})")
     _no_grad(X, router)
     if out is not None:
         _check_out(out, (T, H), X.dtype, "out")
+    _require_gpu(X, router, up_codes, up_scales, down_codes, down_scales, out)
     Y = out if out is not None else X.new_empty(T, H)
-    _require_gpu(X, router, up_codes, up_scales, down_codes, down_scales, Y)
     ws = _mx_workspace(X, nbytes)
     _launch("woq_mxfp4_moe", X.device, X.data_ptr(), _DTYPE[X.dtype], router.data_ptr(), up_codes.data_ptr(),
             up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k, Y.data_ptr(),

@@ -199,6 +199,28 @@ def test_gemm_mx(M, N, K, dtype):
     near(y, A @ W.T, dtype, f"gemm_mx {M} {N} {K}")
 
 
+# a few rows of wide or long matrices (runs of one to several tiles a team, one or
+# two super-steps a wave, rows beyond sixteen of those), and every size of tile
+WIDE = [(5, 12321, 160), (9, 8200, 544), (16, 700, 4704), (20, 9000, 4640), (24, 4100, 1024), (33, 4300, 8160),
+        (50, 13000, 256), (50, 13000, 4640), (64, 5000, 1056), (64, 5000, 4640), (32, 300, 8224), (16, 40, 22016),
+        (70, 27000, 96), (130, 8100, 96), (1200, 7000, 96), (2000, 8100, 96), (640, 1000, 3104)]
+
+
+@pytest.mark.parametrize("M, N, K", WIDE)
+def test_wide_and_long_products(M, N, K):
+    dtype = TYPES[M % 2]
+    x, (codes, scales) = activations(M, K, dtype, M + N + K), weights(N, K, K)
+    a = ops.mxfp4_quantize(x)
+    _say(f"wide {M} {N} {K} {dtype}")
+    y, z = ops.mxfp4_gemm(x, codes, scales), ops.mxfp4_gemm_mx(*a, codes, scales, dtype)
+    torch.cuda.synchronize()
+    X, A, W = host(x), values(*a), values(codes, scales)
+    close(y, X @ W.T, product_bound(X, W, True), dtype, f"gemm {M} {N} {K}")
+    near(y, X @ W.T, dtype, f"gemm {M} {N} {K}", HELD)
+    close(z, A @ W.T, product_bound(A, W, False), dtype, f"gemm_mx {M} {N} {K}")
+    near(z, A @ W.T, dtype, f"gemm_mx {M} {N} {K}")
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 130])
 @pytest.mark.parametrize("N, K", [(70, 32), (70, 224), (70, 480)])
 def test_one_hot_rows_pick_single_weights(M, N, K):
@@ -321,6 +343,10 @@ def moe_bound(x, up, down, ids, logits):
 MOE = [(1, 64, 32, 4, 2), (1, 2080, 1056, 12, 3), (1, 512, 160, 65, 1), (2, 96, 64, 3, 3), (5, 352, 224, 60, 6),
        (16, 256, 128, 8, 2), (17, 256, 96, 8, 4), (31, 128, 32, 130, 8), (33, 608, 128, 6, 2), (64, 512, 256, 16, 4),
        (64, 160, 416, 2, 1), (7, 64, 32, 512, 5)]
+# rows longer than a workgroup's waves hold, more turns than workgroups, as many
+# choices as there may be
+MOE += [(1, 4640, 64, 6, 2), (1, 64, 4640, 5, 3), (3, 4640, 96, 5, 2), (6, 96, 4640, 6, 3), (39, 1056, 1024, 30, 3),
+        (1, 64, 32, 512, 64), (64, 64, 32, 64, 64), (2, 2080, 544, 70, 9)]
 
 
 @pytest.mark.parametrize("T, H, I, E, k", MOE)

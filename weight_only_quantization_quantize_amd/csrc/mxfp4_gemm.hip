@@ -14,9 +14,10 @@
 // the shorter side; two workgroups of that tile share a compute unit, which hides
 // the one's barriers, prologue and stores behind the other's instructions).
 // Below that the number of stages in flight counts: small tiles, K split.
-// 2048 x 11008 x 4096 takes 156 us with split activations (3 x 185 G multiply-adds,
-// 3.5 P flop/s as the matrix unit counts them, of the 6.3 P that it reaches on
-// registers alone) and 62 us with 4-bit ones (3.0 of 6.7).
+// 2048 x 11008 x 4096 takes 145 us with split activations (3 x 185 G flop, 3.8 P
+// flop/s as the matrix unit counts them, of the 6.3 P that it reaches on registers
+// alone) and 61 us with 4-bit ones (3.0 of 6.7): LDS, which hands out 1 KB for each
+// instruction of a 64 x 64 wave tile and takes the next stages in meanwhile.
 //
 // Pipeline.  K goes in stages of 64 KS, kStages of them in LDS, filled by direct
 // loads (global_load_lds: no registers, no instructions to write LDS).  At the top
@@ -40,9 +41,10 @@
 // one block each, chunk c at position c ^ swizzle(row), so that 16 rows read at
 // one chunk lie in 16 different 16-byte slots of the 256-byte bank row.
 //
-// Tile order.  Workgroup b runs on XCD b % 8; each XCD takes one contiguous run
-// of tiles, M fastest, so that the tiles in flight there share few columns of W
-// and all of A in its L2.
+// Tile order.  Workgroup b runs on XCD b % 8; each XCD takes one contiguous run of
+// tiles, in groups of 8 M tiles, M fastest, so that the tiles in flight there (32 or
+// 64) share about as much of A as of W in its L2.  All M tiles in one group took
+// 150 us in place of 145 for 2048 x 11008 x 4096 in three pieces.
 #include <type_traits>
 
 #include "mxfp4_device.h"
@@ -53,6 +55,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kXcds = 8;
+constexpr int kGroup = 8;  // M tiles of a group
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -192,7 +195,9 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) 
   const int per = (tiles + kXcds - 1) / kXcds;
   const int tile = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
   if (tile >= tiles) return;
-  const int m0 = tile % mtiles * C::BM, n0 = tile / mtiles * C::BN;
+  const int gtiles = kGroup * (tiles / mtiles);  // of a group of M tiles
+  const int g = tile / gtiles, gm = mtiles - g * kGroup < kGroup ? mtiles - g * kGroup : kGroup;
+  const int m0 = (g * kGroup + tile % gtiles % gm) * C::BM, n0 = tile % gtiles / gm * C::BN;
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = wave_all % kWaves, group = wave_all / kWaves;

@@ -35,7 +35,8 @@
 // Scales.  The 4-bit operands' scale bytes lie K / 32 bytes apart from row to row
 // at any alignment, which direct loads cannot gather; turn_scales
 // (mxfp4_quantize.hip; in the split's launch where there is one) makes them one
-// dword per row and 128 of K, rows contiguous, with 127 past the row's end.
+// dword per row and 128 of K, rows contiguous, with 127 past the row's end.  Small
+// tiles of two 4-bit operands do that themselves, into LDS, once for all of K.
 //
 // LDS layout of a 4-bit operand: a row's 32 KS bytes of a stage are chunks of
 // one block each, chunk c at position c ^ swizzle(row), so that 16 rows read at
@@ -158,7 +159,8 @@ struct TileSplit {
   }
 };
 
-template <int PIECES, int TM, int TN, int WN, int KS, int KG>
+// RES > 0: the tile's scale bytes for all of K (at most 128 RES) stay in LDS.
+template <int PIECES, int TM, int TN, int WN, int KS, int KG, int RES>
 struct Config {
   static constexpr int kWaves = 2 * WN, kThreads = 64 * kWaves * KG;
   static constexpr bool kSplit = PIECES == kMxPieces;
@@ -166,7 +168,7 @@ struct Config {
   static constexpr int BM = 64 * TM, BN = 32 * WN * TN;
   using TA = std::conditional_t<kSplit, TileSplit<BM, KS>, Tile4<BM, KS>>;
   using TW = Tile4<BN, kKS>;
-  static constexpr int kStage = TA::kBytes + TW::kBytes + TA::kScaleBytes + TW::kScaleBytes;
+  static constexpr int kStage = TA::kBytes + TW::kBytes + (RES ? 0 : TA::kScaleBytes + TW::kScaleBytes);
   // as many stages as leave room for a second workgroup, or, where that would be
   // fewer than two, as fill the LDS; at most 4
   static constexpr int kRoom = (KG * kStage * 2 > 80 * 1024 ? 160 : 80) * 1024;
@@ -174,23 +176,24 @@ struct Config {
   static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
   static constexpr int per_wave(int units) { return (units + kWaves - 1) / kWaves; }
   static constexpr int kALoads = per_wave(TA::kUnits), kWLoads = per_wave(TW::kUnits);
-  static constexpr int kAScaleLoads = per_wave(TA::kScaleUnits), kWScaleLoads = per_wave(TW::kScaleUnits);
+  static constexpr int kAScaleLoads = RES ? 0 : per_wave(TA::kScaleUnits), kWScaleLoads = RES ? 0 : per_wave(TW::kScaleUnits);
   static constexpr int kLoads = kALoads + kWLoads + kAScaleLoads + kWScaleLoads;
 };
 
-template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG>
-__global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
+template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG, int RES>
+__global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads), 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
                                                                  const uint8_t* __restrict__ As,
                                                                  const uint8_t* __restrict__ W,
                                                                  const uint8_t* __restrict__ Ws, int M, int N,
                                                                  int m_pad, int n_pad, int nblk, int mtiles, int tiles,
                                                                  uint16_t* __restrict__ Y) {
-  using C = Config<PIECES, TM, TN, WN, KS, KG>;
+  using C = Config<PIECES, TM, TN, WN, KS, KG, RES>;
   constexpr int kWaves = C::kWaves;
   using TA = typename C::TA;
   using TW = typename C::TW;
   constexpr int kAt = TA::kBytes, kAsAt = kAt + TW::kBytes, kWsAt = kAsAt + TA::kScaleBytes;
   __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KG][C::kStages][C::kStage];
+  __shared__ uint32_t a_scales[RES ? RES : 1][RES ? C::BM : 1], w_scales[RES ? RES : 1][RES ? C::BN : 1];
 
   const int per = (tiles + kXcds - 1) / kXcds;
   const int tile = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
@@ -234,6 +237,20 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) 
 
   float16_t acc[TM][TN] = {};
   for (int st = 0; st + 1 < C::kStages; ++st) issue(h0 + st, st);
+  if constexpr (RES > 0) {  // seen by all behind the first turn's barrier
+    static_assert(KS == 4 && PIECES == 1 && RES % 4 == 0);
+    const int chunks = (nblk + 15) >> 4;
+    for (int i = threadIdx.x; i < (C::BM + C::BN) * chunks; i += C::kThreads) {
+      const int row = i % (C::BM + C::BN), g = i / (C::BM + C::BN);
+      const bool of_a = row < C::BM;
+      const int r = of_a ? m0 + row : n0 + row - C::BM, last = (of_a ? M : N) - 1;
+      const u32x4_t v = mx_scale_chunk((of_a ? As : Ws) + (int64_t)(r < last ? r : last) * nblk, g, nblk);
+      uint32_t* const to = of_a ? &a_scales[4 * g][row] : &w_scales[4 * g][row - C::BM];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) to[q * (of_a ? C::BM : C::BN)] = v[q];
+    }
+  }
+  auto scale_byte = [&](uint32_t v, int s) { return (int)(v >> (8 * (2 * (s & 1) + half))); };
   int buf = 0;
   for (int h = h0; h < h0 + turns; ++h) {
     wait_loads<(C::kStages - 2) * C::kLoads>();
@@ -251,7 +268,10 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) 
       for (int j = 0; j < TN; ++j) {
         const int row = (wn + j) * 32 + r32;
         bf[j] = mx_operand(TW::fragment(lw, row, s, half));
-        bs[j] = TW::scale(la + kWsAt, row, s, half, h);
+        if constexpr (RES > 0)
+          bs[j] = scale_byte(w_scales[2 * h + (s >> 1)][row], s);
+        else
+          bs[j] = TW::scale(la + kWsAt, row, s, half, h);
       }
       if constexpr (!C::kSplit) {
         const bool live = 2 * KS * h + 2 * s + half < nblk;
@@ -260,7 +280,11 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) 
           const int row = (wm + i) * 32 + r32;
           u32x4_t v = TA::fragment(la, row, s, half);
           v = live ? v : u32x4_t{0u, 0u, 0u, 0u};
-          const int as = TA::scale(la + kAsAt, row, s, half, h);
+          int as;
+          if constexpr (RES > 0)
+            as = scale_byte(a_scales[2 * h + (s >> 1)][row], s);
+          else
+            as = TA::scale(la + kAsAt, row, s, half, h);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], mx_operand(v), acc[i][j], kMfmaFp4,
@@ -354,14 +378,14 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG>::kThreads), 2) 
 
 size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)mxfp4_scale_rows(rows) * (size_t)((K + 255) / 256 * 2) * 4; }
 
-template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG>
+template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG, int RES = 0>
 hipError_t launch_tiles(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                         void* Y, hipStream_t stream) {
-  using C = Config<PIECES, TM, TN, WN, KS, KG>;
+  using C = Config<PIECES, TM, TN, WN, KS, KG, RES>;
   const int64_t mt = (M + C::BM - 1) / C::BM, nt = (N + C::BN - 1) / C::BN;
   const int64_t tiles = mt * nt;
   const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds);
-  mxfp4_gemm_kernel<YT, PIECES, TM, TN, WN, KS, KG><<<grid, C::kThreads, 0, stream>>>(
+  mxfp4_gemm_kernel<YT, PIECES, TM, TN, WN, KS, KG, RES><<<grid, C::kThreads, 0, stream>>>(
       static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
       static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)mxfp4_scale_rows(M), (int)mxfp4_scale_rows(N), (int)(K / kMxBlock), (int)mt,
       (int)tiles, static_cast<uint16_t*>(Y));
@@ -378,18 +402,37 @@ hipError_t launch_tiles(const void* A, const void* As, const void* W, const void
 //                 64 x 128  19.5 n        (n = 1: 18 .. 21, 2: 37 .. 41, 4: 75)
 //                 64 x 64   14 n          (n = 1: 15, 2: 27, 4: 52 .. 59)
 // The small ones split K between two groups of waves.
+int64_t per_cu(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256; }
+enum class Tile { kLarge, kMiddle, kSmall };
+Tile tile_mx(int64_t M, int64_t N) {
+  const double large = 36.0 * per_cu(M, N, 256, 256), mid = 6.0 + 10.0 * per_cu(M, N, 128, 128),
+               small = 3.0 + 4.5 * per_cu(M, N, 64, 64);
+  return large <= mid && large <= small ? Tile::kLarge : (mid <= small ? Tile::kMiddle : Tile::kSmall);
+}
+// Small 4-bit tiles keep the scales in LDS where that leaves a second workgroup a
+// compute unit, or none is needed: no pass over them, no workspace.  Whole
+// products, with / without: 333 x 1001 x 5152 9.9 / 11.6 us, 128 x 4096 x 4096 8.2 /
+// 10.2, 512 x 1024 x 1024 4.1 / 6.4, 256 x 8192 x 3584 10.2 / 12.6.
+constexpr int kResident = 28, kResidentAlone = 128;  // dwords a row
+bool resident(int64_t M, int64_t N, int64_t K) {
+  return tile_mx(M, N) == Tile::kSmall && (K <= 128 * kResident || (K <= 128 * kResidentAlone && per_cu(M, N, 64, 64) == 1));
+}
+
 template <class YT, int PIECES>
 hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                   void* Y, hipStream_t stream) {
-  auto per_cu = [&](int64_t bm, int64_t bn) { return (double)(((M + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256); };
   if constexpr (PIECES == 1) {
-    const double large = 36.0 * per_cu(256, 256), mid = 6.0 + 10.0 * per_cu(128, 128), small = 3.0 + 4.5 * per_cu(64, 64);
-    if (large <= mid && large <= small) return launch_tiles<YT, 1, 4, 2, 4, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
-    if (mid <= small) return launch_tiles<YT, 1, 2, 2, 2, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
-    return launch_tiles<YT, 1, 1, 1, 2, 4, 2>(A, As, W, Ws, M, N, K, Y, stream);
+    if (resident(M, N, K))
+      return K <= 128 * kResident ? launch_tiles<YT, 1, 1, 1, 2, 4, 2, kResident>(A, As, W, Ws, M, N, K, Y, stream)
+                                  : launch_tiles<YT, 1, 1, 1, 2, 4, 2, kResidentAlone>(A, As, W, Ws, M, N, K, Y, stream);
+    switch (tile_mx(M, N)) {
+      case Tile::kLarge: return launch_tiles<YT, 1, 4, 2, 4, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
+      case Tile::kMiddle: return launch_tiles<YT, 1, 2, 2, 2, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
+      default: return launch_tiles<YT, 1, 1, 1, 2, 4, 2>(A, As, W, Ws, M, N, K, Y, stream);
+    }
   } else {
-    const double large = 9.0 + 49.0 * per_cu(128, 256), wide = 1.0 + 28.0 * per_cu(64, 256), mid = 19.5 * per_cu(64, 128),
-                 small = 14.0 * per_cu(64, 64);
+    const double large = 9.0 + 49.0 * per_cu(M, N, 128, 256), wide = 1.0 + 28.0 * per_cu(M, N, 64, 256),
+                 mid = 19.5 * per_cu(M, N, 64, 128), small = 14.0 * per_cu(M, N, 64, 64);
     if (large <= wide && large <= mid && large <= small)
       return launch_tiles<YT, kMxPieces, 2, 4, 2, 1, 1>(A, As, W, Ws, M, N, K, Y, stream);
     if (wide <= mid && wide <= small) return launch_tiles<YT, kMxPieces, 1, 2, 4, 2, 1>(A, As, W, Ws, M, N, K, Y, stream);
@@ -404,11 +447,16 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
 //                    16384 x 4096 17 / 19, 28672 x 8192 37 / 53
 //          64 rows   4096 x 4096 12 / 18, 8192 x 8192 26 / 30, 4096 x 11008 39 / 39,
 //                    16384 x 4096 24 / 20, 28672 x 8192 59 / 53
-//   4-bit, 32 rows   4096 x 4096 6 / 10, 28672 x 8192 26 / 35, 4096 x 11008 14 / 20
-//          64 rows   4096 x 4096 8 / 10, 8192 x 8192 17 / 17, 16384 x 4096 14 / 13,
-//                    28672 x 8192 31 / 37, 4096 x 11008 20 / 20
+//   4-bit, 32 rows   4096 x 4096 6 / 8, 8192 x 8192 12 / 13, 4096 x 11008 14 / 17,
+//                    16384 x 4096 10 / 9, 28672 x 8192 26 / 35
+//          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 13, 28672 x 8192 31 / 38,
+//                    and where the tiles keep the scales and N is large:
+//                    8192 x 8192 15 / 14, 16384 x 4096 14 / 10, 11008 x 4096 12 / 9;
+//                    4096 x 11008 17 / 17
 bool skinny(int64_t M, int64_t N, int64_t K) { return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192 && N <= 8192)); }
-bool skinny_mx(int64_t M, int64_t K) { return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192)); }
+bool skinny_mx(int64_t M, int64_t N, int64_t K) {
+  return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192 && (N < 8192 || !resident(M, N, K))));
+}
 constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
 
 int64_t split_row_groups(int64_t M) { return (M + kRowPad - 1) / kRowPad * (kRowPad / 32); }
@@ -439,17 +487,21 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
 }
 
 size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return skinny_mx(M, K) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
+  return skinny_mx(M, N, K) || resident(M, N, K) ? 0 : scale_bytes(M, K) + scale_bytes(N, K);
 }
 
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, void* workspace, hipStream_t stream) {
-  if (skinny_mx(M, K)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
-  uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  uint8_t* const as = ws + scale_bytes(N, K);
-  const hipError_t e = launch_mxfp4_scales(Ws, N, ws, As, M, as, K, stream);
-  if (e != hipSuccess) return e;
-  return ydtype == 0 ? launch<F16, 1>(A, as, W, ws, M, N, K, Y, stream) : launch<BF16, 1>(A, as, W, ws, M, N, K, Y, stream);
+  if (skinny_mx(M, N, K)) return launch_mxfp4_skinny_mx(A, As, W, Ws, M, N, K, ydtype, Y, stream);
+  if (!resident(M, N, K)) {
+    uint8_t* const ws = static_cast<uint8_t*>(workspace);
+    uint8_t* const as = ws + scale_bytes(N, K);
+    const hipError_t e = launch_mxfp4_scales(Ws, N, ws, As, M, as, K, stream);
+    if (e != hipSuccess) return e;
+    As = as;
+    Ws = ws;
+  }
+  return ydtype == 0 ? launch<F16, 1>(A, As, W, Ws, M, N, K, Y, stream) : launch<BF16, 1>(A, As, W, Ws, M, N, K, Y, stream);
 }
 
 }  // namespace woq

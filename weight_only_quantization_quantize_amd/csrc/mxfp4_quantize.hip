@@ -122,16 +122,7 @@ __device__ inline void turn_scales(const ScaleJob& j, int nblk, int block) {
   const int row = (int)(i % j.rows_pad), g = (int)(i / j.rows_pad);
   if (4 * g >= ktiles) return;
   u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
-  if (row < j.rows) {
-    const uint8_t* const p = j.scales + (int64_t)row * nblk + 16 * g;
-    if (16 * g + 16 <= nblk) {
-      __builtin_memcpy(&v, p, 16);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (16 * g + q < nblk) v[q / 4] = (v[q / 4] & ~(0xFFu << (8 * (q % 4)))) | ((uint32_t)p[q] << (8 * (q % 4)));
-    }
-  }
+  if (row < j.rows) v = mx_scale_chunk(j.scales + (int64_t)row * nblk, g, nblk);
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     if (4 * g + q < ktiles) j.out[(int64_t)(4 * g + q) * j.rows_pad + row] = v[q];

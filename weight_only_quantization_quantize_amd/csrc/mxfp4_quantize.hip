@@ -109,17 +109,18 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32
 
 // Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 127 in the
 // place of rows and blocks that are not there.
+constexpr int kScaleWaves = kThreads / 64;
+static_assert(kMxScaleRowPad % 64 == 0, "a wave's rows are whole");
 struct ScaleJob {
   const uint8_t* scales;
   uint32_t* out;
   int rows, rows_pad;
 };
-// Workgroup `block` of a job's.
+// Workgroup `block` of a job's: 64 rows, each wave 16 blocks of them (a lane a row,
+// so the writes are contiguous), the waves next to each other in the rows' lines.
 __device__ inline void turn_scales(const ScaleJob& j, int nblk, int block) {
-  const int64_t i = (int64_t)block * kThreads + threadIdx.x;
-  const int ktiles = (nblk + 7) / 8 * 2;
-  // a thread takes 16 blocks of a row, a wave 64 rows: the writes are contiguous
-  const int row = (int)(i % j.rows_pad), g = (int)(i / j.rows_pad);
+  const int ktiles = (nblk + 7) / 8 * 2, groups = j.rows_pad / 64;
+  const int row = block % groups * 64 + ((int)threadIdx.x & 63), g = block / groups * kScaleWaves + ((int)threadIdx.x >> 6);
   if (4 * g >= ktiles) return;
   u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
   if (row < j.rows) v = mx_scale_chunk(j.scales + (int64_t)row * nblk, g, nblk);
@@ -157,9 +158,10 @@ __global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* _
   mx_store_pieces(s, pieces + (int64_t)f * kMxFragBytes, scales + (int64_t)f * 64, lane);
 }
 
-// Workgroups of a scale job, one row and 512 of K a thread.
-static_assert(kMxScaleRowPad % kThreads == 0, "a workgroup's rows are whole");
-int64_t scale_blocks(int64_t rows, int64_t K) { return mxfp4_scale_rows(rows) * ((K + 511) / 512) / kThreads; }
+// Workgroups of a scale job.
+int64_t scale_blocks(int64_t rows, int64_t K) {
+  return mxfp4_scale_rows(rows) / 64 * ((K + 512 * kScaleWaves - 1) / (512 * kScaleWaves));
+}
 ScaleJob scale_job(const void* scales, int64_t rows, void* out) {
   return ScaleJob{static_cast<const uint8_t*>(scales), static_cast<uint32_t*>(out), (int)rows, (int)mxfp4_scale_rows(rows)};
 }

@@ -204,7 +204,9 @@ def test_gemm_mx(M, N, K, dtype):
 WIDE = [(5, 12321, 160), (9, 8200, 544), (16, 700, 4704), (20, 9000, 4640), (24, 4100, 1024), (33, 4300, 8160),
         (50, 13000, 256), (50, 13000, 4640), (64, 5000, 1056), (64, 5000, 4640), (32, 300, 8224), (16, 40, 22016),
         (70, 27000, 96), (130, 8100, 96), (1200, 7000, 96), (2000, 8100, 96), (640, 1000, 3104),
-        (200, 8000, 3616), (200, 8000, 3584), (66, 300, 16416), (67, 300, 16384), (64, 8200, 4128)]
+        (200, 8000, 3616), (200, 8000, 3584), (66, 300, 16416), (67, 300, 16384), (64, 8200, 4128),
+        (128, 4000, 1056), (512, 1000, 2080), (300, 1500, 4128), (256, 1000, 4128), (512, 500, 8160),
+        (100, 2500, 4640), (64, 28000, 4128), (500, 1, 8192)]
 
 
 @pytest.mark.parametrize("M, N, K", WIDE)

@@ -441,21 +441,26 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   }
 }
 
-// Few rows (and K >= 128) go to the weight-streaming kernels, which need no pass
-// over the scales.  Whole products, us, streaming / tiles:
-//   split, 32 rows   4096 x 4096 10 / 18, 8192 x 8192 20 / 30, 4096 x 11008 24 / 39,
-//                    16384 x 4096 17 / 19, 28672 x 8192 37 / 53
-//          64 rows   4096 x 4096 12 / 18, 8192 x 8192 26 / 30, 4096 x 11008 39 / 39,
-//                    16384 x 4096 24 / 20, 28672 x 8192 59 / 53
+// Few rows, or small outputs, go to the weight-streaming kernels (K >= 128), which
+// need no pass over the scales and cut no tile that is mostly empty.  Whole
+// products, us, streaming / tiles:
+//   split, 32 rows   8192 x 8192 20 / 30, 4096 x 11008 24 / 39, 28672 x 8192 37 / 53
+//          64 rows   4096 x 4096 12 / 18, 8192 x 8192 26 / 30, 11008 x 2048 14 / 13,
+//                    16384 x 4096 24 / 20, 28672 x 8192 59 / 53, 4096 x 11008 39 / 39
+//          128       2048 x 8192 20 / 31, 4096 x 4096 17 / 19, 6144 x 4096 20 / 19
+//          256       1024 x 8192 23 / 32, 2048 x 2048 12 / 13, 4096 x 4096 25 / 21
 //   4-bit, 32 rows   4096 x 4096 6 / 8, 8192 x 8192 12 / 13, 4096 x 11008 14 / 17,
 //                    16384 x 4096 10 / 9, 28672 x 8192 26 / 35
-//          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 13, 28672 x 8192 31 / 38,
-//                    and where the tiles keep the scales and N is large:
-//                    8192 x 8192 15 / 14, 16384 x 4096 14 / 10, 11008 x 4096 12 / 9;
-//                    4096 x 11008 17 / 17
-bool skinny(int64_t M, int64_t N, int64_t K) { return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192 && N <= 8192)); }
+//          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 13, 8192 x 8192 15 / 14,
+//                    4096 x 2048 6 / 5; 28672 x 8192 31 / 38 (scales in a pass)
+//          128       512 x 4096 6 / 7, 2048 x 8192 11 / 12, 4096 x 8192 15 / 13
+//          256       1024 x 8192 10 / 11, 2048 x 2048 7 / 5
+bool skinny(int64_t M, int64_t N, int64_t K) {
+  return K >= 128 && (M <= 32 || (K <= 8192 && M <= 512 && M * N <= 1 << 19));
+}
 bool skinny_mx(int64_t M, int64_t N, int64_t K) {
-  return K >= 128 && (M <= 32 || (M <= 64 && K <= 8192 && (N < 8192 || !resident(M, N, K))));
+  return K >= 128 && (M <= 32 || (K <= 8192 && ((M <= 64 && !resident(M, N, K)) ||
+                                                (M <= 512 && K >= 4096 && M * N <= 1 << 18))));
 }
 constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
 

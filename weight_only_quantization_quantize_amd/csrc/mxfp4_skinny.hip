@@ -1,5 +1,5 @@
-// Products of a few rows of activations (up to 64) with microscaled weights, bound
-// by streaming the weights:
+// Products of a few rows of activations with microscaled weights, or of more with
+// few columns, bound by streaming the weights:
 //   Y[m, n] = sum_b 2^(sA + sW - 254) sum_{k in block b} a[m, k] w[n, k].
 //
 // Work split.  K is cut into super-steps of 512 (four steps of
@@ -299,11 +299,11 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   const auto* wsp = static_cast<const uint8_t*>(Ws);
   auto* yp = static_cast<uint16_t*>(Y);
   const int tiles = (N + 15) / 16, supers = (nblk + kSuper - 1) / kSuper;
-  // workgroups a row group: a column group's lie a multiple of 8 apart in dispatch
-  // order, on one XCD (three row groups of 85 took 28 us where four of 64 take 26)
+  // workgroups a row group: a multiple of 8, so that a column group's are on one XCD
+  // (three row groups of 85 took 28 us where four of 64 take 26)
   const int rgroups = (M + 16 * TC - 1) / (16 * TC);
-  const int target = kTargetGroups / (rgroups == 3 ? 4 : rgroups);
-  if constexpr (TC < 4) {  // more than 32 rows come with K <= 8192 only
+  const int share = kTargetGroups / rgroups & ~7, target = share < 8 ? 8 : share;
+  if constexpr (TC < 4) {  // four chunks come with K <= 8192 only
     if (supers > 2 * kWaves) {
       const dim3 grid((unsigned)(tiles < target ? tiles : target), (unsigned)rgroups);
       mxfp4_skinny_long_kernel<YT, PIECES, TC><<<grid, kLongWaves * 64, 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, supers, yp);
@@ -351,9 +351,10 @@ hipError_t launch_mxfp4_skinny_mx(const void* A, const void* As, const void* cod
                                   int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream) {
   const int nblk = (int)(K / kMxBlock);
   // chunks of 16 rows a workgroup: all of them, so that the weights are read once,
-  // but for 64 rows of few columns, where a workgroup loads more activations than
-  // weights (4096 x 4096: 6.6 us in two row groups, 8.0 in one; 28672 x 8192: 34, 31)
-  const int chunks = M <= 16 ? 1 : (M <= 32 || (M > 48 && N <= 8192) ? 2 : 4);
+  // but two where there are few columns and a workgroup would load more activations
+  // than weights (64 rows of 4096 x 4096: 6.6 us in two row groups, 8.0 in one;
+  // 28672 x 8192: 34, 31)
+  const int chunks = M <= 16 ? 1 : (M <= 32 || N <= 8192 ? 2 : 4);
   auto* const f = chunks == 1   ? (ydtype == 0 ? launch<F16, 1, 1> : launch<BF16, 1, 1>)
                   : chunks == 2 ? (ydtype == 0 ? launch<F16, 1, 2> : launch<BF16, 1, 2>)
                                 : (ydtype == 0 ? launch<F16, 1, 4> : launch<BF16, 1, 4>);

@@ -349,7 +349,8 @@ MOE = [(1, 64, 32, 4, 2), (1, 2080, 1056, 12, 3), (1, 512, 160, 65, 1), (2, 96, 
 # rows longer than a workgroup's waves hold, more turns than workgroups, as many
 # choices as there may be
 MOE += [(1, 4640, 64, 6, 2), (1, 64, 4640, 5, 3), (3, 4640, 96, 5, 2), (6, 96, 4640, 6, 3), (39, 1056, 1024, 30, 3),
-        (1, 64, 32, 512, 64), (64, 64, 32, 64, 64), (2, 2080, 544, 70, 9)]
+        (1, 64, 32, 512, 64), (64, 64, 32, 64, 64), (2, 2080, 544, 70, 9), (16, 128, 1056, 6, 6), (15, 96, 64, 32, 1),
+        (16, 96, 64, 33, 2), (2, 160, 608, 9, 8)]
 
 
 @pytest.mark.parametrize("T, H, I, E, k", MOE)

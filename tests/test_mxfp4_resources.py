@@ -21,7 +21,7 @@ FILES = {
     "mxfp4_gemv.hip": ["mxfp4_gemv_kernel"],
     "mxfp4_skinny.hip": ["mxfp4_skinny_kernel", "mxfp4_skinny_long_kernel"],
     "mxfp4_gemm.hip": ["mxfp4_gemm_kernel"],
-    "mxfp4_moe.hip": ["moe_route_kernel", "moe_choose_kernel", "moe_experts_kernel", "moe_one_down_kernel",
+    "mxfp4_moe.hip": ["moe_route_kernel", "moe_choose_kernel", "moe_experts_kernel", "moe_direct_down_kernel",
                       "moe_combine_kernel"],
 }
 

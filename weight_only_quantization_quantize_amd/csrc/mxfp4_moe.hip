@@ -20,8 +20,8 @@
 //            folded in here, where the values are still fp32.
 //   down     64 columns of a turn's products a time
 //   combine  y from its experts' products, added in the order of choice (no atomics)
-// One token needs no list: up and down work the choices out from the logits, and
-// down adds over the experts itself.
+// A small layer of few tokens has no combine: its down adds over the experts itself.
+// One token needs no list either: up and down work the choices out from the logits.
 //
 // bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 105 us, of which up 63
 // (285 MB of weights, 4.5 TB/s) and down 31 (142 MB, 4.6 TB/s); one token 24 us,
@@ -408,51 +408,66 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
   }
 }
 
-// One token: columns [16 b, 16 b + 16) of y, over all turns' super-steps, which
-// the waves share out; their sums are added in order.  (As items of the general
-// form and a launch for the sum over experts they took 14 us for 4 experts of
-// 4096 x 2048, this takes 8.5.)
+// Few units of weights: columns [16 b, 16 b + 16) of y for up to 16 tokens, over all
+// turns' super-steps, which the waves share out two at a time; their sums are added
+// in order.  NJ as above.
 template <class YT, int NJ>
-__global__ __launch_bounds__(kExpertWaves * 64) void moe_one_down_kernel(const uint8_t* __restrict__ hp,
-                                                                         const uint8_t* __restrict__ hs,
-                                                                         const uint8_t* __restrict__ codes,
-                                                                         const uint8_t* __restrict__ scales,
-                                                                         const float* __restrict__ logits, int top_k,
-                                                                         int H, int I, int E, uint16_t* __restrict__ Y) {
-  __shared__ __attribute__((aligned(16))) uint8_t stage_all[kExpertWaves][kUnitStage];
-  __shared__ float sums[kExpertWaves][16];
+__global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
+    const uint8_t* __restrict__ hp, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ codes,
+    const uint8_t* __restrict__ scales, const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan,
+    const Turn* __restrict__ turns, int T, int H, int I, int E, uint16_t* __restrict__ Y) {
+  constexpr int W = kExpertWaves, kRows = NJ > 0 ? 1 : kChunk;
+  __shared__ __attribute__((aligned(16))) uint8_t stage_all[W][kUnitStage];
+  __shared__ float sums[W][kRows][kChunk + 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nblk = I / kMxBlock, supers = (I + 511) / 512, units = top_k * supers;
+  const int nblk = I / kMxBlock, supers = (I + 511) / 512;
   const int n0 = (int)blockIdx.x * 16;
   uint8_t* const stage = stage_all[wave];
-  float logit[NJ];
-  load_logits(logit, logits, E, lane);
-  const Choice choice = choose(logit, E, top_k, lane);
+  Choice choice = {};
+  if constexpr (NJ > 0) {
+    float logit[NJ];
+    load_logits(logit, logits, E, lane);
+    choice = choose(logit, E, top_k, lane);
+  }
+  const int units = (NJ > 0 ? top_k : plan->turns) * supers;
+  for (int o = lane; o < kRows * (kChunk + 1); o += 64) (&sums[wave][0][0])[o] = 0.0f;
   struct Work {
     MxUnit u;
     MxActivations a[4];
+    uint32_t tokens;  // of rows 4 q .. 4 q + 3
   };
-  auto row_of = [&](int i) { return (int64_t)__builtin_amdgcn_readlane(choice.expert, i / supers) * H + n0; };
-  const MxPlace place = mx_place(0, lane & 48);  // every row is the token's
+  auto row_of = [&](int i) {
+    const int k = i / supers;
+    const int e = NJ > 0 ? __builtin_amdgcn_readlane(choice.expert, k) : turns[k].expert;
+    return (int64_t)e * H + n0;
+  };
+  auto count_of = [&](int i) { return NJ > 0 ? 1 : turns[i / supers].count; };
   auto load = [&](Work& w, int i) {
     const int64_t row = row_of(i);
+    const int count = count_of(i);
+    w.tokens = NJ > 0 ? 0u : reinterpret_cast<const uint32_t*>(turns[i / supers].token)[lane >> 4];
     mx_load_unit(w.u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, i % supers, lane);
+    // rows past the turn's last token repeat it
+    const MxPlace place = mx_place(0, (lane & 48) + ((lane & 15) < count ? lane & 15 : count - 1));
 #pragma unroll
     for (int s = 0; s < 4; ++s)
       mx_load_activations(w.a[s], hp + ((int64_t)i * 4 + s) * kMxFragBytes, hs + ((int64_t)i * 4 + s) * kMxFragScaleBytes, place);
   };
-  float4_t acc = {};
   auto work = [&](const Work& w, int i) {
+    float4_t acc = {};
     mx_stage_unit(w.u, stage, 15, ((int64_t)E * H - row_of(i)) * nblk, nblk, i % supers, lane);
     const int sc = mx_staged_scale(stage, lane);
     mx_each_step([&](auto sel) {
       constexpr int s = decltype(sel)::value;
       mx_multiply<s>(acc, w.a[s], mx_staged_weights(stage, s, lane), sc);
     });
+    const int count = count_of(i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * (lane >> 4) + e < count) sums[wave][w.tokens >> (8 * e) & 15u][lane & 15] += acc[e];
   };
-  // two units at a time; an odd last one is loaded twice and multiplied once
-  constexpr int W = kExpertWaves;
+  // an odd last unit is loaded twice and multiplied once
   for (int i = wave; i < units; i += 2 * W) {
     const bool two = i + W < units;
     Work a, b;
@@ -462,13 +477,13 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_one_down_kernel(const u
     work(a, i);
     if (two) work(b, i + W);
   }
-  if (lane < 16) sums[wave][lane] = acc[0];
   __syncthreads();
-  if (threadIdx.x < 16) {
+  if ((int)threadIdx.x < T * kChunk) {
+    const int t = threadIdx.x / kChunk, n = threadIdx.x % kChunk;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += sums[w][threadIdx.x];
-    Y[n0 + threadIdx.x] = YT::from_f32(v);
+    for (int w = 0; w < W; ++w) v += sums[w][t][n];
+    Y[(int64_t)t * H + n0 + n] = YT::from_f32(v);
   }
 }
 
@@ -556,14 +571,22 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
     return hipGetLastError();
   };
   auto up = [&](auto nj) { return experts(std::true_type{}, nj, ws + l.xp, xs, up_codes, up_scales, H, 2 * I, I / kMxBlock); };
+  // Few units of down's weights go straight to y: whole layers, us, direct / in two
+  // launches, by turns (at most) x super-steps:
+  //   4    2 x 1024 x 512    25 / 34        34   16 x 2048 x 512    30 / 33
+  //   17   8 x 1024 x 512    26 / 28        36   16 x 4096 x 512    42 / 45
+  //   20  16 x 4096 x 1024   31 / 36        68    8 x 2048 x 768    40 / 37
+  //   32   2 x 4096 x 2048   42 / 40        93    5 x 2080 x 1056   61 / 49
+  const bool direct = T == 1 || (T <= kChunk && l.turns * ((I + 511) / 512) <= 36);
   using Nj0 = std::integral_constant<int, 0>;
   using Nj1 = std::integral_constant<int, 1>;
   using NjN = std::integral_constant<int, kLarge>;
   e = T > 1 ? up(Nj0{}) : (E <= 64 ? up(Nj1{}) : up(NjN{}));
   if (e != hipSuccess) return e;
-  if (T == 1) {
-    auto* const f = E <= 64 ? moe_one_down_kernel<XT, 1> : moe_one_down_kernel<XT, kLarge>;
-    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(ws + l.hp, hs, down_codes, down_scales, logits, top_k, H, I, E, Y);
+  if (direct) {
+    auto* const f = T > 1 ? moe_direct_down_kernel<XT, 0> : (E <= 64 ? moe_direct_down_kernel<XT, 1> : moe_direct_down_kernel<XT, kLarge>);
+    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(ws + l.hp, hs, down_codes, down_scales, logits, top_k, plan, turns,
+                                                            T, H, I, E, Y);
     return hipGetLastError();
   }
   e = experts(std::false_type{}, Nj0{}, ws + l.hp, hs, down_codes, down_scales, I, H, (H + 63) / 64);

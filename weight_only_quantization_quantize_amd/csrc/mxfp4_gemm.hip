@@ -446,9 +446,9 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
 // products, us, streaming / tiles:
 //   split, 32 rows   8192 x 8192 20 / 30, 4096 x 11008 24 / 39, 28672 x 8192 37 / 53
 //          64 rows   4096 x 4096 12 / 18, 8192 x 8192 26 / 30, 11008 x 2048 14 / 13,
-//                    16384 x 4096 24 / 20, 28672 x 8192 59 / 53, 4096 x 11008 39 / 39
-//          128       2048 x 8192 20 / 31, 4096 x 4096 17 / 19, 6144 x 4096 20 / 19
-//          256       1024 x 8192 23 / 32, 2048 x 2048 12 / 13, 4096 x 4096 25 / 21
+//                    16384 x 4096 22 / 20, 28672 x 8192 59 / 53, 4096 x 11008 39 / 39
+//          128       2048 x 8192 20 / 31, 4096 x 4096 16 / 19, 6144 x 4096 19 / 19
+//          256       1024 x 8192 23 / 32, 2048 x 2048 12 / 13, 4096 x 4096 22 / 21
 //   4-bit, 32 rows   4096 x 4096 6 / 8, 8192 x 8192 12 / 13, 4096 x 11008 14 / 17,
 //                    16384 x 4096 10 / 9, 28672 x 8192 26 / 35
 //          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 13, 8192 x 8192 15 / 14,
@@ -471,6 +471,7 @@ int64_t split_ksteps(int64_t K) { return (K + 127) / 128 * 2; }
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return 0;
+  if (skinny(M, N, K) && mxfp4_skinny_splits(K)) return 0;
   if (skinny(M, N, K))
     return (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * (kMxFragBytes + kMxFragScaleBytes);
   return (size_t)(split_row_groups(M) * split_ksteps(K)) * (kMxFragBytes + kMxFragScaleBytes) + scale_bytes(N, K);
@@ -481,6 +482,7 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
   if (M == 1 && K <= mxfp4_gemv_max_k()) return launch_mxfp4_gemv(X, xdtype, codes, scales, N, K, Y, stream);
   uint8_t* const pieces = static_cast<uint8_t*>(workspace);
   const bool few = skinny(M, N, K);
+  if (few && mxfp4_skinny_splits(K)) return launch_mxfp4_skinny_raw(X, xdtype, codes, scales, M, N, K, Y, stream);
   const int64_t rg = few ? (M + 15) / 16 : split_row_groups(M), ks = few ? (K + 511) / 512 * 4 : split_ksteps(K);
   uint8_t* const ps = pieces + rg * ks * kMxFragBytes;
   uint8_t* const ws = ps + rg * ks * kMxFragScaleBytes;

@@ -26,6 +26,10 @@ constexpr int kWaves = 8;        // K <= 8192
 constexpr int kLongWaves = 16;   // longer rows
 constexpr int kTargetGroups = 256;  // workgroups: one per compute unit
 
+// Activations: 1, microscaled; kMxPieces, split before; kRaw, 16-bit ones that the
+// kernel splits itself.
+constexpr int kRaw = 4;
+
 // One super-step of a chunk of 16 rows of activations.
 template <int PIECES>
 struct Acts;
@@ -38,8 +42,11 @@ template <>
 struct Acts<kMxPieces> {
   MxActivations a[4];
 };
+template <>
+struct Acts<kRaw> : Acts<kMxPieces> {};
 
 // Chunk t's super-step S; A, As, M: the row group's.
+template <class XT>
 __device__ inline void load_acts(Acts<1>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t, int S,
                                  int M, int nblk, int, int lane) {
   const int r = lane & 15, q = lane >> 4;
@@ -56,12 +63,46 @@ __device__ inline void load_acts(Acts<1>& act, const uint8_t* __restrict__ A, co
   __builtin_memcpy(&act.s, As + (uint32_t)(m * nblk + from), 4);
   act.s >>= 8 * ((b0 - from) & 3);
 }
+template <class XT>
 __device__ inline void load_acts(Acts<kMxPieces>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t,
                                  int S, int, int, int supers, int lane) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int64_t f = ((int64_t)t * supers + S) * 4 + s;
     mx_load_activations(act.a[s], A + f * kMxFragBytes, As + f * kMxFragScaleBytes, mx_place(0, lane));
+  }
+}
+// 16-bit activations of super-step S on their way, and split: a lane's operand at
+// step s is the split of block 4 (lane / 16) + s of its row.
+struct RawActs {
+  u32x4_t x[4][4];
+};
+__device__ inline void load_raw(RawActs& raw, const uint8_t* __restrict__ A, int S, int M, int nblk, int lane) {
+  const int m = (lane & 15) < M ? lane & 15 : M - 1;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int b = kSuper * S + 4 * (lane >> 4) + s;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      raw.x[s][q] = reinterpret_cast<const u32x4_t*>(A)[((int64_t)m * nblk + (b < nblk ? b : nblk - 1)) * 4 + q];
+  }
+}
+template <class XT>
+__device__ inline void split_raw(Acts<kRaw>& act, const RawActs& raw, int S, int nblk, int lane) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const bool live = kSuper * S + 4 * (lane >> 4) + s < nblk;
+    float v[kMxBlock];
+#pragma unroll
+    for (int k = 0; k < kMxBlock; ++k) {
+      const float x = XT::to_f32((uint16_t)(raw.x[s][k / 8][k / 2 % 4] >> (16 * (k % 2))));
+      v[k] = live ? x : 0.0f;
+    }
+    const MxPieces p = mx_split(v);
+    auto piece = [&](int i) {
+      return mx_operand(u32x4_t{p.p[i][0], p.p[i][1], p.p[i][2], p.p[i][3]}, u32x2_t{p.p[i][4], p.p[i][5]});
+    };
+    act.a[s] = MxActivations{piece(0), piece(1), piece(2), (int)p.scale};
   }
 }
 template <int S>
@@ -79,6 +120,8 @@ __device__ inline void enter_row_group(const uint8_t* __restrict__& A, const uin
   if constexpr (PIECES == 1) {
     A += (int64_t)m0 * nblk * 16;
     As += (int64_t)m0 * nblk;
+  } else if constexpr (PIECES == kRaw) {
+    A += (int64_t)m0 * nblk * (2 * kMxBlock);
   } else {
     A += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragBytes;
     As += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragScaleBytes;
@@ -137,25 +180,34 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
     __builtin_amdgcn_sched_barrier(0);
   };
   Acts<PIECES> act[TC][SU];
+  if constexpr (PIECES == kRaw) {
+    static_assert(TC == 1 && SU == 1);
+    RawActs raw;
+    load_raw(raw, A, tw < supers ? tw : supers - 1, M, nblk, lane);
 #pragma unroll
-  for (int t = 0; t < TC; ++t)
+    for (int j = 0; j < NU; ++j) ahead(j, begin);
+    split_raw<YT>(act[0][0], raw, tw, nblk, lane);  // while the weights come
+  } else {
 #pragma unroll
-    for (int i = 0; i < SU; ++i) {
-      load_acts(act[t][i], A, As, t, super_of(i) < supers ? super_of(i) : supers - 1, M, nblk, supers, lane);
-      if constexpr (kSpread) {
-        if (i == 1) {
+    for (int t = 0; t < TC; ++t)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const i32x8_t p = act[t][i].a[s].p2;
-            third4[wave][s][lane] = u32x4_t{(uint32_t)p[0], (uint32_t)p[1], (uint32_t)p[2], (uint32_t)p[3]};
-            third2[wave][s][lane] = u32x2_t{(uint32_t)p[4], (uint32_t)p[5]};
+      for (int i = 0; i < SU; ++i) {
+        load_acts<YT>(act[t][i], A, As, t, super_of(i) < supers ? super_of(i) : supers - 1, M, nblk, supers, lane);
+        if constexpr (kSpread) {
+          if (i == 1) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const i32x8_t p = act[t][i].a[s].p2;
+              third4[wave][s][lane] = u32x4_t{(uint32_t)p[0], (uint32_t)p[1], (uint32_t)p[2], (uint32_t)p[3]};
+              third2[wave][s][lane] = u32x2_t{(uint32_t)p[4], (uint32_t)p[5]};
+            }
           }
         }
       }
-    }
-  // (before the activations instead: 4-bit products took 1 .. 1.5 us more)
+    // (before the activations instead: 4-bit products took 1 .. 1.5 us more)
 #pragma unroll
-  for (int j = 0; j < NU; ++j) ahead(j, begin);
+    for (int j = 0; j < NU; ++j) ahead(j, begin);
+  }
   float4_t acc[TI][TC];
   auto take = [&](int t0, auto more) {
     int l = lane;
@@ -250,7 +302,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void mxfp4_skinny_long_kernel(
       mx_stage_unit(u, stage, N - tile * 16 - 1, left(tile), nblk, S, lane);
       Acts<PIECES> act[TC];
 #pragma unroll
-      for (int t = 0; t < TC; ++t) load_acts(act[t], A, As, t, S < supers ? S : supers - 1, M, nblk, supers, lane);
+      for (int t = 0; t < TC; ++t) load_acts<YT>(act[t], A, As, t, S < supers ? S : supers - 1, M, nblk, supers, lane);
       const int Sn = k + 1 < rounds ? S + team : wave;
       const int tn = k + 1 < rounds ? tile : next;
       load_weights(tn < tiles ? tn : tile, Sn < supers ? Sn : supers - 1);
@@ -303,7 +355,7 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   // (three row groups of 85 took 28 us where four of 64 take 26)
   const int rgroups = (M + 16 * TC - 1) / (16 * TC);
   const int share = kTargetGroups / rgroups & ~7, target = share < 8 ? 8 : share;
-  if constexpr (TC < 4) {  // four chunks come with K <= 8192 only
+  if constexpr (TC < 4 && PIECES != kRaw) {  // those come with K <= 8192 only
     if (supers > 2 * kWaves) {
       const dim3 grid((unsigned)(tiles < target ? tiles : target), (unsigned)rgroups);
       mxfp4_skinny_long_kernel<YT, PIECES, TC><<<grid, kLongWaves * 64, 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, supers, yp);
@@ -322,10 +374,10 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   // cost their loads all the same: 4096 x 4096 takes 9.7 us with one, 11.2 with
   // four) or where 64 rows leave no registers for them
   const int most = (tiles + (int)grid.x * slots - 1) / ((int)grid.x * slots);
-  void (*f)(const uint8_t*, const uint8_t*, const uint8_t*, const uint8_t*, int, int, int, int, int, uint16_t*);
+  void (*f)(const uint8_t*, const uint8_t*, const uint8_t*, const uint8_t*, int, int, int, int, int, uint16_t*) = nullptr;
   if (two) {
-    f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 1>;
-    if constexpr (TC < 4)
+    if constexpr (PIECES != kRaw) f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 1>;
+    if constexpr (TC < 4 && PIECES != kRaw)
       if (most > 1) f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 2>;
   } else {
     f = most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 2> : mxfp4_skinny_kernel<YT, PIECES, TC, 1, 1>;
@@ -337,6 +389,19 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
 }
 
 }  // namespace
+
+// 16-bit activations.  Up to K = 4096 (a super-step a wave) each workgroup splits
+// them itself, while its first weights come: 16 rows of 512 x 512 take 5.5 us in
+// place of 7.3 with a launch for the split, of 4096 x 4096 9.9 / 9.0, of 16384 x 4096
+// 12.2 / 12.6, and the host has a launch and a workspace less.  Two super-steps a
+// wave would take twice that time and more registers than there are.
+bool mxfp4_skinny_splits(int64_t K) { return K <= 512 * kWaves; }
+hipError_t launch_mxfp4_skinny_raw(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
+                                   int64_t K, void* Y, hipStream_t stream) {
+  const int nblk = (int)(K / kMxBlock);
+  return xdtype == 0 ? launch<F16, kRaw, 1>(X, nullptr, codes, scales, (int)M, (int)N, nblk, Y, stream)
+                     : launch<BF16, kRaw, 1>(X, nullptr, codes, scales, (int)M, (int)N, nblk, Y, stream);
+}
 
 // 16-bit activations, split in fragments of 16 rows.
 hipError_t launch_mxfp4_skinny(const void* pieces, const void* piece_scales, const void* codes, const void* scales,

@@ -294,6 +294,37 @@ def test_outputs_stay_inside_their_rows(M):
     assert torch.equal(first, ops.mxfp4_gemm(x, codes, scales))
 
 
+def _shifted(t):
+    """The same bytes one byte further on."""
+    buf = torch.empty(t.numel() + 1, dtype=torch.uint8, device=DEV)
+    out = buf[1:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 70, 1056), (9, 70, 1056), (40, 70, 4640), (100, 300, 1056), (300, 300, 1056),
+                                     (9, 70, 8736), (700, 1100, 352)])
+def test_scales_at_any_alignment(M, N, K):
+    x, (codes, scales) = activations(M, K, torch.float16, 11), weights(N, K, 12)
+    a, asc = ops.mxfp4_quantize(x)
+    want = ops.mxfp4_gemm(x, codes, scales), ops.mxfp4_gemm_mx(a, asc, codes, scales), ops.mxfp4_dequantize(a, asc)
+    s, t = _shifted(scales), _shifted(asc)
+    assert s.data_ptr() % 2 == 1 and t.data_ptr() % 2 == 1
+    assert torch.equal(ops.mxfp4_gemm(x, codes, s), want[0])
+    assert torch.equal(ops.mxfp4_gemm_mx(a, t, codes, s), want[1])
+    assert torch.equal(ops.mxfp4_dequantize(a, t), want[2])
+    again = ops.mxfp4_quantize(x, (torch.zeros_like(a), _shifted(torch.zeros_like(asc))))
+    assert torch.equal(again[0], a) and torch.equal(again[1], asc)
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_moe_scales_at_any_alignment(T):
+    a = list(moe_case(T, 608, 160, 9, torch.bfloat16, 3))
+    want = ops.mxfp4_moe(*a, 3)
+    a[3], a[5] = _shifted(a[3]), _shifted(a[5])
+    assert torch.equal(ops.mxfp4_moe(*a, 3), want)
+
+
 def test_codes_past_two_gigabytes():
     N, K = 140000, 32768  # 2.3e9 bytes of codes, 1.4e8 of scales
     codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)

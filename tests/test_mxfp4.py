@@ -226,9 +226,9 @@ def test_abi_gemm_refuses():
               (3, None, INVALID), (4, 0, INVALID), (5, 0, INVALID), (6, 40, INVALID), (7, None, INVALID),
               (7, FAKE + 2, INVALID), (8, None, INVALID), (8, FAKE + 128, INVALID), (9, need - 1, INVALID),
               (5, 1 << 29, UNSUPPORTED), (4, 1 << 40, UNSUPPORTED)])
-    need = lib.woq_mxfp4_gemm_mx_workspace_bytes(4, 64, 64)
+    need = lib.woq_mxfp4_gemm_mx_workspace_bytes(600, 4096, 4096)  # tiles that read turned scales
     assert need > 0
-    _refused("woq_mxfp4_gemm_mx", [FAKE, FAKE, FAKE, FAKE, 4, 64, 64, 0, FAKE, FAKE, need, None],
+    _refused("woq_mxfp4_gemm_mx", [FAKE, FAKE, FAKE, FAKE, 600, 4096, 4096, 0, FAKE, FAKE, need, None],
              [(0, None, INVALID), (1, None, INVALID), (2, FAKE + 8, INVALID), (3, None, INVALID), (4, 0, INVALID),
               (5, -5, INVALID), (6, 16, INVALID), (7, 2, INVALID), (8, None, INVALID),
               (9, None, INVALID), (9, FAKE + 64, INVALID), (10, need - 1, INVALID)])
@@ -238,6 +238,8 @@ def test_abi_workspace_queries():
     lib = _lib.load()
     assert lib.woq_mxfp4_gemm_workspace_bytes(1, 8192, 8192) == 0      # one row uses none
     assert lib.woq_mxfp4_gemm_workspace_bytes(1, 64, 16416) > 0        # but past the GEMV's K
+    assert lib.woq_mxfp4_gemm_workspace_bytes(16, 4096, 4096) == 0     # split in the product's launch
+    assert lib.woq_mxfp4_gemm_mx_workspace_bytes(4, 64, 64) == 0       # scales kept in LDS
     for bad in ((0, 64, 64), (4, 0, 64), (4, 64, 63), (4, 64, 0)):
         assert lib.woq_mxfp4_gemm_workspace_bytes(*bad) == 0
     assert lib.woq_mxfp4_moe_workspace_bytes(1, 64, 32, 4, 2) > 0

@@ -374,16 +374,21 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   // cost their loads all the same: 4096 x 4096 takes 9.7 us with one, 11.2 with
   // four) or where 64 rows leave no registers for them
   const int most = (tiles + (int)grid.x * slots - 1) / ((int)grid.x * slots);
-  void (*f)(const uint8_t*, const uint8_t*, const uint8_t*, const uint8_t*, int, int, int, int, int, uint16_t*) = nullptr;
-  if (two) {
-    if constexpr (PIECES != kRaw) f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 1>;
-    if constexpr (TC < 4 && PIECES != kRaw)
-      if (most > 1) f = mxfp4_skinny_kernel<YT, PIECES, TC, 2, 2>;
-  } else {
-    f = most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 2> : mxfp4_skinny_kernel<YT, PIECES, TC, 1, 1>;
-    if constexpr (TC < 4)
-      if (most > 2) f = mxfp4_skinny_kernel<YT, PIECES, TC, 1, 4>;
-  }
+  auto* const f = [&] {
+    if constexpr (PIECES == kMxPieces)  // K > 4096
+      return most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 2, 2> : mxfp4_skinny_kernel<YT, PIECES, TC, 2, 1>;
+    else if constexpr (PIECES == kRaw)  // K <= 4096
+      return most > 2   ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 4>
+             : most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 2>
+                        : mxfp4_skinny_kernel<YT, PIECES, TC, 1, 1>;
+    else if constexpr (TC == 4)  // N > 8192: several tiles a team
+      return two ? mxfp4_skinny_kernel<YT, 1, 4, 2, 1> : mxfp4_skinny_kernel<YT, 1, 4, 1, 2>;
+    else
+      return two ? (most > 1 ? mxfp4_skinny_kernel<YT, 1, TC, 2, 2> : mxfp4_skinny_kernel<YT, 1, TC, 2, 1>)
+                 : (most > 2   ? mxfp4_skinny_kernel<YT, 1, TC, 1, 4>
+                    : most > 1 ? mxfp4_skinny_kernel<YT, 1, TC, 1, 2>
+                               : mxfp4_skinny_kernel<YT, 1, TC, 1, 1>);
+  }();
   f<<<grid, (unsigned)(slots * team * 64), 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, team, supers, yp);
   return hipGetLastError();
 }

@@ -162,16 +162,17 @@ __device__ inline void mx_store_pieces(const MxPieces& s, uint8_t* __restrict__ 
   fscale[lane] = s.scale;
 }
 
-// Scale bytes 16 g .. 16 g + 15 of a row of nblk, 127 past its end.
+// Scale bytes 16 g .. 16 g + 15 of a row of nblk, 0 past its end: whatever codes
+// stand there, times 2^-254 they are below fp32's smallest number.
 __device__ inline u32x4_t mx_scale_chunk(const uint8_t* __restrict__ row, int g, int nblk) {
-  u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  u32x4_t v = {0u, 0u, 0u, 0u};
   const uint8_t* const p = row + 16 * g;
   if (16 * g + 16 <= nblk) {
     __builtin_memcpy(&v, p, 16);
   } else {
 #pragma unroll
     for (int q = 0; q < 16; ++q)
-      if (16 * g + q < nblk) v[q / 4] = (v[q / 4] & ~(0xFFu << (8 * (q % 4)))) | ((uint32_t)p[q] << (8 * (q % 4)));
+      if (16 * g + q < nblk) v[q / 4] |= (uint32_t)p[q] << (8 * (q % 4));
   }
   return v;
 }

@@ -16,8 +16,10 @@
 // Below that the number of stages in flight counts: small tiles, K split.
 // 2048 x 11008 x 4096 takes 145 us with split activations (3 x 185 G flop, 3.8 P
 // flop/s as the matrix unit counts them, of the 6.3 P that it reaches on registers
-// alone) and 61 us with 4-bit ones (3.0 of 6.7): LDS, which hands out 1 KB for each
-// instruction of a 64 x 64 wave tile and takes the next stages in meanwhile.
+// alone) and 59 us with 4-bit ones (3.1 of 6.7).  There the vector instructions beside
+// the matrix ones count (LDS is busy for 28% of the time): masks of the last blocks
+// and a shift for every scale, 90 instructions for 16 matrix instructions in place of
+// 44, took 63.
 //
 // Pipeline.  K goes in stages of 64 KS, kStages of them in LDS, filled by direct
 // loads (global_load_lds: no registers, no instructions to write LDS).  At the top
@@ -35,8 +37,10 @@
 // Scales.  The 4-bit operands' scale bytes lie K / 32 bytes apart from row to row
 // at any alignment, which direct loads cannot gather; turn_scales
 // (mxfp4_quantize.hip; in the split's launch where there is one) makes them one
-// dword per row and 128 of K, rows contiguous, with 127 past the row's end.  Small
-// tiles of two 4-bit operands do that themselves, into LDS, once for all of K.
+// dword per row and 128 of K, rows contiguous.  Small tiles of two 4-bit operands do
+// that themselves, into LDS, once for all of K.  Past a row's end stands its last
+// block again, with scale byte 0: the product of two such blocks is below fp32's
+// smallest number (and split activations are zeros there), so no operand is masked.
 //
 // LDS layout of a 4-bit operand: a row's 32 KS bytes of a stage are chunks of
 // one block each, chunk c at position c ^ swizzle(row), so that 16 rows read at
@@ -111,7 +115,7 @@ struct Tile4 {
     r = r < last ? r : last;
     // (KS = 4: a load's 8 rows take every other half of the swizzle)
     int b = 2 * KS * h + (KS == 4 ? chunk ^ ((unit & 1) << 2) : chunk);
-    b = b < nblk ? b : nblk - 1;  // past the row's end: its last block, A is zeros there
+    b = b < nblk ? b : nblk - 1;  // past the row's end: its last block, at scale 2^-127
     load_lds16(codes, (uint32_t)(r * nblk + b) * 16u, to + 1024u * (uint32_t)unit);
   }
   __device__ void load_scales(int unit, int h, uint32_t to) const {
@@ -124,10 +128,13 @@ struct Tile4 {
     const int c = (2 * s + half) ^ swizzle(row);
     return *reinterpret_cast<const u32x4_t*>(lds + row * kRowBytes + c * 16);
   }
+  // the row's scale dword, shifted so that the instruction's byte select (the same
+  // for all lanes) picks step s
   __device__ static int scale(const uint8_t* lds, int row, int s, int half, int h) {
     const uint32_t v = *reinterpret_cast<const uint32_t*>(lds + 4 * (ROWS * (KS == 4 ? s >> 1 : 0) + row));
-    return (int)(v >> (8 * (2 * (KS == 1 ? h & 1 : s & 1) + half)));
+    return (int)(v >> (8 * ((KS == 1 ? 2 * (h & 1) : 0) + half)));
   }
+  static constexpr int select(int s) { return KS == 1 ? 0 : 2 * (s & 1); }
 };
 
 // Split activations: stages of KS fragments (64 of K each) of each 32 rows.
@@ -250,7 +257,6 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
       for (int q = 0; q < 4; ++q) to[q * (of_a ? C::BM : C::BN)] = v[q];
     }
   }
-  auto scale_byte = [&](uint32_t v, int s) { return (int)(v >> (8 * (2 * (s & 1) + half))); };
   int buf = 0;
   for (int h = h0; h < h0 + turns; ++h) {
     wait_loads<(C::kStages - 2) * C::kLoads>();
@@ -260,8 +266,8 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
     const uint8_t* const lw = la + kAt;
     buf = buf + 1 == C::kStages ? 0 : buf + 1;
     if (KG > 1 && h >= h1) continue;
-#pragma unroll
-    for (int s = 0; s < C::kKS; ++s) {
+    auto multiply = [&](auto sel) {
+      constexpr int s = decltype(sel)::value;
       i32x8_t bf[TN];
       int bs[TN];
 #pragma unroll
@@ -269,26 +275,24 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
         const int row = (wn + j) * 32 + r32;
         bf[j] = mx_operand(TW::fragment(lw, row, s, half));
         if constexpr (RES > 0)
-          bs[j] = scale_byte(w_scales[2 * h + (s >> 1)][row], s);
+          bs[j] = (int)(w_scales[2 * h + (s >> 1)][row] >> (8 * half));
         else
           bs[j] = TW::scale(la + kWsAt, row, s, half, h);
       }
       if constexpr (!C::kSplit) {
-        const bool live = 2 * KS * h + 2 * s + half < nblk;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
           const int row = (wm + i) * 32 + r32;
-          u32x4_t v = TA::fragment(la, row, s, half);
-          v = live ? v : u32x4_t{0u, 0u, 0u, 0u};
+          const i32x8_t v = mx_operand(TA::fragment(la, row, s, half));
           int as;
           if constexpr (RES > 0)
-            as = scale_byte(a_scales[2 * h + (s >> 1)][row], s);
+            as = (int)(a_scales[2 * h + (s >> 1)][row] >> (8 * half));
           else
             as = TA::scale(la + kAsAt, row, s, half, h);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], mx_operand(v), acc[i][j], kMfmaFp4,
-                                                                        kMfmaFp4, 0, bs[j], 0, as);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], v, acc[i][j], kMfmaFp4, kMfmaFp4,
+                                                                        TW::select(s), bs[j], TA::select(s), as);
         }
       } else {
 #pragma unroll
@@ -301,17 +305,24 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
           };
           // smallest piece first
           const i32x8_t p2 = piece(2), p1 = piece(1), p0 = piece(0);
+          constexpr int w = TW::select(s);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p2, acc[i][j], kMfmaFp4, kMfmaFp6, 0, bs[j], 2, as);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p2, acc[i][j], kMfmaFp4, kMfmaFp6, w, bs[j], 2, as);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p1, acc[i][j], kMfmaFp4, kMfmaFp6, 0, bs[j], 1, as);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p1, acc[i][j], kMfmaFp4, kMfmaFp6, w, bs[j], 1, as);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p0, acc[i][j], kMfmaFp4, kMfmaFp6, 0, bs[j], 0, as);
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p0, acc[i][j], kMfmaFp4, kMfmaFp6, w, bs[j], 0, as);
         }
       }
+    };
+    multiply(std::integral_constant<int, 0>{});
+    if constexpr (KS > 1) multiply(std::integral_constant<int, 1>{});
+    if constexpr (KS > 2) {
+      multiply(std::integral_constant<int, 2>{});
+      multiply(std::integral_constant<int, 3>{});
     }
   }
   wait_loads<0>();  // none may land in LDS that is another workgroup's by then

@@ -107,8 +107,8 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32
   }
 }
 
-// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 127 in the
-// place of rows and blocks that are not there.
+// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 0 in the place of
+// rows and blocks that are not there.
 constexpr int kScaleWaves = kThreads / 64;
 static_assert(kMxScaleRowPad % 64 == 0, "a wave's rows are whole");
 struct ScaleJob {
@@ -122,7 +122,7 @@ __device__ inline void turn_scales(const ScaleJob& j, int nblk, int block) {
   const int ktiles = (nblk + 7) / 8 * 2, groups = j.rows_pad / 64;
   const int row = block % groups * 64 + ((int)threadIdx.x & 63), g = block / groups * kScaleWaves + ((int)threadIdx.x >> 6);
   if (4 * g >= ktiles) return;
-  u32x4_t v = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  u32x4_t v = {0u, 0u, 0u, 0u};
   if (row < j.rows) v = mx_scale_chunk(j.scales + (int64_t)row * nblk, g, nblk);
 #pragma unroll
   for (int q = 0; q < 4; ++q)

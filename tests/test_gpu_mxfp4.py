@@ -434,9 +434,47 @@ def test_moe_nan_token_stays_alone():
     assert not torch.isfinite(y[7]).all()
 
 
+@pytest.mark.parametrize("T, I, bad", [(1, 64, float("nan")), (1, 2080, float("inf")), (3, 64, float("nan")),
+                                       (16, 96, float("nan")), (5, 4128, float("-inf"))])
+def test_moe_no_finite_value_of_a_spoilt_token(T, I, bad):
+    a = list(moe_case(T, 128, I, 8, torch.bfloat16, 9))
+    clean = ops.mxfp4_moe(*a, 2)
+    a[0] = a[0].clone()
+    a[0][T // 2, 5] = bad
+    y = ops.mxfp4_moe(*a, 2)
+    keep = [t for t in range(T) if t != T // 2]
+    assert torch.equal(y[keep], clean[keep]) and torch.isfinite(clean).all()
+    assert not torch.isfinite(y[T // 2]).any()
+
+
 # ---------------------------------------------------------------------------
 # Together, on streams and in graphs
 # ---------------------------------------------------------------------------
+
+def test_two_streams_at_once():
+    # calls of each operator on two streams with nothing between them, scratch of their own
+    cases = []
+    for i in range(2):
+        w = weights(1000, 4640, 40 + i)
+        cases.append((activations(90 + 7 * i, 4640, torch.float16, 50 + i), w, activations(700, 4640, torch.float16, 60 + i),
+                      moe_case(30, 512, 256, 12, torch.float16, 70 + i)))
+
+    def run(x, w, z, moe):
+        q = ops.mxfp4_quantize(z)
+        return [ops.mxfp4_gemm(x, *w), ops.mxfp4_gemm(z, *w), ops.mxfp4_gemm_mx(*q, *w, torch.float16), ops.mxfp4_moe(*moe, 3)]
+    want = [run(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, (s, c) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(s):
+                got[i].append(run(*c))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(u, v) for u, v in zip(g, want[i]))
+
 
 def _block(x, w1, w2, moe, k):
     """A decoding step's run of the operators: a projection, one with quantised activations, the experts."""

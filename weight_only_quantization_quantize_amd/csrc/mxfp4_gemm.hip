@@ -166,7 +166,9 @@ struct TileSplit {
   }
 };
 
-// RES > 0: the tile's scale bytes for all of K (at most 128 RES) stay in LDS.
+// RES > 0: the tile's scale bytes for all of K (at most 128 RES) stay in LDS, a dword
+// for a row and 128 of K.
+constexpr int kResident = 28, kResidentAlone = 128;
 template <int PIECES, int TM, int TN, int WN, int KS, int KG, int RES>
 struct Config {
   static constexpr int kWaves = 2 * WN, kThreads = 64 * kWaves * KG;
@@ -177,8 +179,8 @@ struct Config {
   using TW = Tile4<BN, kKS>;
   static constexpr int kStage = TA::kBytes + TW::kBytes + (RES ? 0 : TA::kScaleBytes + TW::kScaleBytes);
   // as many stages as leave room for a second workgroup, or, where that would be
-  // fewer than two, as fill the LDS; at most 4
-  static constexpr int kRoom = (KG * kStage * 2 > 80 * 1024 ? 160 : 80) * 1024;
+  // fewer than two or there is none (kResidentAlone), as fill the LDS; at most 4
+  static constexpr int kRoom = RES >= kResidentAlone ? 160 * 1024 - RES * 4 * (BM + BN) : (KG * kStage * 2 > 80 * 1024 ? 160 : 80) * 1024;
   static constexpr int kFit = kRoom / (KG * kStage);
   static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
   static constexpr int per_wave(int units) { return (units + kWaves - 1) / kWaves; }
@@ -423,8 +425,9 @@ Tile tile_mx(int64_t M, int64_t N) {
 // Small 4-bit tiles keep the scales in LDS where that leaves a second workgroup a
 // compute unit, or none is needed: no pass over them, no workspace.  Whole
 // products, with / without: 333 x 1001 x 5152 9.9 / 11.6 us, 128 x 4096 x 4096 8.2 /
-// 10.2, 512 x 1024 x 1024 4.1 / 6.4, 256 x 8192 x 3584 10.2 / 12.6.
-constexpr int kResident = 28, kResidentAlone = 128;  // dwords a row
+// 10.2, 512 x 1024 x 1024 4.1 / 6.4, 256 x 8192 x 3584 10.2 / 12.6.  Those alone on
+// their compute unit have three stages (64 x 8192 x 8192 14.5 us with two, 12.2 with
+// three, 12.8 with four; 333 x 1001 x 5152 9.8, 10.0, 10.4).
 bool resident(int64_t M, int64_t N, int64_t K) {
   return tile_mx(M, N) == Tile::kSmall && (K <= 128 * kResident || (K <= 128 * kResidentAlone && per_cu(M, N, 64, 64) == 1));
 }
@@ -460,11 +463,11 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
 //                    16384 x 4096 22 / 20, 28672 x 8192 59 / 53, 4096 x 11008 39 / 39
 //          128       2048 x 8192 20 / 31, 4096 x 4096 16 / 19, 6144 x 4096 19 / 19
 //          256       1024 x 8192 23 / 32, 2048 x 2048 12 / 13, 4096 x 4096 22 / 21
-//   4-bit, 32 rows   4096 x 4096 6 / 8, 8192 x 8192 12 / 13, 4096 x 11008 14 / 17,
+//   4-bit, 32 rows   4096 x 4096 6 / 8, 8192 x 8192 12 / 12, 4096 x 11008 14 / 16,
 //                    16384 x 4096 10 / 9, 28672 x 8192 26 / 35
-//          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 13, 8192 x 8192 15 / 14,
+//          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 12, 8192 x 8192 15 / 12,
 //                    4096 x 2048 6 / 5; 28672 x 8192 31 / 38 (scales in a pass)
-//          128       512 x 4096 6 / 7, 2048 x 8192 11 / 12, 4096 x 8192 15 / 13
+//          128       512 x 4096 6 / 7, 2048 x 8192 11 / 12, 4096 x 8192 15 / 12
 //          256       1024 x 8192 10 / 11, 2048 x 2048 7 / 5
 bool skinny(int64_t M, int64_t N, int64_t K) {
   return K >= 128 && (M <= 32 || (K <= 8192 && M <= 512 && M * N <= 1 << 19));

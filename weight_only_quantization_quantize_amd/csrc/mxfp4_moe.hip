@@ -54,7 +54,6 @@ struct Turn {
 };
 struct Plan {
   int turns;
-  int pad[3];
 };
 
 // A logit's order as an unsigned number; the zeros are equal and a NaN comes

@@ -160,8 +160,8 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, void* workspace, hipStream_t stream);
 size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K);
-// The same for a few rows: 16-bit activations split in fragments of 16 rows
-// (M <= 16), microscaled activations (M <= 64).
+// The same for a few rows or small outputs: 16-bit activations split in the kernel
+// (K <= 4096) or before, in fragments of 16 rows; microscaled activations.
 bool mxfp4_skinny_splits(int64_t K);
 hipError_t launch_mxfp4_skinny_raw(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
                                    int64_t K, void* Y, hipStream_t stream);

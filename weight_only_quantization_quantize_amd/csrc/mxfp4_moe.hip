@@ -370,8 +370,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
     asm volatile("" : "+v"(l));  // as above
     // value (row m, tile j, column c) of a wave: part[w][j][(m / 4) 16 + c][m % 4]
     auto sum = [&](int m, int j, int c) {
-      float v = 0.0f;
-      for (int w = 0; w < waves; ++w) v += part[w][j][(m >> 2) * 16 + c][m & 3];
+      float p[WAVES], v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) p[w] = part[w][j][(m >> 2) * 16 + c][m & 3];
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) v += w < waves ? p[w] : 0.0f;
       return v;
     };
     if constexpr (UP) {

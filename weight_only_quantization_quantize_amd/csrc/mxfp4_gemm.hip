@@ -123,15 +123,15 @@ struct Tile4 {
     const uint32_t rows = 256u * (uint32_t)(unit % (ROWS / 64));
     load_lds4(scales + (int64_t)kt * scale_step, rows + 4u * (threadIdx.x & 63), to + 256u * (uint32_t)unit);
   }
-  // lane (row, half) multiplies block 2 s + half of its row's stage
-  __device__ static u32x4_t fragment(const uint8_t* lds, int row, int s, int half) {
-    const int c = (2 * s + half) ^ swizzle(row);
-    return *reinterpret_cast<const u32x4_t*>(lds + row * kRowBytes + c * 16);
+  // lane (row, half) multiplies block 2 s + half of its row's stage; 32 rows on, 32
+  // kRowBytes on
+  __device__ static uint32_t place(int row, int s, int half) {
+    return (uint32_t)(row * kRowBytes + ((2 * s + half) ^ swizzle(row)) * 16);
   }
   // the row's scale dword, shifted so that the instruction's byte select (the same
   // for all lanes) picks step s
-  __device__ static int scale(const uint8_t* lds, int row, int s, int half, int h) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(lds + 4 * (ROWS * (KS == 4 ? s >> 1 : 0) + row));
+  __device__ static int scale(const uint8_t* at, int s, int half, int h) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(at + 4 * ROWS * (KS == 4 ? s >> 1 : 0));
     return (int)(v >> (8 * ((KS == 1 ? 2 * (h & 1) : 0) + half)));
   }
   static constexpr int select(int s) { return KS == 1 ? 0 : 2 * (s & 1); }
@@ -244,6 +244,19 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
     for (int j = 0; j < C::kWScaleLoads; ++j) tw.load_scales(unit(j, TW::kScaleUnits), h, to + kWsAt);
   };
 
+  // where the lane's operands lie in a stage: computed once, so that a stage costs one
+  // addition for each step
+  uint32_t a_at[KS], w_at[KS], as_at = 0, ws_at = kWsAt + 4 * (wn * 32 + r32);
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    w_at[s] = kAt + TW::place((wn * 32) + r32, s, half);
+    a_at[s] = 0;
+    if constexpr (!C::kSplit) a_at[s] = TA::place(wm * 32 + r32, s, half);
+    asm volatile("" : "+v"(w_at[s]), "+v"(a_at[s]));
+  }
+  if constexpr (!C::kSplit) as_at = kAsAt + 4 * (wm * 32 + r32);
+  asm volatile("" : "+v"(as_at), "+v"(ws_at));
+
   float16_t acc[TM][TN] = {};
   for (int st = 0; st + 1 < C::kStages; ++st) issue(h0 + st, st);
   if constexpr (RES > 0) {  // seen by all behind the first turn's barrier
@@ -265,7 +278,6 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
     __builtin_amdgcn_s_barrier();
     issue(h + C::kStages - 1, buf == 0 ? C::kStages - 1 : buf - 1);
     const uint8_t* const la = lds[buf];
-    const uint8_t* const lw = la + kAt;
     buf = buf + 1 == C::kStages ? 0 : buf + 1;
     if (KG > 1 && h >= h1) continue;
     auto multiply = [&](auto sel) {
@@ -274,23 +286,21 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
       int bs[TN];
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const int row = (wn + j) * 32 + r32;
-        bf[j] = mx_operand(TW::fragment(lw, row, s, half));
+        bf[j] = mx_operand(*reinterpret_cast<const u32x4_t*>(la + w_at[s] + j * 32 * TW::kRowBytes));
         if constexpr (RES > 0)
-          bs[j] = (int)(w_scales[2 * h + (s >> 1)][row] >> (8 * half));
+          bs[j] = (int)(w_scales[2 * h + (s >> 1)][(wn + j) * 32 + r32] >> (8 * half));
         else
-          bs[j] = TW::scale(la + kWsAt, row, s, half, h);
+          bs[j] = TW::scale(la + ws_at + 128 * j, s, half, h);
       }
       if constexpr (!C::kSplit) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const int row = (wm + i) * 32 + r32;
-          const i32x8_t v = mx_operand(TA::fragment(la, row, s, half));
+          const i32x8_t v = mx_operand(*reinterpret_cast<const u32x4_t*>(la + a_at[s] + i * 32 * TA::kRowBytes));
           int as;
           if constexpr (RES > 0)
-            as = (int)(a_scales[2 * h + (s >> 1)][row] >> (8 * half));
+            as = (int)(a_scales[2 * h + (s >> 1)][(wm + i) * 32 + r32] >> (8 * half));
           else
-            as = TA::scale(la + kAsAt, row, s, half, h);
+            as = TA::scale(la + as_at + 128 * i, s, half, h);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], v, acc[i][j], kMfmaFp4, kMfmaFp4,

@@ -162,8 +162,9 @@ __device__ inline void mx_store_pieces(const MxPieces& s, uint8_t* __restrict__ 
   fscale[lane] = s.scale;
 }
 
-// Scale bytes 16 g .. 16 g + 15 of a row of nblk, 0 past its end: whatever codes
-// stand there, times 2^-254 they are below fp32's smallest number.
+// Scale bytes 16 g .. 16 g + 15 of a row of nblk, 0 past its end (whatever codes
+// stand there, times 2^-254 they are below fp32's smallest number), in each dword in
+// the order 0, 2, 1, 3.
 __device__ inline u32x4_t mx_scale_chunk(const uint8_t* __restrict__ row, int g, int nblk) {
   u32x4_t v = {0u, 0u, 0u, 0u};
   const uint8_t* const p = row + 16 * g;
@@ -174,6 +175,8 @@ __device__ inline u32x4_t mx_scale_chunk(const uint8_t* __restrict__ row, int g,
     for (int q = 0; q < 16; ++q)
       if (16 * g + q < nblk) v[q / 4] |= (uint32_t)p[q] << (8 * (q % 4));
   }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = __builtin_amdgcn_perm(v[q], v[q], 0x03010200u);
   return v;
 }
 

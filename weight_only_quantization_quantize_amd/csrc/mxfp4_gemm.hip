@@ -14,12 +14,12 @@
 // the shorter side; two workgroups of that tile share a compute unit, which hides
 // the one's barriers, prologue and stores behind the other's instructions).
 // Below that the number of stages in flight counts: small tiles, K split.
-// 2048 x 11008 x 4096 takes 145 us with split activations (3 x 185 G flop, 3.8 P
+// 2048 x 11008 x 4096 takes 142 us with split activations (3 x 185 G flop, 3.9 P
 // flop/s as the matrix unit counts them, of the 6.3 P that it reaches on registers
-// alone) and 59 us with 4-bit ones (3.1 of 6.7).  There the vector instructions beside
-// the matrix ones count (LDS is busy for 28% of the time): masks of the last blocks
-// and a shift for every scale, 90 instructions for 16 matrix instructions in place of
-// 44, took 63.
+// alone) and 56 us with 4-bit ones (3.3 of 6.7).  There the vector instructions beside
+// the matrix ones count (LDS is busy for 28% of the time): masks of the last blocks,
+// a shift for every scale and addresses from their parts, 90 instructions for 16
+// matrix instructions in place of 20, took 63.
 //
 // Pipeline.  K goes in stages of 64 KS, kStages of them in LDS, filled by direct
 // loads (global_load_lds: no registers, no instructions to write LDS).  At the top
@@ -58,7 +58,6 @@
 namespace woq {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kXcds = 8;
 constexpr int kGroup = 8;  // M tiles of a group
 
@@ -128,13 +127,15 @@ struct Tile4 {
   __device__ static uint32_t place(int row, int s, int half) {
     return (uint32_t)(row * kRowBytes + ((2 * s + half) ^ swizzle(row)) * 16);
   }
-  // the row's scale dword, shifted so that the instruction's byte select (the same
-  // for all lanes) picks step s
-  __device__ static int scale(const uint8_t* at, int s, int half, int h) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(at + 4 * ROWS * (KS == 4 ? s >> 1 : 0));
-    return (int)(v >> (8 * ((KS == 1 ? 2 * (h & 1) : 0) + half)));
+  // Step s's scale.  A row's dword holds blocks 0, 2, 1, 3 of its 128 K: the lane
+  // reads its half's two (at: 2 half into the row's place), and the instruction's
+  // byte select, the same for all lanes, picks the step; one byte where a stage has
+  // one step.
+  __device__ static int scale(const uint8_t* at, int s, int h) {
+    if constexpr (KS == 1) return (int)at[h & 1];
+    return (int)*reinterpret_cast<const uint16_t*>(at + 4 * ROWS * (KS == 4 ? s >> 1 : 0));
   }
-  static constexpr int select(int s) { return KS == 1 ? 0 : 2 * (s & 1); }
+  static constexpr int select(int s) { return KS == 1 ? 0 : s & 1; }
 };
 
 // Split activations: stages of KS fragments (64 of K each) of each 32 rows.
@@ -246,7 +247,7 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
 
   // where the lane's operands lie in a stage: computed once, so that a stage costs one
   // addition for each step
-  uint32_t a_at[KS], w_at[KS], as_at = 0, ws_at = kWsAt + 4 * (wn * 32 + r32);
+  uint32_t a_at[KS], w_at[KS], as_at = 0, ws_at = kWsAt + 4 * (wn * 32 + r32) + 2 * half;
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     w_at[s] = kAt + TW::place((wn * 32) + r32, s, half);
@@ -254,7 +255,7 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
     if constexpr (!C::kSplit) a_at[s] = TA::place(wm * 32 + r32, s, half);
     asm volatile("" : "+v"(w_at[s]), "+v"(a_at[s]));
   }
-  if constexpr (!C::kSplit) as_at = kAsAt + 4 * (wm * 32 + r32);
+  if constexpr (!C::kSplit) as_at = kAsAt + 4 * (wm * 32 + r32) + 2 * half;
   asm volatile("" : "+v"(as_at), "+v"(ws_at));
 
   float16_t acc[TM][TN] = {};
@@ -288,9 +289,9 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
       for (int j = 0; j < TN; ++j) {
         bf[j] = mx_operand(*reinterpret_cast<const u32x4_t*>(la + w_at[s] + j * 32 * TW::kRowBytes));
         if constexpr (RES > 0)
-          bs[j] = (int)(w_scales[2 * h + (s >> 1)][(wn + j) * 32 + r32] >> (8 * half));
+          bs[j] = (int)reinterpret_cast<const uint16_t*>(&w_scales[2 * h + (s >> 1)][(wn + j) * 32 + r32])[half];
         else
-          bs[j] = TW::scale(la + ws_at + 128 * j, s, half, h);
+          bs[j] = TW::scale(la + ws_at + 128 * j, s, h);
       }
       if constexpr (!C::kSplit) {
 #pragma unroll
@@ -298,9 +299,9 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
           const i32x8_t v = mx_operand(*reinterpret_cast<const u32x4_t*>(la + a_at[s] + i * 32 * TA::kRowBytes));
           int as;
           if constexpr (RES > 0)
-            as = (int)(a_scales[2 * h + (s >> 1)][(wm + i) * 32 + r32] >> (8 * half));
+            as = (int)reinterpret_cast<const uint16_t*>(&a_scales[2 * h + (s >> 1)][(wm + i) * 32 + r32])[half];
           else
-            as = TA::scale(la + as_at + 128 * i, s, half, h);
+            as = TA::scale(la + as_at + 128 * i, s, h);
 #pragma unroll
           for (int j = 0; j < TN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], v, acc[i][j], kMfmaFp4, kMfmaFp4,

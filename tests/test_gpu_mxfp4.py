@@ -411,6 +411,17 @@ def test_moe_ties_take_the_lower_index():
     close(ops.mxfp4_moe(*a, k), y_ref, moe_bound(X, up, down, ids, X @ R.T), torch.float16, "moe ties")
 
 
+@pytest.mark.parametrize("T, E", [(1, 28), (6, 28), (41, 21), (64, 28), (9, 56), (1, 140), (33, 140)])
+def test_moe_ties_at_every_way_of_choosing(T, E):
+    H, I, k = 96, 64, 3
+    a = list(moe_case(T, H, I, E, torch.float16, 6))
+    a[1] = a[1][:7].repeat(E // 7, 1).contiguous()  # experts 7 apart are equal
+    X, R, up, down = host(a[0]), host(a[1]), values(a[2], a[3]), values(a[4], a[5])
+    y_ref, ids = O.moe(X, R, up, down, k)
+    assert (ids == ids[:, :1] + 7 * np.arange(3)).all() and ids.max() < 21
+    close(ops.mxfp4_moe(*a, k), y_ref, moe_bound(X, up, down, ids, X @ R.T), torch.float16, f"moe ties {T} {E}")
+
+
 def test_moe_same_bits_twice_and_on_another_stream():
     a = moe_case(40, 256, 160, 24, torch.bfloat16, 8)
     first = ops.mxfp4_moe(*a, 4)

@@ -23,8 +23,8 @@
 // A small layer of few tokens has no combine: its down adds over the experts itself.
 // One token needs no list either: up and down work the choices out from the logits.
 //
-// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 105 us, of which up 63
-// (285 MB of weights, 4.5 TB/s) and down 31 (142 MB, 4.6 TB/s); one token 24 us,
+// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 99 us, of which up 62
+// (285 MB of weights, 4.6 TB/s) and down 30 (142 MB, 4.7 TB/s); one token 23 us,
 // up 13, down 8.5, logits 5.  A workgroup per 32 columns and turn (up) and per 16
 // columns of y over all turns (down) took 86 and 51: they read the activations again
 // for every 64 (16) weight rows, and a workgroup's first loads had nothing before
@@ -169,6 +169,39 @@ __device__ inline Choice choose(const float (&logit)[NJ], int E, int top_k, int 
   const float w = lane < top_k ? expf(key_value(chosen) - key_value(first)) : 0.0f;
   return Choice{expert, w / team_sum(w, 64)};
 }
+// The same for two tokens of up to 32 experts, one in each half of the wave: lane
+// holds the logit of expert lane % 32, and gets choice lane % 32.
+__device__ inline Choice choose_pair(float logit, int E, int top_k, int lane) {
+  const int l = lane & 31;
+  const bool upper = lane >= 32;
+  const uint32_t key = l < E ? order_key(logit) : 0u;
+  bool taken = l >= E;
+  int expert = 0;
+  uint32_t chosen = 0, first = 0;
+  for (int c = 0; c < top_k; ++c) {
+    uint32_t v = taken ? 0u : key;
+    auto step = [&](auto ctrl, auto rows) {
+      const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+      v = v > o ? v : o;
+    };
+    step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});  // row_shr 1, 2, 4, 8
+    step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
+    step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
+    step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row_bcast 15: lanes 31 and 63
+    const uint32_t m0 = (uint32_t)__builtin_amdgcn_readlane((int)v, 31), m1 = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    const uint32_t m = upper ? m1 : m0;
+    const uint64_t b = __ballot(!taken && key == m);
+    const int i0 = __builtin_ctz((uint32_t)b), i1 = __builtin_ctz((uint32_t)(b >> 32));  // the lowest index of that key
+    const int id = upper ? i1 : i0;
+    taken |= l == id;
+    first = c == 0 ? m : first;
+    expert = l == c ? id : expert;
+    chosen = l == c ? m : chosen;
+  }
+  const float w = l < top_k ? expf(key_value(chosen) - key_value(first)) : 0.0f;
+  return Choice{expert, w / team_sum(w, 32)};
+}
 template <int NJ>
 __device__ inline void load_logits(float (&logit)[NJ], const float* __restrict__ logits, int E, int lane) {
 #pragma unroll
@@ -177,7 +210,7 @@ __device__ inline void load_logits(float (&logit)[NJ], const float* __restrict__
 
 // One workgroup.  logits [T][E] -> the plan, its turns, and the row of the turns'
 // products for each token's choices.
-// NJ: lanes' experts, 64 NJ >= E.
+// NJ: lanes' experts, 64 NJ >= E; 0: two tokens a wave, E <= 32.
 template <int NJ>
 __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const float* __restrict__ logits, int T, int E,
                                                                        int top_k, Plan* __restrict__ plan,
@@ -191,22 +224,39 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const flo
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int e = threadIdx.x; e < E; e += kChooseWaves * 64) tokens[e] = 0;
   __syncthreads();
+  auto note = [&](int t, int c, const Choice& choice) {
+    ids[t * top_k + c] = (uint16_t)choice.expert;
+    shares[t * top_k + c] = choice.share;
+    atomicOr(&tokens[choice.expert], 1ull << t);
+  };
   constexpr int kTokens = kMaxTokens / kChooseWaves;  // of a wave, at most
-  float logit[kTokens][NJ];
+  if constexpr (NJ == 0) {
+    float logit[kTokens / 2];
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
-    const int t = wave + kChooseWaves * i;
-    load_logits(logit[i], logits + (int64_t)(t < T ? t : 0) * E, E, lane);
-  }
+    for (int i = 0; i < kTokens / 2; ++i) {
+      const int t = 2 * (wave + kChooseWaves * i) + (lane >> 5);
+      logit[i] = t < T && (lane & 31) < E ? logits[t * E + (lane & 31)] : 0.0f;
+    }
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
-    const int t = wave + kChooseWaves * i;
-    if (t >= T) break;
-    const Choice c = choose(logit[i], E, top_k, lane);
-    if (lane < top_k) {
-      ids[t * top_k + lane] = (uint16_t)c.expert;
-      shares[t * top_k + lane] = c.share;
-      atomicOr(&tokens[c.expert], 1ull << t);
+    for (int i = 0; i < kTokens / 2; ++i) {
+      const int t = 2 * (wave + kChooseWaves * i);
+      if (t >= T) break;
+      const Choice c = choose_pair(logit[i], E, top_k, lane);
+      if (t + (lane >> 5) < T && (lane & 31) < top_k) note(t + (lane >> 5), lane & 31, c);
+    }
+  } else {
+    float logit[kTokens][NJ];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const int t = wave + kChooseWaves * i;
+      load_logits(logit[i], logits + (int64_t)(t < T ? t : 0) * E, E, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const int t = wave + kChooseWaves * i;
+      if (t >= T) break;
+      const Choice c = choose(logit[i], E, top_k, lane);
+      if (lane < top_k) note(t, lane, c);
     }
   }
   __syncthreads();
@@ -555,7 +605,8 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
   if (e != hipSuccess) return e;
   constexpr int kLarge = kMaxExperts / 64;
   if (T > 1) {
-    auto* const f = E <= 64 ? moe_choose_kernel<1> : moe_choose_kernel<kLarge>;
+    // (64 tokens of 32 experts, four each: 5.2 us two to a wave, 8.0 one by one)
+    auto* const f = E <= 32 ? moe_choose_kernel<0> : (E <= 64 ? moe_choose_kernel<1> : moe_choose_kernel<kLarge>);
     f<<<1, kChooseWaves * 64, 0, stream>>>(logits, T, E, top_k, plan, turns, where);
     e = hipGetLastError();
     if (e != hipSuccess) return e;

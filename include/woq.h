@@ -315,10 +315,8 @@ woq_status woq_mxfp4_dequantize(const void* codes, const void* scales, int64_t M
                                 void* out, void* stream);
 
 /* Y[m, n] = sum_k X[m, k] w[n, k] for microscaled weights w [N, K] and 16-bit
- * X [M, K]; Y [M, N] of X's type, fp32 sums, rounded once.  M = 1 with
- * K <= 16384 uses X as given.  Otherwise X is split, 32 elements at a time,
- * into three 6-bit floats that hold each element to within 2^-13.9 of its
- * block's largest magnitude (and 2^-126 where the block is below 2^-112).
+ * X [M, K], both used as given; exact products, fp32 sums, Y [M, N] of X's
+ * type, rounded once.
  *   workspace : device scratch of woq_mxfp4_gemm_workspace_bytes(M, N, K)
  *               bytes, 256-byte aligned (NULL where that is 0; it is 0 for
  *               invalid sizes too). */
@@ -345,9 +343,10 @@ woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const vo
  *   X [T, H], router [E, H], Y [T, H] of xdtype; up microscaled [E, 2 I, H]
  *   (rows 0 .. I-1 gate, I .. 2I-1 up), down microscaled [E, H, I]; H and I
  *   multiples of 32.
- * X and p h are split into 6-bit pieces as in woq_mxfp4_gemm; sums over k and
- * i, and the sum over experts, are fp32, Y is rounded once.  No atomics: the
- * same inputs give the same bits.  workspace as above. */
+ * X is used as given; p h, computed in fp32, is held as the sum of two bf16
+ * numbers, to within 2^-18 of each element; sums over k and i, and the sum
+ * over experts, are fp32, Y is rounded once.  No atomics on values: the same
+ * inputs give the same bits.  workspace as above. */
 size_t woq_mxfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k);
 woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, const void* up_codes,
                          const void* up_scales, const void* down_codes, const void* down_scales, int64_t T, int64_t H,

@@ -1,0 +1,198 @@
+"""GPU tests that the products use 16-bit activations as given: no element loses
+bits to a larger one beside it, what is not finite gives what the definition
+gives, and every scale byte is exact, however many rows there are.
+
+Tolerances.  Operands and products are exact.  fp32 sums: each matrix step (16 or
+more products) may lose a unit in the last place of the running magnitude, at
+most 2^-23 sum |x w|, over K / 16 steps and a sum over at most 16 waves; the
+one-row kernel rounds as often.  The result is rounded once: off by at most half
+a step of its type, 2^-11 or 2^-8 of the value (and 2^-25 or 2^-134 below the
+normal numbers).  Over many outputs the root mean square of that rounding is at
+most 2^-11 / sqrt(3) of the outputs' (an error uniform over a step), so relative
+L2 may be 0.6 of 2^-11 and what the sums add, under 1e-5 here.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4_oracle as O
+from weight_only_quantization_quantize_amd import ops
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = [torch.float16, torch.bfloat16]
+HALF = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+# rows x columns x K of every way to a product: one row (short, long), streamed rows
+# (one and two super-steps a wave, several tiles a team, long rows), small and large tiles
+PATHS = [(1, 300, 1056), (1, 70, 16416), (2, 48, 128), (5, 300, 4064), (16, 12400, 1056), (20, 300, 8192),
+         (9, 9000, 4640), (9, 70, 8736), (33, 129, 352), (3, 40, 96), (80, 70, 64), (100, 1100, 992),
+         (300, 2500, 608), (600, 3000, 352), (1100, 7200, 96)]
+
+
+def host(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def random_weights(N, K, seed, low=114, high=124):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8),
+            torch.randint(low, high, (N, K // 32), generator=g, dtype=torch.uint8))
+
+
+def values(codes, scales):
+    return O.dequantize(codes.cpu().numpy(), scales.cpu().numpy())
+
+
+def product(x, codes, scales):
+    y = ops.mxfp4_gemm(x.to(DEV), codes.to(DEV), scales.to(DEV))
+    torch.cuda.synchronize()
+    return y
+
+
+def close(y, X, W, dtype, label):
+    ref, K = X @ W.T, X.shape[1]
+    got = host(y)
+    acc = (K / 16 + 16) * 2.0 ** -23 * (np.abs(X) @ np.abs(W).T) * 1.01
+    bound = (1 + HALF[dtype]) * acc + HALF[dtype] * np.abs(ref) + TINY[dtype]
+    r = np.abs(got - ref) / bound
+    i = np.unravel_index(int(np.argmax(np.where(np.isnan(r), np.inf, r))), r.shape)
+    print(f"{label}: worst element {r[i]:.3f} of its bound", flush=True)
+    assert r[i] <= 1.0, (label, i, got[i], ref[i])
+    return got, ref
+
+
+def relative(got, ref, rows=slice(None), cols=slice(None)):
+    return np.linalg.norm((got - ref)[rows, cols]) / np.linalg.norm(ref[rows, cols])
+
+
+@pytest.mark.parametrize("M, N, K", PATHS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_massive_channel_leaves_its_neighbours_alone(M, N, K, dtype):
+    g = torch.Generator().manual_seed(M + N + K)
+    x = torch.randn(M, K, generator=g)
+    x[:, 13] = 20000.0
+    x = x.to(dtype)
+    codes, scales = random_weights(N, K, K)
+    codes[::2, 6] &= 0x0F  # every other row has no weight for channel 13: code 0, a zero
+    X, W = host(x), values(codes, scales)
+    assert (W[::2, 13] == 0).all()
+    got, ref = close(product(x, codes, scales), X, W, dtype, f"massive {M} {N} {K} {dtype}")
+    e = relative(got, ref, cols=slice(None, None, 2))
+    print(f"rel_l2 of the rows without it {e:.2e}", flush=True)
+    if M * N >= 2000:  # enough outputs for their mean
+        assert e <= 0.6 * HALF[dtype] + 1e-5
+
+
+@pytest.mark.parametrize("M, N, K", PATHS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_small_elements_beside_large_ones(M, N, K, dtype):
+    # each row one-hot but for a larger element whose weights are zeros: a product's bits
+    # are those of x w, at every distance of the two
+    codes, scales = random_weights(N, K, 5, 118, 121)
+    codes[:, 0] &= 0xF0  # channel 0: zeros
+    x = torch.zeros(M, K)
+    small = torch.linspace(-14, 9, M) if dtype == torch.float16 else torch.linspace(-100, 90, M)
+    at = torch.arange(M) % (K - 1) + 1
+    x[torch.arange(M), at] = 1.2345 * torch.exp2(small.floor())
+    x[:, 0] = 30000.0 if dtype == torch.float16 else 2.0 ** 100
+    x = x.to(dtype)
+    W = torch.from_numpy(values(codes, scales))
+    want = (x[torch.arange(M), at].double()[:, None] * W.t()[at]).to(dtype)
+    assert torch.equal(product(x, codes, scales).cpu(), want)
+
+
+@pytest.mark.parametrize("M, N, K", PATHS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_infinities_and_nans_as_defined(M, N, K, dtype):
+    g = torch.Generator().manual_seed(M * N + K)
+    x = torch.randn(M, K, generator=g)
+    x[0, K - 1] = float("inf")
+    x[M // 2, 3] = float("-inf")
+    x[M - 1, K // 2] = float("inf")
+    if M > 2:
+        x[1, 5] = float("nan")
+    x = x.to(dtype)
+    codes, scales = random_weights(N, K, 7)
+    with np.errstate(invalid="ignore"):
+        ref = (host(x)[:, None, :] * values(codes, scales)[None, :64, :]).sum(-1) if M <= 64 else None
+        if ref is None:
+            ref = np.stack([(r * values(codes, scales)[:64]).sum(-1) for r in host(x)])
+    got = host(product(x, codes, scales))[:, :64]
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(np.where(np.isinf(ref), ref, 0.0), np.where(np.isinf(got), got, 0.0))
+
+
+@pytest.mark.parametrize("M, N, K", [p for p in PATHS if p[1] >= 255 or p[0] <= 3])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_every_scale_byte_is_exact(M, N, K, dtype):
+    # one-hot rows pick single weights at every scale byte; a power of two brings them into
+    # the type's range (and out of it at both ends: infinities, subnormal numbers, zeros)
+    codes, _ = random_weights(N, K, 11)
+    blocks = torch.arange(N)[:, None] * 7 + torch.arange(K // 32)[None, :] * 3
+    scales = (blocks % 255).to(torch.uint8)
+    powers = torch.tensor([-24, -14, 0, 15] if dtype == torch.float16 else [-133, -120, -64, 0, 64, 127])
+    x = torch.zeros(M, K, dtype=torch.float64)
+    at = (torch.arange(M) * 37 + 11) % K
+    x[torch.arange(M), at] = torch.exp2(powers[torch.arange(M) % len(powers)].double())
+    x = x.to(dtype)
+    W = torch.from_numpy(values(codes, scales))
+    want = (x[torch.arange(M), at].double()[:, None] * W.t()[at]).to(torch.float32).to(dtype)
+    got = product(x, codes, scales).cpu()
+    assert torch.equal(got.float(), want.float())
+
+
+@pytest.mark.parametrize("M, N, K", PATHS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scale_bytes_of_the_whole_range_together(M, N, K, dtype):
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn(M, K, generator=g) * (2.0 ** -14 if dtype == torch.float16 else 2.0 ** -60)).to(dtype)
+    codes, scales = random_weights(N, K, 2, 0, 136 if dtype == torch.float16 else 180)
+    close(product(x, codes, scales), host(x), values(codes, scales), dtype, f"whole range {M} {N} {K}")
+    if dtype == torch.bfloat16:  # weights of 2^128 and more, sums that cancel
+        x = (torch.randn(M, K, generator=g) * 2.0 ** -100).to(dtype)
+        codes, scales = random_weights(N, K, 2, 250, 255)
+        close(product(x, codes, scales), host(x), values(codes, scales), dtype, f"largest scales {M} {N} {K}")
+
+
+def test_nan_blocks_beside_the_lowest_and_highest_scales():
+    for M, N, K in ((2, 40, 256), (40, 40, 96), (300, 400, 160), (9, 40, 8736)):
+        for dtype in TYPES:
+            codes, scales = random_weights(N, K, 4)
+            scales[3, 1], scales[4, 0], scales[5, 1], scales[6, 0] = 255, 0, 1, 254
+            codes[5, 16:32] = 0  # zeros at the scale byte 1
+            y = host(product(torch.full((M, K), 2.0 ** -10, dtype=dtype), codes, scales))
+            assert np.isnan(y[:, 3]).all() and not np.isnan(np.delete(y, 3, 1)).any()
+
+
+def layer(T, H, I, E, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    router = (torch.randn(E, H, generator=g) * (1.5 / H ** 0.5)).to(dtype)
+    up, ups = random_weights(E * 2 * I, H, seed + 2, 118, 121)
+    down, downs = random_weights(E * H, I, seed + 3, 118, 121)
+    return [router, up.view(E, 2 * I, -1), ups.view(E, 2 * I, -1), down.view(E, H, -1), downs.view(E, H, -1)]
+
+
+@pytest.mark.parametrize("T, H, I, E, k", [(1, 608, 160, 6, 2), (1, 2080, 1056, 70, 4), (3, 512, 512, 8, 2), (12, 256, 96, 2, 2),
+                                           (40, 512, 224, 4, 2), (64, 1056, 544, 9, 3)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_with_massive_channels(T, H, I, E, k, dtype):
+    # a channel of x and a column of h far above the others, with no weight for most outputs
+    a = layer(T, H, I, E, dtype, T + H)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g)
+    x[:, 13] = 2000.0
+    a[0][:, 13] = 0  # the router does not look at it
+    a[1][:, :, 6] &= 0x0F          # nor gate and up,
+    a[1][:, 5, 6] |= 0x20          # but for gate row 5 (weight 1 at its scale: silu is its value)
+    a[3][:, 1:, 2] &= 0x0F         # down sees column 5 of h in row 0 only
+    x = x.to(dtype)
+    X, R = host(x), host(a[0])
+    up, down = values(*a[1:3]), values(*a[3:5])
+    ref, ids = O.moe(X, R, up, down, k)
+    got = host(ops.mxfp4_moe(x.to(DEV), *[t.to(DEV) for t in a], k))
+    e = relative(got, ref, cols=slice(1, None))
+    print(f"layer {T} {H} {I} {E} {k} {dtype}: rel_l2 {e:.2e}", flush=True)
+    # h is held to 2^-18 of itself, silu and the shares to a few units of 2^-22
+    assert e <= 0.6 * HALF[dtype] + 5e-5

@@ -1,25 +1,24 @@
 // Matrix products with a microscaled 4-bit right operand W [N, K]:
-//   PIECES = 1: a microscaled 4-bit left operand A [M, K], both as stored;
-//   PIECES = 3: 16-bit activations split into three 6-bit pieces
-//               (mxfp4_split_kernel; mxfp4_device.h says why).
-// Y[m, n] = sum over the 32-element blocks b of 2^(sA + sW - 254) sum_k a w,
-// all of it inside v_mfma_scale_f32_32x32x64_f8f6f4: no element is decoded,
-// the products are exact and the sums are the matrix unit's fp32.
+//   Mx         a microscaled 4-bit left operand A [M, K], both as stored, inside
+//              v_mfma_scale_f32_32x32x64_f8f6f4: no element is decoded;
+//   F16, BF16  16-bit activations, by weights widened to their type in registers on
+//              v_mfma_f32_32x32x16 (mxfp4_device.h).
+// Y[m, n] = sum over the 32-element blocks b of 2^(sA + sW - 254) sum_k a w: the
+// products are exact and the sums are the matrix unit's fp32.
 //
 // Tile.  A group of 2 x WN waves computes 64 TM x 32 WN TN of Y, a wave 32 TM x
 // 32 TN; KG groups of a workgroup share a tile's K and add their sums through
 // LDS at the end.  `launch` chooses: where there is work for all compute units
-// the matrix instructions bound the product and the largest tile wins (with three
-// pieces A is the heavier operand, 2.25 bytes an element against 17 / 32, and gets
-// the shorter side; two workgroups of that tile share a compute unit, which hides
-// the one's barriers, prologue and stores behind the other's instructions).
+// the matrix instructions bound the product and the largest tile wins (16-bit A is
+// the heavier operand, 2 bytes an element against 17 / 32, and gets the shorter side;
+// two workgroups of that tile share a compute unit, which hides the one's barriers,
+// prologue and stores behind the other's instructions).
 // Below that the number of stages in flight counts: small tiles, K split.
-// 2048 x 11008 x 4096 takes 142 us with split activations (3 x 185 G flop, 3.9 P
-// flop/s as the matrix unit counts them, of the 6.3 P that it reaches on registers
-// alone) and 56 us with 4-bit ones (3.3 of 6.7).  There the vector instructions beside
-// the matrix ones count (LDS is busy for 28% of the time): masks of the last blocks,
-// a shift for every scale and addresses from their parts, 90 instructions for 16
-// matrix instructions in place of 20, took 63.
+// 2048 x 11008 x 4096 takes 165 .. 172 us with 16-bit activations (1.1 P flop/s; a
+// library product of 16-bit matrices reaches 1.16 P) and 57 us with 4-bit ones (3.2 P of
+// the 6.7 P that the matrix unit reaches on registers alone).  For 4-bit operands the vector instructions beside the matrix ones count (LDS is busy
+// for 28% of the time): masks of the last blocks, a shift for every scale and addresses
+// from their parts, 90 instructions for 16 matrix instructions in place of 20, took 63.
 //
 // Pipeline.  K goes in stages of 64 KS, kStages of them in LDS, filled by direct
 // loads (global_load_lds: no registers, no instructions to write LDS).  At the top
@@ -30,17 +29,17 @@
 // compiler would wait for all of them before every read of LDS; their counter is
 // waited for by hand, and there is no other vector memory access inside the loop.
 // Longer stages mean fewer barriers: 256 of K for 4-bit operands and K split
-// between two groups of waves took 333 x 1001 x 5152 from 15 to 9 us; the large
-// three-piece tile keeps 64, which leave it two workgroups a compute unit (2048 x
-// 11008 x 4096: 154 us against 169 with 128).
+// between two groups of waves took 333 x 1001 x 5152 from 15 to 10 us; the large
+// tile of 16-bit ones keeps 64, which leave it two workgroups a compute unit (2048 x
+// 11008 x 4096: 177 us with the pass before it, 188 with 128; 184 with 256 x 128 tiles).
 //
 // Scales.  The 4-bit operands' scale bytes lie K / 32 bytes apart from row to row
 // at any alignment, which direct loads cannot gather; turn_scales
-// (mxfp4_quantize.hip; in the split's launch where there is one) makes them one
-// dword per row and 128 of K, rows contiguous.  Small tiles of two 4-bit operands do
+// (mxfp4_quantize.hip; 16-bit activations: in the launch that lays these out) makes
+// them one dword per row and 128 of K, rows contiguous.  Small tiles of two 4-bit operands do
 // that themselves, into LDS, once for all of K.  Past a row's end stands its last
 // block again, with scale byte 0: the product of two such blocks is below fp32's
-// smallest number (and split activations are zeros there), so no operand is masked.
+// smallest number (and 16-bit activations are zeros there), so no operand is masked.
 //
 // LDS layout of a 4-bit operand: a row's 32 KS bytes of a stage are chunks of
 // one block each, chunk c at position c ^ swizzle(row), so that 16 rows read at
@@ -48,8 +47,9 @@
 //
 // Tile order.  Workgroup b runs on XCD b % 8; each XCD takes one contiguous run of
 // tiles, in groups of 8 M tiles, M fastest, so that the tiles in flight there (32 or
-// 64) share about as much of A as of W in its L2.  All M tiles in one group took
-// 150 us in place of 145 for 2048 x 11008 x 4096 in three pieces.
+// 64) share about as much of A as of W in its L2.  All M tiles in one group take 67 us
+// in place of 64 .. 66 for 2048 x 11008 x 4096 of 4-bit operands, and the same 177 with
+// 16-bit activations.
 #include <type_traits>
 
 #include "mxfp4_device.h"
@@ -138,45 +138,40 @@ struct Tile4 {
   static constexpr int select(int s) { return KS == 1 ? 0 : s & 1; }
 };
 
-// Split activations: stages of KS fragments (64 of K each) of each 32 rows.
+// 16-bit activations: stages of KS fragments (64 of K each) of each 32 rows.
 template <int ROWS, int KS>
-struct TileSplit {
+struct TileRows {
   static constexpr int kBytes = ROWS / 32 * KS * kMxFragBytes;
   static constexpr int kUnits = kBytes / 1024;
-  static constexpr int kScaleUnits = ROWS / 32 * KS;
-  static constexpr int kScaleBytes = ROWS * 8 * KS;
-  static_assert(kBytes % 1024 == 0, "whole loads");
-  const uint8_t* pieces;
-  const uint8_t* scales;
+  static constexpr int kScaleUnits = 0, kScaleBytes = 0;
+  const uint8_t* frags;
   uint32_t ksteps;
 
-  __device__ void start(const uint8_t* pieces_, const uint8_t* scales_, int row0, int, int, int, int ksteps_) {
+  __device__ void start(const uint8_t* frags_, const uint8_t*, int row0, int, int, int, int ksteps_) {
     ksteps = (uint32_t)ksteps_;
-    pieces = pieces_ + (int64_t)(row0 / 32) * ksteps * kMxFragBytes;
-    scales = scales_ + (int64_t)(row0 / 32) * ksteps * kMxFragScaleBytes;
+    frags = frags_ + (int64_t)(row0 / 32) * ksteps * kMxFragBytes;
   }
   __device__ void load(int unit, int h, uint32_t to) const {
-    const uint32_t o = 1024u * (uint32_t)unit + 16u * (threadIdx.x & 63);
-    const uint32_t rg = o / (KS * kMxFragBytes), in = o % (KS * kMxFragBytes);
-    load_lds16(pieces + (int64_t)h * KS * kMxFragBytes, rg * ksteps * kMxFragBytes + in, to + 1024u * (uint32_t)unit);
+    constexpr uint32_t kUnitsOf = KS * kMxFragBytes / 1024;  // of 32 rows
+    const uint32_t rg = (uint32_t)unit / kUnitsOf, in = (uint32_t)unit % kUnitsOf;
+    load_lds16(frags + (int64_t)h * KS * kMxFragBytes, rg * ksteps * kMxFragBytes + 1024u * in + 16u * (threadIdx.x & 63),
+               to + 1024u * (uint32_t)unit);
   }
-  __device__ void load_scales(int unit, int h, uint32_t to) const {
-    const uint32_t rg = (uint32_t)unit / KS, in = (uint32_t)unit % KS;
-    load_lds4(scales + ((int64_t)h * KS + in) * kMxFragScaleBytes, rg * ksteps * kMxFragScaleBytes + 4u * (threadIdx.x & 63),
-              to + 256u * (uint32_t)unit);
-  }
+  __device__ void load_scales(int, int, uint32_t) const {}
 };
 
 // RES > 0: the tile's scale bytes for all of K (at most 128 RES) stay in LDS, a dword
 // for a row and 128 of K.
 constexpr int kResident = 28, kResidentAlone = 128;
-template <int PIECES, int TM, int TN, int WN, int KS, int KG, int RES>
+// XT: the activations' 16-bit type, or Mx.
+struct Mx {};
+template <class XT, int TM, int TN, int WN, int KS, int KG, int RES>
 struct Config {
   static constexpr int kWaves = 2 * WN, kThreads = 64 * kWaves * KG;
-  static constexpr bool kSplit = PIECES == kMxPieces;
+  static constexpr bool kRows = !std::is_same_v<XT, Mx>;
   static constexpr int kKS = KS;
   static constexpr int BM = 64 * TM, BN = 32 * WN * TN;
-  using TA = std::conditional_t<kSplit, TileSplit<BM, KS>, Tile4<BM, KS>>;
+  using TA = std::conditional_t<kRows, TileRows<BM, KS>, Tile4<BM, KS>>;
   using TW = Tile4<BN, kKS>;
   static constexpr int kStage = TA::kBytes + TW::kBytes + (RES ? 0 : TA::kScaleBytes + TW::kScaleBytes);
   // as many stages as leave room for a second workgroup, or, where that would be
@@ -190,14 +185,14 @@ struct Config {
   static constexpr int kLoads = kALoads + kWLoads + kAScaleLoads + kWScaleLoads;
 };
 
-template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG, int RES>
-__global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads), 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
+template <class YT, class XT, int TM, int TN, int WN, int KS, int KG, int RES>
+__global__ __launch_bounds__((Config<XT, TM, TN, WN, KS, KG, RES>::kThreads), 2) void mxfp4_gemm_kernel(const uint8_t* __restrict__ A,
                                                                  const uint8_t* __restrict__ As,
                                                                  const uint8_t* __restrict__ W,
                                                                  const uint8_t* __restrict__ Ws, int M, int N,
                                                                  int m_pad, int n_pad, int nblk, int mtiles, int tiles,
                                                                  uint16_t* __restrict__ Y) {
-  using C = Config<PIECES, TM, TN, WN, KS, KG, RES>;
+  using C = Config<XT, TM, TN, WN, KS, KG, RES>;
   constexpr int kWaves = C::kWaves;
   using TA = typename C::TA;
   using TW = typename C::TW;
@@ -252,94 +247,144 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
   for (int s = 0; s < KS; ++s) {
     w_at[s] = kAt + TW::place((wn * 32) + r32, s, half);
     a_at[s] = 0;
-    if constexpr (!C::kSplit) a_at[s] = TA::place(wm * 32 + r32, s, half);
+    if constexpr (!C::kRows) a_at[s] = TA::place(wm * 32 + r32, s, half);
     asm volatile("" : "+v"(w_at[s]), "+v"(a_at[s]));
   }
-  if constexpr (!C::kSplit) as_at = kAsAt + 4 * (wm * 32 + r32) + 2 * half;
+  if constexpr (!C::kRows) as_at = kAsAt + 4 * (wm * 32 + r32) + 2 * half;
+  const uint32_t a_at0 = (uint32_t)(wm * KS * kMxFragBytes + 16 * lane);
   asm volatile("" : "+v"(as_at), "+v"(ws_at));
 
-  float16_t acc[TM][TN] = {};
-  for (int st = 0; st + 1 < C::kStages; ++st) issue(h0 + st, st);
-  if constexpr (RES > 0) {  // seen by all behind the first turn's barrier
-    static_assert(KS == 4 && PIECES == 1 && RES % 4 == 0);
-    const int chunks = (nblk + 15) >> 4;
-    for (int i = threadIdx.x; i < (C::BM + C::BN) * chunks; i += C::kThreads) {
-      const int row = i % (C::BM + C::BN), g = i / (C::BM + C::BN);
-      const bool of_a = row < C::BM;
-      const int r = of_a ? m0 + row : n0 + row - C::BM, last = (of_a ? M : N) - 1;
-      const u32x4_t v = mx_scale_chunk((of_a ? As : Ws) + (int64_t)(r < last ? r : last) * nblk, g, nblk);
-      uint32_t* const to = of_a ? &a_scales[4 * g][row] : &w_scales[4 * g][row - C::BM];
+  float16_t acc[TM][TN];
+  // All of K.  16-bit activations: in the usual way, or the general one; returns whether
+  // the lane met a block that the usual one does not multiply.
+  auto all_of_k = [&](auto way) {
+    constexpr bool kGeneral = decltype(way)::value;
+    bool general = false;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) to[q * (of_a ? C::BM : C::BN)] = v[q];
-    }
-  }
-  int buf = 0;
-  for (int h = h0; h < h0 + turns; ++h) {
-    wait_loads<(C::kStages - 2) * C::kLoads>();
-    __builtin_amdgcn_s_barrier();
-    issue(h + C::kStages - 1, buf == 0 ? C::kStages - 1 : buf - 1);
-    const uint8_t* const la = lds[buf];
-    buf = buf + 1 == C::kStages ? 0 : buf + 1;
-    if (KG > 1 && h >= h1) continue;
-    auto multiply = [&](auto sel) {
-      constexpr int s = decltype(sel)::value;
-      i32x8_t bf[TN];
-      int bs[TN];
+    for (int i = 0; i < TM * TN; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        bf[j] = mx_operand(*reinterpret_cast<const u32x4_t*>(la + w_at[s] + j * 32 * TW::kRowBytes));
-        if constexpr (RES > 0)
-          bs[j] = (int)reinterpret_cast<const uint16_t*>(&w_scales[2 * h + (s >> 1)][(wn + j) * 32 + r32])[half];
-        else
-          bs[j] = TW::scale(la + ws_at + 128 * j, s, h);
+      for (int e = 0; e < 16; ++e) acc[i / TN][i % TN][e] = 0.0f;
+    for (int st = 0; st + 1 < C::kStages; ++st) issue(h0 + st, st);
+    if constexpr (RES > 0) {  // seen by all behind the first turn's barrier
+      static_assert(KS == 4 && !C::kRows && RES % 4 == 0);
+      const int chunks = (nblk + 15) >> 4;
+      for (int i = threadIdx.x; i < (C::BM + C::BN) * chunks; i += C::kThreads) {
+        const int row = i % (C::BM + C::BN), g = i / (C::BM + C::BN);
+        const bool of_a = row < C::BM;
+        const int r = of_a ? m0 + row : n0 + row - C::BM, last = (of_a ? M : N) - 1;
+        const u32x4_t v = mx_scale_chunk((of_a ? As : Ws) + (int64_t)(r < last ? r : last) * nblk, g, nblk, 0u);
+        uint32_t* const to = of_a ? &a_scales[4 * g][row] : &w_scales[4 * g][row - C::BM];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) to[q * (of_a ? C::BM : C::BN)] = v[q];
       }
-      if constexpr (!C::kSplit) {
+    }
+    int buf = 0;
+    for (int h = h0; h < h0 + turns; ++h) {
+      wait_loads<(C::kStages - 2) * C::kLoads>();
+      __builtin_amdgcn_s_barrier();
+      issue(h + C::kStages - 1, buf == 0 ? C::kStages - 1 : buf - 1);
+      const uint8_t* const la = lds[buf];
+      buf = buf + 1 == C::kStages ? 0 : buf + 1;
+      if (KG > 1 && h >= h1) continue;
+      auto multiply = [&](auto sel) {
+        constexpr int s = decltype(sel)::value;
+        u32x4_t wc[TN];
+        int bs[TN];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const i32x8_t v = mx_operand(*reinterpret_cast<const u32x4_t*>(la + a_at[s] + i * 32 * TA::kRowBytes));
-          int as;
+        for (int j = 0; j < TN; ++j) {
+          wc[j] = *reinterpret_cast<const u32x4_t*>(la + w_at[s] + j * 32 * TW::kRowBytes);
           if constexpr (RES > 0)
-            as = (int)reinterpret_cast<const uint16_t*>(&a_scales[2 * h + (s >> 1)][(wm + i) * 32 + r32])[half];
+            bs[j] = (int)reinterpret_cast<const uint16_t*>(&w_scales[2 * h + (s >> 1)][(wn + j) * 32 + r32])[half];
           else
-            as = TA::scale(la + as_at + 128 * i, s, h);
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], v, acc[i][j], kMfmaFp4, kMfmaFp4,
-                                                                        TW::select(s), bs[j], TA::select(s), as);
+            bs[j] = TW::scale(la + ws_at + 128 * j, s, h);
         }
-      } else {
+        if constexpr (!C::kRows) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const uint8_t* const fr = la + ((wm + i) * KS + s) * kMxFragBytes;
-          const int as = (int)reinterpret_cast<const uint32_t*>(la + kAsAt)[((wm + i) * KS + s) * 64 + lane];
-          auto piece = [&](int p) {
-            return mx_operand(*reinterpret_cast<const u32x4_t*>(fr + p * kMxPieceBytes + 16 * lane),
-                              *reinterpret_cast<const u32x2_t*>(fr + p * kMxPieceBytes + 1024 + 8 * lane));
+          for (int i = 0; i < TM; ++i) {
+            const i32x8_t v = mx_operand(*reinterpret_cast<const u32x4_t*>(la + a_at[s] + i * 32 * TA::kRowBytes));
+            int as;
+            if constexpr (RES > 0)
+              as = (int)reinterpret_cast<const uint16_t*>(&a_scales[2 * h + (s >> 1)][(wm + i) * 32 + r32])[half];
+            else
+              as = TA::scale(la + as_at + 128 * i, s, h);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(wc[j]), v, acc[i][j], kMfmaFp4, kMfmaFp4,
+                                                                          TW::select(s), bs[j], TA::select(s), as);
+          }
+        } else {
+          auto acts = [&](int i, int q) {
+            return *reinterpret_cast<const u32x4_t*>(la + a_at0 + ((i * KS + s) * 4 + q) * 1024);
           };
-          // smallest piece first
-          const i32x8_t p2 = piece(2), p1 = piece(1), p0 = piece(0);
-          constexpr int w = TW::select(s);
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p2, acc[i][j], kMfmaFp4, kMfmaFp6, w, bs[j], 2, as);
+          for (int j = 0; j < TN; ++j) bs[j] = bs[j] >> (8 * TW::select(s)) & 0xFF;
+          auto step = [&](auto widen) {
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p1, acc[i][j], kMfmaFp4, kMfmaFp6, w, bs[j], 1, as);
+            for (int q = 0; q < 4; ++q) {
+              u32x4_t w[TN];
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[j], p0, acc[i][j], kMfmaFp4, kMfmaFp6, w, bs[j], 0, as);
+              for (int j = 0; j < TN; ++j) w[j] = widen(wc[j][q], (uint32_t)bs[j]);
+#pragma unroll
+              for (int i = 0; i < TM; ++i) {
+                const u32x4_t x = acts(i, q);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma32x32x16<XT>(w[j], x, acc[i][j]);
+              }
+            }
+          };
+          if constexpr (!kGeneral) {
+            bool unusual = false;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) unusual |= mx_unusual<XT>((uint32_t)bs[j], 1);
+            if (__any(unusual))
+#pragma unroll
+              for (int j = 0; j < TN; ++j) general |= mx_needs_care<XT>(wc[j], (uint32_t)bs[j]);
+            step([](uint32_t c, uint32_t b) { return mx_widen<XT>(c, b); });
+          } else if constexpr (!kMxIsF16<XT>) {
+            step([](uint32_t c, uint32_t b) { return mx_widen_any(c, b); });
+          } else {
+            bool large = false;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) large |= mx_large((uint32_t)bs[j]);
+            large = __any(large);
+#pragma unroll 1
+            for (int p = 0; p < kMxPasses; p += large ? 1 : 4)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                asm volatile("" ::: "memory");  // activations are read again each pass: kept, they spill
+                u32x4_t w[TN];
+#pragma unroll
+                for (int j = 0; j < TN; ++j) w[j] = mx_general_weights(wc[j][q], (uint32_t)bs[j], p);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                  const u32x4_t x = mx_general_activations(acts(i, q), p);
+#pragma unroll
+                  for (int j = 0; j < TN; ++j) acc[i][j] = mfma32x32x16<BF16>(w[j], x, acc[i][j]);
+                }
+              }
+          }
         }
+      };
+      multiply(std::integral_constant<int, 0>{});
+      if constexpr (KS > 1) multiply(std::integral_constant<int, 1>{});
+      if constexpr (KS > 2) {
+        multiply(std::integral_constant<int, 2>{});
+        multiply(std::integral_constant<int, 3>{});
       }
-    };
-    multiply(std::integral_constant<int, 0>{});
-    if constexpr (KS > 1) multiply(std::integral_constant<int, 1>{});
-    if constexpr (KS > 2) {
-      multiply(std::integral_constant<int, 2>{});
-      multiply(std::integral_constant<int, 3>{});
     }
+    wait_loads<0>();  // none may land in LDS that is another workgroup's by then
+    return general;
+  };
+  if constexpr (C::kRows) {
+    __shared__ bool any_general;
+    if (threadIdx.x == 0) any_general = false;  // before the first turn's barrier
+    if (all_of_k(std::false_type{})) any_general = true;
+    __syncthreads();
+    if (any_general) all_of_k(std::true_type{});  // the tile again, for all of its waves
+  } else {
+    all_of_k(std::false_type{});
   }
-  wait_loads<0>();  // none may land in LDS that is another workgroup's by then
-  __syncthreads();  // and nobody reads operands any more
+  __syncthreads();  // nobody reads operands any more
 
   if constexpr (KG > 1) {
     // the groups' sums meet in LDS, [wave][tile][lane], added in order
@@ -366,6 +411,10 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
   // instruction's first operand for that).  Each wave turns 32 rows at a time
   // through LDS of its own, so that Y is written in whole rows of the wave's
   // columns, 16 bytes a lane.
+  constexpr float kGain = [] {
+    if constexpr (C::kRows) return kMxGain<XT>;
+    return 1.0f;
+  }();
   constexpr int kPitch = 64 * TN + 16, kChunks = 4 * TN;
   static_assert(kWaves * 32 * kPitch <= C::kStages * C::kStage, "the turn fits the stages' place");
   uint8_t* const turn = &lds[0][0] + wave * 32 * kPitch;
@@ -375,8 +424,8 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const uint32_t lo = (uint32_t)YT::from_f32(acc[i][j][4 * g]) | (uint32_t)YT::from_f32(acc[i][j][4 * g + 1]) << 16;
-        const uint32_t hi = (uint32_t)YT::from_f32(acc[i][j][4 * g + 2]) | (uint32_t)YT::from_f32(acc[i][j][4 * g + 3]) << 16;
+        const uint32_t lo = (uint32_t)YT::from_f32(acc[i][j][4 * g] * kGain) | (uint32_t)YT::from_f32(acc[i][j][4 * g + 1] * kGain) << 16;
+        const uint32_t hi = (uint32_t)YT::from_f32(acc[i][j][4 * g + 2] * kGain) | (uint32_t)YT::from_f32(acc[i][j][4 * g + 3] * kGain) << 16;
         *reinterpret_cast<u32x2_t*>(turn + r32 * kPitch + 64 * j + 16 * g + 8 * half) = u32x2_t{lo, hi};
       }
     asm volatile("" ::: "memory");
@@ -402,29 +451,33 @@ __global__ __launch_bounds__((Config<PIECES, TM, TN, WN, KS, KG, RES>::kThreads)
 
 size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)mxfp4_scale_rows(rows) * (size_t)((K + 255) / 256 * 2) * 4; }
 
-template <class YT, int PIECES, int TM, int TN, int WN, int KS, int KG, int RES = 0>
+template <class YT, class XT, int TM, int TN, int WN, int KS, int KG, int RES = 0>
 hipError_t launch_tiles(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                         void* Y, hipStream_t stream) {
-  using C = Config<PIECES, TM, TN, WN, KS, KG, RES>;
+  using C = Config<XT, TM, TN, WN, KS, KG, RES>;
   const int64_t mt = (M + C::BM - 1) / C::BM, nt = (N + C::BN - 1) / C::BN;
   const int64_t tiles = mt * nt;
   const unsigned grid = (unsigned)((tiles + kXcds - 1) / kXcds * kXcds);
-  mxfp4_gemm_kernel<YT, PIECES, TM, TN, WN, KS, KG, RES><<<grid, C::kThreads, 0, stream>>>(
+  mxfp4_gemm_kernel<YT, XT, TM, TN, WN, KS, KG, RES><<<grid, C::kThreads, 0, stream>>>(
       static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
       static_cast<const uint8_t*>(Ws), (int)M, (int)N, (int)mxfp4_scale_rows(M), (int)mxfp4_scale_rows(N), (int)(K / kMxBlock), (int)mt,
       (int)tiles, static_cast<uint16_t*>(Y));
   return hipGetLastError();
 }
 
-// The tile with the smallest time by a model of what was measured at K = 4096 (all
-// grow with K alike), in us for n = ceil(tiles / 256) tiles a compute unit:
-//   4-bit A:      256 x 256 36 n          (2048 x 8192: 40;  1024 x 28672, K / 2: 70)
-//                 128 x 128 6 + 10 n      (n = 1: 14 .. 17, 2: 22 .. 24, 4: 45, 6: 63 .. 68)
-//                 64 x 64   3 + 4.5 n     (n = 1: 8, 2: 10, 4: 18 .. 21, 8: 34 .. 40)
-//   three pieces: 128 x 256 9 + 49 n      (n = 1: 59 .. 61, 2: 107, 3: 152)
-//                 64 x 256  1 + 28 n      (n = 1: 27 .. 34, 2: 56 .. 59, 4: 116)
-//                 64 x 128  19.5 n        (n = 1: 18 .. 21, 2: 37 .. 41, 4: 75)
-//                 64 x 64   14 n          (n = 1: 15, 2: 27, 4: 52 .. 59)
+// The tile with the smallest time by a model of what was measured at K = 4096, in us
+// for n = ceil(tiles / 256) tiles a compute unit (16-bit: with the pass before it):
+//   4-bit A:   256 x 256 36 n          (2048 x 8192: 41;  1024 x 28672, K / 2: 49)
+//              128 x 128 6 + 10 n      (n = 1: 15 .. 21, 2: 23 .. 25, 4: 46, 6: 63 .. 65)
+//              64 x 64   3 + 4.5 n     (n = 1: 8, 2: 11, 4: 22, 8: 34 .. 40)
+//   16-bit A:  128 x 256 16 + 54 n     (n = 1: 59 .. 76, 2: 125, 3: 182)
+//              64 x 256  8 + 30.5 n    (n = 1: 34 .. 45, 2: 73, 4: 136, 6: 190)
+//              64 x 128  5 + 21.5 n    (n = 1: 23 .. 29, 2: 50, 4: 91, 8: 173)
+//              64 x 64   6 + 14.5 n    (n = 1: 18 .. 22, 2: 37, 4: 66, 8: 122)
+// Not all of it grows with K, but the order stays: at K = 32 .. 1024 and seven sizes
+// from 16 x 4096 to 2048 x 8192 the choice is within 0.6 us of the best tile, 16-bit
+// 64 x 28672 x 32 for one 7.3 us, with 64 x 256 6.8; 2048 x 8192 x 256 18.7, the others
+// 19.0, 36 and 50; microscaled 1024 x 4096 x 256 7.3, the others 9.2 and 9.9.
 // The small ones split K between two groups of waves.
 int64_t per_cu(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256; }
 enum class Tile { kLarge, kMiddle, kSmall };
@@ -443,51 +496,57 @@ bool resident(int64_t M, int64_t N, int64_t K) {
   return tile_mx(M, N) == Tile::kSmall && (K <= 128 * kResident || (K <= 128 * kResidentAlone && per_cu(M, N, 64, 64) == 1));
 }
 
-template <class YT, int PIECES>
+template <class YT, class XT>
 hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N, int64_t K,
                   void* Y, hipStream_t stream) {
-  if constexpr (PIECES == 1) {
+  if constexpr (std::is_same_v<XT, Mx>) {
     if (resident(M, N, K))
-      return K <= 128 * kResident ? launch_tiles<YT, 1, 1, 1, 2, 4, 2, kResident>(A, As, W, Ws, M, N, K, Y, stream)
-                                  : launch_tiles<YT, 1, 1, 1, 2, 4, 2, kResidentAlone>(A, As, W, Ws, M, N, K, Y, stream);
+      return K <= 128 * kResident ? launch_tiles<YT, XT, 1, 1, 2, 4, 2, kResident>(A, As, W, Ws, M, N, K, Y, stream)
+                                  : launch_tiles<YT, XT, 1, 1, 2, 4, 2, kResidentAlone>(A, As, W, Ws, M, N, K, Y, stream);
     switch (tile_mx(M, N)) {
-      case Tile::kLarge: return launch_tiles<YT, 1, 4, 2, 4, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
-      case Tile::kMiddle: return launch_tiles<YT, 1, 2, 2, 2, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
-      default: return launch_tiles<YT, 1, 1, 1, 2, 4, 2>(A, As, W, Ws, M, N, K, Y, stream);
+      case Tile::kLarge: return launch_tiles<YT, XT, 4, 2, 4, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
+      case Tile::kMiddle: return launch_tiles<YT, XT, 2, 2, 2, 4, 1>(A, As, W, Ws, M, N, K, Y, stream);
+      default: return launch_tiles<YT, XT, 1, 1, 2, 4, 2>(A, As, W, Ws, M, N, K, Y, stream);
     }
   } else {
-    const double large = 9.0 + 49.0 * per_cu(M, N, 128, 256), wide = 1.0 + 28.0 * per_cu(M, N, 64, 256),
-                 mid = 19.5 * per_cu(M, N, 64, 128), small = 14.0 * per_cu(M, N, 64, 64);
+    const double large = 16.0 + 54.0 * per_cu(M, N, 128, 256), wide = 8.0 + 30.5 * per_cu(M, N, 64, 256),
+                 mid = 5.0 + 21.5 * per_cu(M, N, 64, 128), small = 6.0 + 14.5 * per_cu(M, N, 64, 64);
     if (large <= wide && large <= mid && large <= small)
-      return launch_tiles<YT, kMxPieces, 2, 4, 2, 1, 1>(A, As, W, Ws, M, N, K, Y, stream);
-    if (wide <= mid && wide <= small) return launch_tiles<YT, kMxPieces, 1, 2, 4, 2, 1>(A, As, W, Ws, M, N, K, Y, stream);
-    if (mid <= small) return launch_tiles<YT, kMxPieces, 1, 2, 2, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
-    return launch_tiles<YT, kMxPieces, 1, 1, 2, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
+      return launch_tiles<YT, XT, 2, 4, 2, 1, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    if (wide <= mid && wide <= small) return launch_tiles<YT, XT, 1, 2, 4, 2, 1>(A, As, W, Ws, M, N, K, Y, stream);
+    if (mid <= small) return launch_tiles<YT, XT, 1, 2, 2, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
+    return launch_tiles<YT, XT, 1, 1, 2, 2, 2>(A, As, W, Ws, M, N, K, Y, stream);
   }
 }
 
 // Few rows, or small outputs, go to the weight-streaming kernels (K >= 128), which
 // need no pass over the scales and cut no tile that is mostly empty.  Whole
-// products, us, streaming / tiles:
-//   split, 32 rows   8192 x 8192 20 / 30, 4096 x 11008 24 / 39, 28672 x 8192 37 / 53
-//          64 rows   4096 x 4096 12 / 18, 8192 x 8192 26 / 30, 11008 x 2048 14 / 13,
-//                    16384 x 4096 22 / 20, 28672 x 8192 59 / 53, 4096 x 11008 39 / 39
-//          128       2048 x 8192 20 / 31, 4096 x 4096 16 / 19, 6144 x 4096 19 / 19
-//          256       1024 x 8192 23 / 32, 2048 x 2048 12 / 13, 4096 x 4096 22 / 21
-//   4-bit, 32 rows   4096 x 4096 6 / 8, 8192 x 8192 12 / 12, 4096 x 11008 14 / 16,
-//                    16384 x 4096 10 / 9, 28672 x 8192 26 / 35
-//          64 rows   4096 x 4096 7 / 8, 4096 x 8192 11 / 12, 8192 x 8192 15 / 12,
-//                    4096 x 2048 6 / 5; 28672 x 8192 31 / 38 (scales in a pass)
-//          128       512 x 4096 6 / 7, 2048 x 8192 11 / 12, 4096 x 8192 15 / 12
-//          256       1024 x 8192 10 / 11, 2048 x 2048 7 / 5
+// products, us, streaming / the best tile:
+//   16-bit, 32 rows  8192 x 8192 22 / 33, 4096 x 11008 21 / 40, 28672 x 8192 43 .. 50 / 49,
+//                    4096 x 4096 9 / 19, 16384 x 4096 19 / 22
+//          64 rows   4096 x 4096 12 / 18, 8192 x 8192 30 / 33, 11008 x 2048 16 / 13,
+//                    16384 x 4096 27 / 22, 28672 x 8192 79 / 50, 4096 x 128 5 / 6,
+//                    28672 x 128 12 / 7; 4096 x 11008 33 / 41, 8192 x 11008 61 / 41,
+//                    2048 x 16384 26 / 55
+//          96, 128   96 x 4096 x 11008 50 / 41; 128 x 2048 x 8192 21 / 32, 4096 x 4096
+//                    17 / 20, 6144 x 4096 22 / 20, 1024 x 16384 28 / 56
+//          256       1024 x 8192 20 / 34, 2048 x 2048 11 / 13, 4096 x 4096 27 / 22,
+//                    8192 x 128 12 / 7, 1024 x 11008 41 / 42
+//   4-bit, 32 rows   4096 x 4096 6 / 7, 8192 x 8192 13 / 14, 4096 x 11008 15 / 17, 16384 x 4096
+//                    10.5 / 10.7, 28672 x 8192 27 / 35, 28672 x 2048 10.5 / 9.6
+//          64 rows   4096 x 4096 6.9 / 7.8, 4096 x 8192 11 / 13, 8192 x 8192 16 / 15,
+//                    4096 x 2048 6.1 / 5.8, 28672 x 2048 15 / 10; 28672 x 8192 32 / 38, x 4096
+//                    20 / 22 (scales in a pass)
+//          128       512 x 4096 6 / 7, 2048 x 8192 11 / 12, 4096 x 8192 16 / 13
+//          256       1024 x 8192 11 / 12, 2048 x 2048 7 / 6
 bool skinny(int64_t M, int64_t N, int64_t K) {
-  return K >= 128 && (M <= 32 || (K <= 8192 && M <= 512 && M * N <= 1 << 19));
+  return K >= 128 && (M <= 32 || (M <= 512 && M * N <= (K <= 8192 ? 1 << 19 : 1 << 18)));
 }
 bool skinny_mx(int64_t M, int64_t N, int64_t K) {
   return K >= 128 && (M <= 32 || (K <= 8192 && ((M <= 64 && !resident(M, N, K)) ||
                                                 (M <= 512 && K >= 4096 && M * N <= 1 << 18))));
 }
-constexpr int64_t kRowPad = 128;  // rows of split activations are padded to a tile
+constexpr int64_t kRowPad = 128;  // rows of 16-bit activations are padded to a tile
 
 int64_t split_row_groups(int64_t M) { return (M + kRowPad - 1) / kRowPad * (kRowPad / 32); }
 int64_t split_ksteps(int64_t K) { return (K + 127) / 128 * 2; }
@@ -496,26 +555,23 @@ int64_t split_ksteps(int64_t K) { return (K + 127) / 128 * 2; }
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return 0;
-  if (skinny(M, N, K) && mxfp4_skinny_splits(K)) return 0;
   if (skinny(M, N, K))
-    return (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * (kMxFragBytes + kMxFragScaleBytes);
-  return (size_t)(split_row_groups(M) * split_ksteps(K)) * (kMxFragBytes + kMxFragScaleBytes) + scale_bytes(N, K);
+    return K <= mxfp4_skinny_max_k() ? 0 : (size_t)((M + 15) / 16 * ((K + 511) / 512 * 4)) * kMxFragBytes;
+  return (size_t)(split_row_groups(M) * split_ksteps(K)) * kMxFragBytes + scale_bytes(N, K);
 }
 
 hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
                              int64_t K, void* Y, void* workspace, hipStream_t stream) {
   if (M == 1 && K <= mxfp4_gemv_max_k()) return launch_mxfp4_gemv(X, xdtype, codes, scales, N, K, Y, stream);
-  uint8_t* const pieces = static_cast<uint8_t*>(workspace);
   const bool few = skinny(M, N, K);
-  if (few && mxfp4_skinny_splits(K)) return launch_mxfp4_skinny_raw(X, xdtype, codes, scales, M, N, K, Y, stream);
+  if (few && K <= mxfp4_skinny_max_k()) return launch_mxfp4_skinny(X, xdtype, codes, scales, M, N, K, Y, stream);
   const int64_t rg = few ? (M + 15) / 16 : split_row_groups(M), ks = few ? (K + 511) / 512 * 4 : split_ksteps(K);
-  uint8_t* const ps = pieces + rg * ks * kMxFragBytes;
-  uint8_t* const ws = ps + rg * ks * kMxFragScaleBytes;
-  const hipError_t e = launch_mxfp4_split(X, xdtype, M, K, few ? 16 : 32, rg, ks, pieces, ps, few ? nullptr : scales, N, ws, stream);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace) + rg * ks * kMxFragBytes;
+  const hipError_t e = launch_mxfp4_split(X, M, K, few ? 16 : 32, rg, ks, workspace, few ? nullptr : scales, N, ws, stream);
   if (e != hipSuccess) return e;
-  if (few) return launch_mxfp4_skinny(pieces, ps, codes, scales, M, N, K, xdtype, Y, stream);
-  return xdtype == 0 ? launch<F16, kMxPieces>(pieces, ps, codes, ws, M, N, K, Y, stream)
-                     : launch<BF16, kMxPieces>(pieces, ps, codes, ws, M, N, K, Y, stream);
+  if (few) return launch_mxfp4_skinny(workspace, xdtype, codes, scales, M, N, K, Y, stream);
+  return xdtype == 0 ? launch<F16, F16>(workspace, nullptr, codes, ws, M, N, K, Y, stream)
+                     : launch<BF16, BF16>(workspace, nullptr, codes, ws, M, N, K, Y, stream);
 }
 
 size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -533,7 +589,7 @@ hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, co
     As = as;
     Ws = ws;
   }
-  return ydtype == 0 ? launch<F16, 1>(A, As, W, Ws, M, N, K, Y, stream) : launch<BF16, 1>(A, As, W, Ws, M, N, K, Y, stream);
+  return ydtype == 0 ? launch<F16, Mx>(A, As, W, Ws, M, N, K, Y, stream) : launch<BF16, Mx>(A, As, W, Ws, M, N, K, Y, stream);
 }
 
 }  // namespace woq

@@ -12,23 +12,24 @@
 // L2.  (All chunks in one turn needs 64 sums a lane more and spilled.)
 //
 // Launches:
-//   route    logits, one workgroup per expert and 8 tokens; x split into pieces
+//   route    logits, one workgroup per expert and 8 tokens
 //   choose   one workgroup: the tokens' experts and shares, and the list of turns
 //            (an expert and up to 16 of its tokens, in ascending order)
-//   up       32 columns of h a time: gate and up rows, then p silu(g) u, split into
-//            pieces again (14 bits of a block's largest magnitude).  The share is
-//            folded in here, where the values are still fp32.
+//   up       32 columns of h a time: gate and up rows, then p silu(g) u.  The share is
+//            folded in here, where the values are still fp32; they are kept as two
+//            bf16 numbers each (off by at most 2^-18 of the value, where fp32 would
+//            need three and the registers hold two).
 //   down     64 columns of a turn's products a time
 //   combine  y from its experts' products, added in the order of choice (no atomics)
 // A small layer of few tokens has no combine: its down adds over the experts itself.
 // One token needs no list either: up and down work the choices out from the logits.
 //
-// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 99 us, of which up 62
-// (285 MB of weights, 4.6 TB/s) and down 30 (142 MB, 4.7 TB/s); one token 23 us,
-// up 13, down 8.5, logits 5.  A workgroup per 32 columns and turn (up) and per 16
-// columns of y over all turns (down) took 86 and 51: they read the activations again
-// for every 64 (16) weight rows, and a workgroup's first loads had nothing before
-// them to hide behind.
+// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 114 us, of which up 71
+// (285 MB of weights, 4.0 TB/s) and down 36 (142 MB, 4.0 TB/s); one token 23 us, up
+// 13.7, down 8.3, logits 4.5.  Before, a workgroup per 32 columns and turn (up) and per
+// 16 columns of y over all turns (down) read the activations again for every 64 (16)
+// weight rows, and its first loads had nothing before them to hide behind: 24 and 21 us
+// more.
 #include <cstddef>
 
 #include "mxfp4_stream.h"
@@ -81,25 +82,12 @@ __device__ inline uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// logits [64][E].  Workgroups [0, groups E) compute logits, the rest split x
-// (fragments of 16 rows, super-step order).
+// logits [64][E]; a workgroup an expert and TOKENS tokens.
 template <class XT, int TOKENS>
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const uint16_t* __restrict__ X,
                                                                   const uint16_t* __restrict__ router, int T, int H,
-                                                                  int E, int groups, float* __restrict__ logits,
-                                                                  uint8_t* __restrict__ xp, uint32_t* __restrict__ xs) {
+                                                                  int E, int groups, float* __restrict__ logits) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if ((int)blockIdx.x >= groups * E) {
-    const int supers = (H + 511) / 512;
-    const int i = ((int)blockIdx.x - groups * E) * kRouteThreads + (int)threadIdx.x;  // block of x
-    const int t = i / (kSuper * supers), b = i % (kSuper * supers);
-    if (t >= T) return;
-    float v[kMxBlock] = {};
-    if (b * kMxBlock < H) mx_load_block<XT>(X + (int64_t)t * H + b * kMxBlock, v);
-    const int64_t f = ((int64_t)(t / kChunk) * supers + b / kSuper) * 4 + b % 4;
-    mx_store_pieces(mx_split(v), xp + f * kMxFragBytes, xs + f * 64, (b % kSuper / 4) * kChunk + t % kChunk);
-    return;
-  }
   __shared__ float part[kRouteThreads / 64][TOKENS];
   const int e = (int)blockIdx.x / groups, t0 = (int)blockIdx.x % groups * TOKENS;
   const int n = T - t0 < TOKENS ? T - t0 : TOKENS;
@@ -294,6 +282,43 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const flo
   }
 }
 
+// Two numbers bf16 that hold v to within 2^-18 of itself: hi the nearest (the next
+// one inside where that is not finite), lo the nearest to the rest.
+struct Halves {
+  uint16_t hi, lo;
+};
+__device__ inline Halves halves(float v) {
+  const uint32_t bits = __builtin_bit_cast(uint32_t, v);
+  uint16_t hi = BF16::from_f32(v);
+  if ((hi & 0x7FFFu) == 0x7F80u) hi = (uint16_t)(bits >> 16);
+  const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
+  return Halves{hi, finite ? BF16::from_f32(v - BF16::to_f32(hi)) : (uint16_t)0};
+}
+
+// h, p folded in, for down: of each turn and super-step four fragments
+// (mxfp4_device.h) of the 16 tokens' hi, then four of their lo.  Up to 8 tokens are
+// multiplied in one matrix step, their hi as the rows 0 .. 7 and their lo as the rows
+// 8 .. 15, which join_halves adds; more in two steps into the same sums.
+constexpr int kHalfTokens = 8;
+__host__ __device__ inline int64_t h_fragment(int64_t turn, int supers, int S) { return (turn * supers + S) * 8; }
+// A lane's place in the fragments of hi: its token (rows past the turn's last one
+// repeat it) and, of up to 8 tokens (first: of the group of 8), its half.
+__device__ inline uint32_t h_place(int count, int lane) {
+  const int r = lane & 15;
+  return (uint32_t)(16 * ((lane & 48) + (r < count ? r : count - 1)));
+}
+__device__ inline uint32_t h_place_halves(int first, int count, int lane) {
+  const int t = first + (lane & 7);
+  return (uint32_t)(16 * ((lane & 48) + (t < count ? t : count - 1)) + (lane & 8 ? 4 * kMxFragBytes : 0));
+}
+// The products of a group of 8 tokens and of the next one -> rows 0 .. 15.
+__device__ inline float4_t join_halves(float4_t a, float4_t b, int lane) {
+  float4_t v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (lane < 32 ? a[e] : b[e]) + __shfl_xor(lane < 32 ? b[e] : a[e], 32, 64);
+  return v;
+}
+
 // The experts' products.  Item: a turn and 64 weight rows of its expert: UP, 32
 // gate rows and their 32 up rows, which make 32 columns of h; else 64 rows of
 // down, 64 columns of y.  A workgroup takes a run of items, K split between its
@@ -301,13 +326,12 @@ __global__ __launch_bounds__(kChooseWaves * 64) void moe_choose_kernel(const flo
 // registers while the turn does not change, and the next item's weights are on
 // their way while an item's sums meet in LDS.
 // NJ > 0: one token; every wave works its choices out from the logits, and turn k
-// is choice k.
-template <bool UP, int WAVES, int NJ>
+// is choice k.  XT: of the activations; BF16 for h.
+template <bool UP, int WAVES, int NJ, class XT>
 __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
-    const uint8_t* __restrict__ xp, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ codes,
-    const uint8_t* __restrict__ scales, const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan,
-    const Turn* __restrict__ turns, int K, int rows, int E, int groups, uint8_t* __restrict__ hp,
-    uint32_t* __restrict__ hs, float* __restrict__ products) {
+    const uint16_t* __restrict__ X, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+    const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan, const Turn* __restrict__ turns, int K,
+    int rows, int E, int groups, uint8_t* __restrict__ h, float* __restrict__ products) {
   constexpr int NT = 4;  // tiles of 16 rows; UP: gate rows, up rows, gate rows, up rows
   __shared__ __attribute__((aligned(16))) uint8_t stage_all[WAVES][kUnitStage];
   __shared__ float4_t parts[2][WAVES][NT][64];  // alternating: one barrier an item
@@ -336,7 +360,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
   };
   // a turn's record, a dword a lane; on its way before the weights of its first item
   static_assert(sizeof(Turn) == 4 * 22 && offsetof(Turn, share) == 8 && offsetof(Turn, token) == 72, "read as dwords");
-  auto record = [&](int k) { return reinterpret_cast<const uint32_t*>(turns + k)[lane < 22 ? lane : 21]; };
+  auto record = [&](int k) {
+    int l = lane;
+    asm volatile("" : "+v"(l));  // addresses are worked out each time: kept, they spill
+    return reinterpret_cast<const uint32_t*>(turns + k)[(uint32_t)(l < 22 ? l : 21)];
+  };
   // rows past the expert's last (its columns are a multiple of 32) repeat the first tile
   auto tile_row = [&](int j, int item) {
     return UP ? (j & 1) * (rows / 2) + (j >> 1) * 16 : (item % groups * 64 + 16 * j < rows ? 16 * j : 0);
@@ -347,17 +375,17 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
   uint32_t rec_n = NJ > 0 ? 0u : record(i0 / groups);
   int64_t row_n = first_row(i0);
   MxUnit u[NT];
-  auto ahead = [&](int j) {
+  auto ahead = [&](int j, int l) {
     const int64_t row = row_n + tile_row(j, item_n);
     __builtin_amdgcn_sched_barrier(0);
-    mx_load_unit(u[j], codes + row * nblk * 16, scales + row * nblk, 15, (all - row) * nblk, nblk, S_n, lane);
+    mx_load_unit(u[j], codes + row * nblk * 16, scales + row * nblk, 15, (all - row) * nblk, nblk, S_n, l);
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
-  for (int j = 0; j < NT; ++j) ahead(j);
+  for (int j = 0; j < NT; ++j) ahead(j, lane);
 
   if (threadIdx.x < kMxBlock) hbuf[kChunk][threadIdx.x] = 0.0f;
-  MxActivations a[4];
+  MxActivations a, lo;
   int turn = -1, count = 0, token = 0;
   float share = 0.0f;  // of row lane % 16; rows past the turn's last token repeat it
   for (int item = i0; item < i1; ++item) {
@@ -372,18 +400,24 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
         count = __builtin_amdgcn_readlane((int)rec_n, 1);
         const int m = (lane & 15) < count ? lane & 15 : count - 1;
         share = __builtin_bit_cast(float, __shfl((int)rec_n, 2 + m, 64));
-        token = UP ? __shfl((int)rec_n, 18 + m / 4, 64) >> (8 * (m & 3)) & 0xFF : m;
+        token = UP ? __shfl((int)rec_n, 18 + m / 4, 64) >> (8 * (m & 3)) & 0xFF : 0;
       }
     }
+    const bool two = !UP && count > kHalfTokens;  // matrix steps
     float4_t acc[NT] = {};
     const int64_t row0 = row_n;
     for (int S = wave; S < supers; S += waves) {
       if (changed || supers > waves) {
-        const MxPlace place = mx_place(UP ? token / kChunk * supers * 4 : 0, (lane & 48) + token % kChunk);
-        const int64_t f = ((int64_t)(UP ? 0 : k) * supers + S) * 4;
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          mx_load_activations(a[s], xp + (f + s) * kMxFragBytes, xs + (f + s) * kMxFragScaleBytes, place);
+        int l = lane;
+        asm volatile("" : "+v"(l));  // as above
+        if constexpr (UP) {
+          mx_load_activations(a, X + (int64_t)token * K, nblk, S, l);
+          mx_mask_activations(a, nblk, S, l);
+        } else {
+          const uint8_t* const f = h + h_fragment(k, supers, S) * kMxFragBytes;
+          mx_load_fragments(a, f, two ? h_place(count, l) : h_place_halves(0, count, l));
+          if (two) mx_load_fragments(lo, f + 4 * kMxFragBytes, h_place(count, l));
+        }
       }
       S_n = S + waves;
       if (S_n >= supers) {
@@ -394,17 +428,16 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
         }
       }
       auto multiply = [&](auto more) {
-        int l = lane;
-        asm volatile("" : "+v"(l));  // LDS addresses are worked out each time: kept, they spill
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          int l = lane;
+          asm volatile("" : "+v"(l));  // as above
           mx_stage_unit(u[j], stage, 15, (all - (row0 + tile_row(j, item))) * nblk, nblk, S, l);
-          if constexpr (decltype(more)::value) ahead(j);
-          const int sc = mx_staged_scale(stage, l);
-          mx_each_step([&](auto sel) {
-            constexpr int s = decltype(sel)::value;
-            mx_multiply<s>(acc[j], a[s], mx_staged_weights(stage, s, l), sc);
-          });
+          if constexpr (decltype(more)::value) ahead(j, l);
+          if constexpr (UP)
+            mx_multiply_unit<XT>(acc[j], a, stage, l);
+          else
+            mx_multiply_unit<XT>(acc[j], a, lo, two, stage, l);
         }
       };
       if (item_n < i1)
@@ -413,11 +446,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
         multiply(std::false_type{});
     }
     float4_t(*const part)[NT][64] = parts[(item - i0) & 1];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
-    __syncthreads();
     int l = lane;
     asm volatile("" : "+v"(l));  // as above
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[wave][j][l] = UP || two ? acc[j] : join_halves(acc[j], float4_t{}, l);
+    __syncthreads();
     // value (row m, tile j, column c) of a wave: part[w][j][(m / 4) 16 + c][m % 4]
     auto sum = [&](int m, int j, int c) {
       float p[WAVES], v = 0.0f;
@@ -425,7 +458,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
       for (int w = 0; w < WAVES; ++w) p[w] = part[w][j][(m >> 2) * 16 + c][m & 3];
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) v += w < waves ? p[w] : 0.0f;
-      return v;
+      return v * kMxGain<XT>;
     };
     if constexpr (UP) {
       // wave w takes the rows 2 w, 2 w + 1, + 2 waves, ...
@@ -437,7 +470,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      // a lane splits a row's block; behind the last block of h the rest of its
+      // a lane writes a row's block; behind the last block of h the rest of its
       // super-step is zeros
       const int m = l & 15, hsupers = (groups + kSuper - 1) / kSuper;
       const int end = group == groups - 1 ? kSuper * hsupers : group + 1;
@@ -445,17 +478,25 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
         for (int b = group + (l >> 4); b < end; b += 4) {
           const float* const row = hbuf[b == group ? m : kChunk];
           const float scale = b == group ? share : 0.0f;
-          float v[kMxBlock];
+          uint8_t* const to = h + (h_fragment(k, hsupers, b / kSuper) + b % 4) * kMxFragBytes + 16 * ((b % kSuper / 4) * kChunk + m);
 #pragma unroll
-          for (int c = 0; c < kMxBlock; ++c) v[c] = scale * row[c];
-          const int64_t f = ((int64_t)k * hsupers + b / kSuper) * 4 + b % 4;
-          mx_store_pieces(mx_split(v), hp + f * kMxFragBytes, hs + f * 64, (b % kSuper / 4) * kChunk + m);
+          for (int q = 0; q < 4; ++q) {
+            u32x4_t hi = {}, lo = {};
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const Halves v = halves(scale * row[8 * q + c]);
+              hi[c / 2] |= (uint32_t)v.hi << (16 * (c % 2));
+              lo[c / 2] |= (uint32_t)v.lo << (16 * (c % 2));
+            }
+            *reinterpret_cast<u32x4_t*>(to + 1024 * q) = hi;
+            *reinterpret_cast<u32x4_t*>(to + 4 * kMxFragBytes + 1024 * q) = lo;
+          }
         }
       }
     } else {
       const int n = group * 64 + l;
       for (int m = wave; m < count; m += waves)
-        if (n < rows) products[((int64_t)k * kChunk + m) * rows + n] = sum(m, l >> 4, l & 15);
+        if (n < rows) (products + (int64_t)k * kChunk * rows)[(uint32_t)(m * rows + n)] = sum(m, l >> 4, l & 15);
     }
   }
 }
@@ -465,9 +506,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
 // in order.  NJ as above.
 template <class YT, int NJ>
 __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
-    const uint8_t* __restrict__ hp, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ codes,
-    const uint8_t* __restrict__ scales, const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan,
-    const Turn* __restrict__ turns, int T, int H, int I, int E, uint16_t* __restrict__ Y) {
+    const uint8_t* __restrict__ h, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+    const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan, const Turn* __restrict__ turns, int T,
+    int H, int I, int E, uint16_t* __restrict__ Y) {
   constexpr int W = kExpertWaves, kRows = NJ > 0 ? 1 : kChunk;
   __shared__ __attribute__((aligned(16))) uint8_t stage_all[W][kUnitStage];
   __shared__ float sums[W][kRows][kChunk + 1];
@@ -486,7 +527,7 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
   for (int o = lane; o < kRows * (kChunk + 1); o += 64) (&sums[wave][0][0])[o] = 0.0f;
   struct Work {
     MxUnit u;
-    MxActivations a[4];
+    MxActivations a;
     uint32_t tokens;  // of rows 4 q .. 4 q + 3
   };
   auto row_of = [&](int i) {
@@ -495,26 +536,25 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
     return (int64_t)e * H + n0;
   };
   auto count_of = [&](int i) { return NJ > 0 ? 1 : turns[i / supers].count; };
+  auto activations = [&](MxActivations& a, int i, int first) {
+    mx_load_fragments(a, h + h_fragment(i / supers, supers, i % supers) * kMxFragBytes, h_place_halves(first, count_of(i), lane));
+  };
   auto load = [&](Work& w, int i) {
     const int64_t row = row_of(i);
-    const int count = count_of(i);
     w.tokens = NJ > 0 ? 0u : reinterpret_cast<const uint32_t*>(turns[i / supers].token)[lane >> 4];
     mx_load_unit(w.u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, i % supers, lane);
-    // rows past the turn's last token repeat it
-    const MxPlace place = mx_place(0, (lane & 48) + ((lane & 15) < count ? lane & 15 : count - 1));
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      mx_load_activations(w.a[s], hp + ((int64_t)i * 4 + s) * kMxFragBytes, hs + ((int64_t)i * 4 + s) * kMxFragScaleBytes, place);
+    activations(w.a, i, 0);
   };
-  auto work = [&](const Work& w, int i) {
-    float4_t acc = {};
+  auto work = [&](Work& w, int i) {
+    float4_t acc = {}, more = {};
     mx_stage_unit(w.u, stage, 15, ((int64_t)E * H - row_of(i)) * nblk, nblk, i % supers, lane);
-    const int sc = mx_staged_scale(stage, lane);
-    mx_each_step([&](auto sel) {
-      constexpr int s = decltype(sel)::value;
-      mx_multiply<s>(acc, w.a[s], mx_staged_weights(stage, s, lane), sc);
-    });
+    mx_multiply_unit<BF16>(acc, w.a, stage, lane);
     const int count = count_of(i);
+    if (NJ == 0 && count > kHalfTokens) {
+      activations(w.a, i, kHalfTokens);
+      mx_multiply_unit<BF16>(more, w.a, stage, lane);
+    }
+    acc = join_halves(acc, more, lane);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (4 * (lane >> 4) + e < count) sums[wave][w.tokens >> (8 * e) & 15u][lane & 15] += acc[e];
@@ -535,7 +575,7 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) v += sums[w][t][n];
-    Y[(int64_t)t * H + n0 + n] = YT::from_f32(v);
+    Y[(int64_t)t * H + n0 + n] = YT::from_f32(v * kMxGain<BF16>);
   }
 }
 
@@ -557,25 +597,20 @@ __global__ __launch_bounds__(64) void moe_combine_kernel(const float* __restrict
 }
 
 struct Layout {
-  int64_t turns, xfrags, hfrags;
-  size_t logits, plan, records, where, xp, xs, hp, hs, products, bytes;
+  int64_t turns;
+  size_t logits, plan, records, where, h, products, bytes;
 };
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Layout layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
   Layout l;
   // a turn for each chosen expert and one for each further 16 tokens of it
   l.turns = (T * top_k < E ? T * top_k : E) + T * top_k / kChunk;
-  l.xfrags = (T + kChunk - 1) / kChunk * ((H + 511) / 512 * 4);
-  l.hfrags = l.turns * ((I + 511) / 512 * 4);
   l.logits = 0;
   l.plan = up256((size_t)E * T * 4);
   l.records = l.plan + 256;
   l.where = up256(l.records + (size_t)l.turns * sizeof(Turn));
-  l.xp = up256(l.where + (size_t)(T * top_k) * 4);
-  l.xs = l.xp + (size_t)l.xfrags * kMxFragBytes;
-  l.hp = l.xs + (size_t)l.xfrags * kMxFragScaleBytes;
-  l.hs = l.hp + (size_t)l.hfrags * kMxFragBytes;
-  l.products = l.hs + (size_t)l.hfrags * kMxFragScaleBytes;
+  l.h = up256(l.where + (size_t)(T * top_k) * 4);
+  l.products = l.h + (size_t)h_fragment(l.turns, (int)((I + 511) / 512), 0) * kMxFragBytes;
   l.bytes = l.products + (size_t)(l.turns * kChunk * H) * 4;
   return l;
 }
@@ -589,18 +624,14 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
   Turn* const turns = reinterpret_cast<Turn*>(ws + l.records);
   int* const where = reinterpret_cast<int*>(ws + l.where);
   float* const products = reinterpret_cast<float*>(ws + l.products);
-  uint8_t* const xs = ws + l.xs;
-  uint8_t* const hs = ws + l.hs;
+  uint8_t* const h = ws + l.h;
   const int tokens = T == 1 ? 1 : kRouteTokens;
   const int groups = (T + tokens - 1) / tokens;
-  const int blocks = T * kSuper * ((H + 511) / 512);
-  const unsigned grid = (unsigned)(groups * E + (blocks + kRouteThreads - 1) / kRouteThreads);
+  const unsigned grid = (unsigned)(groups * E);
   if (T == 1)
-    moe_route_kernel<XT, 1><<<grid, kRouteThreads, 0, stream>>>(X, router, T, H, E, groups, logits, ws + l.xp,
-                                                                reinterpret_cast<uint32_t*>(xs));
+    moe_route_kernel<XT, 1><<<grid, kRouteThreads, 0, stream>>>(X, router, T, H, E, groups, logits);
   else
-    moe_route_kernel<XT, kRouteTokens><<<grid, kRouteThreads, 0, stream>>>(X, router, T, H, E, groups, logits, ws + l.xp,
-                                                                           reinterpret_cast<uint32_t*>(xs));
+    moe_route_kernel<XT, kRouteTokens><<<grid, kRouteThreads, 0, stream>>>(X, router, T, H, E, groups, logits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr int kLarge = kMaxExperts / 64;
@@ -612,18 +643,17 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
     if (e != hipSuccess) return e;
   }
   // a wave for every super-step of a row, up to 8; 8 waves fill a compute unit
-  auto experts = [&](auto up, auto nj, const uint8_t* acts, const uint8_t* act_scales, const uint8_t* codes,
-                     const uint8_t* scales, int K, int rows, int groups) {
+  auto experts = [&](auto up, auto nj, const uint8_t* codes, const uint8_t* scales, int K, int rows, int groups) {
     constexpr bool kUp = decltype(up)::value;
     constexpr int kNj = decltype(nj)::value;
+    using AT = std::conditional_t<kUp, XT, BF16>;
     const int supers = (K + 511) / 512, waves = supers < kExpertWaves ? supers : kExpertWaves;
-    auto* const f = waves > 4 ? moe_experts_kernel<kUp, kExpertWaves, kNj> : moe_experts_kernel<kUp, 4, kNj>;
-    f<<<256u * (unsigned)(kExpertWaves / waves), (unsigned)(waves * 64), 0, stream>>>(
-        acts, act_scales, codes, scales, logits, top_k, plan, turns, K, rows, E, groups, ws + l.hp,
-        reinterpret_cast<uint32_t*>(hs), products);
+    auto* const f = waves > 4 ? moe_experts_kernel<kUp, kExpertWaves, kNj, AT> : moe_experts_kernel<kUp, 4, kNj, AT>;
+    f<<<256u * (unsigned)(kExpertWaves / waves), (unsigned)(waves * 64), 0, stream>>>(X, codes, scales, logits, top_k, plan, turns,
+                                                                                      K, rows, E, groups, h, products);
     return hipGetLastError();
   };
-  auto up = [&](auto nj) { return experts(std::true_type{}, nj, ws + l.xp, xs, up_codes, up_scales, H, 2 * I, I / kMxBlock); };
+  auto up = [&](auto nj) { return experts(std::true_type{}, nj, up_codes, up_scales, H, 2 * I, I / kMxBlock); };
   // Few units of down's weights go straight to y: whole layers, us, direct / in two
   // launches, by turns (at most) x super-steps:
   //   4    2 x 1024 x 512    25 / 34        34   16 x 2048 x 512    30 / 33
@@ -638,11 +668,10 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
   if (e != hipSuccess) return e;
   if (direct) {
     auto* const f = T > 1 ? moe_direct_down_kernel<XT, 0> : (E <= 64 ? moe_direct_down_kernel<XT, 1> : moe_direct_down_kernel<XT, kLarge>);
-    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(ws + l.hp, hs, down_codes, down_scales, logits, top_k, plan, turns,
-                                                            T, H, I, E, Y);
+    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(h, down_codes, down_scales, logits, top_k, plan, turns, T, H, I, E, Y);
     return hipGetLastError();
   }
-  e = experts(std::false_type{}, Nj0{}, ws + l.hp, hs, down_codes, down_scales, I, H, (H + 63) / 64);
+  e = experts(std::false_type{}, Nj0{}, down_codes, down_scales, I, H, (H + 63) / 64);
   if (e != hipSuccess) return e;
   moe_combine_kernel<XT><<<dim3((unsigned)((H + 255) / 256), (unsigned)T), 64, 0, stream>>>(products, where, H, top_k, Y);
   return hipGetLastError();

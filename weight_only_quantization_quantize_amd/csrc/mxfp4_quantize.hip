@@ -1,5 +1,5 @@
 // Microscaled 4-bit floats (MXFP4): quantization, its inverse, and the split
-// of 16-bit activations into 6-bit pieces for the products.
+// of 16-bit activations into the fragments that the products' kernels read.
 //
 // Quantization of a block of 32 values x (format in mxfp4_device.h):
 //   b    = clamp(floor(log2 max|x|) - 2 + 127, 0, 254), 0 for a zero block
@@ -107,14 +107,15 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32
   }
 }
 
-// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], 0 in the place of
-// rows and blocks that are not there.
+// Scale bytes [rows, nblk] -> dwords [2 ceil(nblk / 8)][rows_pad], `past` in the place
+// of rows and blocks that are not there.
 constexpr int kScaleWaves = kThreads / 64;
 static_assert(kMxScaleRowPad % 64 == 0, "a wave's rows are whole");
 struct ScaleJob {
   const uint8_t* scales;
   uint32_t* out;
   int rows, rows_pad;
+  uint32_t past;
 };
 // Workgroup `block` of a job's: 64 rows, each wave 16 blocks of them (a lane a row,
 // so the writes are contiguous), the waves next to each other in the rows' lines.
@@ -122,8 +123,9 @@ __device__ inline void turn_scales(const ScaleJob& j, int nblk, int block) {
   const int ktiles = (nblk + 7) / 8 * 2, groups = j.rows_pad / 64;
   const int row = block % groups * 64 + ((int)threadIdx.x & 63), g = block / groups * kScaleWaves + ((int)threadIdx.x >> 6);
   if (4 * g >= ktiles) return;
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (row < j.rows) v = mx_scale_chunk(j.scales + (int64_t)row * nblk, g, nblk);
+  const uint32_t past = j.past * 0x01010101u;
+  u32x4_t v = {past, past, past, past};
+  if (row < j.rows) v = mx_scale_chunk(j.scales + (int64_t)row * nblk, g, nblk, j.past);
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     if (4 * g + q < ktiles) j.out[(int64_t)(4 * g + q) * j.rows_pad + row] = v[q];
@@ -137,10 +139,10 @@ __global__ __launch_bounds__(kThreads) void mxfp4_scales_kernel(ScaleJob w, Scal
 // Workgroups [0, split) split X, the rest turn W's scales.
 // One wave per fragment of R rows x 2048 / R elements (layout in
 // mxfp4_device.h).
-template <class XT, int R>
+template <int R>
 __global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* __restrict__ X, int M, int K,
-                                                               int ksteps, int frags, uint8_t* __restrict__ pieces,
-                                                               uint32_t* __restrict__ scales, ScaleJob w, int split) {
+                                                               int ksteps, int frags, uint8_t* __restrict__ out,
+                                                               ScaleJob w, int split) {
   if ((int)blockIdx.x >= split) {
     turn_scales(w, K / kMxBlock, (int)blockIdx.x - split);
     return;
@@ -152,18 +154,21 @@ __global__ __launch_bounds__(kThreads) void mxfp4_split_kernel(const uint16_t* _
   const int ks = f % ksteps;
   const int blk = R == 32 ? 2 * ks + lane / 32 : 16 * (ks / 4) + 4 * (lane / 16) + ks % 4;
   const int k = blk * kMxBlock;
-  float v[kMxBlock] = {};
-  if (row < M && k < K) mx_load_block<XT>(X + (int64_t)row * K + k, v);
-  const MxPieces s = mx_split(v);
-  mx_store_pieces(s, pieces + (int64_t)f * kMxFragBytes, scales + (int64_t)f * 64, lane);
+  u32x4_t v[4] = {};
+  if (row < M && k < K)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = reinterpret_cast<const u32x4_t*>(X + (int64_t)row * K + k)[j];
+  uint8_t* const to = out + (int64_t)f * kMxFragBytes + 16 * lane;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(to + 1024 * j) = v[j];
 }
 
 // Workgroups of a scale job.
 int64_t scale_blocks(int64_t rows, int64_t K) {
   return mxfp4_scale_rows(rows) / 64 * ((K + 512 * kScaleWaves - 1) / (512 * kScaleWaves));
 }
-ScaleJob scale_job(const void* scales, int64_t rows, void* out) {
-  return ScaleJob{static_cast<const uint8_t*>(scales), static_cast<uint32_t*>(out), (int)rows, (int)mxfp4_scale_rows(rows)};
+ScaleJob scale_job(const void* scales, int64_t rows, void* out, uint32_t past) {
+  return ScaleJob{static_cast<const uint8_t*>(scales), static_cast<uint32_t*>(out), (int)rows, (int)mxfp4_scale_rows(rows), past};
 }
 
 unsigned grid_for(int64_t units) {
@@ -204,23 +209,18 @@ hipError_t launch_mxfp4_scales(const void* Ws, int64_t N, void* wout, const void
                                hipStream_t stream) {
   const int64_t wblocks = scale_blocks(N, K), ablocks = scale_blocks(M, K);
   mxfp4_scales_kernel<<<(unsigned)(wblocks + ablocks), kThreads, 0, stream>>>(
-      scale_job(Ws, N, wout), scale_job(As, M, aout), (int)(K / kMxBlock), (int)wblocks);
+      scale_job(Ws, N, wout, 0u), scale_job(As, M, aout, 0u), (int)(K / kMxBlock), (int)wblocks);
   return hipGetLastError();
 }
 
-hipError_t launch_mxfp4_split(const void* X, int xdtype, int64_t M, int64_t K, int R, int64_t row_groups,
-                              int64_t ksteps, void* pieces, void* scales, const void* Ws, int64_t N, void* wout,
-                              hipStream_t stream) {
+hipError_t launch_mxfp4_split(const void* X, int64_t M, int64_t K, int R, int64_t row_groups, int64_t ksteps, void* out,
+                              const void* Ws, int64_t N, void* wout, hipStream_t stream) {
   const int frags = (int)(row_groups * ksteps);
   const int split = (frags + kThreads / 64 - 1) / (kThreads / 64);
   const unsigned grid = (unsigned)(split + (Ws ? scale_blocks(N, K) : 0));
-  const ScaleJob w = scale_job(Ws, N, wout);
-  const auto* xp = static_cast<const uint16_t*>(X);
-  auto* pp = static_cast<uint8_t*>(pieces);
-  auto* sp = static_cast<uint32_t*>(scales);
-  auto* const f = R == 32 ? (xdtype == 0 ? mxfp4_split_kernel<F16, 32> : mxfp4_split_kernel<BF16, 32>)
-                          : (xdtype == 0 ? mxfp4_split_kernel<F16, 16> : mxfp4_split_kernel<BF16, 16>);
-  f<<<grid, kThreads, 0, stream>>>(xp, (int)M, (int)K, (int)ksteps, frags, pp, sp, w, split);
+  auto* const f = R == 32 ? mxfp4_split_kernel<32> : mxfp4_split_kernel<16>;
+  f<<<grid, kThreads, 0, stream>>>(static_cast<const uint16_t*>(X), (int)M, (int)K, (int)ksteps, frags, static_cast<uint8_t*>(out),
+                                   scale_job(Ws, N, wout, 127u), split);
   return hipGetLastError();
 }
 

@@ -2,20 +2,23 @@
 // few columns, bound by streaming the weights:
 //   Y[m, n] = sum_b 2^(sA + sW - 254) sum_{k in block b} a[m, k] w[n, k].
 //
-// Work split.  K is cut into super-steps of 512 (four steps of
-// v_mfma_scale_f32_16x16x128).  A workgroup of 8 waves holds `slots` teams of `team`
-// waves; a wave owns one or two super-steps, whose activations stay in registers
+// Work split.  K is cut into super-steps of 512 (four steps of 128).  A workgroup of 8
+// waves holds `slots` teams of `team` waves; a wave owns one or two super-steps, whose activations stay in registers
 // for the whole launch, and the team walks over its run of tiles of 16 columns of
 // Y: the only traffic left is the weights'.  The team's partial sums of a tile meet
 // in LDS and are added in a fixed order.  More rows than the registers hold (16 of
-// split activations, 64 of 4-bit ones) are cut into row groups, workgroups of their
+// 16-bit activations, 64 of 4-bit ones) are cut into row groups, workgroups of their
 // own that read the same weights at the same time from the same L2.
+//
+// 16-bit activations are read from X as the matrix operands: a lane's part of a
+// step is the 64 contiguous bytes of one block.
 //
 // Loads.  Units of 16 rows by 512 K in runs of 256 bytes (mxfp4_stream.h): loads
 // of 16 rows x 64 bytes straight into the matrix operands reached 2.2 TB/s.  A wave
 // has up to four units on their way, 139 KB a compute unit; 16 waves with one each
-// had half of that and took 34 us for 16 rows of 28672 x 8192 (125 MB), where this
-// takes 26 (4.8 TB/s); 16 rows of 4-bit activations take 23.
+// had half of that and took 34 us for 16 rows of 28672 x 8192 (125 MB, 4-bit
+// activations), where this takes 23; 16-bit ones take 32: the conversions and the
+// longer matrix steps hold a unit's registers longer, and the loads wait for them.
 #include "mxfp4_stream.h"
 #include "woq_internal.h"
 
@@ -26,28 +29,24 @@ constexpr int kWaves = 8;        // K <= 8192
 constexpr int kLongWaves = 16;   // longer rows
 constexpr int kTargetGroups = 256;  // workgroups: one per compute unit
 
-// Activations: 1, microscaled; kMxPieces, split before; kRaw, 16-bit ones that the
-// kernel splits itself.
-constexpr int kRaw = 4;
+// Activations: kMx, microscaled; kRows, 16-bit rows; kFragments, 16-bit ones laid out
+// in fragments of 16 rows before (rows longer than the registers hold, read again for
+// every tile).
+enum Operand { kMx, kRows, kFragments };
 
 // One super-step of a chunk of 16 rows of activations.
-template <int PIECES>
-struct Acts;
+template <Operand OP>
+struct Acts {
+  MxActivations x;
+};
 template <>
-struct Acts<1> {
+struct Acts<kMx> {
   u32x4_t v[4];
   uint32_t s;
 };
-template <>
-struct Acts<kMxPieces> {
-  MxActivations a[4];
-};
-template <>
-struct Acts<kRaw> : Acts<kMxPieces> {};
 
 // Chunk t's super-step S; A, As, M: the row group's.
-template <class XT>
-__device__ inline void load_acts(Acts<1>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t, int S,
+__device__ inline void load_acts(Acts<kMx>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t, int S,
                                  int M, int nblk, int, int lane) {
   const int r = lane & 15, q = lane >> 4;
   int m = 16 * t + r;
@@ -63,101 +62,83 @@ __device__ inline void load_acts(Acts<1>& act, const uint8_t* __restrict__ A, co
   __builtin_memcpy(&act.s, As + (uint32_t)(m * nblk + from), 4);
   act.s >>= 8 * ((b0 - from) & 3);
 }
-template <class XT>
-__device__ inline void load_acts(Acts<kMxPieces>& act, const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int t,
-                                 int S, int, int, int supers, int lane) {
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int64_t f = ((int64_t)t * supers + S) * 4 + s;
-    mx_load_activations(act.a[s], A + f * kMxFragBytes, As + f * kMxFragScaleBytes, mx_place(0, lane));
-  }
+__device__ inline void load_acts(Acts<kRows>& act, const uint8_t* __restrict__ A, const uint8_t*, int t, int S, int M, int nblk,
+                                 int, int lane) {
+  int m = 16 * t + (lane & 15);
+  m = m < M ? m : M - 1;
+  mx_load_activations(act.x, reinterpret_cast<const uint16_t*>(A) + (int64_t)m * nblk * kMxBlock, nblk, S, lane);
 }
-// 16-bit activations of super-step S on their way, and split: a lane's operand at
-// step s is the split of block 4 (lane / 16) + s of its row.
-struct RawActs {
-  u32x4_t x[4][4];
-};
-__device__ inline void load_raw(RawActs& raw, const uint8_t* __restrict__ A, int S, int M, int nblk, int lane) {
-  const int m = (lane & 15) < M ? lane & 15 : M - 1;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int b = kSuper * S + 4 * (lane >> 4) + s;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      raw.x[s][q] = reinterpret_cast<const u32x4_t*>(A)[((int64_t)m * nblk + (b < nblk ? b : nblk - 1)) * 4 + q];
-  }
-}
-template <class XT>
-__device__ inline void split_raw(Acts<kRaw>& act, const RawActs& raw, int S, int nblk, int lane) {
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const bool live = kSuper * S + 4 * (lane >> 4) + s < nblk;
-    float v[kMxBlock];
-#pragma unroll
-    for (int k = 0; k < kMxBlock; ++k) {
-      const float x = XT::to_f32((uint16_t)(raw.x[s][k / 8][k / 2 % 4] >> (16 * (k % 2))));
-      v[k] = live ? x : 0.0f;
-    }
-    const MxPieces p = mx_split(v);
-    auto piece = [&](int i) {
-      return mx_operand(u32x4_t{p.p[i][0], p.p[i][1], p.p[i][2], p.p[i][3]}, u32x2_t{p.p[i][4], p.p[i][5]});
-    };
-    act.a[s] = MxActivations{piece(0), piece(1), piece(2), (int)p.scale};
-  }
-}
-template <int S>
-__device__ inline void multiply(float4_t& acc, const Acts<1>& act, i32x8_t w, int scale) {
-  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(act.v[S]), w, acc, kMfmaFp4, kMfmaFp4, S, (int)act.s, S, scale);
+__device__ inline void load_acts(Acts<kFragments>& act, const uint8_t* __restrict__ A, const uint8_t*, int t, int S, int, int,
+                                 int supers, int lane) {
+  mx_load_fragments(act.x, A + ((int64_t)t * supers + S) * 4 * kMxFragBytes, 16u * (uint32_t)lane);
 }
 
+// acc[t] += a staged unit of weights times chunk t's super-step of activations, of(t).
+template <class XT, Operand OP, int TC, class F>
+__device__ __forceinline__ void multiply(float4_t (&acc)[TC], F&& of, const uint8_t* __restrict__ stage, int lane) {
+  if constexpr (OP == kMx) {
+    const int scale = (int)mx_staged_scale(stage, lane);
+    mx_each_step([&](auto sel) {
+      constexpr int s = decltype(sel)::value;
+      const i32x8_t w = mx_operand(mx_staged_weights(stage, s, lane));
+#pragma unroll
+      for (int t = 0; t < TC; ++t)
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(of(t).v[s]), w, acc[t], kMfmaFp4, kMfmaFp4, s,
+                                                                  (int)of(t).s, s, scale);
+    });
+  } else {
+    static_assert(TC == 1, "16 rows");
+    mx_multiply_unit<XT>(acc[0], of(0).x, stage, lane);
+  }
+}
+// What the sums of products are multiplied by.
+template <class XT, Operand OP>
+constexpr float kGain = OP == kMx ? 1.0f : kMxGain<XT>;
+
 // What a row group's workgroups see of the operands.
-template <int PIECES, int TC>
+template <Operand OP, int TC>
 __device__ inline void enter_row_group(const uint8_t* __restrict__& A, const uint8_t* __restrict__& As, int& M,
                                        uint16_t* __restrict__& Y, int N, int nblk, int supers) {
   const int m0 = (int)blockIdx.y * 16 * TC;
   M = M - m0 < 16 * TC ? M - m0 : 16 * TC;
   Y += (int64_t)m0 * N;
-  if constexpr (PIECES == 1) {
+  if constexpr (OP == kMx) {
     A += (int64_t)m0 * nblk * 16;
     As += (int64_t)m0 * nblk;
-  } else if constexpr (PIECES == kRaw) {
+  } else if constexpr (OP == kRows) {
     A += (int64_t)m0 * nblk * (2 * kMxBlock);
   } else {
     A += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragBytes;
-    As += (int64_t)blockIdx.y * TC * supers * 4 * kMxFragScaleBytes;
   }
 }
 
 // Rows 4 q .. 4 q + 3 of chunk t, column n of Y.
 template <class YT>
-__device__ inline void store(uint16_t* __restrict__ Y, int M, int N, int t, int n, int q, const float4_t& v) {
+__device__ inline void store(uint16_t* __restrict__ Y, int M, int N, int t, int n, int q, const float4_t& v, float gain) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int m = 16 * t + 4 * q + e;
-    if (m < M && n < N) Y[(int64_t)m * N + n] = YT::from_f32(v[e]);
+    if (m < M && n < N) Y[(int64_t)m * N + n] = YT::from_f32(v[e] * gain);
   }
 }
 
 // K <= 8192.  A team's wave owns SU super-steps (tw, tw + team) whose activations
 // stay in registers; the team takes TI tiles at a time while the next ones' units
 // are on their way.
-template <class YT, int PIECES, int TC, int SU, int TI>
+template <class YT, Operand OP, int TC, int SU, int TI>
 __global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ W,
     const uint8_t* __restrict__ Ws, int M, int N, int nblk, int team, int supers, uint16_t* __restrict__ Y) {
   constexpr int NU = SU * TI;  // units a turn
-  constexpr bool kSpread = PIECES == kMxPieces && SU == 2;  // one super-step's third pieces go to LDS: the registers are full
   constexpr int kBuffers = TI * TC > 4 ? 1 : 2;
   __shared__ __attribute__((aligned(16))) uint8_t stage_all[kWaves][kUnitStage];
   __shared__ float4_t part[kBuffers][kWaves][TI * TC][64];
-  __shared__ u32x4_t third4[kSpread ? kWaves : 1][4][64];
-  __shared__ u32x2_t third2[kSpread ? kWaves : 1][4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int slots = (int)(blockDim.x >> 6) / team;
   const int slot = wave / team, tw = wave % team;
   uint8_t* const stage = stage_all[wave];
-  enter_row_group<PIECES, TC>(A, As, M, Y, N, nblk, supers);
+  enter_row_group<OP, TC>(A, As, M, Y, N, nblk, supers);
 
   // the team's run of tiles; all teams of the workgroup make as many turns
   const int tiles = (N + 15) >> 4, teams = (int)gridDim.x * slots;
@@ -179,34 +160,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
     mx_load_unit(u[j], W + row * nblk * 16, Ws + row * nblk, (int)(N - row - 1), (N - row) * nblk, live ? nblk : 1, live ? S : 0, lane);
     __builtin_amdgcn_sched_barrier(0);
   };
-  Acts<PIECES> act[TC][SU];
-  if constexpr (PIECES == kRaw) {
-    static_assert(TC == 1 && SU == 1);
-    RawActs raw;
-    load_raw(raw, A, tw < supers ? tw : supers - 1, M, nblk, lane);
+  Acts<OP> act[TC][SU];
 #pragma unroll
-    for (int j = 0; j < NU; ++j) ahead(j, begin);
-    split_raw<YT>(act[0][0], raw, tw, nblk, lane);  // while the weights come
-  } else {
+  for (int t = 0; t < TC; ++t)
+#pragma unroll
+    for (int i = 0; i < SU; ++i)
+      load_acts(act[t][i], A, As, t, super_of(i) < supers ? super_of(i) : supers - 1, M, nblk, supers, lane);
+  // (before the activations instead: 4-bit products took 1 .. 1.5 us more)
+#pragma unroll
+  for (int j = 0; j < NU; ++j) ahead(j, begin);
+  if constexpr (OP == kRows) {  // while the weights come
 #pragma unroll
     for (int t = 0; t < TC; ++t)
 #pragma unroll
-      for (int i = 0; i < SU; ++i) {
-        load_acts<YT>(act[t][i], A, As, t, super_of(i) < supers ? super_of(i) : supers - 1, M, nblk, supers, lane);
-        if constexpr (kSpread) {
-          if (i == 1) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const i32x8_t p = act[t][i].a[s].p2;
-              third4[wave][s][lane] = u32x4_t{(uint32_t)p[0], (uint32_t)p[1], (uint32_t)p[2], (uint32_t)p[3]};
-              third2[wave][s][lane] = u32x2_t{(uint32_t)p[4], (uint32_t)p[5]};
-            }
-          }
-        }
-      }
-    // (before the activations instead: 4-bit products took 1 .. 1.5 us more)
-#pragma unroll
-    for (int j = 0; j < NU; ++j) ahead(j, begin);
+      for (int i = 0; i < SU; ++i) mx_mask_activations(act[t][i].x, nblk, super_of(i), lane);
   }
   float4_t acc[TI][TC];
   auto take = [&](int t0, auto more) {
@@ -219,22 +186,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
       const bool live = tile < end && S < supers;
       if (live) mx_stage_unit(u[j], stage, (int)(N - row - 1), (N - row) * nblk, nblk, S, l);
       if constexpr (decltype(more)::value) ahead(j, t0 + TI);
-      if (live) {
-        const int scale = mx_staged_scale(stage, l);
-        mx_each_step([&](auto sel) {
-          constexpr int s = decltype(sel)::value;
-          const i32x8_t w = mx_staged_weights(stage, s, l);
-          if constexpr (PIECES == 1) {
-#pragma unroll
-            for (int t = 0; t < TC; ++t) multiply<s>(acc[j / SU][t], act[t][j % SU], w, scale);
-          } else {
-            static_assert(TC == 1);
-            MxActivations a = act[0][j % SU].a[s];
-            if (kSpread && j % SU == 1) a.p2 = mx_operand(third4[wave][s][l], third2[wave][s][l]);
-            mx_multiply<s>(acc[j / SU][0], a, w, scale);
-          }
-        });
-      }
+      if (live) multiply<YT, OP>(acc[j / SU], [&](int t) -> const Acts<OP>& { return act[t][j % SU]; }, stage, l);
     }
   };
   const int turns = (longest + TI - 1) / TI;
@@ -263,7 +215,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += p[e];
         }
-        store<YT>(Y, M, N, i % TC, tile * 16 + (l & 15), l >> 4, v);
+        store<YT>(Y, M, N, i % TC, tile * 16 + (l & 15), l >> 4, v, kGain<YT, OP>);
       }
     }
     if (kBuffers == 1) __syncthreads();
@@ -272,7 +224,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void mxfp4_skinny_kernel(
 
 // Longer rows: wave w takes the super-steps w, w + 16, ... of a tile and loads the
 // activations of each; the next unit is on its way meanwhile.
-template <class YT, int PIECES, int TC>
+template <class YT, Operand OP, int TC>
 __global__ __launch_bounds__(kLongWaves * 64) void mxfp4_skinny_long_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, const uint8_t* __restrict__ W,
     const uint8_t* __restrict__ Ws, int M, int N, int nblk, int supers, uint16_t* __restrict__ Y) {
@@ -283,7 +235,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void mxfp4_skinny_long_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (N + 15) >> 4;
   uint8_t* const stage = stage_all[wave];
-  enter_row_group<PIECES, TC>(A, As, M, Y, N, nblk, supers);
+  enter_row_group<OP, TC>(A, As, M, Y, N, nblk, supers);
 
   MxUnit u;
   auto left = [&](int tile) { return (int64_t)(N - tile * 16) * nblk; };  // scale bytes from the tile on
@@ -299,69 +251,65 @@ __global__ __launch_bounds__(kLongWaves * 64) void mxfp4_skinny_long_kernel(
     float4_t acc[TC] = {};
     for (int k = 0; k < rounds; ++k) {
       const int S = wave + k * team;
-      mx_stage_unit(u, stage, N - tile * 16 - 1, left(tile), nblk, S, lane);
-      Acts<PIECES> act[TC];
+      int l = lane;
+      if constexpr (OP == kFragments) asm volatile("" : "+v"(l));  // addresses are worked out each time: kept, they spill
+      mx_stage_unit(u, stage, N - tile * 16 - 1, left(tile), nblk, S, l);
+      Acts<OP> act[TC];
 #pragma unroll
-      for (int t = 0; t < TC; ++t) load_acts<YT>(act[t], A, As, t, S < supers ? S : supers - 1, M, nblk, supers, lane);
+      for (int t = 0; t < TC; ++t) load_acts(act[t], A, As, t, S < supers ? S : supers - 1, M, nblk, supers, l);
       const int Sn = k + 1 < rounds ? S + team : wave;
       const int tn = k + 1 < rounds ? tile : next;
       load_weights(tn < tiles ? tn : tile, Sn < supers ? Sn : supers - 1);
-      if (S < supers) {
-        const int scale = mx_staged_scale(stage, lane);
-        mx_each_step([&](auto sel) {
-          constexpr int s = decltype(sel)::value;
-          const i32x8_t w = mx_staged_weights(stage, s, lane);
-#pragma unroll
-          for (int t = 0; t < TC; ++t) {
-            if constexpr (PIECES == 1)
-              multiply<s>(acc[t], act[t], w, scale);
-            else
-              mx_multiply<s>(acc[t], act[t].a[s], w, scale);
-          }
-        });
-      }
+      if (S < supers) multiply<YT, OP>(acc, [&](int t) -> const Acts<OP>& { return act[t]; }, stage, l);
     }
     const int buf = it & 1;
+    int l = lane;
+    if constexpr (OP == kFragments) asm volatile("" : "+v"(l));
 #pragma unroll
-    for (int t = 0; t < TC; ++t) part[buf][wave][t][lane] = acc[t];
+    for (int t = 0; t < TC; ++t) part[buf][wave][t][l] = acc[t];
     __syncthreads();
     // a wave a chunk adds the partials, other ones each turn
 #pragma unroll
     for (int t = 0; t < TC; ++t) {
       if (wave == (it + t) % team) {
-        float4_t v = part[buf][0][t][lane];
+        float4_t v = part[buf][0][t][l];
         for (int w = 1; w < team; ++w) {
-          const float4_t p = part[buf][w][t][lane];
+          const float4_t p = part[buf][w][t][l];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += p[e];
         }
-        store<YT>(Y, M, N, t, tile * 16 + (lane & 15), lane >> 4, v);
+        store<YT>(Y, M, N, t, tile * 16 + (l & 15), l >> 4, v, kGain<YT, OP>);
       }
     }
     tile = next;
   }
 }
 
-template <class YT, int PIECES, int TC>
+// Workgroups a row group: a multiple of 8, so that a column group's are on one XCD
+// (three row groups of 85 took 28 us where four of 64 take 26).
+int share(int rgroups) {
+  const int n = kTargetGroups / rgroups & ~7;
+  return n < 8 ? 8 : n;
+}
+
+template <class YT, Operand OP, int TC>
+hipError_t launch_long(const void* A, const void* As, const void* W, const void* Ws, int M, int N, int nblk, void* Y,
+                       hipStream_t stream) {
+  const int tiles = (N + 15) / 16, rgroups = (M + 16 * TC - 1) / (16 * TC), target = share(rgroups);
+  const dim3 grid((unsigned)(tiles < target ? tiles : target), (unsigned)rgroups);
+  mxfp4_skinny_long_kernel<YT, OP, TC><<<grid, kLongWaves * 64, 0, stream>>>(
+      static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As), static_cast<const uint8_t*>(W),
+      static_cast<const uint8_t*>(Ws), M, N, nblk, (nblk + kSuper - 1) / kSuper, static_cast<uint16_t*>(Y));
+  return hipGetLastError();
+}
+
+template <class YT, Operand OP, int TC>
 hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, int M, int N, int nblk, void* Y,
                   hipStream_t stream) {
-  const auto* ap = static_cast<const uint8_t*>(A);
-  const auto* asp = static_cast<const uint8_t*>(As);
-  const auto* wp = static_cast<const uint8_t*>(W);
-  const auto* wsp = static_cast<const uint8_t*>(Ws);
-  auto* yp = static_cast<uint16_t*>(Y);
   const int tiles = (N + 15) / 16, supers = (nblk + kSuper - 1) / kSuper;
-  // workgroups a row group: a multiple of 8, so that a column group's are on one XCD
-  // (three row groups of 85 took 28 us where four of 64 take 26)
-  const int rgroups = (M + 16 * TC - 1) / (16 * TC);
-  const int share = kTargetGroups / rgroups & ~7, target = share < 8 ? 8 : share;
-  if constexpr (TC < 4 && PIECES != kRaw) {  // those come with K <= 8192 only
-    if (supers > 2 * kWaves) {
-      const dim3 grid((unsigned)(tiles < target ? tiles : target), (unsigned)rgroups);
-      mxfp4_skinny_long_kernel<YT, PIECES, TC><<<grid, kLongWaves * 64, 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, supers, yp);
-      return hipGetLastError();
-    }
-  }
+  const int rgroups = (M + 16 * TC - 1) / (16 * TC), target = share(rgroups);
+  if constexpr (OP == kMx && TC < 4)  // 64 rows at once come with K <= 8192 only
+    if (supers > 2 * kWaves) return launch_long<YT, OP, TC>(A, As, W, Ws, M, N, nblk, Y, stream);
   const bool two = supers > kWaves;
   const int team = two ? (supers + 1) / 2 : supers;
   // short rows: several teams a workgroup, where there are tiles for them
@@ -375,45 +323,30 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   // four) or where 64 rows leave no registers for them
   const int most = (tiles + (int)grid.x * slots - 1) / ((int)grid.x * slots);
   auto* const f = [&] {
-    if constexpr (PIECES == kMxPieces)  // K > 4096
-      return most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 2, 2> : mxfp4_skinny_kernel<YT, PIECES, TC, 2, 1>;
-    else if constexpr (PIECES == kRaw)  // K <= 4096
-      return most > 2   ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 4>
-             : most > 1 ? mxfp4_skinny_kernel<YT, PIECES, TC, 1, 2>
-                        : mxfp4_skinny_kernel<YT, PIECES, TC, 1, 1>;
-    else if constexpr (TC == 4)  // N > 8192: several tiles a team
-      return two ? mxfp4_skinny_kernel<YT, 1, 4, 2, 1> : mxfp4_skinny_kernel<YT, 1, 4, 1, 2>;
+    if constexpr (TC == 4)  // N > 8192: several tiles a team
+      return two ? mxfp4_skinny_kernel<YT, kMx, 4, 2, 1> : mxfp4_skinny_kernel<YT, kMx, 4, 1, 2>;
     else
-      return two ? (most > 1 ? mxfp4_skinny_kernel<YT, 1, TC, 2, 2> : mxfp4_skinny_kernel<YT, 1, TC, 2, 1>)
-                 : (most > 2   ? mxfp4_skinny_kernel<YT, 1, TC, 1, 4>
-                    : most > 1 ? mxfp4_skinny_kernel<YT, 1, TC, 1, 2>
-                               : mxfp4_skinny_kernel<YT, 1, TC, 1, 1>);
+      return two ? (most > 1 ? mxfp4_skinny_kernel<YT, OP, TC, 2, 2> : mxfp4_skinny_kernel<YT, OP, TC, 2, 1>)
+                 : (most > 2   ? mxfp4_skinny_kernel<YT, OP, TC, 1, 4>
+                    : most > 1 ? mxfp4_skinny_kernel<YT, OP, TC, 1, 2>
+                               : mxfp4_skinny_kernel<YT, OP, TC, 1, 1>);
   }();
-  f<<<grid, (unsigned)(slots * team * 64), 0, stream>>>(ap, asp, wp, wsp, M, N, nblk, team, supers, yp);
+  f<<<grid, (unsigned)(slots * team * 64), 0, stream>>>(static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(As),
+                                                        static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(Ws), M, N,
+                                                        nblk, team, supers, static_cast<uint16_t*>(Y));
   return hipGetLastError();
 }
 
 }  // namespace
 
-// 16-bit activations.  Up to K = 4096 (a super-step a wave) each workgroup splits
-// them itself, while its first weights come: 16 rows of 512 x 512 take 5.5 us in
-// place of 7.3 with a launch for the split, of 4096 x 4096 9.9 / 9.0, of 16384 x 4096
-// 12.2 / 12.6, and the host has a launch and a workspace less.  Two super-steps a
-// wave would take twice that time and more registers than there are.
-bool mxfp4_skinny_splits(int64_t K) { return K <= 512 * kWaves; }
-hipError_t launch_mxfp4_skinny_raw(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
-                                   int64_t K, void* Y, hipStream_t stream) {
+// 16-bit activations: rows of X (K <= mxfp4_skinny_max_k()), or fragments of 16 rows.
+int64_t mxfp4_skinny_max_k() { return 2 * kWaves * 512; }
+hipError_t launch_mxfp4_skinny(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N, int64_t K,
+                               void* Y, hipStream_t stream) {
   const int nblk = (int)(K / kMxBlock);
-  return xdtype == 0 ? launch<F16, kRaw, 1>(X, nullptr, codes, scales, (int)M, (int)N, nblk, Y, stream)
-                     : launch<BF16, kRaw, 1>(X, nullptr, codes, scales, (int)M, (int)N, nblk, Y, stream);
-}
-
-// 16-bit activations, split in fragments of 16 rows.
-hipError_t launch_mxfp4_skinny(const void* pieces, const void* piece_scales, const void* codes, const void* scales,
-                               int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream) {
-  const int nblk = (int)(K / kMxBlock);
-  return ydtype == 0 ? launch<F16, kMxPieces, 1>(pieces, piece_scales, codes, scales, (int)M, (int)N, nblk, Y, stream)
-                     : launch<BF16, kMxPieces, 1>(pieces, piece_scales, codes, scales, (int)M, (int)N, nblk, Y, stream);
+  auto* const f = K <= mxfp4_skinny_max_k() ? (xdtype == 0 ? launch<F16, kRows, 1> : launch<BF16, kRows, 1>)
+                                            : (xdtype == 0 ? launch_long<F16, kFragments, 1> : launch_long<BF16, kFragments, 1>);
+  return f(X, nullptr, codes, scales, (int)M, (int)N, nblk, Y, stream);
 }
 
 // Microscaled activations.
@@ -425,9 +358,9 @@ hipError_t launch_mxfp4_skinny_mx(const void* A, const void* As, const void* cod
   // than weights (64 rows of 4096 x 4096: 6.6 us in two row groups, 8.0 in one;
   // 28672 x 8192: 34, 31)
   const int chunks = M <= 16 ? 1 : (M <= 32 || N <= 8192 ? 2 : 4);
-  auto* const f = chunks == 1   ? (ydtype == 0 ? launch<F16, 1, 1> : launch<BF16, 1, 1>)
-                  : chunks == 2 ? (ydtype == 0 ? launch<F16, 1, 2> : launch<BF16, 1, 2>)
-                                : (ydtype == 0 ? launch<F16, 1, 4> : launch<BF16, 1, 4>);
+  auto* const f = chunks == 1   ? (ydtype == 0 ? launch<F16, kMx, 1> : launch<BF16, kMx, 1>)
+                  : chunks == 2 ? (ydtype == 0 ? launch<F16, kMx, 2> : launch<BF16, kMx, 2>)
+                                : (ydtype == 0 ? launch<F16, kMx, 4> : launch<BF16, kMx, 4>);
   return f(A, As, codes, scales, (int)M, (int)N, nblk, Y, stream);
 }
 

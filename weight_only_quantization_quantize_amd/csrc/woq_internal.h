@@ -137,11 +137,10 @@ hipError_t launch_mxfp4_quantize(const void* x, int xdtype, int64_t M, int64_t K
                                  hipStream_t stream);
 hipError_t launch_mxfp4_dequantize(const void* codes, const void* scales, int64_t M, int64_t K, int outdtype,
                                    void* out, hipStream_t stream);
-// Splits 16-bit X [M, K] into 6-bit pieces, fragment-major: row_groups groups
-// of R rows (32 or 16) by ksteps steps of 2048 / R elements.
-hipError_t launch_mxfp4_split(const void* X, int xdtype, int64_t M, int64_t K, int R, int64_t row_groups,
-                              int64_t ksteps, void* pieces, void* scales, const void* Ws, int64_t N, void* wout,
-                              hipStream_t stream);
+// Lays 16-bit X [M, K] out in fragments: row_groups groups of R rows (32 or 16) by
+// ksteps steps of 2048 / R elements.
+hipError_t launch_mxfp4_split(const void* X, int64_t M, int64_t K, int R, int64_t row_groups, int64_t ksteps, void* out,
+                              const void* Ws, int64_t N, void* wout, hipStream_t stream);
 // Scale bytes [rows, K / 32] in the tile kernels' order: one dword per row and
 // 128 of K, [K tile][mxfp4_scale_rows(rows)]; launch_mxfp4_split does W's beside
 // the split where Ws is given.
@@ -160,13 +159,11 @@ hipError_t launch_mxfp4_gemm(const void* X, int xdtype, const void* codes, const
 hipError_t launch_mxfp4_gemm_mx(const void* A, const void* As, const void* W, const void* Ws, int64_t M, int64_t N,
                                 int64_t K, int ydtype, void* Y, void* workspace, hipStream_t stream);
 size_t mxfp4_gemm_mx_workspace_bytes(int64_t M, int64_t N, int64_t K);
-// The same for a few rows or small outputs: 16-bit activations split in the kernel
-// (K <= 4096) or before, in fragments of 16 rows; microscaled activations.
-bool mxfp4_skinny_splits(int64_t K);
-hipError_t launch_mxfp4_skinny_raw(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N,
-                                   int64_t K, void* Y, hipStream_t stream);
-hipError_t launch_mxfp4_skinny(const void* pieces, const void* piece_scales, const void* codes, const void* scales,
-                               int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream);
+// The same for a few rows or small outputs: 16-bit rows (K <= mxfp4_skinny_max_k()) or
+// fragments of 16 of them; microscaled activations.
+int64_t mxfp4_skinny_max_k();
+hipError_t launch_mxfp4_skinny(const void* X, int xdtype, const void* codes, const void* scales, int64_t M, int64_t N, int64_t K,
+                               void* Y, hipStream_t stream);
 hipError_t launch_mxfp4_skinny_mx(const void* A, const void* As, const void* codes, const void* scales, int64_t M,
                                   int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream);
 // A mixture-of-experts layer on a few tokens.

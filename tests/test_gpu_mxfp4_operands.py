@@ -156,6 +156,24 @@ def test_scale_bytes_of_the_whole_range_together(M, N, K, dtype):
         close(product(x, codes, scales), host(x), values(codes, scales), dtype, f"largest scales {M} {N} {K}")
 
 
+@pytest.mark.parametrize("M", [1, 2, 40])
+@pytest.mark.parametrize("K", [32, 1056, 4096])
+def test_sums_of_a_block_stay_finite_at_both_ends(M, K):
+    # 32 bf16 activations of up to 2^128 by small weights, and subnormal ones by large weights:
+    # raw codes times activations are out of fp32's range, their products are not
+    g = torch.Generator().manual_seed(K)
+    for top, low, high in ((127, 0, 30), (-124, 220, 250)):
+        x = (torch.randn(M, K, generator=g).sign().double() * (1 + torch.rand(M, K, generator=g).double()) * 2.0 ** top)
+        x[:, ::5] = x[:, ::5].abs()  # not all of them cancel
+        if top < 0:
+            x = x * torch.exp2(-10 * torch.rand(M, K, generator=g).double())
+        x = x.clamp(-3.38e38, 3.38e38).to(torch.bfloat16)
+        codes, scales = random_weights(45, K, K + 1, low, high)
+        codes[::3] |= 0x77  # rows of the largest magnitude
+        codes[6] &= 0x77    # and one of one sign
+        close(product(x, codes, scales), host(x), values(codes, scales), torch.bfloat16, f"ends {M} {K} 2^{top}")
+
+
 def test_nan_blocks_beside_the_lowest_and_highest_scales():
     for M, N, K in ((2, 40, 256), (40, 40, 96), (300, 400, 160), (9, 40, 8736)):
         for dtype in TYPES:

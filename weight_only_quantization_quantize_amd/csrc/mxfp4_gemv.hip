@@ -4,10 +4,12 @@
 // Bound by streaming the codes and scales once: 17/32 byte per weight.  A lane
 // owns one block of 32 K (16 bytes of codes, one scale byte); its 32
 // activations stay in 16 registers while rows stream past.  A code pair is
-// widened to the activation's type by one conversion at scale 1 (every e2m1
-// value is exact there) and multiplied by one dot2 with fp32 accumulation; the
-// block's sum is then scaled in fp32, so no weight is rounded whatever its
-// scale and x is used as given.
+// widened to the activation's type by one conversion at a fixed scale, where every
+// e2m1 value is exact, and multiplied by one dot2 with fp32 accumulation; the
+// block's sum is then scaled in fp32, so no weight is rounded whatever its scale
+// and x is used as given.  The fixed scale is 1 for fp16 (a block's sum is below
+// 2^24) and 2^-8 for bf16: 32 products of up to 6 2^-8 2^128 stay below 2^128, and
+// those of bf16's smallest number 2^-133 are multiples of 2^-142, which fp32 holds.
 //
 // Rows.  A row's blocks are spread over `team` lanes (a power of two up to 64;
 // longer rows over several waves, `segs` of them).  A workgroup holds 8 waves
@@ -24,24 +26,22 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kMaxSegs = 8;  // K <= 8 * 64 * 32 = 16384 here
 
+// sum of x times the weights of scale byte b
 template <class XT>
-__device__ inline float block_dot(u32x4_t c, const uint32_t (&x)[16]) {
-  float a = 0.0f, b = 0.0f;
+__device__ inline float block_dot(u32x4_t c, const uint32_t (&x)[16], uint32_t b) {
+  float p = 0.0f, q = 0.0f;
+  constexpr float kScale = kMxIsF16<XT> ? 1.0f : 0x1p-8f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if constexpr (XT::kMagic2 == F16::kMagic2) {
-      a = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 0)), x[4 * j], a);
-      b = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 1)), x[4 * j + 1], b);
-      a = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 2)), x[4 * j + 2], a);
-      b = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 3)), x[4 * j + 3], b);
-    } else {
-      a = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], 1.0f, 0)), x[4 * j], a);
-      b = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], 1.0f, 1)), x[4 * j + 1], b);
-      a = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], 1.0f, 2)), x[4 * j + 2], a);
-      b = XT::dot2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], 1.0f, 3)), x[4 * j + 3], b);
-    }
+    const u32x4_t w = mx_widen_as_is<XT>(c[j], __builtin_bit_cast(uint32_t, kScale) >> 23);
+    p = XT::dot2(w[0], x[4 * j], p);
+    q = XT::dot2(w[1], x[4 * j + 1], q);
+    p = XT::dot2(w[2], x[4 * j + 2], p);
+    q = XT::dot2(w[3], x[4 * j + 3], q);
   }
-  return a + b;
+  if constexpr (kMxIsF16<XT>) return (p + q) * mx_pow2(b);
+  const float d = ldexpf(p + q, (int)b - 127 + 8);  // 2^(b - 119) itself may be out of range
+  return b == (uint32_t)kMxNan ? __builtin_bit_cast(float, 0x7FC00000u) : d;
 }
 
 // nblk: blocks per row.  Thread layout: wave = slot * segs + seg; a wave holds
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kWaves * 64) void mxfp4_gemv_kernel(const uint16_t*
   }
 #pragma unroll
   for (int st = 0; st < STEPS; ++st) {
-    const float d = block_dot<XT>(c[st], xr) * mx_pow2(s[st]);
+    const float d = block_dot<XT>(c[st], xr, s[st]);
     part[st][wave][lane] = live ? d : 0.0f;
   }
   __syncthreads();

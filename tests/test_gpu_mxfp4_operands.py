@@ -214,3 +214,24 @@ def test_layer_with_massive_channels(T, H, I, E, k, dtype):
     print(f"layer {T} {H} {I} {E} {k} {dtype}: rel_l2 {e:.2e}", flush=True)
     # h is held to 2^-18 of itself, silu and the shares to a few units of 2^-22
     assert e <= 0.6 * HALF[dtype] + 5e-5
+
+
+# small layers whose down adds over the experts itself, others, turns of more and of fewer
+# than 8 tokens as the batch changes, several super-steps of both products
+@pytest.mark.parametrize("T, H, I, E, k", [(5, 4096, 64, 16, 6), (2, 4096, 544, 9, 8), (16, 4096, 128, 8, 4), (12, 2048, 1056, 5, 3),
+                                           (6, 96, 4640, 6, 3), (20, 128, 96, 4, 2), (40, 1056, 544, 10, 3),
+                                           (64, 96, 4640, 12, 5), (33, 64, 32, 2, 2)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_token_does_not_depend_on_the_batch(T, H, I, E, k, dtype):
+    a = [t.to(DEV) for t in layer(T, H, I, E, dtype, T + E)]
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).to(dtype).to(DEV)
+    first = ops.mxfp4_moe(x, *a, k)
+    for round_ in range(4):
+        keep = torch.rand(T, generator=g) < (0.5 if T > 8 else 0.3)
+        keep[round_ % T] = True
+        other = torch.randn(T, H, generator=g).to(dtype).to(DEV)
+        other = other * torch.randn(H, generator=g).to(dtype).to(DEV).abs()  # towards other experts
+        mixed = torch.where(keep.to(DEV)[:, None], x, other)
+        y = ops.mxfp4_moe(mixed, *a, k)
+        assert torch.equal(y[keep.to(DEV)], first[keep.to(DEV)])

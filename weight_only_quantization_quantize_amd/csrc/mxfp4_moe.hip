@@ -298,7 +298,9 @@ __device__ inline Halves halves(float v) {
 // h, p folded in, for down: of each turn and super-step four fragments
 // (mxfp4_device.h) of the 16 tokens' hi, then four of their lo.  Up to 8 tokens are
 // multiplied in one matrix step, their hi as the rows 0 .. 7 and their lo as the rows
-// 8 .. 15, which join_halves adds; more in two steps into the same sums.
+// 8 .. 15, which join_halves adds; more in two steps.  Either way a unit's products
+// with hi and with lo are sums of their own, added once: a token's bits do not depend
+// on how many others share its turn.
 constexpr int kHalfTokens = 8;
 __host__ __device__ inline int64_t h_fragment(int64_t turn, int supers, int S) { return (turn * supers + S) * 8; }
 // A lane's place in the fragments of hi: its token (rows past the turn's last one
@@ -404,7 +406,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
       }
     }
     const bool two = !UP && count > kHalfTokens;  // matrix steps
-    float4_t acc[NT] = {};
+    float4_t acc[NT] = {};  // UP; down adds its super-steps' products in LDS, which leaves registers for lo
+    float4_t(*const part)[NT][64] = parts[(item - i0) & 1];
     const int64_t row0 = row_n;
     for (int S = wave; S < supers; S += waves) {
       if (changed || supers > waves) {
@@ -434,10 +437,17 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
           asm volatile("" : "+v"(l));  // as above
           mx_stage_unit(u[j], stage, 15, (all - (row0 + tile_row(j, item))) * nblk, nblk, S, l);
           if constexpr (decltype(more)::value) ahead(j, l);
-          if constexpr (UP)
+          if constexpr (UP) {
             mx_multiply_unit<XT>(acc[j], a, stage, l);
-          else
-            mx_multiply_unit<XT>(acc[j], a, lo, two, stage, l);
+          } else {
+            float4_t v = {}, w = {};
+            mx_multiply_unit<XT>(v, a, w, lo, two, stage, l);
+            if (!two) v = join_halves(v, w, l);
+            float4_t& sum = part[wave][j][l];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (S == wave ? 0.0f : sum[e]) + (two ? v[e] + w[e] : v[e]);
+            sum = v;
+          }
         }
       };
       if (item_n < i1)
@@ -445,11 +455,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
       else
         multiply(std::false_type{});
     }
-    float4_t(*const part)[NT][64] = parts[(item - i0) & 1];
     int l = lane;
     asm volatile("" : "+v"(l));  // as above
+    if constexpr (UP)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) part[wave][j][l] = UP || two ? acc[j] : join_halves(acc[j], float4_t{}, l);
+      for (int j = 0; j < NT; ++j) part[wave][j][l] = acc[j];
     __syncthreads();
     // value (row m, tile j, column c) of a wave: part[w][j][(m / 4) 16 + c][m % 4]
     auto sum = [&](int m, int j, int c) {
@@ -502,16 +512,20 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
 }
 
 // Few units of weights: columns [16 b, 16 b + 16) of y for up to 16 tokens, over all
-// turns' super-steps, which the waves share out two at a time; their sums are added
-// in order.  NJ as above.
+// turns' super-steps, which the waves share out two at a time.  A unit's products meet
+// in LDS; a token's are added in its order of choice, a choice's super-steps in theirs,
+// so that they do not depend on the other tokens.  NJ as above: then the units are in
+// that order themselves, and go in rounds.
+constexpr int kDirectUnits = 36, kRoundUnits = 64;
 template <class YT, int NJ>
 __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
     const uint8_t* __restrict__ h, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-    const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan, const Turn* __restrict__ turns, int T,
-    int H, int I, int E, uint16_t* __restrict__ Y) {
-  constexpr int W = kExpertWaves, kRows = NJ > 0 ? 1 : kChunk;
+    const float* __restrict__ logits, int top_k, const Plan* __restrict__ plan, const Turn* __restrict__ turns,
+    const int* __restrict__ where, int T, int H, int I, int E, uint16_t* __restrict__ Y) {
+  constexpr int W = kExpertWaves, kRows = NJ > 0 ? 1 : kChunk, kUnits = NJ > 0 ? kRoundUnits : kDirectUnits;
   __shared__ __attribute__((aligned(16))) uint8_t stage_all[W][kUnitStage];
-  __shared__ float sums[W][kRows][kChunk + 1];
+  __shared__ float parts[kUnits][kRows][kChunk + 1];
+  __shared__ int rows[NJ > 0 ? 1 : kChunk * kMaxTopK];  // of the tokens' choices, [token][choice]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nblk = I / kMxBlock, supers = (I + 511) / 512;
@@ -522,13 +536,13 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
     float logit[NJ];
     load_logits(logit, logits, E, lane);
     choice = choose(logit, E, top_k, lane);
+  } else {
+    for (int i = threadIdx.x; i < T * top_k; i += W * 64) rows[i] = where[i];
   }
   const int units = (NJ > 0 ? top_k : plan->turns) * supers;
-  for (int o = lane; o < kRows * (kChunk + 1); o += 64) (&sums[wave][0][0])[o] = 0.0f;
   struct Work {
     MxUnit u;
     MxActivations a;
-    uint32_t tokens;  // of rows 4 q .. 4 q + 3
   };
   auto row_of = [&](int i) {
     const int k = i / supers;
@@ -541,7 +555,6 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
   };
   auto load = [&](Work& w, int i) {
     const int64_t row = row_of(i);
-    w.tokens = NJ > 0 ? 0u : reinterpret_cast<const uint32_t*>(turns[i / supers].token)[lane >> 4];
     mx_load_unit(w.u, codes + row * nblk * 16, scales + row * nblk, 15, ((int64_t)E * H - row) * nblk, nblk, i % supers, lane);
     activations(w.a, i, 0);
   };
@@ -557,24 +570,43 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
     acc = join_halves(acc, more, lane);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (4 * (lane >> 4) + e < count) sums[wave][w.tokens >> (8 * e) & 15u][lane & 15] += acc[e];
+      if (4 * (lane >> 4) + e < count) parts[i % kUnits][NJ > 0 ? 0 : 4 * (lane >> 4) + e][lane & 15] = acc[e];
   };
-  // an odd last unit is loaded twice and multiplied once
-  for (int i = wave; i < units; i += 2 * W) {
-    const bool two = i + W < units;
-    Work a, b;
-    load(a, i);
-    load(b, two ? i + W : i);
-    __builtin_amdgcn_sched_barrier(0);  // all loads start before the first product
-    work(a, i);
-    if (two) work(b, i + W);
+  float v = 0.0f, p = 0.0f;  // NJ: of thread n's column, and of the choice that a round may cut
+  for (int i0 = 0; i0 < units; i0 += kUnits) {
+    const int i1 = i0 + kUnits < units ? i0 + kUnits : units;
+    // an odd last unit is loaded twice and multiplied once
+    for (int i = i0 + wave; i < i1; i += 2 * W) {
+      const bool two = i + W < i1;
+      Work a, b;
+      load(a, i);
+      load(b, two ? i + W : i);
+      __builtin_amdgcn_sched_barrier(0);  // all loads start before the first product
+      work(a, i);
+      if (two) work(b, i + W);
+    }
+    __syncthreads();
+    if constexpr (NJ > 0) {
+      if ((int)threadIdx.x < kChunk)
+        for (int i = i0; i < i1; ++i) {
+          p += parts[i - i0][0][threadIdx.x];
+          if ((i + 1) % supers == 0) {
+            v += p;
+            p = 0.0f;
+          }
+        }
+      if (i1 < units) __syncthreads();
+    }
   }
-  __syncthreads();
   if ((int)threadIdx.x < T * kChunk) {
     const int t = threadIdx.x / kChunk, n = threadIdx.x % kChunk;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) v += sums[w][t][n];
+    if constexpr (NJ == 0)
+      for (int c = 0; c < top_k; ++c) {
+        const int row = rows[t * top_k + c];
+        p = 0.0f;
+        for (int S = 0; S < supers; ++S) p += parts[row / kChunk * supers + S][row % kChunk][n];
+        v += p;
+      }
     Y[(int64_t)t * H + n0 + n] = YT::from_f32(v * kMxGain<BF16>);
   }
 }
@@ -660,7 +692,7 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
   //   17   8 x 1024 x 512    26 / 28        36   16 x 4096 x 512    42 / 45
   //   20  16 x 4096 x 1024   31 / 36        68    8 x 2048 x 768    40 / 37
   //   32   2 x 4096 x 2048   42 / 40        93    5 x 2080 x 1056   61 / 49
-  const bool direct = T == 1 || (T <= kChunk && l.turns * ((I + 511) / 512) <= 36);
+  const bool direct = T == 1 || (T <= kChunk && l.turns * ((I + 511) / 512) <= kDirectUnits);
   using Nj0 = std::integral_constant<int, 0>;
   using Nj1 = std::integral_constant<int, 1>;
   using NjN = std::integral_constant<int, kLarge>;
@@ -668,7 +700,7 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
   if (e != hipSuccess) return e;
   if (direct) {
     auto* const f = T > 1 ? moe_direct_down_kernel<XT, 0> : (E <= 64 ? moe_direct_down_kernel<XT, 1> : moe_direct_down_kernel<XT, kLarge>);
-    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(h, down_codes, down_scales, logits, top_k, plan, turns, T, H, I, E, Y);
+    f<<<(unsigned)(H / 16), kExpertWaves * 64, 0, stream>>>(h, down_codes, down_scales, logits, top_k, plan, turns, where, T, H, I, E, Y);
     return hipGetLastError();
   }
   e = experts(std::false_type{}, Nj0{}, down_codes, down_scales, I, H, (H + 63) / 64);

@@ -11,6 +11,7 @@ import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -385,10 +386,14 @@ def _check_mxfp4(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int
     return (*rows, 2 * half)
 
 
-def _no_grad(*ts: torch.Tensor) -> None:
-    """These operators are for inference: a gradient asked of them is refused, not dropped."""
+def _no_grad(*ts: Optional[torch.Tensor]) -> None:
+    """These operators are for inference: a gradient or a forward-mode tangent asked
+    of them is refused, not dropped."""
+    dual = forward_ad._current_level >= 0
     for t in ts:
-        if t.requires_grad and torch.is_grad_enabled():
+        if t is None:
+            continue
+        if (t.requires_grad and torch.is_grad_enabled()) or (dual and forward_ad.unpack_dual(t).tangent is not None):
             raise ValueError("the mxfp4 operators have no gradient (use torch.no_grad() or detach the input)")
 
 
@@ -470,7 +475,7 @@ def mxfp4_gemm(
     M = shape[0]
     if M < 1 or N < 1:
         raise ValueError("need at least one row of X and of the weights")
-    _no_grad(X)
+    _no_grad(X, out)
     if out is not None:
         _check_out(out, (M, N), X.dtype, "out")
     _require_gpu(X, codes, scales, out)
@@ -500,6 +505,7 @@ def mxfp4_gemm_mx(
         raise ValueError(f"dtype must be float16 or bfloat16 (got {dtype})")
     if M < 1 or N < 1:
         raise ValueError("need at least one row of activations and of weights")
+    _no_grad(out)
     if out is not None:
         _check_out(out, (M, N), dtype, "out")
     _require_gpu(a_codes, a_scales, codes, scales, out)
@@ -541,7 +547,7 @@ def mxfp4_moe(
     if nbytes == 0:
         raise ValueError(f"mxfp4_moe takes 1 to 64 tokens, up to 512 experts and a top_k of up to 64 (got T={T}, H={H}, "
                          f"I={I}, E={E}, top_k={top_k})")
-    _no_grad(X, router)
+    _no_grad(X, router, out)
     if out is not None:
         _check_out(out, (T, H), X.dtype, "out")
     _require_gpu(X, router, up_codes, up_scales, down_codes, down_scales, out)

@@ -300,8 +300,11 @@ woq_status woq_gptq_quantize_pack(const void* X, const void* W, int64_t T, int64
  * A block with an infinity or a NaN gives b = 255 and zero codes.
  *
  * For these entry points: codes, X and Y 16-byte aligned, scales of any
- * alignment, everything else as for the calls above.  A block with b = 255
- * makes every output that it takes part in a NaN. */
+ * alignment, outputs and workspaces apart from each other and from every other
+ * argument (WOQ_ERR_INVALID_ARGUMENT where they overlap; only the layer's Y may
+ * be its X), everything else as for the calls above.  A block with b = 255
+ * makes every output that it takes part in a NaN; infinities and NaNs of 16-bit
+ * activations act as in the sums that define the outputs. */
 
 /* x [M, K] of xdtype (WOQ_F16 or WOQ_BF16) -> codes, scales (weights or
  * activations). */

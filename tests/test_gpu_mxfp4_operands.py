@@ -235,3 +235,20 @@ def test_a_token_does_not_depend_on_the_batch(T, H, I, E, k, dtype):
         mixed = torch.where(keep.to(DEV)[:, None], x, other)
         y = ops.mxfp4_moe(mixed, *a, k)
         assert torch.equal(y[keep.to(DEV)], first[keep.to(DEV)])
+
+
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_layer_in_place_and_products_that_would_be(T):
+    H, I, E, k = 256, 96, 10, 3
+    a = [t.to(DEV) for t in layer(T, H, I, E, torch.float16, T)]
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).half().to(DEV)
+    want = ops.mxfp4_moe(x, *a, k)
+    assert torch.equal(ops.mxfp4_moe(x, *a, k, out=x), want) and torch.equal(x, want)
+    w = [t.to(DEV) for t in random_weights(H, H, 3)]
+    with pytest.raises(RuntimeError, match="Y and X overlap"):
+        ops.mxfp4_gemm(x, *w, out=x)
+    buf = torch.zeros(3 * T * H, dtype=torch.float16, device=DEV)
+    with pytest.raises(RuntimeError, match="overlap"):
+        ops.mxfp4_gemm(buf[:T * H].view(T, H), *w, out=buf[T * H - 8:2 * T * H - 8].view(T, H))
+    y = ops.mxfp4_gemm(buf[:T * H].view(T, H), *w, out=buf[T * H:2 * T * H].view(T, H))  # next to each other
+    assert (y == 0).all()

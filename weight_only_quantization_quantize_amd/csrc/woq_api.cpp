@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -159,6 +160,28 @@ woq_status check_workspace(const void* workspace, size_t workspace_bytes, size_t
     return fail(WOQ_ERR_INVALID_ARGUMENT, "workspace must be non-NULL and 256-byte aligned");
   if (workspace_bytes < need)
     return fail(WOQ_ERR_INVALID_ARGUMENT, "workspace too small (%zu bytes, need %zu)", workspace_bytes, need);
+  return WOQ_OK;
+}
+
+// Memory of an argument; NULL or empty ones overlap nothing.
+struct Range {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+  return x <= y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes;
+}
+// Kernels write the outputs while others still read the inputs.
+woq_status check_apart(std::initializer_list<Range> outputs, std::initializer_list<Range> inputs) {
+  for (const Range* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Range* p = outputs.begin(); p != o; ++p)
+      if (overlap(*o, *p)) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s and %s overlap", p->name, o->name);
+    for (const Range& i : inputs)
+      if (overlap(*o, i)) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s and %s overlap", o->name, i.name);
+  }
   return WOQ_OK;
 }
 
@@ -396,6 +419,7 @@ woq_status woq_mxfp4_quantize(const void* x, int32_t xdtype, int64_t M, int64_t 
     return fail(WOQ_ERR_INVALID_ARGUMENT, "xdtype must be WOQ_F16 or WOQ_BF16 (got %d)", xdtype);
   if (!x || !aligned(x, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "x must be non-NULL and 16-byte aligned");
   WOQ_TRY(check_mxfp4_arrays(codes, scales, "output"));
+  WOQ_TRY(check_apart({{"codes", codes, M * K / 2}, {"scales", scales, M * K / 32}}, {{"x", x, 2 * M * K}}));
   return from_hip(woq::launch_mxfp4_quantize(x, xdtype, M, K, codes, scales, static_cast<hipStream_t>(stream)),
                   "mxfp4_quantize launch");
   WOQ_GUARD_END
@@ -409,6 +433,8 @@ woq_status woq_mxfp4_dequantize(const void* codes, const void* scales, int64_t M
     return fail(WOQ_ERR_INVALID_ARGUMENT, "outdtype must be WOQ_F16, WOQ_BF16 or WOQ_F32 (got %d)", outdtype);
   WOQ_TRY(check_mxfp4_arrays(codes, scales, "input"));
   if (!out || !aligned(out, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "out must be non-NULL and 16-byte aligned");
+  WOQ_TRY(check_apart({{"out", out, M * K * (outdtype == WOQ_F32 ? 4 : 2)}},
+                      {{"codes", codes, M * K / 2}, {"scales", scales, M * K / 32}}));
   return from_hip(woq::launch_mxfp4_dequantize(codes, scales, M, K, outdtype, out, static_cast<hipStream_t>(stream)),
                   "mxfp4_dequantize launch");
   WOQ_GUARD_END
@@ -425,7 +451,10 @@ woq_status woq_mxfp4_gemm(const void* X, int32_t xdtype, const void* codes, cons
   WOQ_TRY(check_mxfp4_gemm(M, N, K));
   WOQ_TRY(check_activations(X, xdtype, Y));
   WOQ_TRY(check_mxfp4_arrays(codes, scales, "weight"));
-  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_gemm_workspace_bytes(M, N, K)));
+  const size_t need = woq::mxfp4_gemm_workspace_bytes(M, N, K);
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  WOQ_TRY(check_apart({{"Y", Y, 2 * M * N}, {"workspace", workspace, (int64_t)need}},
+                      {{"X", X, 2 * M * K}, {"codes", codes, N * K / 2}, {"scales", scales, N * K / 32}}));
   return from_hip(woq::launch_mxfp4_gemm(X, xdtype, codes, scales, M, N, K, Y, workspace,
                                          static_cast<hipStream_t>(stream)),
                   "mxfp4_gemm launch");
@@ -445,7 +474,11 @@ woq_status woq_mxfp4_gemm_mx(const void* a_codes, const void* a_scales, const vo
   WOQ_TRY(check_mxfp4_arrays(a_codes, a_scales, "activation"));
   WOQ_TRY(check_mxfp4_arrays(codes, scales, "weight"));
   WOQ_TRY(check_activations(a_codes, ydtype, Y));
-  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_gemm_mx_workspace_bytes(M, N, K)));
+  const size_t need = woq::mxfp4_gemm_mx_workspace_bytes(M, N, K);
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  WOQ_TRY(check_apart({{"Y", Y, 2 * M * N}, {"workspace", workspace, (int64_t)need}},
+                      {{"activation codes", a_codes, M * K / 2}, {"activation scales", a_scales, M * K / 32},
+                       {"codes", codes, N * K / 2}, {"scales", scales, N * K / 32}}));
   return from_hip(woq::launch_mxfp4_gemm_mx(a_codes, a_scales, codes, scales, M, N, K, ydtype, Y, workspace,
                                             static_cast<hipStream_t>(stream)),
                   "mxfp4_gemm_mx launch");
@@ -468,7 +501,15 @@ woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, cons
     return fail(WOQ_ERR_INVALID_ARGUMENT, "router must be non-NULL and 16-byte aligned");
   WOQ_TRY(check_mxfp4_arrays(up_codes, up_scales, "up"));
   WOQ_TRY(check_mxfp4_arrays(down_codes, down_scales, "down"));
-  WOQ_TRY(check_workspace(workspace, workspace_bytes, woq::mxfp4_moe_workspace_bytes(T, H, I, E, top_k)));
+  const size_t need = woq::mxfp4_moe_workspace_bytes(T, H, I, E, top_k);
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  // Y may be X: all of X is read before the launch that writes Y
+  const Range weights[] = {{"router", router, 2 * E * H},           {"up codes", up_codes, E * I * H},
+                           {"up scales", up_scales, E * I * H / 16}, {"down codes", down_codes, E * H * I / 2},
+                           {"down scales", down_scales, E * H * I / 32}};
+  const Range y = {"Y", Y, 2 * T * H}, ws = {"workspace", workspace, (int64_t)need};
+  WOQ_TRY(check_apart({y, ws}, {weights[0], weights[1], weights[2], weights[3], weights[4]}));
+  WOQ_TRY(check_apart({ws}, {{"X", X, 2 * T * H}}));
   return from_hip(woq::launch_mxfp4_moe(X, xdtype, router, up_codes, up_scales, down_codes, down_scales, T, H, I, E,
                                         top_k, Y, workspace, static_cast<hipStream_t>(stream)),
                   "mxfp4_moe launch");

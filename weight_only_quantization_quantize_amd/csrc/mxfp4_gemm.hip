@@ -68,13 +68,19 @@ __device__ inline uint32_t lds_address(const void* p) { return (uint32_t)(uintpt
 // Direct loads to LDS: lane l's 16 (4) bytes from base + offset go to to + 16 l
 // (4 l).  M0 holds the LDS address.  The five wait states cover the write of M0
 // and a base address that a vector instruction wrote just before.  The caller
-// waits for the data with wait_loads.
+// waits for the data with wait_loads.  (The compiler reserves M0 and warns of it on a
+// clobber list; it heeds the clobber where it sets M0 for itself.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ inline void load_lds16(const uint8_t* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base)
+               : "m0", "memory");
 }
 __device__ inline void load_lds4(const uint8_t* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base)
+               : "m0", "memory");
 }
+#pragma clang diagnostic pop
 // Until at most N of the wave's vector memory loads are under way and its LDS
 // reads are done.
 template <int N>

@@ -143,3 +143,19 @@ def test_moe_refuses_overlap():
     _assert_overlaps_refused(lambda lib, p: lib.woq_mxfp4_moe(p["x"], 0, p["router"], p["up"], p["ups"], p["down"], p["downs"], T,
                                                               h, i, e, k, p["y"], p["ws"], need, None), sizes, ["y", "ws"],
                              allowed=[("y", "x")])  # in place: x is read before y is written
+
+
+def test_products_of_too_many_rows_are_refused():
+    # 2^28 rows: past it the scales' row stride (4 bytes a row) and the grid's threads would
+    # pass 32 bits
+    lib = _lib.load()
+    at = 1 << 44  # never dereferenced: refused, or (the last rows that are taken) for its workspace
+    for M in ((1 << 28) + 1, (1 << 30) - 1):
+        assert lib.woq_mxfp4_gemm_workspace_bytes(M, 8, 32) == 0
+        assert lib.woq_mxfp4_gemm_mx_workspace_bytes(M, 8, 32) == 0
+        assert lib.woq_mxfp4_gemm(at, 0, 2 * at, 3 * at, M, 8, 32, 4 * at, 5 * at, 1 << 42, None) == _lib.WOQ_ERR_UNSUPPORTED
+        assert lib.woq_mxfp4_gemm_mx(at, 6 * at, 2 * at, 3 * at, M, 8, 32, 0, 4 * at, 5 * at, 1 << 42, None) == _lib.WOQ_ERR_UNSUPPORTED
+    M = 1 << 28
+    need = lib.woq_mxfp4_gemm_workspace_bytes(M, 8, 32)
+    assert need > 0
+    assert lib.woq_mxfp4_gemm(at, 0, 2 * at, 3 * at, M, 8, 32, 4 * at, 5 * at, need - 1, None) == _lib.WOQ_ERR_INVALID_ARGUMENT

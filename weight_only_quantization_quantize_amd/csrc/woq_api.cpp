@@ -185,11 +185,11 @@ woq_status check_apart(std::initializer_list<Range> outputs, std::initializer_li
   return WOQ_OK;
 }
 
-// A product whose tiles and activation fragments 32-bit indexes count.
+// A product whose tiles, activation fragments, scale strides and threads 32 bits count.
 woq_status check_mxfp4_gemm(int64_t M, int64_t N, int64_t K) {
   WOQ_TRY(check_mxfp4_shape(M, K, "M"));
   WOQ_TRY(check_mxfp4_shape(N, K, "N"));
-  if (N > (1 << 26) || (M + 63) / 64 * ((N + 63) / 64) > INT32_MAX - 8 || (M + 255) / 32 * (K / 64 + 16) > INT32_MAX ||
+  if (M > (1 << 28) || N > (1 << 26) || (M + 63) / 64 * ((N + 63) / 64) > INT32_MAX - 8 || (M + 255) / 32 * (K / 64 + 16) > INT32_MAX ||
       K > (1 << 23))
     return fail(WOQ_ERR_UNSUPPORTED, "product too large for this library (M=%lld, N=%lld, K=%lld)", (long long)M,
                 (long long)N, (long long)K);

@@ -252,3 +252,45 @@ def test_layer_in_place_and_products_that_would_be(T):
         ops.mxfp4_gemm(buf[:T * H].view(T, H), *w, out=buf[T * H - 8:2 * T * H - 8].view(T, H))
     y = ops.mxfp4_gemm(buf[:T * H].view(T, H), *w, out=buf[T * H:2 * T * H].view(T, H))  # next to each other
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 1, 32), (1, 5, 64), (1, 1021, 1056), (1, 300, 2048), (1, 257, 2080), (1, 64, 5152),
+                                     (1, 96, 16384), (1, 4100, 8192), (1, 30000, 96)] + [p for p in PATHS if p[0] > 1])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ordinary_products(M, N, K, dtype):
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M + K)).to(dtype)
+    codes, scales = random_weights(N, K, N)
+    got, ref = close(product(x, codes, scales), host(x), values(codes, scales), dtype, f"ordinary {M} {N} {K} {dtype}")
+    if M * N >= 2000:
+        assert relative(got, ref) <= 0.6 * HALF[dtype] + 1e-5
+
+
+@pytest.mark.parametrize("M, K", [(9001, 4128), (1100000, 32)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_and_back_in_several_passes_of_the_grid(M, K, dtype):
+    # 33.5 million elements are one pass of all threads
+    assert M * K > 33554432
+    g = torch.Generator(device=DEV).manual_seed(K)
+    x = (torch.randn(M, K, generator=g, device=DEV) * torch.exp2(4 * torch.randn(M, 1, generator=g, device=DEV))).to(dtype)
+    codes, scales = ops.mxfp4_quantize(x)
+    torch.cuda.synchronize()
+    first = 33554432 // K
+    rows = sorted({0, 1, first - 1, first, first + 1, M // 2, M - 2, M - 1} | set(range(5, M, M // 40)))
+    want = O.quantize(host(x[rows]))
+    assert np.array_equal(codes[rows].cpu().numpy(), want[0]) and np.array_equal(scales[rows].cpu().numpy(), want[1])
+    for out in (torch.float32, torch.bfloat16, torch.float16):
+        got = ops.mxfp4_dequantize(codes, scales, out)[rows].double().cpu().numpy()
+        assert np.array_equal(got, torch.from_numpy(O.dequantize(*want)).to(out).double().numpy())
+
+
+@pytest.mark.parametrize("T, H, I, E, k", [(20, 128, 64, 8, 2), (64, 608, 544, 9, 3), (6, 96, 64, 16, 6)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_layer_gives_nothing_finite_for_a_spoilt_token(T, H, I, E, k, bad):
+    a = [t.to(DEV) for t in layer(T, H, I, E, torch.float16, 9)]
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(3)).half().to(DEV)
+    clean = ops.mxfp4_moe(x, *a, k)
+    x[T // 3, 3] = bad
+    y = ops.mxfp4_moe(x, *a, k)
+    keep = [t for t in range(T) if t != T // 3]
+    assert torch.equal(y[keep], clean[keep]) and torch.isfinite(clean).all()
+    assert not torch.isfinite(y[T // 3]).any()

@@ -294,3 +294,16 @@ def test_layer_gives_nothing_finite_for_a_spoilt_token(T, H, I, E, k, bad):
     keep = [t for t in range(T) if t != T // 3]
     assert torch.equal(y[keep], clean[keep]) and torch.isfinite(clean).all()
     assert not torch.isfinite(y[T // 3]).any()
+
+
+@pytest.mark.parametrize("M, N, K", PATHS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weights_with_blocks_of_zeros(M, N, K, dtype):
+    # as the quantizer leaves them: scale byte 0, codes 0 (and 8 for negative zeros)
+    g = torch.Generator().manual_seed(N)
+    w = torch.randn(N, K, generator=g) * 0.05
+    w = (w.view(N, -1, 32) * (torch.rand(N, K // 32, 1, generator=g) < 0.5)).view(N, K)
+    codes, scales = ops.mxfp4_quantize(w.to(dtype).to(DEV))
+    assert (scales == 0).any()
+    x = torch.randn(M, K, generator=g).to(dtype)
+    close(product(x, codes, scales), host(x), values(codes, scales), dtype, f"zero blocks {M} {N} {K}")

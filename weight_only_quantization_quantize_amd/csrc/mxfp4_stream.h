@@ -141,10 +141,10 @@ __device__ __forceinline__ void mx_multiply_unit(float4_t& acc, const MxActivati
     constexpr int s = decltype(sel)::value;
     const uint32_t b = scale >> (8 * s) & 0xFFu;
     const u32x4_t c = mx_staged_weights(stage, s, lane);
-    if constexpr (!kMxIsF16<XT>) {
-      step(sel, [](uint32_t c, uint32_t b) { return mx_widen_any(c, b); });
-    } else if (!__any(mx_needs_care<XT>(c, b))) {
+    if (!__any(mx_needs_care<XT>(c, b))) {
       step(sel, usual);
+    } else if constexpr (!kMxIsF16<XT>) {
+      step(sel, [](uint32_t c, uint32_t b) { return mx_widen_any(c, b); });
     } else {
       const bool large = __any(mx_large(b));
 #pragma unroll 1

@@ -440,12 +440,19 @@ __global__ __launch_bounds__(WAVES * 64, 2) void moe_experts_kernel(
           if constexpr (UP) {
             mx_multiply_unit<XT>(acc[j], a, stage, l);
           } else {
-            float4_t v = {}, w = {};
-            mx_multiply_unit<XT>(v, a, w, lo, two, stage, l);
-            if (!two) v = join_halves(v, w, l);
+            float4_t v = {};
+            if (two) {
+              float4_t w = {};
+              mx_multiply_unit<XT, true>(v, a, w, lo, stage, l);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += w[e];
+            } else {
+              mx_multiply_unit<XT>(v, a, stage, l);
+              v = join_halves(v, float4_t{}, l);
+            }
             float4_t& sum = part[wave][j][l];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (S == wave ? 0.0f : sum[e]) + (two ? v[e] + w[e] : v[e]);
+            for (int e = 0; e < 4; ++e) v[e] += S == wave ? 0.0f : sum[e];
             sum = v;
           }
         }

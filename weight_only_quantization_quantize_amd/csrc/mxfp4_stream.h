@@ -115,12 +115,12 @@ __device__ inline void mx_each_step(F&& f) {
 }
 
 // acc (rows: activations, columns: weights) += the staged unit's product over kMxGain
-// with its super-step of 16-bit activations x, and also += that with more, where two is
+// with its super-step of 16-bit activations x, and also += that with more, where TWO is
 // set.  The usual way is straight code of its own, so that conversions run beside the
 // matrix instructions.
-template <class XT>
+template <class XT, bool TWO>
 __device__ __forceinline__ void mx_multiply_unit(float4_t& acc, const MxActivations& x, float4_t& also, const MxActivations& more,
-                                                 bool two, const uint8_t* __restrict__ stage, int lane) {
+                                                 const uint8_t* __restrict__ stage, int lane) {
   const uint32_t scale = mx_staged_scale(stage, lane);
   auto step = [&](auto sel, auto widen) {
     constexpr int s = decltype(sel)::value;
@@ -128,7 +128,7 @@ __device__ __forceinline__ void mx_multiply_unit(float4_t& acc, const MxActivati
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const u32x4_t w = widen(c[j], scale >> (8 * s) & 0xFFu);
-      if (two) also = XT::mfma16x16x32(more[s][j], w, also);
+      if constexpr (TWO) also = XT::mfma16x16x32(more[s][j], w, also);
       acc = XT::mfma16x16x32(x[s][j], w, acc);
     }
   };
@@ -158,7 +158,7 @@ __device__ __forceinline__ void mx_multiply_unit(float4_t& acc, const MxActivati
 template <class XT>
 __device__ __forceinline__ void mx_multiply_unit(float4_t& acc, const MxActivations& x, const uint8_t* __restrict__ stage, int lane) {
   float4_t none;
-  mx_multiply_unit<XT>(acc, x, none, x, false, stage, lane);
+  mx_multiply_unit<XT, false>(acc, x, none, x, stage, lane);
 }
 
 }  // namespace woq

@@ -580,6 +580,7 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
       if (4 * (lane >> 4) + e < count) parts[i % kUnits][NJ > 0 ? 0 : 4 * (lane >> 4) + e][lane & 15] = acc[e];
   };
   float v = 0.0f, p = 0.0f;  // NJ: of thread n's column, and of the choice that a round may cut
+  int left = supers;
   for (int i0 = 0; i0 < units; i0 += kUnits) {
     const int i1 = i0 + kUnits < units ? i0 + kUnits : units;
     // an odd last unit is loaded twice and multiplied once
@@ -595,12 +596,13 @@ __global__ __launch_bounds__(kExpertWaves * 64) void moe_direct_down_kernel(
     __syncthreads();
     if constexpr (NJ > 0) {
       if ((int)threadIdx.x < kChunk)
-        for (int i = i0; i < i1; ++i) {
-          p += parts[i - i0][0][threadIdx.x];
-          if ((i + 1) % supers == 0) {
-            v += p;
-            p = 0.0f;
-          }
+#pragma unroll 8
+        for (int i = 0; i < i1 - i0; ++i) {
+          p += parts[i][0][threadIdx.x];
+          const bool last = --left == 0;  // of a choice
+          v += last ? p : 0.0f;
+          p = last ? 0.0f : p;
+          left = last ? supers : left;
         }
       if (i1 < units) __syncthreads();
     }

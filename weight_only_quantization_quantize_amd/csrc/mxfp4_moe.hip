@@ -24,9 +24,9 @@
 // A small layer of few tokens has no combine: its down adds over the experts itself.
 // One token needs no list either: up and down work the choices out from the logits.
 //
-// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 114 us, of which up 71
-// (285 MB of weights, 4.0 TB/s) and down 36 (142 MB, 4.0 TB/s); one token 23 us, up
-// 13.7, down 8.3, logits 4.5.  Before, a workgroup per 32 columns and turn (up) and per
+// bf16, H = 4096, I = 2048, 32 experts, 4 a token: 64 tokens 115 us, of which up 72
+// (285 MB of weights, 4.0 TB/s) and down 36 (142 MB, 3.9 TB/s); one token 24 us, up
+// 13.6, down 9.1, logits 4.5.  Before, a workgroup per 32 columns and turn (up) and per
 // 16 columns of y over all turns (down) read the activations again for every 64 (16)
 // weight rows, and its first loads had nothing before them to hide behind: 24 and 21 us
 // more.

@@ -493,11 +493,11 @@ Tile tile_mx(int64_t M, int64_t N) {
   return large <= mid && large <= small ? Tile::kLarge : (mid <= small ? Tile::kMiddle : Tile::kSmall);
 }
 // Small 4-bit tiles keep the scales in LDS where that leaves a second workgroup a
-// compute unit, or none is needed: no pass over them, no workspace.  Whole
-// products, with / without: 333 x 1001 x 5152 9.9 / 11.6 us, 128 x 4096 x 4096 8.2 /
-// 10.2, 512 x 1024 x 1024 4.1 / 6.4, 256 x 8192 x 3584 10.2 / 12.6.  Those alone on
-// their compute unit have three stages (64 x 8192 x 8192 14.5 us with two, 12.2 with
-// three, 12.8 with four; 333 x 1001 x 5152 9.8, 10.0, 10.4).
+// compute unit, or none is needed: no pass over them, no workspace.  Whole products
+// with weights out of HBM, with / without: 333 x 1001 x 5152 10.3 / 12.9 us, 128 x 4096
+// x 4096 8.0 / 10.7, 512 x 1024 x 1024 4.1 / 6.5, 256 x 8192 x 3584 11.7 / 14.3, 64 x 8192
+// x 8192 15.4 / 21.4.  Those alone on their compute unit have three stages (with two:
+// 64 x 8192 x 8192 18.9 us, 333 x 1001 x 5152 11.0).
 bool resident(int64_t M, int64_t N, int64_t K) {
   return tile_mx(M, N) == Tile::kSmall && (K <= 128 * kResident || (K <= 128 * kResidentAlone && per_cu(M, N, 64, 64) == 1));
 }

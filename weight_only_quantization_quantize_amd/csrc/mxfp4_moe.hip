@@ -695,12 +695,14 @@ hipError_t launch(const uint16_t* X, const uint16_t* router, const uint8_t* up_c
     return hipGetLastError();
   };
   auto up = [&](auto nj) { return experts(std::true_type{}, nj, up_codes, up_scales, H, 2 * I, I / kMxBlock); };
-  // Few units of down's weights go straight to y: whole layers, us, direct / in two
-  // launches, by turns (at most) x super-steps:
-  //   4    2 x 1024 x 512    25 / 34        34   16 x 2048 x 512    30 / 33
-  //   17   8 x 1024 x 512    26 / 28        36   16 x 4096 x 512    42 / 45
-  //   20  16 x 4096 x 1024   31 / 36        68    8 x 2048 x 768    40 / 37
-  //   32   2 x 4096 x 2048   42 / 40        93    5 x 2080 x 1056   61 / 49
+  // Few units of down's weights go straight to y.  Whole layers of T x H x I, us, direct /
+  // in two launches, by turns (at most) x super-steps:
+  //   4    2 x 1024 x 512    25 / 26        20  16 x 4096 x 1024   32 / 40
+  //   10   3 x 4096 x 1024   28 / 35        32   2 x 4096 x 2048   42 / 43
+  //   16   4 x 2048 x 512    27 / 41        34  16 x 2048 x 512    31 / 36
+  //   17   8 x 1024 x 512    26 / 32        36  16 x 4096 x 512    44 / 53
+  // More units' products would not leave two workgroups a compute unit their LDS; with
+  // sums of another order, 68 (8 x 2048 x 768) took 40 / 37 and 93 (5 x 2080 x 1056) 61 / 49.
   const bool direct = T == 1 || (T <= kChunk && l.turns * ((I + 511) / 512) <= kDirectUnits);
   using Nj0 = std::integral_constant<int, 0>;
   using Nj1 = std::integral_constant<int, 1>;

@@ -3,12 +3,12 @@
 //   Y[m, n] = sum_b 2^(sA + sW - 254) sum_{k in block b} a[m, k] w[n, k].
 //
 // Work split.  K is cut into super-steps of 512 (four steps of 128).  A workgroup of 8
-// waves holds `slots` teams of `team` waves; a wave owns one or two super-steps, whose activations stay in registers
-// for the whole launch, and the team walks over its run of tiles of 16 columns of
-// Y: the only traffic left is the weights'.  The team's partial sums of a tile meet
-// in LDS and are added in a fixed order.  More rows than the registers hold (16 of
-// 16-bit activations, 64 of 4-bit ones) are cut into row groups, workgroups of their
-// own that read the same weights at the same time from the same L2.
+// waves holds `slots` teams of `team` waves; a wave owns one or two super-steps, whose
+// activations stay in registers for the whole launch, and the team walks over its run
+// of tiles of 16 columns of Y: the only traffic left is the weights'.  The team's
+// partial sums of a tile meet in LDS and are added in a fixed order.  More rows than the
+// registers hold (16 of 16-bit activations, 64 of 4-bit ones) are cut into row groups,
+// workgroups of their own that read the same weights at the same time from the same L2.
 //
 // 16-bit activations are read from X as the matrix operands: a lane's part of a
 // step is the 64 contiguous bytes of one block.
@@ -318,9 +318,10 @@ hipError_t launch(const void* A, const void* As, const void* W, const void* Ws, 
   slots = slots < per ? slots : per;
   const int groups = (tiles + slots - 1) / slots;
   const dim3 grid((unsigned)(groups < target ? groups : target), (unsigned)rgroups);
-  // four units ahead, fewer where a team has fewer tiles (units that are not there
-  // cost their loads all the same: 4096 x 4096 takes 9.7 us with one, 11.2 with
-  // four) or where 64 rows leave no registers for them
+  // four units ahead (16 rows of 16384 x 4096: 13.7 us, with one 15), fewer where a team
+  // has fewer tiles (units that are not there cost their loads all the same: 4096 x
+  // 4096 takes 8.2 us with one, 9.9 with four) or where 64 rows leave no registers for
+  // them
   const int most = (tiles + (int)grid.x * slots - 1) / ((int)grid.x * slots);
   auto* const f = [&] {
     if constexpr (TC == 4)  // N > 8192: several tiles a team

@@ -261,15 +261,23 @@ __global__ __launch_bounds__((Config<XT, TM, TN, WN, KS, KG, RES>::kThreads), 2)
   asm volatile("" : "+v"(as_at), "+v"(ws_at));
 
   float16_t acc[TM][TN];
-  // All of K.  16-bit activations: in the usual way, or the general one; returns whether
-  // the lane met a block that the usual one does not multiply.
-  auto all_of_k = [&](auto way) {
-    constexpr bool kGeneral = decltype(way)::value;
+  // All of K.  16-bit activations: in the usual way (part 0), or (part 1, and 2 for the
+  // second half of the columns of a tile whose sums fill the registers) each step in the
+  // way it needs; returns whether the lane met a block that the usual one does not
+  // multiply.  Both ways in one loop spill or hold up the usual one.  A block of scale
+  // byte 100 in every 256 rows, fp16: 2048 x 11008 x 4096 190 -> 430 us, 64 x 11008 x 4096
+  // 19 -> 34 (every step of such a tile in the general way: 890 and 109).
+  constexpr int kParts = TM * TN > 4 ? 2 : 1;
+  auto all_of_k = [&](auto part) {
+    constexpr bool kGeneral = decltype(part)::value > 0;
+    constexpr int kFrom = kGeneral ? (decltype(part)::value - 1) * (TN / kParts) : 0, kTo = kGeneral ? kFrom + TN / kParts : TN;
     bool general = false;
 #pragma unroll
-    for (int i = 0; i < TM * TN; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i / TN][i % TN][e] = 0.0f;
+      for (int j = kFrom; j < kTo; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     for (int st = 0; st + 1 < C::kStages; ++st) issue(h0 + st, st);
     if constexpr (RES > 0) {  // seen by all behind the first turn's barrier
       static_assert(KS == 4 && !C::kRows && RES % 4 == 0);
@@ -297,7 +305,7 @@ __global__ __launch_bounds__((Config<XT, TM, TN, WN, KS, KG, RES>::kThreads), 2)
         u32x4_t wc[TN];
         int bs[TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
+        for (int j = kFrom; j < kTo; ++j) {
           wc[j] = *reinterpret_cast<const u32x4_t*>(la + w_at[s] + j * 32 * TW::kRowBytes);
           if constexpr (RES > 0)
             bs[j] = (int)reinterpret_cast<const uint16_t*>(&w_scales[2 * h + (s >> 1)][(wn + j) * 32 + r32])[half];
@@ -314,7 +322,7 @@ __global__ __launch_bounds__((Config<XT, TM, TN, WN, KS, KG, RES>::kThreads), 2)
             else
               as = TA::scale(la + as_at + 128 * i, s, h);
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+            for (int j = kFrom; j < kTo; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(wc[j]), v, acc[i][j], kMfmaFp4, kMfmaFp4,
                                                                           TW::select(s), bs[j], TA::select(s), as);
           }
@@ -323,51 +331,58 @@ __global__ __launch_bounds__((Config<XT, TM, TN, WN, KS, KG, RES>::kThreads), 2)
             return *reinterpret_cast<const u32x4_t*>(la + a_at0 + ((i * KS + s) * 4 + q) * 1024);
           };
 #pragma unroll
-          for (int j = 0; j < TN; ++j) bs[j] = bs[j] >> (8 * TW::select(s)) & 0xFF;
+          for (int j = kFrom; j < kTo; ++j) bs[j] = bs[j] >> (8 * TW::select(s)) & 0xFF;
           auto step = [&](auto widen) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               u32x4_t w[TN];
 #pragma unroll
-              for (int j = 0; j < TN; ++j) w[j] = widen(wc[j][q], (uint32_t)bs[j]);
+              for (int j = kFrom; j < kTo; ++j) w[j] = widen(wc[j][q], (uint32_t)bs[j]);
 #pragma unroll
               for (int i = 0; i < TM; ++i) {
                 const u32x4_t x = acts(i, q);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma32x32x16<XT>(w[j], x, acc[i][j]);
+                for (int j = kFrom; j < kTo; ++j) acc[i][j] = mfma32x32x16<XT>(w[j], x, acc[i][j]);
               }
             }
           };
           if constexpr (!kGeneral) {
             bool unusual = false;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) unusual |= mx_unusual<XT>((uint32_t)bs[j], 1);
+            for (int j = kFrom; j < kTo; ++j) unusual |= mx_unusual<XT>((uint32_t)bs[j], 1);
             if (__any(unusual))
 #pragma unroll
-              for (int j = 0; j < TN; ++j) general |= mx_needs_care<XT>(wc[j], (uint32_t)bs[j]);
+              for (int j = kFrom; j < kTo; ++j) general |= mx_needs_care<XT>(wc[j], (uint32_t)bs[j]);
             step([](uint32_t c, uint32_t b) { return mx_widen<XT>(c, b); });
-          } else if constexpr (!kMxIsF16<XT>) {
-            step([](uint32_t c, uint32_t b) { return mx_widen_any(c, b); });
           } else {
-            bool large = false;
+            bool care = false;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) large |= mx_large((uint32_t)bs[j]);
-            large = __any(large);
+            for (int j = kFrom; j < kTo; ++j) care |= mx_needs_care<XT>(wc[j], (uint32_t)bs[j]);
+            if (!__any(care)) {
+              step([](uint32_t c, uint32_t b) { return mx_widen<XT>(c, b); });
+            } else if constexpr (!kMxIsF16<XT>) {
+              step([](uint32_t c, uint32_t b) { return mx_widen_any(c, b); });
+            } else {
+              bool large = false;
+#pragma unroll
+              for (int j = kFrom; j < kTo; ++j) large |= mx_large((uint32_t)bs[j]);
+              large = __any(large);
 #pragma unroll 1
-            for (int p = 0; p < kMxPasses; p += large ? 1 : 4)
+              for (int p = 0; p < kMxPasses; p += large ? 1 : 4)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                asm volatile("" ::: "memory");  // activations are read again each pass: kept, they spill
-                u32x4_t w[TN];
+                for (int q = 0; q < 4; ++q) {
+                  asm volatile("" ::: "memory");  // activations are read again each pass: kept, they spill
+                  u32x4_t w[TN];
 #pragma unroll
-                for (int j = 0; j < TN; ++j) w[j] = mx_general_weights(wc[j][q], (uint32_t)bs[j], p);
+                  for (int j = kFrom; j < kTo; ++j) w[j] = mx_general_weights(wc[j][q], (uint32_t)bs[j], p);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                  const u32x4_t x = mx_general_activations(acts(i, q), p);
+                  for (int i = 0; i < TM; ++i) {
+                    const u32x4_t x = mx_general_activations(acts(i, q), p);
 #pragma unroll
-                  for (int j = 0; j < TN; ++j) acc[i][j] = mfma32x32x16<BF16>(w[j], x, acc[i][j]);
+                    for (int j = kFrom; j < kTo; ++j) acc[i][j] = mfma32x32x16<BF16>(w[j], x, acc[i][j]);
+                  }
                 }
-              }
+            }
           }
         }
       };
@@ -384,11 +399,17 @@ __global__ __launch_bounds__((Config<XT, TM, TN, WN, KS, KG, RES>::kThreads), 2)
   if constexpr (C::kRows) {
     __shared__ bool any_general;
     if (threadIdx.x == 0) any_general = false;  // before the first turn's barrier
-    if (all_of_k(std::false_type{})) any_general = true;
+    if (all_of_k(std::integral_constant<int, 0>{})) any_general = true;
     __syncthreads();
-    if (any_general) all_of_k(std::true_type{});  // the tile again, for all of its waves
+    if (any_general) {  // the tile again, for all of its waves
+      all_of_k(std::integral_constant<int, 1>{});
+      if constexpr (kParts == 2) {
+        __syncthreads();
+        all_of_k(std::integral_constant<int, 2>{});
+      }
+    }
   } else {
-    all_of_k(std::false_type{});
+    all_of_k(std::integral_constant<int, 0>{});
   }
   __syncthreads();  // nobody reads operands any more
 

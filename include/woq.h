@@ -356,6 +356,97 @@ woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, cons
                          int64_t I, int64_t E, int32_t top_k, void* Y, void* workspace, size_t workspace_bytes,
                          void* stream);
 
+/* 8-bit integers with a scale a row (W8A8).
+ *
+ * Format of a matrix [M, K], K a multiple of 16 and at most 131056 (sums of K
+ * products of two codes are exact in 32 bits): codes int8 [M, K], scales fp32
+ * [M]; the element k of row m stands for codes[m, k] scales[m].  Quantization of
+ * a row y, a = max|y|:
+ *   scale = a / 127
+ *   code  = the integer nearest to 127 y / a, ties to the even one, exactly
+ * A row of zeros has scale 0; one with an infinity or a NaN has scale NaN and
+ * zero codes, and makes every output that it takes part in a NaN.  The products
+ * take any codes -128 .. 127 and any scales.
+ *
+ * For these entry points: x, X, Y, codes and act_scale 16-byte aligned, scales,
+ * bias and lists of experts 4-byte aligned, outputs and workspaces apart from
+ * each other and from every other argument (WOQ_ERR_INVALID_ARGUMENT where they
+ * overlap), everything else as for the calls above. */
+
+/* x [M, K] of xdtype (WOQ_F16, WOQ_BF16 or WOQ_F32) -> codes, scales.
+ *   act_scale : fp32 [K] or NULL: y = x / act_scale (activations), or
+ *               y = x act_scale where multiply != 0 (weights), in fp32. */
+woq_status woq_int8_quantize(const void* x, int32_t xdtype, const float* act_scale, int32_t multiply, int64_t M,
+                             int64_t K, void* codes, float* scales, void* stream);
+
+/* Y[m, n] = (acc a_scales[m]) scales[n] + bias[n], acc = sum_k a[m, k] w[n, k]
+ * over the codes of a [M, K] and w [N, K], exact; fp32 from there, Y [M, N] of
+ * ydtype (WOQ_F16, WOQ_BF16 or WOQ_F32) rounded once.
+ *   bias : fp32 [N] or NULL. */
+woq_status woq_int8_gemm(const void* a_codes, const float* a_scales, const void* codes, const float* scales,
+                         const float* bias, int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream);
+
+/* The same for 16-bit activations X [M, K], quantized by rows in the call
+ * (divided by act_scale [K] before, where given); Y of X's type.
+ *   workspace : device scratch of woq_int8_linear_workspace_bytes(M, N, K)
+ *               bytes, 256-byte aligned (NULL where that is 0; it is 0 for
+ *               invalid sizes too). */
+size_t woq_int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+woq_status woq_int8_linear(const void* X, int32_t xdtype, const float* act_scale, const void* codes,
+                           const float* scales, const float* bias, int64_t M, int64_t N, int64_t K, void* Y,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Routing of tokens to experts (E <= 512, top_k <= 64).  Of a token's logits x [E]:
+ *   s       = softmax(x) (WOQ_SOFTMAX) or 1 / (1 + exp(-x)) (WOQ_SIGMOID)
+ *   key     = x, or, with a bias b [E], s + b computed in 64 bits
+ *   groups  : E / groups neighbours each.  Only the top_groups groups with the
+ *             largest sum of their group_top (1 or 2) largest keys (of two,
+ *             without a bias, of their s) are chosen from; groups = 1: all
+ *   experts : the top_k experts by descending key
+ *   weights = scale s[expert], over the sum of the chosen experts' s where
+ *             renormalize != 0 (softmax: over that of the chosen experts' exp(x))
+ * Equal keys: the lower index first.  A logit of -infinity masks its expert: it
+ * comes after every number, bias or not, and its weight is 0; a key that is a
+ * NaN comes last.  Weights whose sum is 0 (all masked) are 0.  A NaN or +infinity
+ * among the logits makes every softmax weight that it takes part in a NaN.
+ *   logits  : [T, E] of dtype (WOQ_F16, WOQ_BF16 or WOQ_F32)
+ *   bias    : fp32 [E] or NULL; it steers the choice only
+ *   experts : out, int32 [T, top_k];  weights : out, fp32 [T, top_k] */
+#define WOQ_SOFTMAX 0
+#define WOQ_SIGMOID 1
+woq_status woq_moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int32_t top_k, int32_t scoring,
+                         const float* bias, int32_t groups, int32_t top_groups, int32_t group_top, int32_t renormalize,
+                         float scale, int32_t* experts, float* weights, void* stream);
+
+/* The gradient of those weights: dlogits [T, E] of dtype from dweights fp32
+ * [T, top_k] and the experts that were chosen (the choice itself has no
+ * gradient); computed in 64 bits, rounded once.  An entry of experts outside
+ * 0 .. E - 1 takes no part. */
+woq_status woq_moe_route_backward(const void* logits, int32_t dtype, const int32_t* experts, const float* dweights,
+                                  int64_t T, int64_t E, int32_t top_k, int32_t scoring, int32_t renormalize, float scale,
+                                  void* dlogits, void* stream);
+
+/* A layer of gated experts with 8-bit integer weights on routed tokens (E <= 512,
+ * top_k <= 64):
+ *   X[t]   quantized by rows as above
+ *   h      = silu(X[t] . up[e, i]) (X[t] . up[e, I + i]),  silu(g) = g / (1 + exp(-g)),
+ *            fp32; quantized by rows as above
+ *   Y[t]   = sum over the choices c of weights[t, c] sum_i h[t, c, i] down[e, ., i],
+ *            e = experts[t, c]
+ *   X [T, H], Y [T, H] of xdtype (WOQ_F16 or WOQ_BF16); experts int32, weights fp32
+ *   [T, top_k] (woq_moe_route); up codes [E, 2 I, H], scales [E, 2 I] (rows 0 .. I-1
+ *   gate, I .. 2I-1 up), down codes [E, H, I], scales [E, H]; H and I multiples of 16.
+ * A choice outside 0 .. E - 1 (an expert kept elsewhere) takes no part; a token
+ * without any has a row of zeros.  Products are exact sums times the two scales,
+ * as above; the choices are added in their order in fp32, Y is rounded once.  The
+ * same inputs give the same bits, whatever the other tokens are.  workspace as
+ * above. */
+size_t woq_int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k);
+woq_status woq_int8_moe(const void* X, int32_t xdtype, const int32_t* experts, const float* weights,
+                        const void* up_codes, const float* up_scales, const void* down_codes, const float* down_scales,
+                        int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k, void* Y, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* Measurement aids.  Not part of the method: they measure the ceilings the
  * quantized kernels are compared with.  A decode GEMV reads its weights once
  * and does about one flop per byte, so its floor is the time to stream those

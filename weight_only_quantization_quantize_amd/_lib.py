@@ -21,9 +21,11 @@ WOQ_ERR_INTERNAL = 4
 WOQ_F16 = 0
 WOQ_BF16 = 1
 WOQ_F32 = 2
+WOQ_SOFTMAX = 0
+WOQ_SIGMOID = 1
 WOQ_LAYOUT_V2 = 2
 
-_i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+_i32, _i64, _f32, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
 
 
 class QMatrix(ctypes.Structure):
@@ -59,6 +61,14 @@ SIGNATURES = {
     "woq_mxfp4_gemm_mx": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     "woq_mxfp4_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i32]),
     "woq_mxfp4_moe": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
+    "woq_int8_quantize": (_i32, [_vp, _i32, _vp, _i32, _i64, _i64, _vp, _vp, _vp]),
+    "woq_int8_gemm": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "woq_int8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "woq_int8_linear": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "woq_moe_route": (_i32, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp]),
+    "woq_moe_route_backward": (_i32, [_vp, _i32, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _f32, _vp, _vp]),
+    "woq_int8_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i32]),
+    "woq_int8_moe": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _sz, _vp]),
     "woq_probe_stream_read": (_i32, [_vp, _sz, _i32, _i32, _i32, _vp, _i32, _vp]),
     "woq_probe_empty": (_i32, [_i32, _i32, _vp]),
     "woq_probe_mfma_rate": (_i32, [_vp, _i32, _i32, _vp, _i32, _vp]),

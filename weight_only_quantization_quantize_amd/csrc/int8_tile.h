@@ -1,0 +1,244 @@
+// Tiles of products of 8-bit integer matrices: sums over K of a[m, k] w[n, k], exact in
+// 32-bit integers, for A [., K] and W [., K] with rows as stored (K a multiple of 16).
+//
+// Tile.  A group of 2 x WN waves computes 64 TM x 32 WN TN sums, a wave 32 TM x 32 TN, on
+// v_mfma_i32_32x32x32_i8; KG groups of a workgroup share the tile's K and add their sums
+// through LDS at the end.
+//
+// Pipeline.  K goes in stages of 32 KS, kStages of them in LDS, filled by direct loads
+// (global_load_lds: no registers, no instructions to write LDS).  At the top of a turn a
+// wave waits until its own loads of this stage are done, meets the others at the barrier,
+// which also says that everybody is through with the previous stage, starts the loads of
+// the stage kStages - 1 ahead into that one's place, and multiplies.  The loads are written
+// out in assembly because the compiler would wait for all of them before every read of
+// LDS; their counter is waited for by hand, and there is no other vector memory access
+// inside the loop.  Loads past a row's end repeat its last 16 bytes; the last stage masks
+// them on W's side.
+//
+// LDS layout: a row's 32 KS bytes of a stage are chunks of 16, chunk c at position
+// c ^ swizzle(row), so that 16 rows read at one chunk lie in 16 different 16-byte slots of
+// the 256-byte bank row.
+#pragma once
+
+#include <type_traits>
+
+#include "int8_device.h"
+
+namespace woq {
+
+typedef __attribute__((address_space(3))) uint8_t int8_lds_byte;
+__device__ inline uint32_t int8_lds_address(const void* p) { return (uint32_t)(uintptr_t)(const int8_lds_byte*)p; }
+
+// Direct load to LDS: lane l's 16 bytes from base + offset go to to + 16 l.  M0 holds the
+// LDS address.  The five wait states cover the write of M0 and a base address that a
+// vector instruction wrote just before.  The caller waits for the data.  (The compiler
+// reserves M0 and warns of it on a clobber list; it heeds the clobber where it sets M0 for
+// itself.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ inline void int8_load_lds(const int8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base)
+               : "m0", "memory");
+}
+#pragma clang diagnostic pop
+// Until at most N of the wave's vector memory loads are under way and its LDS reads are
+// done.
+template <int N>
+__device__ inline void int8_wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+template <int TM_, int TN_, int WN_, int KS_, int KG_>
+struct Int8Tile {
+  static constexpr int TM = TM_, TN = TN_, WN = WN_, KS = KS_, KG = KG_;
+  static constexpr int kWaves = 2 * WN, kThreads = 64 * kWaves * KG;
+  static constexpr int BM = 64 * TM, BN = 32 * WN * TN;
+  static constexpr int kRow = 32 * KS;      // bytes of a row's stage
+  static constexpr int kChunks = 2 * KS;    // of 16 bytes
+  static constexpr int kUnitRows = 1024 / kRow;
+  static constexpr int kAUnits = BM / kUnitRows, kWUnits = BN / kUnitRows;
+  static constexpr int kStage = (BM + BN) * kRow;
+  // as many stages as leave room for a second workgroup, or, where that would be fewer
+  // than two, as fill the LDS; at most 4
+  static constexpr int kRoom = (KG * kStage * 2 > 80 * 1024 ? 160 : 80) * 1024;
+  static constexpr int kFit = kRoom / (KG * kStage);
+  static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
+  static constexpr int kALoads = (kAUnits + kWaves - 1) / kWaves, kWLoads = (kWUnits + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kALoads + kWLoads;
+  static constexpr int kLdsBytes = KG * kStages * kStage;
+  static_assert(kLdsBytes <= 160 * 1024 && KS % 2 == 0);
+
+  typedef int16v_t Sums[TM][TN];
+
+  __device__ static int swizzle(int row) { return KS == 4 ? (row >> 1) & 7 : (row >> 2) & 3; }
+
+  // acc[i][j] of the first group's waves: the lane's sums of row m = 32 (wm + i) + lane % 32
+  // of A and, element e, row n = 32 (wn + j) + 8 (e / 4) + 4 (lane / 32) + e % 4 of W, with
+  // wm = TM (wave % 2), wn = TN (wave / 2); false for the other groups' waves.
+  // a_row(r), w_row(r): byte offsets (below 2^32) of the tile's rows from a and w, for
+  // every r of the tile.  All threads call; LDS may be used again behind the next barrier.
+  template <class AR, class WR>
+  __device__ static bool multiply(Sums& acc, uint8_t* __restrict__ lds_all, const int8_t* __restrict__ a, AR&& a_row,
+                                  const int8_t* __restrict__ w, WR&& w_row, int K) {
+    const int lane = threadIdx.x & 63;
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = wave_all % kWaves, group = wave_all / kWaves;
+    const int wm = (wave & 1) * TM, wn = (wave >> 1) * TN;
+    const int half = lane >> 5, r32 = lane & 31;
+    const int chunks = K >> 4;
+    const int stages = (chunks + kChunks - 1) / kChunks;
+    // K group `group` takes `turns` stages from h0 on; what is missing is missing at the first
+    // group's begin (h < 0), so that a short last stage is everybody's last turn
+    const int turns = (stages + KG - 1) / KG;
+    const int h0 = stages - (KG - group) * turns;
+    uint8_t* const lds = lds_all + group * (kStages * kStage);
+    const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)int8_lds_address(lds));
+
+    // Every wave starts the same number of loads a stage: past an operand's units the last
+    // one is loaded again, past the last stage that stage.
+    auto unit = [&](int j, int units) {
+      const int u = wave + kWaves * j;
+      return u < units ? u : units - 1;
+    };
+    uint32_t a_off[kALoads], w_off[kWLoads];
+    const int lr = lane / kChunks;
+    const int chunk = (lane & (kChunks - 1)) ^ swizzle(lr);
+#pragma unroll
+    for (int j = 0; j < kALoads; ++j) a_off[j] = a_row(unit(j, kAUnits) * kUnitRows + lr);
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j) w_off[j] = w_row(unit(j, kWUnits) * kUnitRows + lr);
+    auto issue = [&](int h_, int buf) {
+      const int h = h_ < 0 ? 0 : (h_ < stages ? h_ : stages - 1);
+      const uint32_t to = lds0 + (uint32_t)(buf * kStage);
+      // (the swizzle of a unit's rows: that of its first 1024 / kRow rows, and, of an odd
+      // unit of 8 rows, the other half)
+      int at[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c = kChunks * h + (KS == 4 ? chunk ^ (p << 2) : chunk);
+        at[p] = 16 * (c < chunks ? c : chunks - 1);
+      }
+#pragma unroll
+      for (int j = 0; j < kALoads; ++j) {
+        const int u = unit(j, kAUnits);
+        int8_load_lds(a, a_off[j] + (uint32_t)(KS == 4 && (u & 1) ? at[1] : at[0]), to + 1024u * (uint32_t)u);
+      }
+#pragma unroll
+      for (int j = 0; j < kWLoads; ++j) {
+        const int u = unit(j, kWUnits);
+        int8_load_lds(w, w_off[j] + (uint32_t)(KS == 4 && (u & 1) ? at[1] : at[0]), to + (uint32_t)(BM * kRow) + 1024u * (uint32_t)u);
+      }
+    };
+
+    // where the lane's operands lie in a stage
+    uint32_t a_at[KS], w_at[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      a_at[s] = (uint32_t)((wm * 32 + r32) * kRow + ((2 * s + half) ^ swizzle(r32)) * 16);
+      w_at[s] = (uint32_t)((BM + wn * 32 + r32) * kRow + ((2 * s + half) ^ swizzle(r32)) * 16);
+      asm volatile("" : "+v"(w_at[s]), "+v"(a_at[s]));
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+    for (int st = 0; st + 1 < kStages; ++st) issue(h0 + st, st);
+    int buf = 0;
+    auto turn = [&](int h, auto masked) {
+      int8_wait_loads<(kStages - 2) * kLoads>();
+      __builtin_amdgcn_s_barrier();
+      issue(h + kStages - 1, buf == 0 ? kStages - 1 : buf - 1);
+      const uint8_t* const la = lds + buf * kStage;
+      buf = buf + 1 == kStages ? 0 : buf + 1;
+      if (KG > 1 && h < 0) return;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        int4v_t wc[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          wc[j] = *reinterpret_cast<const int4v_t*>(la + w_at[s] + j * 32 * kRow);
+          if constexpr (decltype(masked)::value)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) wc[j][e] = h * kChunks + 2 * s + half < chunks ? wc[j][e] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int4v_t v = *reinterpret_cast<const int4v_t*>(la + a_at[s] + i * 32 * kRow);
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wc[j], v, acc[i][j], 0, 0, 0);
+        }
+      }
+    };
+    const bool rest = stages * kChunks > chunks;
+    const int end = h0 + turns - (rest ? 1 : 0);
+    for (int h = h0; h < end; ++h) turn(h, std::false_type{});
+    if (rest) turn(end, std::true_type{});
+    int8_wait_loads<0>();  // none may land in LDS that is another workgroup's by then
+    __syncthreads();       // nobody reads operands any more
+
+    if constexpr (KG > 1) {
+      // the groups' sums meet in LDS, [wave][tile][lane]
+      static_assert(TM * TN * kWaves * 4096 <= kStages * kStage, "a group's sums fit its stages' place");
+      int16v_t* const mine = reinterpret_cast<int16v_t*>(lds) + wave * TM * TN * 64 + lane;
+      if (group)
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i) mine[i * 64] = acc[i / TN][i % TN];
+      __syncthreads();
+      if (group) return false;
+#pragma unroll
+      for (int g = 1; g < KG; ++g) {
+        const int16v_t* const other = reinterpret_cast<const int16v_t*>(lds_all + g * kStages * kStage) + wave * TM * TN * 64 + lane;
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i) acc[i / TN][i % TN] += other[i * 64];
+      }
+    }
+    return true;
+  }
+};
+
+// A wave's COLS columns of 32 rows of values, value(row, column block of 4) as a float4_t
+// of the lane's row lane % 32, turned through LDS of the wave's own and written in whole
+// runs of a row, 16 bytes a lane.  y: of row 0 and the first column; rows, cols: how many
+// there are; block b of 4 columns is asked of the half (lane / 32) = b % 2 only.
+template <class YT, int COLS, class F>
+__device__ inline void int8_store_rows(uint8_t* __restrict__ turn, typename Int8Out<YT>::type* __restrict__ y, int64_t pitch,
+                                       int rows, int cols, F&& value) {
+  typedef typename Int8Out<YT>::type T;
+  constexpr int kSize = (int)sizeof(T), kPitch = COLS * kSize + 16, kLaneCols = 16 / kSize, kRuns = COLS / kLaneCols;
+  const int lane = threadIdx.x & 63, half = lane >> 5, r32 = lane & 31;
+#pragma unroll
+  for (int b = 0; b < COLS / 8; ++b) {
+    const float4_t v = value(b);
+    T* const to = reinterpret_cast<T*>(turn + r32 * kPitch) + 8 * b + 4 * half;
+    if constexpr (kSize == 4) {
+      *reinterpret_cast<float4_t*>(to) = v;
+    } else {
+      *reinterpret_cast<u32x2_t*>(to) = u32x2_t{(uint32_t)Int8Out<YT>::of(v[0]) | (uint32_t)Int8Out<YT>::of(v[1]) << 16,
+                                                (uint32_t)Int8Out<YT>::of(v[2]) | (uint32_t)Int8Out<YT>::of(v[3]) << 16};
+    }
+  }
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int q = 0; q < 32 * kRuns / 64; ++q) {
+    const int row = (64 * q + lane) / kRuns, c = (64 * q + lane) % kRuns * kLaneCols;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(turn + row * kPitch + c * kSize);
+    if (row < rows && c < cols) {
+      T* const to = y + row * pitch + c;
+      if (c + kLaneCols <= cols) {
+        __builtin_memcpy(to, &v, 16);  // of any alignment: the pitch may be odd
+      } else {
+        T e[kLaneCols];
+        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+        for (int i = 0; i < kLaneCols; ++i)
+          if (c + i < cols) to[i] = e[i];
+      }
+    }
+  }
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace woq

@@ -210,6 +210,74 @@ woq_status check_mxfp4_moe(int64_t T, int64_t H, int64_t I, int64_t E, int32_t t
   return WOQ_OK;
 }
 
+// Sizes of a matrix of 8-bit integers [M, K]: sums of K products of two codes stay in 32 bits.
+constexpr int64_t kInt8MaxK = 131056;
+woq_status check_int8_shape(int64_t M, int64_t K, const char* rows) {
+  if (M < 1) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s must be >= 1 (got %lld)", rows, (long long)M);
+  if (K < 16 || K % 16 != 0)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "the row length must be a positive multiple of 16 (got %lld)", (long long)K);
+  if (M > (1 << 28) || K > kInt8MaxK)
+    return fail(WOQ_ERR_UNSUPPORTED, "matrix too large for this library (%s=%lld, row length %lld)", rows, (long long)M,
+                (long long)K);
+  return WOQ_OK;
+}
+
+woq_status check_int8_arrays(const void* codes, const void* scales, const char* name) {
+  if (!codes || !scales) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s codes and scales must not be NULL", name);
+  if (!aligned(codes, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s codes must be 16-byte aligned", name);
+  if (!aligned(scales, 4)) return fail(WOQ_ERR_INVALID_ARGUMENT, "%s scales must be 4-byte aligned", name);
+  return WOQ_OK;
+}
+
+woq_status check_any_dtype(int32_t dtype, const char* name) {
+  if (dtype != WOQ_F16 && dtype != WOQ_BF16 && dtype != WOQ_F32)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "%s must be WOQ_F16, WOQ_BF16 or WOQ_F32 (got %d)", name, dtype);
+  return WOQ_OK;
+}
+int64_t dtype_bytes(int32_t dtype) { return dtype == WOQ_F32 ? 4 : 2; }
+
+woq_status check_int8_gemm(int64_t M, int64_t N, int64_t K) {
+  WOQ_TRY(check_int8_shape(M, K, "M"));
+  WOQ_TRY(check_int8_shape(N, K, "N"));
+  if ((M + 63) / 64 * ((N + 63) / 64) > INT32_MAX - 8)
+    return fail(WOQ_ERR_UNSUPPORTED, "product too large for this library (M=%lld, N=%lld)", (long long)M, (long long)N);
+  return WOQ_OK;
+}
+
+woq_status check_bias(const void* bias) {
+  if (bias && !aligned(bias, 4)) return fail(WOQ_ERR_INVALID_ARGUMENT, "bias must be 4-byte aligned");
+  return WOQ_OK;
+}
+
+// Sizes and scores of a routing.
+woq_status check_route(int64_t T, int64_t E, int32_t top_k, int32_t dtype, int32_t scoring) {
+  if (T < 1 || E < 1) return fail(WOQ_ERR_INVALID_ARGUMENT, "T and E must be >= 1 (got %lld, %lld)", (long long)T, (long long)E);
+  if (top_k < 1 || top_k > E)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "top_k must be in [1, E] (got %d of %lld)", top_k, (long long)E);
+  WOQ_TRY(check_any_dtype(dtype, "dtype"));
+  if (scoring != WOQ_SOFTMAX && scoring != WOQ_SIGMOID)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "scoring must be WOQ_SOFTMAX or WOQ_SIGMOID (got %d)", scoring);
+  if (T > (1 << 28) || E > woq::moe_route_max_experts() || top_k > woq::moe_route_max_top_k())
+    return fail(WOQ_ERR_UNSUPPORTED, "a routing takes up to 2^28 tokens, %d experts and a top_k of %d (got %lld, %lld, %d)",
+                woq::moe_route_max_experts(), woq::moe_route_max_top_k(), (long long)T, (long long)E, top_k);
+  return WOQ_OK;
+}
+
+woq_status check_int8_moe(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k) {
+  WOQ_TRY(check_int8_shape(T, H, "T"));
+  WOQ_TRY(check_int8_shape(E, I, "E"));
+  if (top_k < 1) return fail(WOQ_ERR_INVALID_ARGUMENT, "top_k must be >= 1 (got %d)", top_k);
+  if (E > woq::int8_moe_max_experts() || top_k > woq::moe_route_max_top_k())
+    return fail(WOQ_ERR_UNSUPPORTED, "int8_moe takes up to %d experts and a top_k of %d (got %lld, %d)",
+                woq::int8_moe_max_experts(), woq::moe_route_max_top_k(), (long long)E, top_k);
+  // rows of X and of an expert at 32-bit offsets; tiles of 64 rows and columns counted in 32 bits
+  const int64_t wide = (H > I ? H : I) / 64 + 1;
+  if (T * H > UINT32_MAX || 2 * I * H > UINT32_MAX || T * top_k > (1 << 28) || (T * top_k / 64 + E) * wide > INT32_MAX)
+    return fail(WOQ_ERR_UNSUPPORTED, "layer too large for this library (T=%lld, H=%lld, I=%lld, top_k=%d)", (long long)T,
+                (long long)H, (long long)I, top_k);
+  return WOQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -513,6 +581,137 @@ woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, cons
   return from_hip(woq::launch_mxfp4_moe(X, xdtype, router, up_codes, up_scales, down_codes, down_scales, T, H, I, E,
                                         top_k, Y, workspace, static_cast<hipStream_t>(stream)),
                   "mxfp4_moe launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_int8_quantize(const void* x, int32_t xdtype, const float* act_scale, int32_t multiply, int64_t M, int64_t K,
+                             void* codes, float* scales, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_int8_shape(M, K, "M"));
+  WOQ_TRY(check_any_dtype(xdtype, "xdtype"));
+  if (!x || !aligned(x, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "x must be non-NULL and 16-byte aligned");
+  WOQ_TRY(check_act_scale(act_scale));
+  WOQ_TRY(check_int8_arrays(codes, scales, "output"));
+  WOQ_TRY(check_apart({{"codes", codes, M * K}, {"scales", scales, 4 * M}},
+                      {{"x", x, dtype_bytes(xdtype) * M * K}, {"act_scale", act_scale, 4 * K}}));
+  return from_hip(woq::launch_int8_quantize(x, xdtype, act_scale, multiply != 0, M, K, codes, scales,
+                                            static_cast<hipStream_t>(stream)),
+                  "int8_quantize launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_int8_gemm(const void* a_codes, const float* a_scales, const void* codes, const float* scales, const float* bias,
+                         int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_int8_gemm(M, N, K));
+  WOQ_TRY(check_any_dtype(ydtype, "ydtype"));
+  WOQ_TRY(check_int8_arrays(a_codes, a_scales, "activation"));
+  WOQ_TRY(check_int8_arrays(codes, scales, "weight"));
+  WOQ_TRY(check_bias(bias));
+  if (!Y || !aligned(Y, 16)) return fail(WOQ_ERR_INVALID_ARGUMENT, "Y must be non-NULL and 16-byte aligned");
+  WOQ_TRY(check_apart({{"Y", Y, dtype_bytes(ydtype) * M * N}},
+                      {{"activation codes", a_codes, M * K}, {"activation scales", a_scales, 4 * M}, {"codes", codes, N * K},
+                       {"scales", scales, 4 * N}, {"bias", bias, 4 * N}}));
+  return from_hip(woq::launch_int8_gemm(a_codes, a_scales, codes, scales, bias, M, N, K, ydtype, Y,
+                                        static_cast<hipStream_t>(stream)),
+                  "int8_gemm launch");
+  WOQ_GUARD_END
+}
+
+size_t woq_int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_int8_gemm(M, N, K) != WOQ_OK) return 0;
+  return woq::int8_linear_workspace_bytes(M, N, K);
+}
+
+woq_status woq_int8_linear(const void* X, int32_t xdtype, const float* act_scale, const void* codes, const float* scales,
+                           const float* bias, int64_t M, int64_t N, int64_t K, void* Y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_int8_gemm(M, N, K));
+  WOQ_TRY(check_activations(X, xdtype, Y));
+  WOQ_TRY(check_act_scale(act_scale));
+  WOQ_TRY(check_int8_arrays(codes, scales, "weight"));
+  WOQ_TRY(check_bias(bias));
+  const size_t need = woq::int8_linear_workspace_bytes(M, N, K);
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  WOQ_TRY(check_apart({{"Y", Y, 2 * M * N}, {"workspace", workspace, (int64_t)need}},
+                      {{"X", X, 2 * M * K}, {"act_scale", act_scale, 4 * K}, {"codes", codes, N * K},
+                       {"scales", scales, 4 * N}, {"bias", bias, 4 * N}}));
+  return from_hip(woq::launch_int8_linear(X, xdtype, act_scale, codes, scales, bias, M, N, K, Y, workspace,
+                                          static_cast<hipStream_t>(stream)),
+                  "int8_linear launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int32_t top_k, int32_t scoring,
+                         const float* bias, int32_t groups, int32_t top_groups, int32_t group_top, int32_t renormalize,
+                         float scale, int32_t* experts, float* weights, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_route(T, E, top_k, dtype, scoring));
+  if (groups < 1 || E % groups != 0)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "groups must divide E (got %d of %lld)", groups, (long long)E);
+  if (top_groups < 1 || top_groups > groups)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "top_groups must be in [1, groups] (got %d of %d)", top_groups, groups);
+  if ((group_top != 1 && group_top != 2) || group_top > E / groups)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "group_top must be 1 or 2 and at most a group's experts (got %d)", group_top);
+  if (top_k > E / groups * top_groups)
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "top_k must be at most the experts of top_groups groups (got %d)", top_k);
+  if (!logits || !aligned(logits, dtype_bytes(dtype)))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "logits must be non-NULL and aligned to their type");
+  WOQ_TRY(check_bias(bias));
+  if (!experts || !aligned(experts, 4) || !weights || !aligned(weights, 4))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "experts and weights must be non-NULL and 4-byte aligned");
+  WOQ_TRY(check_apart({{"experts", experts, 4 * T * top_k}, {"weights", weights, 4 * T * top_k}},
+                      {{"logits", logits, dtype_bytes(dtype) * T * E}, {"bias", bias, 4 * E}}));
+  return from_hip(woq::launch_moe_route(logits, dtype, T, (int)E, top_k, scoring == WOQ_SIGMOID, bias, groups, top_groups,
+                                        group_top, renormalize != 0, scale, experts, weights,
+                                        static_cast<hipStream_t>(stream)),
+                  "moe_route launch");
+  WOQ_GUARD_END
+}
+
+woq_status woq_moe_route_backward(const void* logits, int32_t dtype, const int32_t* experts, const float* dweights, int64_t T,
+                                  int64_t E, int32_t top_k, int32_t scoring, int32_t renormalize, float scale, void* dlogits,
+                                  void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_route(T, E, top_k, dtype, scoring));
+  if (!logits || !aligned(logits, dtype_bytes(dtype)) || !dlogits || !aligned(dlogits, dtype_bytes(dtype)))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "logits and dlogits must be non-NULL and aligned to their type");
+  if (!experts || !aligned(experts, 4) || !dweights || !aligned(dweights, 4))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "experts and dweights must be non-NULL and 4-byte aligned");
+  WOQ_TRY(check_apart({{"dlogits", dlogits, dtype_bytes(dtype) * T * E}},
+                      {{"logits", logits, dtype_bytes(dtype) * T * E}, {"experts", experts, 4 * T * top_k},
+                       {"dweights", dweights, 4 * T * top_k}}));
+  return from_hip(woq::launch_moe_route_backward(logits, dtype, experts, dweights, T, (int)E, top_k, scoring == WOQ_SIGMOID,
+                                                 renormalize != 0, scale, dlogits, static_cast<hipStream_t>(stream)),
+                  "moe_route_backward launch");
+  WOQ_GUARD_END
+}
+
+size_t woq_int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k) {
+  if (check_int8_moe(T, H, I, E, top_k) != WOQ_OK) return 0;
+  return woq::int8_moe_workspace_bytes(T, H, I, E, top_k);
+}
+
+woq_status woq_int8_moe(const void* X, int32_t xdtype, const int32_t* experts, const float* weights, const void* up_codes,
+                        const float* up_scales, const void* down_codes, const float* down_scales, int64_t T, int64_t H,
+                        int64_t I, int64_t E, int32_t top_k, void* Y, void* workspace, size_t workspace_bytes, void* stream) {
+  WOQ_GUARD_BEGIN
+  WOQ_TRY(check_int8_moe(T, H, I, E, top_k));
+  WOQ_TRY(check_activations(X, xdtype, Y));
+  if (!experts || !aligned(experts, 4) || !weights || !aligned(weights, 4))
+    return fail(WOQ_ERR_INVALID_ARGUMENT, "experts and weights must be non-NULL and 4-byte aligned");
+  WOQ_TRY(check_int8_arrays(up_codes, up_scales, "up"));
+  WOQ_TRY(check_int8_arrays(down_codes, down_scales, "down"));
+  const size_t need = woq::int8_moe_workspace_bytes(T, H, I, E, top_k);
+  WOQ_TRY(check_workspace(workspace, workspace_bytes, need));
+  WOQ_TRY(check_apart({{"Y", Y, 2 * T * H}, {"workspace", workspace, (int64_t)need}},
+                      {{"X", X, 2 * T * H}, {"experts", experts, 4 * T * top_k}, {"weights", weights, 4 * T * top_k},
+                       {"up codes", up_codes, 2 * E * I * H}, {"up scales", up_scales, 8 * E * I},
+                       {"down codes", down_codes, E * H * I}, {"down scales", down_scales, 4 * E * H}}));
+  return from_hip(woq::launch_int8_moe(X, xdtype, experts, weights, up_codes, up_scales, down_codes, down_scales, T, H, I, E,
+                                       top_k, Y, workspace, static_cast<hipStream_t>(stream)),
+                  "int8_moe launch");
   WOQ_GUARD_END
 }
 

@@ -175,6 +175,31 @@ hipError_t launch_mxfp4_moe(const void* X, int xdtype, const void* router, const
                             const void* up_scales, const void* down_codes, const void* down_scales, int64_t T,
                             int64_t H, int64_t I, int64_t E, int top_k, void* Y, void* workspace, hipStream_t stream);
 
+// 8-bit integers: codes int8 [M, K], one fp32 scale a row; K % 16 == 0.  xdtype, ydtype as
+// above (fp32 included); act_scale, bias: or NULL.
+hipError_t launch_int8_quantize(const void* x, int xdtype, const float* act_scale, bool multiply, int64_t M, int64_t K,
+                                void* codes, float* scales, hipStream_t stream);
+hipError_t launch_int8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, const float* bias,
+                            int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream);
+size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_linear(const void* X, int xdtype, const float* act_scale, const void* W, const float* w_scales,
+                              const float* bias, int64_t M, int64_t N, int64_t K, void* Y, void* workspace, hipStream_t stream);
+// Routing to experts and its gradient.
+int moe_route_max_experts();
+int moe_route_max_top_k();
+hipError_t launch_moe_route(const void* logits, int dtype, int64_t T, int E, int top_k, bool sigmoid, const float* bias,
+                            int groups, int top_groups, int group_top, bool renormalize, float scale, int32_t* experts,
+                            float* weights, hipStream_t stream);
+hipError_t launch_moe_route_backward(const void* logits, int dtype, const int32_t* experts, const float* dweights, int64_t T,
+                                     int E, int top_k, bool sigmoid, bool renormalize, float scale, void* dlogits,
+                                     hipStream_t stream);
+// A layer of experts on routed tokens.
+int int8_moe_max_experts();
+size_t int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
+hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, const float* weights, const void* up,
+                           const float* up_scales, const void* down, const float* down_scales, int64_t T, int64_t H, int64_t I,
+                           int64_t E, int top_k, void* Y, void* workspace, hipStream_t stream);
+
 // Measurement aids (no quantization): a read-only stream over `bytes` bytes
 // with a given launch shape, an empty kernel, and back-to-back fp16 MFMAs.
 hipError_t launch_stream_read(const void* p, int64_t bytes, int blocks, int threads, int unroll, void* sink,

@@ -386,7 +386,7 @@ def _check_mxfp4(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int
     return (*rows, 2 * half)
 
 
-def _no_grad(*ts: Optional[torch.Tensor]) -> None:
+def _no_grad(*ts: Optional[torch.Tensor], what: str = "the mxfp4 operators have no gradient") -> None:
     """These operators are for inference: a gradient or a forward-mode tangent asked
     of them is refused, not dropped."""
     dual = forward_ad._current_level >= 0
@@ -394,7 +394,7 @@ def _no_grad(*ts: Optional[torch.Tensor]) -> None:
         if t is None:
             continue
         if (t.requires_grad and torch.is_grad_enabled()) or (dual and forward_ad.unpack_dual(t).tangent is not None):
-            raise ValueError("the mxfp4 operators have no gradient (use torch.no_grad() or detach the input)")
+            raise ValueError(f"{what} (use torch.no_grad() or detach the input)")
 
 
 def _launch(name: str, device: torch.device, *args) -> None:
@@ -556,4 +556,248 @@ def mxfp4_moe(
     _launch("woq_mxfp4_moe", X.device, X.data_ptr(), _DTYPE[X.dtype], router.data_ptr(), up_codes.data_ptr(),
             up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k, Y.data_ptr(),
             _ptr(ws), nbytes)
+    return Y
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integers: codes int8 [M, K] and scales fp32 [M], as include/woq.h
+# defines them; routing to experts.
+# ---------------------------------------------------------------------------
+
+_INT8_NO_GRAD = "the int8 operators have no gradient"
+_SCORING = {"softmax": _lib.WOQ_SOFTMAX, "sigmoid": _lib.WOQ_SIGMOID}
+_INT8_MAX_K = 131056
+
+
+def _check_int8(codes: torch.Tensor, scales: torch.Tensor, name: str, dims: int = 2) -> Tuple[int, ...]:
+    """The sizes of a set of 8-bit integers [..., M, K]."""
+    shape = codes.shape
+    if codes.dtype != torch.int8 or len(shape) != dims or shape[-1] < 16 or shape[-1] % 16 or shape[-1] > _INT8_MAX_K:
+        raise ValueError(f"{name} codes must be {dims}-D int8 with K columns, K a positive multiple of 16 up to "
+                         f"{_INT8_MAX_K} (got {codes.dtype}, {tuple(shape)})")
+    if scales.dtype != torch.float32 or scales.shape != shape[:-1]:
+        raise ValueError(f"{name} scales must be float32 of shape {tuple(shape[:-1])} "
+                         f"(got {scales.dtype}, {tuple(scales.shape)})")
+    return tuple(shape)
+
+
+def _check_bias(bias: Optional[torch.Tensor], n: int) -> None:
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (n,)):
+        raise ValueError(f"bias must be float32 of shape ({n},) (got {bias.dtype}, {tuple(bias.shape)})")
+
+
+def int8_quantize(
+    x: torch.Tensor,
+    act_scale: Optional[torch.Tensor] = None,
+    weight: bool = False,
+    out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Quantize the rows of x [M, K] (fp16, bf16 or fp32) to 8-bit integers ->
+    (codes int8 [M, K], scales fp32 [M]).  act_scale fp32 [K] divides the
+    channels of activations before, or multiplies those of a weight."""
+    xdtype, shape = _MX_OUT.get(x.dtype), x.shape
+    if (xdtype is None or len(shape) != 2 or shape[0] < 1 or shape[1] < 16 or shape[1] % 16 or shape[1] > _INT8_MAX_K):
+        raise ValueError(f"x must be fp16/bf16/fp32 [M, K] with M >= 1 and K a positive multiple of 16 up to "
+                         f"{_INT8_MAX_K} (got {x.dtype}, {tuple(shape)})")
+    M, K = shape
+    _check_act_scale(act_scale, K)
+    _no_grad(x, act_scale, what=_INT8_NO_GRAD)
+    if out is None:
+        _require_gpu(x, act_scale)
+        codes = x.new_empty(M, K, dtype=torch.int8)
+        scales = x.new_empty(M, dtype=torch.float32)
+    else:
+        codes, scales = out
+        _check_out(codes, (M, K), torch.int8, "out codes")
+        _check_out(scales, (M,), torch.float32, "out scales")
+        _no_grad(scales, what=_INT8_NO_GRAD)
+        _require_gpu(x, act_scale, codes, scales)
+    _launch("woq_int8_quantize", x.device, x.data_ptr(), xdtype, _ptr(act_scale), int(weight), M, K, codes.data_ptr(),
+            scales.data_ptr())
+    return codes, scales
+
+
+def int8_gemm(
+    a_codes: torch.Tensor,
+    a_scales: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    bias: Optional[torch.Tensor] = None,
+    dtype: torch.dtype = torch.bfloat16,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Y [M, N] = a @ w^T + bias of dtype (fp16, bf16 or fp32) for activations a
+    [M, K] and weights w [N, K] in 8-bit integers (int8_quantize); bias fp32 [N]."""
+    M, K = _check_int8(a_codes, a_scales, "activation")
+    N, Kw = _check_int8(codes, scales, "weight")
+    if K != Kw:
+        raise ValueError(f"activations and weights must share K (got {K} and {Kw})")
+    if dtype not in _MX_OUT:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16 (got {dtype})")
+    if M < 1 or N < 1:
+        raise ValueError("need at least one row of activations and of weights")
+    _check_bias(bias, N)
+    _no_grad(a_scales, scales, bias, out, what=_INT8_NO_GRAD)
+    if out is not None:
+        _check_out(out, (M, N), dtype, "out")
+    _require_gpu(a_codes, a_scales, codes, scales, bias, out)
+    Y = out if out is not None else a_codes.new_empty(M, N, dtype=dtype)
+    _launch("woq_int8_gemm", a_codes.device, a_codes.data_ptr(), a_scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+            _ptr(bias), M, N, K, _MX_OUT[dtype], Y.data_ptr())
+    return Y
+
+
+def int8_linear(
+    X: torch.Tensor,
+    codes: torch.Tensor,
+    scales: torch.Tensor,
+    act_scale: Optional[torch.Tensor] = None,
+    bias: Optional[torch.Tensor] = None,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Y [M, N] = q(X / act_scale) @ w^T + bias for X [M, K] (fp16 or bf16), quantized
+    by rows in the call, and weights w [N, K] in 8-bit integers."""
+    N, K = _check_int8(codes, scales, "weight")
+    xdtype, shape = _DTYPE.get(X.dtype), X.shape
+    if xdtype is None or len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"X must be fp16/bf16 [M, {K}] (got {X.dtype}, {tuple(shape)})")
+    M = shape[0]
+    if M < 1 or N < 1:
+        raise ValueError("need at least one row of X and of the weights")
+    _check_act_scale(act_scale, K)
+    _check_bias(bias, N)
+    _no_grad(X, scales, act_scale, bias, out, what=_INT8_NO_GRAD)
+    if out is not None:
+        _check_out(out, (M, N), X.dtype, "out")
+    _require_gpu(X, codes, scales, act_scale, bias, out)
+    Y = out if out is not None else X.new_empty(M, N)
+    nbytes = _mx_workspace_bytes("woq_int8_linear_workspace_bytes", M, N, K)
+    ws = _mx_workspace(X, nbytes)
+    _launch("woq_int8_linear", X.device, X.data_ptr(), xdtype, _ptr(act_scale), codes.data_ptr(), scales.data_ptr(),
+            _ptr(bias), M, N, K, Y.data_ptr(), _ptr(ws), nbytes)
+    return Y
+
+
+def _check_logits(logits: torch.Tensor, scoring: str) -> Tuple[int, int]:
+    if logits.dtype not in _MX_OUT or logits.dim() != 2 or logits.shape[0] < 1 or not 1 <= logits.shape[1] <= 512:
+        raise ValueError(f"logits must be fp16/bf16/fp32 [T, E] with T >= 1 and 1 to 512 experts (got {logits.dtype}, "
+                         f"{tuple(logits.shape)})")
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid' (got {scoring!r})")
+    return logits.shape[0], logits.shape[1]
+
+
+def moe_route(
+    logits: torch.Tensor,
+    top_k: int,
+    scoring: str = "softmax",
+    bias: Optional[torch.Tensor] = None,
+    groups: int = 1,
+    top_groups: Optional[int] = None,
+    group_top: int = 1,
+    renormalize: bool = True,
+    scale: float = 1.0,
+    out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The top_k experts of each token and their weights from the router's logits
+    [T, E] (fp16, bf16 or fp32) -> (experts int32 [T, top_k], weights fp32 [T, top_k]).
+    bias fp32 [E] steers the choice; only the best top_groups (default: all) of
+    `groups` groups of experts are chosen from; see woq_moe_route in include/woq.h.
+    moe_route_backward is the weights' gradient."""
+    T, E = _check_logits(logits, scoring)
+    _check_bias(bias, E)
+    top_groups = groups if top_groups is None else top_groups
+    if groups < 1 or E % groups or not 1 <= top_groups <= groups:
+        raise ValueError(f"groups must divide E and top_groups be in [1, groups] (got E={E}, groups={groups}, "
+                         f"top_groups={top_groups})")
+    if group_top not in (1, 2) or group_top > E // groups:
+        raise ValueError(f"group_top must be 1 or 2 and at most a group's {E // groups} experts (got {group_top})")
+    if not 1 <= top_k <= min(64, E // groups * top_groups):
+        raise ValueError(f"top_k must be in [1, {min(64, E // groups * top_groups)}] (got {top_k})")
+    _no_grad(logits, bias, what="moe_route records no gradient: its weights' is moe_route_backward")
+    if out is None:
+        _require_gpu(logits, bias)
+        experts = logits.new_empty(T, top_k, dtype=torch.int32)
+        weights = logits.new_empty(T, top_k, dtype=torch.float32)
+    else:
+        experts, weights = out
+        _check_out(experts, (T, top_k), torch.int32, "out experts")
+        _check_out(weights, (T, top_k), torch.float32, "out weights")
+        _no_grad(weights, what="moe_route records no gradient")
+        _require_gpu(logits, bias, experts, weights)
+    _launch("woq_moe_route", logits.device, logits.data_ptr(), _MX_OUT[logits.dtype], T, E, top_k, _SCORING[scoring],
+            _ptr(bias), groups, top_groups, group_top, int(renormalize), scale, experts.data_ptr(), weights.data_ptr())
+    return experts, weights
+
+
+def moe_route_backward(
+    logits: torch.Tensor,
+    experts: torch.Tensor,
+    dweights: torch.Tensor,
+    scoring: str = "softmax",
+    renormalize: bool = True,
+    scale: float = 1.0,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """dlogits [T, E] of logits' type from the gradient dweights fp32 [T, top_k] of
+    moe_route's weights, for the experts int32 [T, top_k] that it chose and the same
+    scoring, renormalize and scale."""
+    T, E = _check_logits(logits, scoring)
+    if experts.dtype != torch.int32 or experts.dim() != 2 or experts.shape[0] != T or not 1 <= experts.shape[1] <= min(64, E):
+        raise ValueError(f"experts must be int32 [{T}, top_k] (got {experts.dtype}, {tuple(experts.shape)})")
+    top_k = experts.shape[1]
+    if dweights.dtype != torch.float32 or dweights.shape != experts.shape:
+        raise ValueError(f"dweights must be float32 of shape {tuple(experts.shape)} (got {dweights.dtype}, "
+                         f"{tuple(dweights.shape)})")
+    _no_grad(logits, dweights, out, what="moe_route_backward has no gradient of its own")
+    if out is not None:
+        _check_out(out, (T, E), logits.dtype, "out")
+    _require_gpu(logits, experts, dweights, out)
+    dlogits = out if out is not None else torch.empty_like(logits)
+    _launch("woq_moe_route_backward", logits.device, logits.data_ptr(), _MX_OUT[logits.dtype], experts.data_ptr(),
+            dweights.data_ptr(), T, E, top_k, _SCORING[scoring], int(renormalize), scale, dlogits.data_ptr())
+    return dlogits
+
+
+def int8_moe(
+    X: torch.Tensor,
+    experts: torch.Tensor,
+    weights: torch.Tensor,
+    up_codes: torch.Tensor,
+    up_scales: torch.Tensor,
+    down_codes: torch.Tensor,
+    down_scales: torch.Tensor,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """A layer of gated experts on tokens X [T, H] (fp16 or bf16) routed to experts
+    int32 [T, top_k] with weights fp32 [T, top_k] (moe_route; an expert outside
+    0 .. E-1 takes no part): up in 8-bit integers [E, 2 I, H] (gate rows, then up rows),
+    down [E, H, I] -> Y [T, H].  Activations are quantized by rows in the call; see
+    woq_int8_moe in include/woq.h."""
+    E, I2, H = _check_int8(up_codes, up_scales, "up", 3)
+    I = I2 // 2
+    if I2 % 2 or _check_int8(down_codes, down_scales, "down", 3) != (E, H, I):
+        raise ValueError(f"up must be [E, 2 I, H] and down [E, H, I] (got {(E, I2, H)} and {tuple(down_codes.shape)})")
+    if X.dtype not in _DTYPE or X.dim() != 2 or X.shape[1] != H:
+        raise ValueError(f"X must be fp16/bf16 [T, {H}] (got {X.dtype}, {tuple(X.shape)})")
+    T = X.shape[0]
+    if experts.dtype != torch.int32 or experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError(f"experts must be int32 [{T}, top_k] (got {experts.dtype}, {tuple(experts.shape)})")
+    if weights.dtype != torch.float32 or weights.shape != experts.shape:
+        raise ValueError(f"weights must be float32 of shape {tuple(experts.shape)} (got {weights.dtype}, "
+                         f"{tuple(weights.shape)})")
+    top_k = experts.shape[1]
+    nbytes = _mx_workspace_bytes("woq_int8_moe_workspace_bytes", T, H, I, E, top_k)
+    if nbytes == 0:
+        raise ValueError(f"int8_moe takes at least one token, up to 512 experts and a top_k of 1 to 64, in sizes that 32 "
+                         f"bits address (got T={T}, H={H}, I={I}, E={E}, top_k={top_k})")
+    _no_grad(X, weights, up_scales, down_scales, out, what=_INT8_NO_GRAD)
+    if out is not None:
+        _check_out(out, (T, H), X.dtype, "out")
+    _require_gpu(X, experts, weights, up_codes, up_scales, down_codes, down_scales, out)
+    Y = out if out is not None else X.new_empty(T, H)
+    ws = _mx_workspace(X, nbytes)
+    _launch("woq_int8_moe", X.device, X.data_ptr(), _DTYPE[X.dtype], experts.data_ptr(), weights.data_ptr(),
+            up_codes.data_ptr(), up_scales.data_ptr(), down_codes.data_ptr(), down_scales.data_ptr(), T, H, I, E, top_k,
+            Y.data_ptr(), _ptr(ws), nbytes)
     return Y

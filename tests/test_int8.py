@@ -257,6 +257,7 @@ def test_workspace_sizes_of_invalid_sizes_are_zero():
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 FILES = {
     "int8_quantize.hip": ["int8_quantize_kernel"],
+    "int8_gemv.hip": ["int8_gemv_kernel"],
     "int8_gemm.hip": ["int8_gemm_kernel"],
     "moe_route.hip": ["moe_route_kernel", "moe_route_backward_kernel"],
     "int8_moe.hip": ["int8_moe_plan_kernel", "int8_moe_product_kernel", "int8_moe_combine_kernel"],

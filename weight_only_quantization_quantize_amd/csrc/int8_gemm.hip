@@ -14,7 +14,7 @@ constexpr int kGroup = 8;  // M tiles of a group
 // in groups of 8 M tiles, M fastest, so that the tiles in flight there share about as much
 // of A as of W in its L2.
 template <class YT, class C>
-__global__ __launch_bounds__(C::kThreads, 2) void int8_gemm_kernel(
+__global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_gemm_kernel(
     const int8_t* __restrict__ A, const float* __restrict__ sa, const int8_t* __restrict__ W, const float* __restrict__ sw,
     const float* __restrict__ bias, int M, int N, int K, int mtiles, int tiles, typename Int8Out<YT>::type* __restrict__ Y) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLdsBytes];
@@ -32,12 +32,12 @@ __global__ __launch_bounds__(C::kThreads, 2) void int8_gemm_kernel(
 
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m1 = m0 + (wave & 1) * (32 * C::TM), n1 = n0 + (wave >> 1) * (32 * C::TN);
-  constexpr int kCols = 32 * C::TN, kTurn = 32 * (kCols * 4 + 16) + kCols * 8;
+  const int m1 = m0 + wave % C::WM * (32 * C::TM), n1 = n0 + wave / C::WM * (32 * C::TN);
+  constexpr int kCols = 32 * C::TN, kPitch = kCols * (int)sizeof(*Y) + 16, kTurn = 32 * kPitch + kCols * 8;
   // a wave's LDS: the turn, then its columns' scales and biases
   static_assert(C::kWaves * kTurn <= C::kStages * C::kStage, "the turn fits the stages' place");
   uint8_t* const turn = lds + wave * kTurn;
-  float* const cols = reinterpret_cast<float*>(turn + 32 * (kCols * 4 + 16));
+  float* const cols = reinterpret_cast<float*>(turn + 32 * kPitch);
   for (int c = lane; c < kCols; c += 64) {
     const int n = n1 + c < N ? n1 + c : N - 1;
     cols[c] = sw[n];
@@ -70,22 +70,61 @@ hipError_t launch_tiles(const int8_t* A, const float* sa, const int8_t* W, const
   return hipGetLastError();
 }
 
-int64_t per_cu(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256; }
+// The tile with the smallest time by a model of what was measured (weights out of HBM, 327
+// sizes from 2 x 36 x 64 to 4096 x 11008 x 4096), in us for r tiles a compute unit and s
+// stages of 128 K:  fixed + r (tile + stage s).  Where the choice is not the fastest of all
+// it costs 3% in the mean.  Large tiles read LDS least for a matrix instruction (2048 x 11008
+// x 4096: 256 x 384 85 us, 192 x 256 95, 128 x 128 107, 256 x 256, whose 344 tiles fill two
+// rounds badly, 111; 8192 x 8192 x 8192: 459, 510, 539 and 450); small ones are there for
+// outputs of few tiles, where K is split between four groups of waves and many stages are in
+// flight (16 x 4096 x 11008: 32 x 32 16.4 us, 64 x 32 18.1, 64 x 64 23.7; 128 x 4096 x 4096:
+// 15, 9.3 and 10.4; 16 x 28672 x 8192: 55, 58 and 45.5).
+struct Model {
+  int bm, bn;
+  double fixed, tile, stage;
+};
+constexpr Model kModels[] = {{256, 256, 0.0, 7.95, 1.24}, {256, 384, 0.0, 11.08, 1.73}, {192, 256, 0.0, 6.61, 1.02},
+                             {128, 256, 0.0, 5.91, 0.75}, {128, 128, 0.0, 5.17, 0.47},  {64, 128, 0.49, 3.09, 0.30},
+                             {64, 64, 2.3, 1.11, 0.21},   {64, 32, 0.85, 3.12, 0.16},   {32, 32, 1.36, 2.63, 0.14}};
+// wide: the second tile too (its registers hold the sums and 16-bit outputs, not fp32 ones)
+int choose(int64_t M, int64_t N, int64_t K, bool wide) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < (int)(sizeof(kModels) / sizeof(kModels[0])); ++i) {
+    if (i == 1 && !wide) continue;
+    const Model& m = kModels[i];
+    const double r = (double)(((M + m.bm - 1) / m.bm * ((N + m.bn - 1) / m.bn) + 255) / 256);
+    const double t = m.fixed + r * (m.tile + m.stage * (double)((K + 127) / 128));
+    if (i == 0 || t < least) least = t, best = i;
+  }
+  return best;
+}
 
 template <class YT>
 hipError_t launch(const int8_t* A, const float* sa, const int8_t* W, const float* sw, const float* bias, int64_t M,
                   int64_t N, int64_t K, void* Y, hipStream_t stream) {
-  const double large = 48.0 * per_cu(M, N, 256, 256), mid = 6.0 + 14.0 * per_cu(M, N, 128, 128),
-               small = 3.0 + 6.0 * per_cu(M, N, 64, 64);
-  if (large <= mid && large <= small) return launch_tiles<YT, Int8Tile<4, 2, 4, 4, 1>>(A, sa, W, sw, bias, M, N, K, Y, stream);
-  if (mid <= small) return launch_tiles<YT, Int8Tile<2, 2, 2, 4, 1>>(A, sa, W, sw, bias, M, N, K, Y, stream);
-  return launch_tiles<YT, Int8Tile<1, 1, 2, 4, 2>>(A, sa, W, sw, bias, M, N, K, Y, stream);
+  auto run = [&](auto tag) { return launch_tiles<YT, decltype(tag)>(A, sa, W, sw, bias, M, N, K, Y, stream); };
+  constexpr bool kWide = !std::is_same_v<YT, F32>;
+  switch (choose(M, N, K, kWide)) {
+    case 0: return run(Int8Tile<4, 2, 4, 4, 1, 2>{});
+    case 1:
+      if constexpr (kWide) return run(Int8Tile<4, 3, 4, 4, 1, 2>{});
+      [[fallthrough]];
+    case 2: return run(Int8Tile<3, 2, 4, 4, 1, 2>{});
+    case 3: return run(Int8Tile<2, 2, 4, 4, 1, 3>{});
+    case 4: return run(Int8Tile<2, 2, 2, 4, 1, 4, 1>{});
+    case 5: return run(Int8Tile<1, 1, 4, 4, 1, 4>{});
+    case 6: return run(Int8Tile<1, 1, 2, 4, 1, 4>{});
+    case 7: return run(Int8Tile<1, 1, 1, 4, 4, 3>{});
+    default: return run(Int8Tile<1, 1, 1, 4, 4, 4, 1, 1>{});
+  }
 }
 
 }  // namespace
 
 hipError_t launch_int8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, const float* bias,
                             int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream) {
+  if (M == 1 && K <= int8_gemv_max_k()) return launch_int8_gemv(A, a_scales, W, w_scales, bias, N, K, ydtype, Y, stream);
   auto* const f = ydtype == 0 ? launch<F16> : (ydtype == 1 ? launch<BF16> : launch<F32>);
   return f(static_cast<const int8_t*>(A), a_scales, static_cast<const int8_t*>(W), w_scales, bias, M, N, K, Y, stream);
 }
@@ -94,10 +133,14 @@ namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
-size_t int8_linear_workspace_bytes(int64_t M, int64_t, int64_t K) { return up256((size_t)(M * K)) + (size_t)M * 4; }
+// The row's codes and scales, or nothing where one launch does it all.
+size_t int8_linear_workspace_bytes(int64_t M, int64_t, int64_t K) {
+  return M == 1 && K <= int8_gemv_max_k() ? 0 : up256((size_t)(M * K)) + (size_t)M * 4;
+}
 
 hipError_t launch_int8_linear(const void* X, int xdtype, const float* act_scale, const void* W, const float* w_scales,
                               const float* bias, int64_t M, int64_t N, int64_t K, void* Y, void* workspace, hipStream_t stream) {
+  if (M == 1 && K <= int8_gemv_max_k()) return launch_int8_linear_row(X, xdtype, act_scale, W, w_scales, bias, N, K, Y, stream);
   float* const scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256((size_t)(M * K)));
   const hipError_t e = launch_int8_quantize(X, xdtype, act_scale, false, M, K, workspace, scales, stream);
   if (e != hipSuccess) return e;

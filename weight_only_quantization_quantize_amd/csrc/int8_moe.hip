@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kPlanThreads) void int8_moe_plan_kernel(const int32
 // UP: A = X's codes, gathered; W's tile is blocks of 32 gate rows and the 32 up rows of the
 // same columns in turn.  Else A = h's codes.  ntiles: of columns of h (of y).
 template <bool UP, class C>
-__global__ __launch_bounds__(C::kThreads, 2) void int8_moe_product_kernel(
+__global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_moe_product_kernel(
     const int8_t* __restrict__ A, const float* __restrict__ sa, const int8_t* __restrict__ W, const float* __restrict__ sw,
     const Plan* __restrict__ plan, const Tile* __restrict__ tiles, const int* __restrict__ token, int K, int N, int ntiles,
     float* __restrict__ out) {
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void int8_moe_product_kernel(
   constexpr int kTurn = 32 * (kCols * 4 + 16) + kCols * 8;
   static_assert(C::kWaves * kTurn <= C::kStages * C::kStage, "the turn fits the stages' place");
   static_assert(!UP || C::TN % 2 == 0, "a wave has gate and up columns");
-  const int m1 = (wave & 1) * (32 * C::TM), n1 = n0 + (wave >> 1) * kCols;
+  const int m1 = wave % C::WM * (32 * C::TM), n1 = n0 + wave / C::WM * kCols;
   uint8_t* const turn = lds + wave * kTurn;
   float* const cols = reinterpret_cast<float*>(turn + 32 * (kCols * 4 + 16));
   for (int c = lane; c < kCols; c += 64) {
@@ -164,8 +164,8 @@ __global__ __launch_bounds__(256) void int8_moe_combine_kernel(const float* __re
   }
 }
 
-typedef Int8Tile<1, 2, 2, 4, 1> Small;
-typedef Int8Tile<2, 2, 2, 4, 1> Middle;
+typedef Int8Tile<1, 2, 2, 4, 1, 3> Small;
+typedef Int8Tile<2, 2, 2, 4, 1, 2> Middle;
 
 // Tiles of rows, at most: one for each expert that is taken and one for each further BM.
 int64_t most_tiles(int64_t choices, int64_t E, int64_t BM) { return (choices < E ? choices : E) + choices / BM; }

@@ -1,7 +1,7 @@
 // Tiles of products of 8-bit integer matrices: sums over K of a[m, k] w[n, k], exact in
 // 32-bit integers, for A [., K] and W [., K] with rows as stored (K a multiple of 16).
 //
-// Tile.  A group of 2 x WN waves computes 64 TM x 32 WN TN sums, a wave 32 TM x 32 TN, on
+// Tile.  A group of WM x WN waves computes 32 WM TM x 32 WN TN sums, a wave 32 TM x 32 TN, on
 // v_mfma_i32_32x32x32_i8; KG groups of a workgroup share the tile's K and add their sums
 // through LDS at the end.
 //
@@ -48,21 +48,17 @@ __device__ inline void int8_wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <int TM_, int TN_, int WN_, int KS_, int KG_>
+// OCC: waves a SIMD that the registers are shared among.
+template <int TM_, int TN_, int WN_, int KS_, int KG_, int NS_, int OCC_ = 2, int WM_ = 2>
 struct Int8Tile {
-  static constexpr int TM = TM_, TN = TN_, WN = WN_, KS = KS_, KG = KG_;
-  static constexpr int kWaves = 2 * WN, kThreads = 64 * kWaves * KG;
-  static constexpr int BM = 64 * TM, BN = 32 * WN * TN;
+  static constexpr int TM = TM_, TN = TN_, WN = WN_, KS = KS_, KG = KG_, kStages = NS_, kOccupancy = OCC_, WM = WM_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves * KG;
+  static constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   static constexpr int kRow = 32 * KS;      // bytes of a row's stage
   static constexpr int kChunks = 2 * KS;    // of 16 bytes
   static constexpr int kUnitRows = 1024 / kRow;
   static constexpr int kAUnits = BM / kUnitRows, kWUnits = BN / kUnitRows;
   static constexpr int kStage = (BM + BN) * kRow;
-  // as many stages as leave room for a second workgroup, or, where that would be fewer
-  // than two, as fill the LDS; at most 4
-  static constexpr int kRoom = (KG * kStage * 2 > 80 * 1024 ? 160 : 80) * 1024;
-  static constexpr int kFit = kRoom / (KG * kStage);
-  static constexpr int kStages = kFit > 4 ? 4 : (kFit < 2 ? 2 : kFit);
   static constexpr int kALoads = (kAUnits + kWaves - 1) / kWaves, kWLoads = (kWUnits + kWaves - 1) / kWaves;
   static constexpr int kLoads = kALoads + kWLoads;
   static constexpr int kLdsBytes = KG * kStages * kStage;
@@ -74,7 +70,7 @@ struct Int8Tile {
 
   // acc[i][j] of the first group's waves: the lane's sums of row m = 32 (wm + i) + lane % 32
   // of A and, element e, row n = 32 (wn + j) + 8 (e / 4) + 4 (lane / 32) + e % 4 of W, with
-  // wm = TM (wave % 2), wn = TN (wave / 2); false for the other groups' waves.
+  // wm = TM (wave % WM), wn = TN (wave / WM); false for the other groups' waves.
   // a_row(r), w_row(r): byte offsets (below 2^32) of the tile's rows from a and w, for
   // every r of the tile.  All threads call; LDS may be used again behind the next barrier.
   template <class AR, class WR>
@@ -83,7 +79,7 @@ struct Int8Tile {
     const int lane = threadIdx.x & 63;
     const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = wave_all % kWaves, group = wave_all / kWaves;
-    const int wm = (wave & 1) * TM, wn = (wave >> 1) * TN;
+    const int wm = wave % WM * TM, wn = wave / WM * TN;
     const int half = lane >> 5, r32 = lane & 31;
     const int chunks = K >> 4;
     const int stages = (chunks + kChunks - 1) / kChunks;
@@ -145,32 +141,63 @@ struct Int8Tile {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-    for (int st = 0; st + 1 < kStages; ++st) issue(h0 + st, st);
-    int buf = 0;
-    auto turn = [&](int h, auto masked) {
+    // A unit is row block i of step s: TN matrix instructions.  Operands are read from LDS a
+    // unit ahead; the last kTail units of a stage run behind the barrier that ends it, with
+    // their operands in registers, and cover the next stage's first reads.
+    constexpr int kUnits = KS * TM, kTail = TM < 3 ? 1 : TM - 1, kSlots = kTail + 1;
+    static_assert(kUnits % kSlots == 0, "a stage's first unit follows the last one's place");
+    int4v_t v[kSlots], wc[2][TN];
+    auto read_a = [&](const uint8_t* la, int u) {
+      v[u % kSlots] = *reinterpret_cast<const int4v_t*>(la + a_at[u / TM] + u % TM * 32 * kRow);
+    };
+    auto read_w = [&](const uint8_t* la, int s) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) wc[s & 1][j] = *reinterpret_cast<const int4v_t*>(la + w_at[s] + j * 32 * kRow);
+    };
+    // Until stage h's own loads are done, everybody's, and everybody has read the stage
+    // before, whose place takes the stage kStages - 1 ahead.
+    int buf = 0;  // of stage h
+    auto enter = [&](int h) {
       int8_wait_loads<(kStages - 2) * kLoads>();
       __builtin_amdgcn_s_barrier();
       issue(h + kStages - 1, buf == 0 ? kStages - 1 : buf - 1);
-      const uint8_t* const la = lds + buf * kStage;
-      buf = buf + 1 == kStages ? 0 : buf + 1;
-      if (KG > 1 && h < 0) return;
+    };
+    for (int st = 0; st + 1 < kStages; ++st) issue(h0 + st, st);
+    enter(h0);
+    read_w(lds, 0);
+    read_a(lds, 0);
+    auto turn = [&](int h, auto masked) {
+      const uint8_t* la = lds + buf * kStage;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        int4v_t wc[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          wc[j] = *reinterpret_cast<const int4v_t*>(la + w_at[s] + j * 32 * kRow);
-          if constexpr (decltype(masked)::value)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) wc[j][e] = h * kChunks + 2 * s + half < chunks ? wc[j][e] : 0;
+      for (int u = 0; u < kUnits; ++u) {
+        const int s = u / TM, i = u % TM;
+        if (u == kUnits - kTail) {
+          buf = buf + 1 == kStages ? 0 : buf + 1;
+          la = lds + buf * kStage;
+          enter(h + 1);
+          read_w(la, 0);
+          read_a(la, 0);
         }
+        if (i == (TM > 1 ? TM - 2 : 0) && s + 1 < KS) read_w(la, s + 1);
+        if (u < kUnits - kTail - 1) read_a(la, u + 1);
+        if (u == kUnits - kTail - 1)
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const int4v_t v = *reinterpret_cast<const int4v_t*>(la + a_at[s] + i * 32 * kRow);
+          for (int p = u + 1; p < kUnits; ++p) read_a(la, p);
+        if constexpr (decltype(masked)::value) {
+          if (i == 0)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wc[j], v, acc[i][j], 0, 0, 0);
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) wc[s & 1][j][e] = h * kChunks + 2 * s + half < chunks ? wc[s & 1][j][e] : 0;
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wc[s & 1][j], v[u % kSlots], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (KG > 1 && h < 0)  // what a stage that is not there gave
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i) acc[i / TN][i % TN] = int16v_t{};
     };
     const bool rest = stages * kChunks > chunks;
     const int end = h0 + turns - (rest ? 1 : 0);

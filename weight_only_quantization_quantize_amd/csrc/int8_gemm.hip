@@ -24,40 +24,43 @@ __global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_gemm_kernel(
   const int gtiles = kGroup * (tiles / mtiles);  // of a group of M tiles
   const int g = tile / gtiles, gm = mtiles - g * kGroup < kGroup ? mtiles - g * kGroup : kGroup;
   const int m0 = (g * kGroup + tile % gtiles % gm) * C::BM, n0 = tile % gtiles / gm * C::BN;
-  typename C::Sums acc;
-  const bool mine = C::multiply(
-      acc, lds, A + (int64_t)m0 * K, [&](int r) { return (uint32_t)((m0 + r < M ? r : M - 1 - m0) * K); },
-      W + (int64_t)n0 * K, [&](int r) { return (uint32_t)((n0 + r < N ? r : N - 1 - n0) * K); }, K);
-  if (!mine) return;
+  C::for_blocks(M - m0, [&](auto blocks) {
+    constexpr int kBlocks = decltype(blocks)::value;
+    typename C::template Sums<kBlocks> acc;
+    const bool mine = C::template multiply<kBlocks>(
+        acc, lds, A + (int64_t)m0 * K, [&](int r) { return (uint32_t)((m0 + r < M ? r : M - 1 - m0) * K); },
+        W + (int64_t)n0 * K, [&](int r) { return (uint32_t)((n0 + r < N ? r : N - 1 - n0) * K); }, K);
+    if (!mine) return;
 
-  const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m1 = m0 + wave % C::WM * (32 * C::TM), n1 = n0 + wave / C::WM * (32 * C::TN);
-  constexpr int kCols = 32 * C::TN, kPitch = kCols * (int)sizeof(*Y) + 16, kTurn = 32 * kPitch + kCols * 8;
-  // a wave's LDS: the turn, then its columns' scales and biases
-  static_assert(C::kWaves * kTurn <= C::kStages * C::kStage, "the turn fits the stages' place");
-  uint8_t* const turn = lds + wave * kTurn;
-  float* const cols = reinterpret_cast<float*>(turn + 32 * kPitch);
-  for (int c = lane; c < kCols; c += 64) {
-    const int n = n1 + c < N ? n1 + c : N - 1;
-    cols[c] = sw[n];
-    cols[kCols + c] = bias ? bias[n] : 0.0f;
-  }
-  asm volatile("" ::: "memory");
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n1 = n0 + wave / C::WM * (32 * C::TN);
+    constexpr int kCols = 32 * C::TN, kPitch = kCols * (int)sizeof(*Y) + 16, kTurn = 32 * kPitch + kCols * 8;
+    // a wave's LDS: the turn, then its columns' scales and biases
+    static_assert(C::kWaves * kTurn <= C::kGroupBytes, "the turn fits the stages' place");
+    uint8_t* const turn = lds + wave * kTurn;
+    float* const cols = reinterpret_cast<float*>(turn + 32 * kPitch);
+    for (int c = lane; c < kCols; c += 64) {
+      const int n = n1 + c < N ? n1 + c : N - 1;
+      cols[c] = sw[n];
+      cols[kCols + c] = bias ? bias[n] : 0.0f;
+    }
+    asm volatile("" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
-    const int m = m1 + 32 * i, r = m + (lane & 31);
-    if (m >= M) break;
-    const float f = sa[r < M ? r : M - 1];
-    int8_store_rows<YT, kCols>(turn, Y + (int64_t)m * N + n1, N, M - m, N - n1, [&](int b) {
-      const float4_t s = *reinterpret_cast<const float4_t*>(cols + 8 * b + 4 * half);
-      const float4_t t = *reinterpret_cast<const float4_t*>(cols + kCols + 8 * b + 4 * half);
-      float4_t v;
+    for (int i = 0; i < kBlocks; ++i) {
+      const int m = m0 + 32 * C::row_block(wave, i), r = m + (lane & 31);
+      if (m >= M) break;
+      const float f = sa[r < M ? r : M - 1];
+      int8_store_rows<YT, kCols>(turn, Y + (int64_t)m * N + n1, N, M - m, N - n1, [&](int b) {
+        const float4_t s = *reinterpret_cast<const float4_t*>(cols + 8 * b + 4 * half);
+        const float4_t t = *reinterpret_cast<const float4_t*>(cols + kCols + 8 * b + 4 * half);
+        float4_t v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][b / 4][4 * (b % 4) + e] * f * s[e] + t[e];
-      return v;
-    });
-  }
+        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][b / 4][4 * (b % 4) + e] * f * s[e] + t[e];
+        return v;
+      });
+    }
+  });
 }
 
 template <class YT, class C>

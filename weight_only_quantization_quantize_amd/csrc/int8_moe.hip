@@ -6,10 +6,22 @@
 //   Y[t]   = sum over the token's choices c of weights[t, c] y[t, c], rounded once
 // A choice whose expert is none of 0 .. E - 1 is left out.
 //
-// Launches: the rows of X are quantised; `plan` sorts the choices by expert into rows and
-// cuts each expert's rows into tiles; `up` and `down` are tile products (int8_tile.h) over
-// those tiles; h's rows are quantised between them; `combine` adds up.  The rows' order in
-// the plan changes no result: every row is computed by itself.
+// Launches: `prepare` quantizes the rows of X and, in its first workgroup, sorts the choices
+// by expert into rows and cuts each expert's rows into tiles; `up` and `down` are tile
+// products (int8_tile.h) over those tiles; h's rows are quantized between them; `combine`
+// adds up.  The rows' order in the plan changes no result: every row is computed by itself.
+//
+// Work of the products.  Experts' row counts differ, and a tile of few rows is cheap
+// (int8_tile.h: it multiplies its own blocks of rows only), so tiles are taken, not dealt: a
+// workgroup a compute unit's place takes tile after tile, those of the experts with the most
+// rows first.  With many tokens the weights' bytes bound the products as much as the matrix
+// units do (a dense product of 256 rows with as many weight bytes takes 165 us, one with few
+// weights 115 .. 130), so an expert's weights should come out of HBM once: its row tiles of
+// one column tile are neighbours in the run of one XCD, are multiplied at the same time and
+// share the weights in its L2.  The column tiles go around the XCDs, which so have the same
+// work.  2048 tokens of 32 experts 4096 x 2048, four each, whole layer: 389 us; each XCD an
+// eighth of all tiles, experts in a row, 412, with the idle ones helping out 417.
+#include "int8_rows.h"
 #include "int8_tile.h"
 #include "woq_internal.h"
 
@@ -17,97 +29,107 @@ namespace woq {
 namespace {
 
 constexpr int kMaxExperts = 512;
-constexpr int kPlanThreads = 1024;
+constexpr int kXcds = 8;
 
-// Up to BM rows of an expert.
+// Up to BM rows of an expert, whose rank by rows is `rank`.
 struct Tile {
-  int expert, row, count;
+  int expert, row, count, rank;
 };
+// Row tiles; how many items of each XCD's run were taken so far (beside the first ones, which
+// are dealt), of up and of down.
 struct Plan {
   int tiles;
+  int taken[2][kXcds];
 };
 
-// One workgroup.  where [T top_k]: a choice's row, -1 of none; token [rows].
-__global__ __launch_bounds__(kPlanThreads) void int8_moe_plan_kernel(const int32_t* __restrict__ experts, int choices,
-                                                                    int top_k, int E, int BM, Plan* __restrict__ plan,
-                                                                    Tile* __restrict__ tiles, int* __restrict__ where,
-                                                                    int* __restrict__ token) {
-  __shared__ int count[kMaxExperts], first[kMaxExperts], tile[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += kPlanThreads) count[e] = 0;
+// One workgroup of at least 64 threads.  where [T top_k]: a choice's row, -1 of none; token [rows].
+__device__ void int8_moe_plan(const int32_t* __restrict__ experts, int choices, int top_k, int E, int BM, Plan* __restrict__ plan,
+                              Tile* __restrict__ tiles, int* __restrict__ where, int* __restrict__ token) {
+  __shared__ int count[kMaxExperts], first[kMaxExperts], by_rank[kMaxExperts];
+  const int threads = blockDim.x;
+  for (int e = threadIdx.x; e < E; e += threads) count[e] = 0;
+  if (threadIdx.x < 2 * kXcds) plan->taken[threadIdx.x / kXcds][threadIdx.x % kXcds] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < choices; i += kPlanThreads) {
-    const int e = experts[i];
+  // the choices, 8 a thread on their way at a time
+  auto each = [&](auto f) {
+    for (int i0 = threadIdx.x; i0 < choices; i0 += 8 * threads) {
+      int e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = experts[i0 + j * threads < choices ? i0 + j * threads : i0];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * threads < choices) f(i0 + j * threads, e[j]);
+    }
+  };
+  each([&](int, int e) {
     if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  });
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += threads) {
+    const int n = count[e];
+    int rank = 0;
+    for (int o = 0; o < E; ++o) rank += count[o] > n || (count[o] == n && o < e);
+    by_rank[rank] = e;
   }
   __syncthreads();
-  if (threadIdx.x < 64) {
+  if (threadIdx.x < 64) {  // rows and row tiles before each rank
     const int lane = threadIdx.x;
     int rows = 0, of = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane, n = e < E ? count[e] : 0, m = (n + BM - 1) / BM;
-      int upto = n, tupto = m;
+    for (int r0 = 0; r0 < E; r0 += 64) {
+      const int r = r0 + lane, e = by_rank[r < E ? r : 0], n = r < E ? count[e] : 0, m = (n + BM - 1) / BM;
+      int a = n, b = m;
       for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(upto, off, 64), p = __shfl_up(tupto, off, 64);
-        if (lane >= off) upto += o, tupto += p;
+        const int p = __shfl_up(a, off, 64), q = __shfl_up(b, off, 64);
+        if (lane >= off) a += p, b += q;
       }
-      if (e < E) first[e] = rows + upto - n, tile[e] = of + tupto - m;
-      rows += __shfl(upto, 63, 64);
-      of += __shfl(tupto, 63, 64);
+      if (r < E) {
+        const int row = rows + a - n;
+        first[e] = row;
+        for (int i = 0; i < m; ++i)
+          tiles[of + b - m + i] = Tile{e, row + i * BM, n - i * BM < BM ? n - i * BM : BM, r};
+      }
+      rows += __shfl(a, 63, 64);
+      of += __shfl(b, 63, 64);
     }
     if (lane == 0) plan->tiles = of;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kPlanThreads) {
-    for (int i = 0; i * BM < count[e]; ++i) {
-      const int left = count[e] - i * BM;
-      tiles[tile[e] + i] = Tile{e, first[e] + i * BM, left < BM ? left : BM};
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < choices; i += kPlanThreads) {
-    const int e = experts[i];
+  each([&](int i, int e) {
     int row = -1;
     if (e >= 0 && e < E) {
       row = atomicAdd(&first[e], 1);
       token[row] = i / top_k;
     }
     where[i] = row;
-  }
+  });
 }
 
-// UP: A = X's codes, gathered; W's tile is blocks of 32 gate rows and the 32 up rows of the
-// same columns in turn.  Else A = h's codes.  ntiles: of columns of h (of y).
-template <bool UP, class C>
-__global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_moe_product_kernel(
-    const int8_t* __restrict__ A, const float* __restrict__ sa, const int8_t* __restrict__ W, const float* __restrict__ sw,
-    const Plan* __restrict__ plan, const Tile* __restrict__ tiles, const int* __restrict__ token, int K, int N, int ntiles,
-    float* __restrict__ out) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLdsBytes];
-  const int mt = (int)blockIdx.x / ntiles, n0 = (int)blockIdx.x % ntiles * (UP ? C::BN / 2 : C::BN);
-  if (mt >= plan->tiles) return;
-  const Tile tile = tiles[mt];
-  const int rows = UP ? 2 * N : N;  // of an expert's weights
-  const int8_t* const w = W + (int64_t)tile.expert * rows * K;
-  const float* const s = sw + (int64_t)tile.expert * rows;
-  auto clamped = [&](int r) { return r < tile.count ? r : tile.count - 1; };
-  typename C::Sums acc;
-  const bool mine = C::multiply(
-      acc, lds, UP ? A : A + (int64_t)tile.row * K,
-      [&](int r) { return (uint32_t)(UP ? token[tile.row + clamped(r)] : clamped(r)) * (uint32_t)K; }, w,
-      [&](int r) {
-        const int n = UP ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
-        return ((uint32_t)(n < N ? n : N - 1) + (UP && (r & 32) ? (uint32_t)N : 0u)) * (uint32_t)K;
-      },
-      K);
-  if (!mine) return;
+template <class XT, int STEPS>
+__global__ __launch_bounds__(kRowMaxWaves * 64) void int8_moe_prepare_kernel(
+    const void* __restrict__ X, int64_t T, int H, int W, int rounds, int8_t* __restrict__ codes, float* __restrict__ scales,
+    const int32_t* __restrict__ experts, int top_k, int E, int BM, Plan* __restrict__ plan, Tile* __restrict__ tiles,
+    int* __restrict__ where, int* __restrict__ token) {
+  if (blockIdx.x == 0)
+    int8_moe_plan(experts, (int)T * top_k, top_k, E, BM, plan, tiles, where, token);
+  else
+    int8_quantize_rows<XT, kNone, STEPS>(X, nullptr, T, H, W, rounds, (int64_t)blockIdx.x - 1, codes, scales);
+}
 
-  const int lane = threadIdx.x & 63, half = lane >> 5;
+// The outputs of a tile's sums: h of its gate and up columns, or its products.
+template <bool UP, class C, int TME>
+__device__ __forceinline__ void finish(const typename C::template Sums<TME>& acc, uint8_t* __restrict__ lds, const float* __restrict__ sa,
+                                       const float* __restrict__ s, const int* __restrict__ token, const Tile& tile, int N, int n0,
+                                       float* __restrict__ out) {
+  auto clamped = [&](int r) { return r < tile.count ? r : tile.count - 1; };
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // addresses are worked out for each tile: kept, they spill
+  const int half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kCols = UP ? 16 * C::TN : 32 * C::TN;
   constexpr int kTurn = 32 * (kCols * 4 + 16) + kCols * 8;
-  static_assert(C::kWaves * kTurn <= C::kStages * C::kStage, "the turn fits the stages' place");
+  static_assert(C::kWaves * kTurn <= C::kGroupBytes, "the turn fits the stages' place");
   static_assert(!UP || C::TN % 2 == 0, "a wave has gate and up columns");
-  const int m1 = wave % C::WM * (32 * C::TM), n1 = n0 + wave / C::WM * kCols;
+  const int n1 = n0 + wave / C::WM * kCols;
   uint8_t* const turn = lds + wave * kTurn;
   float* const cols = reinterpret_cast<float*>(turn + 32 * (kCols * 4 + 16));
   for (int c = lane; c < kCols; c += 64) {
@@ -117,8 +139,8 @@ __global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_moe_product_k
   }
   asm volatile("" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
-    const int m = m1 + 32 * i, r = clamped(m + (lane & 31));
+  for (int i = 0; i < TME; ++i) {
+    const int m = 32 * C::row_block(wave, i), r = clamped(m + (lane & 31));
     if (m >= tile.count) break;
     const float f = sa[UP ? token[tile.row + r] : tile.row + r];
     int8_store_rows<F32, kCols>(turn, out + (int64_t)(tile.row + m) * N + n1, N, tile.count - m, N - n1, [&](int b) {
@@ -138,6 +160,50 @@ __global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_moe_product_k
       }
       return v;
     });
+  }
+}
+
+// UP: A = X's codes, gathered; W's tile is blocks of 32 gate rows and the 32 up rows of the
+// same columns in turn.  Else A = h's codes.  ntiles: of columns of h (of y).
+template <bool UP, class C>
+__global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_moe_product_kernel(
+    const int8_t* __restrict__ A, const float* __restrict__ sa, const int8_t* __restrict__ W, const float* __restrict__ sw,
+    Plan* __restrict__ plan, const Tile* __restrict__ tiles, const int* __restrict__ token, int K, int N, int ntiles,
+    float* __restrict__ out) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLdsBytes];
+  __shared__ int next;
+  // item k of XCD x is number x + 8 k of the pairs of a row tile and a column tile; large
+  // tiles' columns are counted as a multiple of 8, which keeps a column tile on its XCD
+  const int x = (int)blockIdx.x % kXcds, own = (int)gridDim.x / kXcds;  // workgroups of an XCD: their first items are dealt
+  const int columns = C::TM > 1 ? (ntiles + kXcds - 1) / kXcds * kXcds : ntiles, items = plan->tiles * columns;
+  for (int item = (int)blockIdx.x; item < items;) {
+    const Tile tile = tiles[item / columns];
+    const int nt = (item % columns + (C::TM > 1 ? tile.rank : 0)) % columns;
+    const int n0 = nt * (UP ? C::BN / 2 : C::BN);
+    const int rows = UP ? 2 * N : N;  // of an expert's weights
+    const int8_t* const w = W + (int64_t)tile.expert * rows * K;
+    const float* const s = sw + (int64_t)tile.expert * rows;
+    auto clamped = [&](int r) { return r < tile.count ? r : tile.count - 1; };
+    int after = 0;
+    if (threadIdx.x == 0) after = atomicAdd(&plan->taken[UP ? 0 : 1][x], 1);  // on its way meanwhile
+    if (nt < ntiles)
+      C::for_blocks(tile.count, [&](auto blocks) {
+        constexpr int kBlocks = decltype(blocks)::value;
+        typename C::template Sums<kBlocks> acc;
+        const bool mine = C::template multiply<kBlocks>(
+            acc, lds, UP ? A : A + (int64_t)tile.row * K,
+            [&](int r) { return (uint32_t)(UP ? token[tile.row + clamped(r)] : clamped(r)) * (uint32_t)K; }, w,
+            [&](int r) {
+              const int n = UP ? n0 + (r >> 6) * 32 + (r & 31) : n0 + r;
+              return ((uint32_t)(n < N ? n : N - 1) + (UP && (r & 32) ? (uint32_t)N : 0u)) * (uint32_t)K;
+            },
+            K);
+        if (mine) finish<UP, C, kBlocks>(acc, lds, sa, s, token, tile, N, n0, out);
+      });
+    __syncthreads();  // `next` and the LDS were read
+    if (threadIdx.x == 0) next = after;
+    __syncthreads();
+    item = x + kXcds * (own + next);
   }
 }
 
@@ -165,11 +231,15 @@ __global__ __launch_bounds__(256) void int8_moe_combine_kernel(const float* __re
 }
 
 typedef Int8Tile<1, 2, 2, 4, 1, 3> Small;
-typedef Int8Tile<2, 2, 2, 4, 1, 2> Middle;
+typedef Int8Tile<2, 2, 2, 4, 1, 4, 1> Middle;
+typedef Int8Tile<4, 2, 4, 4, 1, 2> Large;
 
 // Tiles of rows, at most: one for each expert that is taken and one for each further BM.
 int64_t most_tiles(int64_t choices, int64_t E, int64_t BM) { return (choices < E ? choices : E) + choices / BM; }
-int64_t tile_rows(int64_t T, int64_t E, int64_t top_k) { return T * top_k <= 64 * E ? Small::BM : Middle::BM; }
+int64_t tile_rows(int64_t T, int64_t E, int64_t top_k) {
+  const int64_t rows = T * top_k / E;
+  return rows <= 48 ? Small::BM : (rows <= 96 ? Middle::BM : Large::BM);
+}
 
 struct Layout {
   size_t codes, scales, plan, tiles, where, token, h, h_codes, h_scales, products, bytes;
@@ -214,10 +284,15 @@ hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, co
   float* const products = reinterpret_cast<float*>(ws + l.products);
   float* const h_scales = reinterpret_cast<float*>(ws + l.h_scales);
   float* const x_scales = reinterpret_cast<float*>(ws + l.scales);
-  hipError_t e = launch_int8_quantize(X, xdtype, nullptr, false, T, H, ws + l.codes, x_scales, stream);
-  if (e != hipSuccess) return e;
-  int8_moe_plan_kernel<<<1, kPlanThreads, 0, stream>>>(experts, (int)choices, top_k, (int)E, (int)BM, plan, tiles, where, token);
-  e = hipGetLastError();
+  const Int8RowsPlan p = int8_rows_plan(T, H);
+  auto prepare = [&](auto tag) {
+    using XT = decltype(tag);
+    auto* const f = p.per <= 1 ? int8_moe_prepare_kernel<XT, 1> : (p.per <= 2 ? int8_moe_prepare_kernel<XT, 2> : int8_moe_prepare_kernel<XT, 4>);
+    f<<<p.groups + 1, (unsigned)p.threads(), 0, stream>>>(X, T, (int)H, p.W, p.rounds(), reinterpret_cast<int8_t*>(ws + l.codes), x_scales,
+                                                          experts, top_k, (int)E, (int)BM, plan, tiles, where, token);
+    return hipGetLastError();
+  };
+  hipError_t e = xdtype == 0 ? prepare(F16{}) : prepare(BF16{});
   if (e != hipSuccess) return e;
   const int64_t mt = most_tiles(choices, E, BM);
   auto product = [&](auto is_up, auto tag, const void* a, const float* sa, const void* w, const float* sw, int64_t K, int64_t N,
@@ -225,8 +300,10 @@ hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, co
     using C = decltype(tag);
     constexpr bool kUp = decltype(is_up)::value;
     constexpr int kCols = kUp ? C::BN / 2 : C::BN;
-    const int64_t nt = (N + kCols - 1) / kCols;
-    int8_moe_product_kernel<kUp, C><<<(unsigned)(mt * nt), C::kThreads, 0, stream>>>(
+    const int64_t nt = (N + kCols - 1) / kCols, most = (mt * nt + kXcds - 1) / kXcds * kXcds;
+    // the workgroups that the compute units have room for
+    constexpr int64_t kRoom = 256 * (C::kLdsBytes <= 80 * 1024 ? 2 : 1);
+    int8_moe_product_kernel<kUp, C><<<(unsigned)(most < kRoom ? most : kRoom), C::kThreads, 0, stream>>>(
         static_cast<const int8_t*>(a), sa, static_cast<const int8_t*>(w), sw, plan, tiles, token, (int)K, (int)N, (int)nt, out);
     return hipGetLastError();
   };
@@ -237,7 +314,7 @@ hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, co
     if (e != hipSuccess) return e;
     return product(std::false_type{}, tag, ws + l.h_codes, h_scales, down, down_scales, I, H, products);
   };
-  e = BM == Small::BM ? products_of(Small{}) : products_of(Middle{});
+  e = BM == Small::BM ? products_of(Small{}) : (BM == Middle::BM ? products_of(Middle{}) : products_of(Large{}));
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((H + 1023) / 1024), (unsigned)(T < 65535 ? T : 65535));
   auto* const f = xdtype == 0 ? int8_moe_combine_kernel<F16> : int8_moe_combine_kernel<BF16>;

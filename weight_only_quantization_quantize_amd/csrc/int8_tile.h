@@ -5,7 +5,7 @@
 // v_mfma_i32_32x32x32_i8; KG groups of a workgroup share the tile's K and add their sums
 // through LDS at the end.
 //
-// Pipeline.  K goes in stages of 32 KS, kStages of them in LDS, filled by direct loads
+// Pipeline.  K goes in stages of 32 KS, two or more of them in LDS, filled by direct loads
 // (global_load_lds: no registers, no instructions to write LDS).  At the top of a turn a
 // wave waits until its own loads of this stage are done, meets the others at the barrier,
 // which also says that everybody is through with the previous stage, starts the loads of
@@ -51,35 +51,57 @@ __device__ inline void int8_wait_loads() {
 // OCC: waves a SIMD that the registers are shared among.
 template <int TM_, int TN_, int WN_, int KS_, int KG_, int NS_, int OCC_ = 2, int WM_ = 2>
 struct Int8Tile {
-  static constexpr int TM = TM_, TN = TN_, WN = WN_, KS = KS_, KG = KG_, kStages = NS_, kOccupancy = OCC_, WM = WM_;
+  static constexpr int TM = TM_, TN = TN_, WN = WN_, KS = KS_, KG = KG_, kOccupancy = OCC_, WM = WM_;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves * KG;
   static constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   static constexpr int kRow = 32 * KS;      // bytes of a row's stage
   static constexpr int kChunks = 2 * KS;    // of 16 bytes
   static constexpr int kUnitRows = 1024 / kRow;
-  static constexpr int kAUnits = BM / kUnitRows, kWUnits = BN / kUnitRows;
-  static constexpr int kStage = (BM + BN) * kRow;
-  static constexpr int kALoads = (kAUnits + kWaves - 1) / kWaves, kWLoads = (kWUnits + kWaves - 1) / kWaves;
-  static constexpr int kLoads = kALoads + kWLoads;
-  static constexpr int kLdsBytes = KG * kStages * kStage;
-  static_assert(kLdsBytes <= 160 * 1024 && KS % 2 == 0);
+  static constexpr int kWUnits = BN / kUnitRows;
+  // LDS: NS stages of whole tiles, or all of it where a second workgroup has no place anyway.
+  // A tile of few rows has shorter stages, and more of them: it has less to hide its loads
+  // behind (a layer of 2048 tokens, where two tiles of three are short ones: @@).
+  __host__ __device__ static constexpr int stage_bytes(int blocks) { return (32 * WM * blocks + BN) * kRow; }
+  static constexpr int kWhole = KG * NS_ * stage_bytes(TM);
+  static constexpr int kMost = 159 * 1024;  // of the 160 KB; the rest is the caller's
+  static constexpr int kLdsBytes = kWhole > 80 * 1024 && kWhole < kMost ? kMost : kWhole;
+  static constexpr int kGroupBytes = kLdsBytes / KG / 1024 * 1024;
+  __host__ __device__ static constexpr int stages(int blocks) {
+    const int n = blocks == TM ? NS_ : kGroupBytes / stage_bytes(blocks);
+    return n > 8 ? 8 : n;
+  }
+  static constexpr int kWLoads = (kWUnits + kWaves - 1) / kWaves;
+  static_assert(kWhole <= 160 * 1024 && KS % 2 == 0);
 
-  typedef int16v_t Sums[TM][TN];
+  template <int TME>
+  using Sums = int16v_t[TME][TN];
 
   __device__ static int swizzle(int row) { return KS == 4 ? (row >> 1) & 7 : (row >> 2) & 3; }
 
-  // acc[i][j] of the first group's waves: the lane's sums of row m = 32 (wm + i) + lane % 32
-  // of A and, element e, row n = 32 (wn + j) + 8 (e / 4) + 4 (lane / 32) + e % 4 of W, with
-  // wm = TM (wave % WM), wn = TN (wave / WM); false for the other groups' waves.
+  // The tile's row blocks of 32 go around its WM rows of waves: wave row wm holds the blocks
+  // wm, WM + wm, ...  A tile of few rows has blocks at the end that nobody needs, and the
+  // work is the same for all waves still.
+  __device__ static int row_block(int wave, int i) { return i * WM + wave % WM; }
+  // Wave rows of blocks that `rows` rows need, 1 .. TM.
+  __device__ static int blocks(int rows) { return rows >= BM ? TM : (rows + 32 * WM - 1) / (32 * WM); }
+
+  // acc[i][j] of the first group's waves: the lane's sums of row 32 row_block(wave, i) +
+  // lane % 32 of A and, element e, row 32 (wave / WM TN + j) + 8 (e / 4) + 4 (lane / 32) +
+  // e % 4 of W, for the tile's first TME wave rows of blocks; false for the other groups'
+  // waves.
   // a_row(r), w_row(r): byte offsets (below 2^32) of the tile's rows from a and w, for
   // every r of the tile.  All threads call; LDS may be used again behind the next barrier.
-  template <class AR, class WR>
-  __device__ static bool multiply(Sums& acc, uint8_t* __restrict__ lds_all, const int8_t* __restrict__ a, AR&& a_row,
-                                  const int8_t* __restrict__ w, WR&& w_row, int K) {
-    const int lane = threadIdx.x & 63;
+  template <int TME, class AR, class WR>
+  __device__ __forceinline__ static bool multiply(Sums<TME>& acc, uint8_t* __restrict__ lds_all, const int8_t* __restrict__ a,
+                                                  AR&& a_row, const int8_t* __restrict__ w, WR&& w_row, int K) {
+    constexpr int kAUnits = 32 * WM * TME / kUnitRows, kALoads = (kAUnits + kWaves - 1) / kWaves, kLoads = kALoads + kWLoads;
+    constexpr int kStage = stage_bytes(TME), kStages = stages(TME), kAt = 32 * WM * TME * kRow;
+    static_assert(kStages >= 2 && kStages * kStage <= kGroupBytes);
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // addresses are worked out for each tile: kept, they spill
     const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = wave_all % kWaves, group = wave_all / kWaves;
-    const int wm = wave % WM * TM, wn = wave / WM * TN;
+    const int wm = wave % WM, wn = wave / WM * TN;
     const int half = lane >> 5, r32 = lane & 31;
     const int chunks = K >> 4;
     const int stages = (chunks + kChunks - 1) / kChunks;
@@ -87,7 +109,7 @@ struct Int8Tile {
     // group's begin (h < 0), so that a short last stage is everybody's last turn
     const int turns = (stages + KG - 1) / KG;
     const int h0 = stages - (KG - group) * turns;
-    uint8_t* const lds = lds_all + group * (kStages * kStage);
+    uint8_t* const lds = lds_all + group * kGroupBytes;
     const uint32_t lds0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)int8_lds_address(lds));
 
     // Every wave starts the same number of loads a stage: past an operand's units the last
@@ -122,20 +144,15 @@ struct Int8Tile {
 #pragma unroll
       for (int j = 0; j < kWLoads; ++j) {
         const int u = unit(j, kWUnits);
-        int8_load_lds(w, w_off[j] + (uint32_t)(KS == 4 && (u & 1) ? at[1] : at[0]), to + (uint32_t)(BM * kRow) + 1024u * (uint32_t)u);
+        int8_load_lds(w, w_off[j] + (uint32_t)(KS == 4 && (u & 1) ? at[1] : at[0]), to + (uint32_t)kAt + 1024u * (uint32_t)u);
       }
     };
 
-    // where the lane's operands lie in a stage
-    uint32_t a_at[KS], w_at[KS];
+    // where the lane's operands of step 0 lie in a stage; step s: bits 5 and 6 flipped by s
+    const uint32_t a_at = (uint32_t)((wm * 32 + r32) * kRow + (half ^ swizzle(r32)) * 16);
+    const uint32_t w_at = (uint32_t)(kAt + (wn * 32 + r32) * kRow + (half ^ swizzle(r32)) * 16);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      a_at[s] = (uint32_t)((wm * 32 + r32) * kRow + ((2 * s + half) ^ swizzle(r32)) * 16);
-      w_at[s] = (uint32_t)((BM + wn * 32 + r32) * kRow + ((2 * s + half) ^ swizzle(r32)) * 16);
-      asm volatile("" : "+v"(w_at[s]), "+v"(a_at[s]));
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TME; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -144,15 +161,14 @@ struct Int8Tile {
     // A unit is row block i of step s: TN matrix instructions.  Operands are read from LDS a
     // unit ahead; the last kTail units of a stage run behind the barrier that ends it, with
     // their operands in registers, and cover the next stage's first reads.
-    constexpr int kUnits = KS * TM, kTail = TM < 3 ? 1 : TM - 1, kSlots = kTail + 1;
+    constexpr int kUnits = KS * TME, kTail = TME < 3 ? 1 : TME - 1, kSlots = kTail + 1;
     static_assert(kUnits % kSlots == 0, "a stage's first unit follows the last one's place");
     int4v_t v[kSlots], wc[2][TN];
-    auto read_a = [&](const uint8_t* la, int u) {
-      v[u % kSlots] = *reinterpret_cast<const int4v_t*>(la + a_at[u / TM] + u % TM * 32 * kRow);
-    };
-    auto read_w = [&](const uint8_t* la, int s) {
+    auto read = [&](uint32_t at) { return *reinterpret_cast<const __attribute__((address_space(3))) int4v_t*>(at); };
+    auto read_a = [&](uint32_t la, int u) { v[u % kSlots] = read(((la + a_at) ^ (uint32_t)(32 * (u / TME))) + u % TME * WM * 32 * kRow); };
+    auto read_w = [&](uint32_t la, int s) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) wc[s & 1][j] = *reinterpret_cast<const int4v_t*>(la + w_at[s] + j * 32 * kRow);
+      for (int j = 0; j < TN; ++j) wc[s & 1][j] = read(((la + w_at) ^ (uint32_t)(32 * s)) + j * 32 * kRow);
     };
     // Until stage h's own loads are done, everybody's, and everybody has read the stage
     // before, whose place takes the stage kStages - 1 ahead.
@@ -164,21 +180,21 @@ struct Int8Tile {
     };
     for (int st = 0; st + 1 < kStages; ++st) issue(h0 + st, st);
     enter(h0);
-    read_w(lds, 0);
-    read_a(lds, 0);
+    read_w(lds0, 0);
+    read_a(lds0, 0);
     auto turn = [&](int h, auto masked) {
-      const uint8_t* la = lds + buf * kStage;
+      uint32_t la = lds0 + (uint32_t)(buf * kStage);
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int s = u / TM, i = u % TM;
+        const int s = u / TME, i = u % TME;
         if (u == kUnits - kTail) {
           buf = buf + 1 == kStages ? 0 : buf + 1;
-          la = lds + buf * kStage;
+          la = lds0 + (uint32_t)(buf * kStage);
           enter(h + 1);
           read_w(la, 0);
           read_a(la, 0);
         }
-        if (i == (TM > 1 ? TM - 2 : 0) && s + 1 < KS) read_w(la, s + 1);
+        if (i == (TME > 1 ? TME - 2 : 0) && s + 1 < KS) read_w(la, s + 1);
         if (u < kUnits - kTail - 1) read_a(la, u + 1);
         if (u == kUnits - kTail - 1)
 #pragma unroll
@@ -197,7 +213,7 @@ struct Int8Tile {
       }
       if (KG > 1 && h < 0)  // what a stage that is not there gave
 #pragma unroll
-        for (int i = 0; i < TM * TN; ++i) acc[i / TN][i % TN] = int16v_t{};
+        for (int i = 0; i < TME * TN; ++i) acc[i / TN][i % TN] = int16v_t{};
     };
     const bool rest = stages * kChunks > chunks;
     const int end = h0 + turns - (rest ? 1 : 0);
@@ -208,21 +224,34 @@ struct Int8Tile {
 
     if constexpr (KG > 1) {
       // the groups' sums meet in LDS, [wave][tile][lane]
-      static_assert(TM * TN * kWaves * 4096 <= kStages * kStage, "a group's sums fit its stages' place");
-      int16v_t* const mine = reinterpret_cast<int16v_t*>(lds) + wave * TM * TN * 64 + lane;
+      static_assert(TME * TN * kWaves * 4096 <= kGroupBytes, "a group's sums fit its stages' place");
+      int16v_t* const mine = reinterpret_cast<int16v_t*>(lds) + wave * TME * TN * 64 + lane;
       if (group)
 #pragma unroll
-        for (int i = 0; i < TM * TN; ++i) mine[i * 64] = acc[i / TN][i % TN];
+        for (int i = 0; i < TME * TN; ++i) mine[i * 64] = acc[i / TN][i % TN];
       __syncthreads();
       if (group) return false;
 #pragma unroll
       for (int g = 1; g < KG; ++g) {
-        const int16v_t* const other = reinterpret_cast<const int16v_t*>(lds_all + g * kStages * kStage) + wave * TM * TN * 64 + lane;
+        const int16v_t* const other = reinterpret_cast<const int16v_t*>(lds_all + g * kGroupBytes) + wave * TME * TN * 64 + lane;
 #pragma unroll
-        for (int i = 0; i < TM * TN; ++i) acc[i / TN][i % TN] += other[i * 64];
+        for (int i = 0; i < TME * TN; ++i) acc[i / TN][i % TN] += other[i * 64];
       }
     }
     return true;
+  }
+
+  // f(integral_constant blocks(rows)), code of its own for each.
+  template <class F>
+  __device__ __forceinline__ static void for_blocks(int rows, F&& f) {
+    const int n = blocks(rows);
+    if constexpr (TM > 3)
+      if (n == 3) return f(std::integral_constant<int, 3>{});
+    if constexpr (TM > 2)
+      if (n == 2) return f(std::integral_constant<int, 2>{});
+    if constexpr (TM > 1)
+      if (n == 1) return f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, TM>{});
   }
 };
 
@@ -235,7 +264,9 @@ __device__ inline void int8_store_rows(uint8_t* __restrict__ turn, typename Int8
                                        int rows, int cols, F&& value) {
   typedef typename Int8Out<YT>::type T;
   constexpr int kSize = (int)sizeof(T), kPitch = COLS * kSize + 16, kLaneCols = 16 / kSize, kRuns = COLS / kLaneCols;
-  const int lane = threadIdx.x & 63, half = lane >> 5, r32 = lane & 31;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // as above
+  const int half = lane >> 5, r32 = lane & 31;
 #pragma unroll
   for (int b = 0; b < COLS / 8; ++b) {
     const float4_t v = value(b);

@@ -291,6 +291,30 @@ def test_route_masks_ties_and_spoilt_logits(scoring, E, groups):
                         group_top=1 if groups == 1 else 2, renormalize=renormalize)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(64, 6, 1, 1), (256, 8, 8, 4), (160, 5, 4, 2), (512, 12, 16, 3), (48, 13, 1, 1), (32, 14, 1, 1)])
+def test_route_of_near_keys(scoring, E, k, groups, top_groups):
+    """Keys that 32 bits cannot put in order: s + b nearly the same for many experts of a token,
+    further apart than the 64 bits of either side are off (2^-50)."""
+    for seed in range(12):
+        g = rng(18, seed, E)
+        x = g.normal(size=(1, E)).astype(np.float32)
+        s = O.scores(x, scoring)[0]
+        few = g.random(E) < (0.1, 0.5, 1.0)[seed % 3]
+        apart = 2.0 ** -g.integers(16, 24, E) * g.normal(size=E)
+        bias = np.where(few, 1.0 - s + apart, 0.1 * g.normal(size=E)).astype(np.float32)
+        keys = np.sort(s + bias.astype(np.float64))
+        assert np.diff(keys).min() > 2.0 ** -50 or np.diff(keys).min() == 0
+        rows = np.repeat(x, 5, 0)
+        rows[1:4] += 0.01 * g.normal(size=(3, E)).astype(np.float32)  # other tokens of the same wave
+        check_route(tensor(rows), k, f"{scoring} {E}", bias, scoring=scoring, groups=groups, top_groups=top_groups,
+                    group_top=1 + seed % 2 if groups > 1 else 1)
+        # logits themselves that differ in their last bits, and equal ones
+        y = (1.0 + g.integers(0, 40, (5, E)) * 2.0 ** -23).astype(np.float32)
+        check_route(tensor(y), k, f"logits {E}", None, scoring=scoring, groups=groups, top_groups=top_groups,
+                    group_top=1 + seed % 2 if groups > 1 and scoring == "sigmoid" else 1)
+
+
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 60, 6), (33, 8, 2), (10, 65, 9), (5, 256, 8), (3, 512, 64), (70, 128, 6)])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [True, False])

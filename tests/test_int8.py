@@ -260,6 +260,7 @@ FILES = {
     "int8_gemv.hip": ["int8_gemv_kernel"],
     "int8_gemm.hip": ["int8_gemm_kernel"],
     "moe_route.hip": ["moe_route_kernel", "moe_route_wide_kernel", "moe_route_backward_kernel"],
+    "int8_moe_row.hip": ["int8_moe_row_up_kernel", "int8_moe_row_down_kernel"],
     "int8_moe.hip": ["int8_moe_prepare_kernel", "int8_moe_product_kernel", "int8_moe_combine_kernel"],
 }
 

@@ -122,6 +122,12 @@ def check(status: int, what: str) -> None:
         raise WoqError(status, f"{what} failed: {name}: {detail}")
 
 
+_entries: dict = {}
+
+
 def call(name: str, *args) -> int:
     """Call an entry point by name and return its raw result."""
-    return getattr(load(), name)(*args)
+    entry = _entries.get(name)
+    if entry is None:
+        entry = _entries[name] = getattr(load(), name)
+    return entry(*args)

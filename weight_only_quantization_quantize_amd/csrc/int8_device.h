@@ -94,6 +94,9 @@ __device__ inline uint32_t int8_pack(float a, float b, float c, float d) {
          (uint32_t)(int)d << 24;
 }
 
+// silu(g) u
+__device__ inline float int8_gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
 __device__ inline uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
 __device__ inline uint32_t wave_max_bits(uint32_t v) {
 #pragma unroll

@@ -9,7 +9,7 @@
 // `segs` waves, the slots of a workgroup being 8 / segs rows).  Workgroup b takes the row
 // groups b, b + B, ..., so the whole GPU reads one window of rows at a time, kSteps of them
 // a batch, the next batch on its way while one is multiplied (v_dot4) and summed.
-#include "int8_device.h"
+#include "int8_row.h"
 #include "woq_internal.h"
 
 namespace woq {
@@ -20,20 +20,6 @@ constexpr int kMaxChunks = 4;   // a lane's
 constexpr int kTargetGroups = 512;
 
 struct Codes {};  // of the row: given
-
-// The sum over a wave, in lane 63.
-__device__ inline int wave_sum_last(int v) {
-  auto step = [&](auto ctrl, auto rows) {
-    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-  };
-  step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});  // row_shr 1, 2, 4, 8
-  step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
-  step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
-  step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
-  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row_bcast 15, 31
-  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
-  return v;
-}
 
 template <class XT, class YT, int CH>
 __global__ __launch_bounds__(kWaves * 64) void int8_gemv_kernel(const void* __restrict__ x, const float* __restrict__ sa,
@@ -82,46 +68,15 @@ __global__ __launch_bounds__(kWaves * 64) void int8_gemv_kernel(const void* __re
 #pragma unroll
       for (int e = 0; e < 4; ++e) q[j][e] = chunk[j] < chunks ? v[j][e] : 0u;
   } else {
-    u32x4_t v[CH][2];
-    float4_t s[CH][4];
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const u32x4_t* const p = reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(x) + at[j]);
-      v[j][0] = p[0], v[j][1] = p[1];
-      if (act_scale)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = *reinterpret_cast<const float4_t*>(act_scale + at[j] + 4 * e);
-    }
+    Int8RowLoad<CH> in;
+    in.start(x, act_scale, at);
     __builtin_amdgcn_sched_barrier(0);
     load(c[0], row);
     __builtin_amdgcn_sched_barrier(0);
-    float f[CH][16];
-    uint32_t top = 0;
+    bool live[CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        f[j][e] = XT::to_f32((uint16_t)(v[j][e / 8][e % 8 / 2] >> (16 * (e % 2))));
-        if (act_scale) f[j][e] /= s[j][e / 4][e % 4];
-        const uint32_t b = magnitude(f[j][e]);
-        top = top > b ? top : b;
-      }
-    top = wave_max_bits(top);
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    for (int i = 0; i < waves; ++i) {
-      const uint32_t o = tops[i];
-      top = top > o ? top : o;
-    }
-    const Int8Row p = int8_row(top);
-    scale = p.scale;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      int8_codes(f[j], p);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q[j][e] = chunk[j] < chunks ? int8_pack(f[j][4 * e], f[j][4 * e + 1], f[j][4 * e + 2], f[j][4 * e + 3]) : 0u;
-    }
+    for (int j = 0; j < CH; ++j) live[j] = chunk[j] < chunks;
+    scale = in.template codes<XT>(q, act_scale != nullptr, live, tops);
   }
   auto store = [&](int n, int sum) {
     float v = (float)sum * scale * sw[n];
@@ -135,9 +90,7 @@ __global__ __launch_bounds__(kWaves * 64) void int8_gemv_kernel(const void* __re
     for (int st = 0; st < kSteps; ++st) {
       int d = 0;
 #pragma unroll
-      for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d = __builtin_amdgcn_sdot4((int)from[st][j][e], (int)q[j][e], d, false);
+      for (int j = 0; j < CH; ++j) d = int8_dot16(from[st][j], q[j], d);
       sum[st] = d;
     }
     if (segs == 1) {  // a row inside a wave

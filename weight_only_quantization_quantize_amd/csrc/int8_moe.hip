@@ -11,6 +11,8 @@
 // products (int8_tile.h) over those tiles; h's rows are quantized between them; `combine`
 // adds up.  The rows' order in the plan changes no result: every row is computed by itself.
 //
+// One token has two launches of its own (int8_moe_row.hip).
+//
 // Work of the products.  Experts' row counts differ, and a tile of few rows is cheap
 // (int8_tile.h: it multiplies its own blocks of rows only), so tiles are taken, not dealt: a
 // workgroup a compute unit's place takes tile after tile, those of the experts with the most
@@ -152,7 +154,7 @@ __device__ __forceinline__ void finish(const typename C::template Sums<TME>& acc
         for (int e = 0; e < 4; ++e) {
           const float g = (float)acc[i][b / 4 * 2][4 * (b % 4) + e] * f * c[e];
           const float u = (float)acc[i][b / 4 * 2 + 1][4 * (b % 4) + e] * f * d[e];
-          v[e] = g / (1.0f + expf(-g)) * u;
+          v[e] = int8_gated(g, u);
         }
       } else {
 #pragma unroll
@@ -222,7 +224,7 @@ __global__ __launch_bounds__(256) void int8_moe_combine_kernel(const float* __re
       const float w = weights[(int64_t)t * top_k + c];
       const float4_t p = *reinterpret_cast<const float4_t*>(products + (int64_t)row * H + n);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += w * p[e];
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(w, p[e], v[e]);
     }
     const uint32_t lo = (uint32_t)YT::from_f32(v[0]) | (uint32_t)YT::from_f32(v[1]) << 16;
     const uint32_t hi = (uint32_t)YT::from_f32(v[2]) | (uint32_t)YT::from_f32(v[3]) << 16;
@@ -267,12 +269,15 @@ Layout layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
 int int8_moe_max_experts() { return kMaxExperts; }
 
 size_t int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
+  if (T == 1 && int8_moe_row_supported(H, I, top_k)) return (size_t)(top_k * I) * 4;
   return layout(T, H, I, E, top_k).bytes;
 }
 
 hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, const float* weights, const void* up,
                            const float* up_scales, const void* down, const float* down_scales, int64_t T, int64_t H, int64_t I,
                            int64_t E, int top_k, void* Y, void* workspace, hipStream_t stream) {
+  if (T == 1 && int8_moe_row_supported(H, I, top_k))
+    return launch_int8_moe_row(X, xdtype, experts, weights, up, up_scales, down, down_scales, H, I, E, top_k, Y, workspace, stream);
   const Layout l = layout(T, H, I, E, top_k);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   const int64_t choices = T * top_k, BM = tile_rows(T, E, top_k);

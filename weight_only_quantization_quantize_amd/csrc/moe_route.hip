@@ -7,16 +7,21 @@
 //   w = scale s, over the sum of the chosen experts' s where that is asked for
 //
 // Bound by vector instructions: a logit is 2 or 4 bytes, its score and its part in the
-// choice some fifty instructions a token's 256 experts.  So the usual routing (route_row) has
-// four tokens a wave, 16 lanes each, NJ neighbouring experts a lane, and works in 32 bits:
-//   scores p = 1 / (1 + 2^(-x log2 e)) and 2^((x - max) log2 e) / sum are off by at most 2^-20,
-//   s + b by 2^-24 of itself more.  Two keys further apart than kClose (1 + |key|) = 2^-18
-//   (1 + |key|) are in their right order, and so are two groups' sums further apart than
-//   twice that.  Where a chosen key (or the best one left out), or the last group kept and
-//   the best one dropped, are nearer than that (equal ones, infinities and NaN among them), the
-//   token goes the exact way (route_token): a wave a token, keys in 64 bits.
-// Without a bias the logits themselves are the keys, and exact.  More than 16 choices, or
-// groups that are not whole lanes of experts, take the exact way at once.
+// choice some dozens of instructions.  So the usual routing (route_row) has four tokens a
+// wave, 16 lanes each, neighbouring experts in a lane, and decides in 32 bits what they decide:
+//   scores p = 1 / (1 + 2^(-x log2 e)) are off by at most 2^-21, 2^((x - max) log2 e) / sum
+//   by 2^-19, s + b by 2^-24 of itself more;
+//   a key is cut to make room for its expert's index in its low bits (8, or 9 from 257
+//   experts on), so that keys are distinct, lanes sort theirs by a network of min and max,
+//   and a round of choice is a maximum over 16 lanes;
+//   where two neighbours among the chosen and the best one left out are too near to be told
+//   apart, the exact keys (64 bits; the logits where there is no bias) of the chosen and the
+//   two next put them in order, one a lane; no others can be meant as long as the third is
+//   further away.  Groups too near to be told apart have their sums worked out in 64 bits.
+// What is left (three near neighbours more, NaN, infinities) goes the exact way (route_token),
+// a wave a token, as do more than 13 choices and groups that are not whole lanes of experts.
+#include <utility>
+
 #include "int8_device.h"
 #include "woq_internal.h"
 
@@ -191,16 +196,16 @@ __device__ __noinline__ void route_token(const void* __restrict__ logits, int64_
 
 constexpr int kRow = 16;            // lanes of a token
 constexpr int kRowTokens = 4;       // tokens of a wave
-constexpr float kClose = 0x1p-18f;
+constexpr int kMore = 3;            // candidates beside the chosen
 
 // A number's order as an unsigned one; the zeros are equal, a NaN comes below -infinity.
 __device__ inline uint32_t order_key32(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 1u;
-  return (b >> 31) ? ~b : (b | 0x80000000u);
+  const uint32_t k = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+  return v != v ? 0x10000u : k;
 }
-__device__ inline float key_value(uint32_t k) {
-  return __builtin_bit_cast(float, k <= 1u ? 0x7FC00000u : ((k >> 31) ? k & 0x7FFFFFFFu : ~k));
+__device__ inline float key_value(uint32_t k) {  // of a NaN's, and of a cut -infinity's, a NaN
+  return __builtin_bit_cast(float, (k >> 31) ? k & 0x7FFFFFFFu : ~k);
 }
 // f over the 16 lanes of a row, in all of them.
 template <class T, class F>
@@ -216,35 +221,86 @@ __device__ inline T row_all(T v, F&& f) {
   step(std::integral_constant<int, 1>{});
   return v;
 }
+// Keys of n elements in descending order, by Batcher's odd-even merge network.
+template <int N>
+struct Network {
+  int count = 0;
+  uint8_t a[N * 8] = {}, b[N * 8] = {};
+  constexpr Network() {
+    for (int p = 1; p < N; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int j = k % p; j + k < N; j += 2 * k)
+          for (int i = 0; i < k && i + j + k < N; ++i)
+            if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) a[count] = (uint8_t)(i + j), b[count++] = (uint8_t)(i + j + k);
+  }
+};
+template <int N, int... I>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N], std::integer_sequence<int, I...>) {
+  constexpr Network<N> net;
+  auto exchange = [&](int i, int j) {
+    const uint32_t x = v[i], y = v[j];
+    v[i] = x > y ? x : y;
+    v[j] = x > y ? y : x;
+  };
+  (exchange(net.a[I], net.b[I]), ...);
+}
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+  sort_descending(v, std::make_integer_sequence<int, Network<N>().count>{});
+}
+
 template <class T>
 __device__ inline T row_rotated(T v, int n) {  // of the lane n further on
   return __shfl(v, ((int)threadIdx.x & 48) | (((int)threadIdx.x + n) & 15), 64);
 }
 
+// A lane's `own` elements from at on, of any alignment; -infinity behind them.
+template <class XT, int NJ>
+__device__ __forceinline__ void load_lane(float (&x)[NJ], const void* __restrict__ from, int64_t at, int own) {
+  typedef typename Int8Out<XT>::type T;
+  constexpr int kVector = kElementBytes<XT> == 4 || NJ < 8 ? 4 : 8;
+#pragma unroll
+  for (int j0 = 0; j0 < NJ; j0 += kVector) {
+    if (j0 + kVector <= own) {
+      T v[kVector];
+      __builtin_memcpy(v, static_cast<const T*>(from) + at + j0, sizeof(v));
+#pragma unroll
+      for (int j = 0; j < kVector; ++j) x[j0 + j] = load_logit<XT>(v, j);
+    } else if (j0 < own) {
+#pragma unroll
+      for (int j = j0; j < j0 + kVector; ++j) x[j] = load_logit<XT>(from, at + (j < own ? j : own - 1));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) x[j] = j < own ? x[j] : -__builtin_inff();
+}
+
+// A logit's score in 64 bits (max, sum: a softmax's).
+__device__ inline double score64(float x, bool sigmoid, float max, double sum) {
+  return sigmoid ? sigmoid64(x) : exp((double)x - (double)max) / sum;
+}
+template <int NJ>
+__device__ inline double softmax_sum(const float (&x)[NJ], float max) {
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) sum += exp((double)x[j] - (double)max);
+  return wave_sum<kRow>(sum);
+}
+
 // Four tokens by a wave, lane l of a row of 16 the n = ceil(E / 16) experts from l n on, n <=
-// NJ.  Returns whether the row's choice is exact; then it is written.
+// NJ.  Returns whether the row's choice is decided; then it is written.
 template <class XT, int NJ>
 __device__ __forceinline__ bool route_row(const void* __restrict__ logits, int64_t t, const Routing& r,
                                           const float* __restrict__ bias, int32_t* __restrict__ experts,
                                           float* __restrict__ weights) {
+  constexpr uint32_t kIndex = NJ > 16 ? 511u : 255u;
+  const float kClose = r.sigmoid ? 0x1p-20f : 0x1p-18f;  // of two scores, and of 1 + |key|
   constexpr float kLog2e = 1.44269504088896341f;
   const int E = r.E, top_k = r.top_k, l = threadIdx.x & (kRow - 1), n = (E + kRow - 1) / kRow, e0 = l * n;
   const int own = E - e0 < n ? E - e0 : n;  // of the lane; the rest counts as masked
   const float inf = __builtin_inff();
   float x[NJ], max = -inf;
-  constexpr int kVector = kElementBytes<XT> == 4 || NJ < 8 ? 4 : 8;  // elements a load, of any alignment
-#pragma unroll
-  for (int j0 = 0; j0 < NJ; j0 += kVector) {
-    if (j0 + kVector <= own) {
-      typename Int8Out<XT>::type v[kVector];
-      __builtin_memcpy(v, static_cast<const typename Int8Out<XT>::type*>(logits) + t * E + e0 + j0, sizeof(v));
-#pragma unroll
-      for (int j = 0; j < kVector; ++j) x[j0 + j] = load_logit<XT>(v, j);
-    } else {
-#pragma unroll
-      for (int j = j0; j < j0 + kVector; ++j) x[j] = j < own ? load_logit<XT>(logits, t * E + e0 + j) : -inf;
-    }
-  }
+  load_lane<XT, NJ>(x, logits, t * E + e0, own);
   auto larger = [](float a, float b) { return fmaxf(a, b); };
   const bool all = !r.sigmoid && !r.renormalize;
   const bool scored = bias || (r.groups > 1 && r.group_top > 1);
@@ -255,43 +311,54 @@ __device__ __forceinline__ bool route_row(const void* __restrict__ logits, int64
     max = row_all(max, larger);
     max = is_masked(max) ? 0.0f : max;
   }
-  if (all) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) sum += exp((double)x[j] - (double)max);
-    sum = wave_sum<kRow>(sum);
-  }
+  if (all) sum = softmax_sum(x, max);
   float by[NJ];  // what groups are compared by
   uint32_t key[NJ];
+  // (each uniform question is asked once, not for every expert: a branch and a wait each took
+  // 16384 tokens of 256 experts 46 us)
   if (scored) {
-    float part = 0.0f;
+    if (r.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      by[j] = __builtin_amdgcn_exp2f((r.sigmoid ? -x[j] : x[j] - max) * kLog2e);
-      part += by[j];
-    }
-    float inverse = 0.0f;
-    if (!r.sigmoid) inverse = __builtin_amdgcn_rcpf(row_all(part, [](float a, float b) { return a + b; }));
+      for (int j = 0; j < NJ; ++j) by[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x[j] * kLog2e));
+    } else {
+      float part = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      by[j] = r.sigmoid ? __builtin_amdgcn_rcpf(1.0f + by[j]) : by[j] * inverse;
-      if (bias) by[j] += bias[j < own ? e0 + j : 0];
-      by[j] = is_masked(x[j]) ? x[j] : by[j];
-      key[j] = j < own ? order_key32(bias ? by[j] : x[j]) : 0u;
+      for (int j = 0; j < NJ; ++j) {
+        by[j] = __builtin_amdgcn_exp2f((x[j] - max) * kLog2e);
+        part += by[j];
+      }
+      const float inverse = __builtin_amdgcn_rcpf(row_all(part, [](float a, float b) { return a + b; }));
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) by[j] *= inverse;
     }
+    if (bias) {
+      float b[NJ];
+      load_lane<F32, NJ>(b, bias, e0, own);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) by[j] += b[j];
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) by[j] = is_masked(x[j]) ? x[j] : by[j];
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      by[j] = x[j];
-      key[j] = j < own ? order_key32(x[j]) : 0u;
-    }
+    for (int j = 0; j < NJ; ++j) by[j] = x[j];
   }
+  if (bias) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = order_key32(by[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = order_key32(x[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) key[j] = j < own ? key[j] : 0u;
   bool sure = true;
   if (r.groups > 1) {  // a group is kRow / groups lanes
     float best = -inf, next = -inf;
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      odd |= by[j] != by[j];
+      odd |= j < own && !(fabsf(by[j]) < inf) && !is_masked(x[j]);
       next = fmaxf(next, fminf(best, by[j]));
       best = fmaxf(best, by[j]);
     }
@@ -305,41 +372,92 @@ __device__ __forceinline__ bool route_row(const void* __restrict__ logits, int64
     int before = 0;
 #pragma unroll
     for (int n = 1; n < kRow; ++n) before += row_rotated(rank, n) > rank ? 1 : 0;
-    const bool kept = before < r.top_groups * lanes;
+    bool kept = before < r.top_groups * lanes;
+    const float last = -row_all(kept ? -rank : -inf, larger), first = row_all(kept ? -inf : rank, larger);
+    // (a best logit is exact, but equal ones are not told apart here)
+    const float close = scored ? 2.0f * kClose * (1.0f + fabsf(last)) : 0.0f;
+    const int keeps = row_all(kept ? 1 : 0, [](int a, int b) { return a + b; });
+    const bool told = r.top_groups == r.groups || (last - first > close && keeps == r.top_groups * lanes);
+    if (__any(!told)) {  // the groups' sums in 64 bits
+      const double total = scored && !r.sigmoid ? softmax_sum(x, max) : 1.0;
+      double best = -inf, next = -inf;
+#pragma unroll 1
+      for (int j = 0; j < own; ++j) {
+        const float y = load_logit<XT>(logits, t * E + e0 + j);
+        double v = y;
+        if (scored && !is_masked(y)) v = score64(y, r.sigmoid, max, total) + (bias ? (double)bias[e0 + j] : 0.0);
+        next = fmax(next, fmin(best, v));
+        best = fmax(best, v);
+      }
+      for (int off = 1; off < lanes; off <<= 1) {
+        const double b = __shfl_xor(best, off, 64), n = __shfl_xor(next, off, 64);
+        next = fmax(fmin(best, b), fmax(next, n));
+        best = fmax(best, b);
+      }
+      const double mine = r.group_top > 1 ? best + next : best;
+      int ahead = 0;
+#pragma unroll 1
+      for (int n = 1; n < kRow; ++n) {
+        const double o = row_rotated(mine, n);
+        ahead += o > mine || (o == mine && ((l + n) & (kRow - 1)) / lanes < l / lanes) ? 1 : 0;
+      }
+      kept = told ? kept : ahead < r.top_groups * lanes;
+    }
+    // NaN and infinities may have no order above
+    sure = !row_all(odd ? 1 : 0, [](int a, int b) { return a | b; });
     if (!kept)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) key[j] = 0u;
-    const float last = -row_all(kept ? -rank : -inf, larger), first = row_all(kept ? -inf : rank, larger);
-    // (one group's best alone is exact where it is a logit; equal ones are not told apart here)
-    const float close = bias || r.group_top > 1 ? 2.0f * kClose * (1.0f + fabsf(last)) : 0.0f;
-    const int keeps = row_all(kept ? 1 : 0, [](int a, int b) { return a + b; });
-    sure = r.top_groups == r.groups || (last - first > close && keeps == r.top_groups * lanes);
-    sure = sure && !row_all(odd ? 1 : 0, [](int a, int b) { return a | b; });
   }
-  int expert = 0;
-  float before = inf;
-  const int rounds = bias ? top_k + 1 : top_k;  // with the best one left out
-  for (int c = 0; c < rounds; ++c) {
-    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) m = key[j] > m ? key[j] : m;
-    m = row_all(m, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  for (int j = 0; j < NJ; ++j) key[j] = key[j] ? (key[j] & ~kIndex) | (kIndex - (uint32_t)(e0 + j)) : 0u;
+  sort_descending(key);
+  // choice c in lane c, and kMore more
+  uint32_t choice = 0;
+  for (int c = 0; c < top_k + kMore; ++c) {
+    const uint32_t m = row_all(key[0], [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    const uint32_t mine = key[0] == m ? ~0u : 0u;  // (a mask: a choice of two places is not kept in registers)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = (key[j] & ~mine) | ((j + 1 < NJ ? key[j + 1] : 0u) & mine);
+    choice = l == c ? m : choice;
+  }
+  int expert = choice ? (int)(kIndex - (choice & kIndex)) : 0;
+  // whether a comes before b whatever the cut and the scores' errors (16-bit logits are not cut)
+  auto apart = [&](uint32_t a, uint32_t b) {
+    if (b == 0u) return true;
+    const uint32_t x = a & ~kIndex, y = b & ~kIndex;
+    if (!bias) return kElementBytes<XT> == 2 || x != y;
+    const float v = key_value(x), w = key_value(y), cut = (float)(kIndex + 1) * 0x1p-22f;
+    return v - w > kClose * (1.0f + fabsf(w)) + cut * (fabsf(v) + fabsf(w));
+  };
+  // (read by all lanes: those of a branch not taken give 0)
+  const uint32_t following = row_rotated(choice, 1), third = row_rotated(choice, kMore);
+  const bool near = l < top_k && !apart(choice, following);
+  if (__any(near)) {
+    const bool mixed = row_all(near ? 1 : 0, [](int a, int b) { return a | b; });
+    const bool enough = l != top_k - 1 || apart(choice, third);
+    sure = sure && (!mixed || row_all(enough ? 1 : 0, [](int a, int b) { return a & b; }));
+    // the exact order of all but the last
+    const bool there = l < top_k + kMore - 1 && choice != 0u;
+    const float y = load_logit<XT>(logits, t * E + (there ? expert : 0));
+    double exact = y;
     if (bias) {
-      const float v = key_value(m);
-      if (c > 0 && m > 0u) sure = sure && before - v > kClose * (1.0f + fabsf(v));
-      before = v;
+      const double total = r.sigmoid ? 1.0 : softmax_sum(x, max);
+      exact = is_masked(y) ? (double)y : score64(y, r.sigmoid, max, total) + (double)bias[there ? expert : 0];
     }
-    int id = 1 << 20;  // the lowest index of that key
+    const uint64_t mine = there ? order_key(exact) : 0ull;
+    int rank = 0;
 #pragma unroll
-    for (int j = NJ - 1; j >= 0; --j) id = key[j] == m && j < own ? e0 + j : id;
-    id = row_all(id, [](int a, int b) { return a < b ? a : b; });
-    const int mine = id - e0;  // outside 0 .. n - 1: another lane's
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = mine == j ? 0u : key[j];
-    expert = l == c ? id : expert;
+    for (int n = 1; n < kRow; ++n) {
+      const uint64_t o = (uint64_t)row_rotated((unsigned long long)mine, n);
+      const int e = row_rotated(expert, n);
+      rank += o > mine || (o == mine && e < expert) ? 1 : 0;
+    }
+    const int sorted = __builtin_amdgcn_ds_permute(4 * (((int)threadIdx.x & 48) | (there ? rank : l)), expert);
+    expert = mixed ? sorted : expert;
   }
   const bool used = l < top_k;
-  const float chosen = used && expert < E ? load_logit<XT>(logits, t * E + expert) : -inf;
+  const float chosen = used ? load_logit<XT>(logits, t * E + expert) : -inf;
   const double w = weight_of<kRow>(chosen, used, r.sigmoid, r.renormalize, max, sum);
   if (used && sure) {
     experts[t * top_k + l] = expert;
@@ -467,7 +585,7 @@ hipError_t launch_moe_route(const void* logits, int dtype, int64_t T, int E, int
                             float* weights, hipStream_t stream) {
   const Routing r = {E, top_k, sigmoid, groups, top_groups, group_top, renormalize, scale};
   const int nj = (E + kRow - 1) / kRow;  // experts a lane of a row; groups are whole lanes
-  const bool rows = top_k <= kRow && (groups == 1 || (kRow % groups == 0 && E % kRow == 0));
+  const bool rows = top_k <= kRow - kMore && (groups == 1 || (kRow % groups == 0 && E % kRow == 0));
   return by_type(dtype, [&](auto tag) {
     using XT = decltype(tag);
     if (!rows)

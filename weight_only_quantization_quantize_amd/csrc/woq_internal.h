@@ -201,6 +201,11 @@ hipError_t launch_moe_route_backward(const void* logits, int dtype, const int32_
                                      hipStream_t stream);
 // A layer of experts on routed tokens.
 int int8_moe_max_experts();
+// One token: workspace top_k I floats.
+bool int8_moe_row_supported(int64_t H, int64_t I, int64_t top_k);
+hipError_t launch_int8_moe_row(const void* X, int xdtype, const int32_t* experts, const float* weights, const void* up,
+                               const float* up_scales, const void* down, const float* down_scales, int64_t H, int64_t I, int64_t E,
+                               int top_k, void* Y, void* workspace, hipStream_t stream);
 size_t int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
 hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, const float* weights, const void* up,
                            const float* up_scales, const void* down, const float* down_scales, int64_t T, int64_t H, int64_t I,

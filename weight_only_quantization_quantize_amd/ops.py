@@ -42,17 +42,18 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _require_gpu(*ts: Optional[torch.Tensor]) -> None:
-    dev = None
+    index = -1
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()  # -1 on the CPU
+        if i < 0:
             raise ValueError("libwoq works on GPU tensors only")
         if not t.is_contiguous():
             raise ValueError("libwoq needs contiguous tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+        if index < 0:
+            index = i
+        elif i != index:
             raise ValueError("all tensors must be on the same device")
 
 

@@ -3,9 +3,9 @@
 //
 // A row y is held as codes q in -127 .. 127 and a scale a / 127, a = max|y|:
 //   q = the integer nearest to 127 y / a, ties to the even one, decided exactly.
-// t = |y| r with r = fl(127 / a) is off by at most 127 2^-23 < 2^-16, so it decides every
-// element but those within kNear of a tie; there the sign of 254 |y| - (2 floor(t) + 1) a
-// decides.  Both products are exact as a float and its error term (fmaf), their
+// y r with r = fl(127 / a) is off by at most 127 2^-24 < 2^-17 (and 2^-18 more where it is
+// rounded), so it decides every element but those within kNear of a tie; there the sign of
+// 254 |y| - (2 floor(|y| r) + 1) a decides.  Both products are exact as a float and its error term (fmaf), their
 // difference next to a tie is exact too, and 0 only at a tie.
 #pragma once
 
@@ -44,6 +44,7 @@ struct Int8Row {
   float scale;
 };
 __device__ inline Int8Row int8_row(uint32_t bits) {
+  bits = (uint32_t)__builtin_amdgcn_readfirstlane((int)bits);
   const float a = __builtin_bit_cast(float, bits);
   Int8Row p;
   p.factor = a < 0x1p-60f ? 0x1p80f : (a > 0x1p60f ? 0x1p-80f : 1.0f);
@@ -58,40 +59,47 @@ __device__ inline Int8Row int8_row(uint32_t bits) {
 }
 
 constexpr float kNear = 0x1p-14f;
+constexpr float kWhole = 0x1.8p23f;  // adding it rounds to an integer, ties to even, in the low bits
 
-// The codes of N elements, as floats.  (A spoilt row's infinities and NaNs are
-// masked by its factor 0 below.)
+// The codes of N elements of a row, four in a word, the first in the low byte.  The row is
+// one for all lanes of the wave.
 template <int N>
-__device__ inline void int8_codes(float (&y)[N], const Int8Row& p) {
-  bool near = false;
-  float t[N];
+__device__ inline void int8_codes(const float (&y)[N], const Int8Row& p, uint32_t (&q)[N / 4]) {
+  static_assert(N % 4 == 0);
+  if (p.r == 0.0f) {  // spoilt, or zeros
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) q[i] = 0u;
+    return;
+  }
+  float v[N], z[N], far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = y[i];
+  if (p.factor != 1.0f)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= p.factor;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    y[i] *= p.factor;
-    t[i] = y[i] * p.r;
-    near |= fabsf(fabsf(t[i] - truncf(t[i])) - 0.5f) < kNear;
+    z[i] = fmaf(v[i], p.r, kWhole);
+    far = fmaxf(far, fabsf(fmaf(v[i], p.r, -(z[i] - kWhole))));
   }
-  if (__any(near)) {
+  if (__any(far > 0.5f - kNear)) {
 #pragma clang fp contract(off)  // f and s are the rounded products
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float u = fabsf(y[i]), low = floorf(fabsf(t[i])), h = 2.0f * low + 1.0f;
+      const float u = fabsf(v[i]), t = u * p.r, low = floorf(t), h = 2.0f * low + 1.0f;
       const float f = 254.0f * u, s = h * p.a;
       const float d = (f - s) + (fmaf(254.0f, u, -f) - fmaf(h, p.a, -s));
       const float even = 2.0f * rintf(0.5f * low + 0.25f);  // the even one of low, low + 1
-      const float q = d > 0.0f ? low + 1.0f : (d < 0.0f ? low : even);
-      const bool tie = fabsf(fabsf(t[i]) - low - 0.5f) < kNear;
-      t[i] = tie ? copysignf(q, y[i]) : t[i];
+      const float c = d > 0.0f ? low + 1.0f : (d < 0.0f ? low : even);
+      const bool tie = fabsf(t - low - 0.5f) < 2.0f * kNear;
+      z[i] = tie ? copysignf(c, v[i]) + kWhole : z[i];
     }
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = p.r > 0.0f ? rintf(t[i]) : 0.0f;
-}
-
-// Four codes in a word, the first in the low byte.
-__device__ inline uint32_t int8_pack(float a, float b, float c, float d) {
-  return ((uint32_t)(int)a & 0xFFu) | ((uint32_t)(int)b & 0xFFu) << 8 | ((uint32_t)(int)c & 0xFFu) << 16 |
-         (uint32_t)(int)d << 24;
+  for (int i = 0; i < N / 4; ++i) {
+    auto bits = [&](int k) { return __builtin_bit_cast(uint32_t, z[4 * i + k]); };
+    q[i] = __builtin_amdgcn_perm(bits(1), bits(0), 0x0C0C0400u) | __builtin_amdgcn_perm(bits(3), bits(2), 0x04000C0Cu);
+  }
 }
 
 // silu(g) u

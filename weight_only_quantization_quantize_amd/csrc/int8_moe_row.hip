@@ -175,10 +175,9 @@ __global__ __launch_bounds__(kWaves * 64) void int8_moe_row_down_kernel(
       top = top > o ? top : o;
     }
     const Int8Row p = int8_row(top);
-    int8_codes(f[j], p);
+    int8_codes(f[j], p, q[j]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      q[j][e] = live[j] ? int8_pack(f[j][4 * e], f[j][4 * e + 1], f[j][4 * e + 2], f[j][4 * e + 3]) : 0u;
+    for (int e = 0; e < 4; ++e) q[j][e] = live[j] ? q[j][e] : 0u;
     if (lane == 0 && wave + kWaves * j < pieces && (wave + kWaves * j) % segs == 0) scales[of] = p.scale;
   }
   const int batches = (H + stride * kSteps - 1) / (stride * kSteps);

@@ -67,10 +67,9 @@ struct Int8RowLoad {
     const Int8Row p = int8_row(top);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      int8_codes(f[j], p);
+      int8_codes(f[j], p, q[j]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q[j][e] = live[j] ? int8_pack(f[j][4 * e], f[j][4 * e + 1], f[j][4 * e + 2], f[j][4 * e + 3]) : 0u;
+      for (int e = 0; e < 4; ++e) q[j][e] = live[j] ? q[j][e] : 0u;
     }
     return p.scale;
   }

@@ -43,6 +43,36 @@ __device__ inline void widen(float (&y)[kLaneElements], const Raw<XT>& raw, cons
   }
 }
 
+// The largest magnitude's bits so far.  16-bit elements as they come are compared in pairs
+// (their bits are in the order of their magnitudes, infinity and NaN above all).
+template <class XT, Fold F>
+struct Largest {
+  static constexpr bool kPairs = kElementBytes<XT> == 2 && F == kNone;
+  typedef uint16_t pair_t __attribute__((ext_vector_type(2)));
+  uint32_t top = 0;
+  __device__ inline void take(const Raw<XT>& raw, const float (&y)[kLaneElements]) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(pair_t, top),
+                                                                      __builtin_bit_cast(pair_t, (uint32_t)raw.v[0][i] & 0x7FFF7FFFu)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLaneElements; ++i) {
+        const uint32_t b = magnitude(y[i]);
+        top = top > b ? top : b;
+      }
+    }
+  }
+  __device__ inline uint32_t bits() const {
+    if constexpr (kPairs) {
+      const uint32_t a = top & 0xFFFFu, b = top >> 16;
+      return magnitude(XT::to_f32((uint16_t)(a > b ? a : b)));
+    }
+    return top;
+  }
+};
+
 // W waves a row, as many rows as they are times in a workgroup, the block-th of its kind.
 // rounds: times STEPS steps of the row's waves cover the row; 1: it stays in registers.
 template <class XT, Fold F, int STEPS>
@@ -57,8 +87,8 @@ __device__ __forceinline__ void int8_quantize_rows(const void* __restrict__ x, c
   const bool live = m < M;
   const uint8_t* const row = static_cast<const uint8_t*>(x) + (live ? m : 0) * K * kElementBytes<XT>;
   Raw<XT> raw[STEPS];
-  float y[kLaneElements];
-  uint32_t top = 0;
+  float y[STEPS][kLaneElements];
+  Largest<XT, F> largest;
   auto at = [&](int round, int i) { return ((round * STEPS + i) * W + w) * kStepElements + kLaneElements * lane; };
   for (int round = 0; round < rounds; ++round) {
 #pragma unroll
@@ -67,14 +97,11 @@ __device__ __forceinline__ void int8_quantize_rows(const void* __restrict__ x, c
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
       if (at(round, i) < K) {
-        widen<XT, F>(y, raw[i], s, at(round, i));
-#pragma unroll
-        for (int e = 0; e < kLaneElements; ++e) {
-          const uint32_t b = magnitude(y[e]);
-          top = top > b ? top : b;
-        }
+        widen<XT, F>(y[i], raw[i], s, at(round, i));
+        largest.take(raw[i], y[i]);
       }
   }
+  uint32_t top = largest.bits();
   top = wave_max_bits(top);
   if (W > 1) {
     if (lane == 0) tops[wave] = top;
@@ -91,11 +118,13 @@ __device__ __forceinline__ void int8_quantize_rows(const void* __restrict__ x, c
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
       if (at(round, i) < K) {
-        if (rounds > 1) load_raw<XT>(raw[i], row, at(round, i));
-        widen<XT, F>(y, raw[i], s, at(round, i));
-        int8_codes(y, p);
-        *reinterpret_cast<u32x2_t*>(codes + m * K + at(round, i)) =
-            u32x2_t{int8_pack(y[0], y[1], y[2], y[3]), int8_pack(y[4], y[5], y[6], y[7])};
+        if (rounds > 1) {
+          load_raw<XT>(raw[i], row, at(round, i));
+          widen<XT, F>(y[i], raw[i], s, at(round, i));
+        }
+        uint32_t q[2];
+        int8_codes(y[i], p, q);
+        *reinterpret_cast<u32x2_t*>(codes + m * K + at(round, i)) = u32x2_t{q[0], q[1]};
       }
   }
 }

@@ -74,9 +74,9 @@ hipError_t launch_tiles(const int8_t* A, const float* sa, const int8_t* W, const
 }
 
 // The tile with the smallest time by a model of what was measured (weights out of HBM, 327
-// sizes from 2 x 36 x 64 to 4096 x 11008 x 4096), in us for r tiles a compute unit and s
-// stages of 128 K:  fixed + r (tile + stage s).  Where the choice is not the fastest of all
-// it costs 3% in the mean.  Large tiles read LDS least for a matrix instruction (2048 x 11008
+// sizes from 2 x 36 x 64 to 4096 x 11008 x 4096, and 260 small ones), in us for r tiles a
+// compute unit and s stages of 128 K:  fixed + r (tile + stage s).  The choice takes 3% more
+// than the fastest of all in the mean, of the small ones 0.5%.  Large tiles read LDS least for a matrix instruction (2048 x 11008
 // x 4096: 256 x 384 85 us, 192 x 256 95, 128 x 128 107, 256 x 256, whose 344 tiles fill two
 // rounds badly, 111; 8192 x 8192 x 8192: 459, 510, 539 and 450); small ones are there for
 // outputs of few tiles, where K is split between four groups of waves and many stages are in
@@ -87,8 +87,9 @@ struct Model {
   double fixed, tile, stage;
 };
 constexpr Model kModels[] = {{256, 256, 0.0, 7.95, 1.24}, {256, 384, 0.0, 11.08, 1.73}, {192, 256, 0.0, 6.61, 1.02},
-                             {128, 256, 0.0, 5.91, 0.75}, {128, 128, 0.0, 5.17, 0.47},  {64, 128, 0.49, 3.09, 0.30},
-                             {64, 64, 2.3, 1.11, 0.21},   {64, 32, 0.85, 3.12, 0.16},   {32, 32, 1.36, 2.63, 0.14}};
+                             {128, 256, 0.0, 5.91, 0.75}, {128, 128, 0.0, 5.17, 0.47},  {64, 128, 0.19, 3.24, 0.35},
+                             {64, 64, 1.9, 1.3, 0.24},    {32, 64, 2.44, 1.08, 0.22},   {64, 32, 0.85, 3.46, 0.18},
+                             {32, 32, 1.19, 2.84, 0.15}};
 // wide: the second tile too (its registers hold the sums and 16-bit outputs, not fp32 ones)
 int choose(int64_t M, int64_t N, int64_t K, bool wide) {
   int best = 0;
@@ -118,7 +119,8 @@ hipError_t launch(const int8_t* A, const float* sa, const int8_t* W, const float
     case 4: return run(Int8Tile<2, 2, 2, 4, 1, 4, 1>{});
     case 5: return run(Int8Tile<1, 1, 4, 4, 1, 4>{});
     case 6: return run(Int8Tile<1, 1, 2, 4, 1, 4>{});
-    case 7: return run(Int8Tile<1, 1, 1, 4, 4, 3>{});
+    case 7: return run(Int8Tile<1, 1, 2, 4, 1, 6, 1, 1>{});
+    case 8: return run(Int8Tile<1, 1, 1, 4, 4, 3>{});
     default: return run(Int8Tile<1, 1, 1, 4, 4, 4, 1, 1>{});
   }
 }
@@ -127,7 +129,7 @@ hipError_t launch(const int8_t* A, const float* sa, const int8_t* W, const float
 
 hipError_t launch_int8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, const float* bias,
                             int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream) {
-  if (M == 1 && K <= int8_gemv_max_k()) return launch_int8_gemv(A, a_scales, W, w_scales, bias, N, K, ydtype, Y, stream);
+  if (M <= int8_gemv_max_rows(K)) return launch_int8_gemv(A, a_scales, W, w_scales, bias, M, N, K, ydtype, Y, stream);
   auto* const f = ydtype == 0 ? launch<F16> : (ydtype == 1 ? launch<BF16> : launch<F32>);
   return f(static_cast<const int8_t*>(A), a_scales, static_cast<const int8_t*>(W), w_scales, bias, M, N, K, Y, stream);
 }
@@ -136,14 +138,14 @@ namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
-// The row's codes and scales, or nothing where one launch does it all.
+// The rows' codes and scales, or nothing where one launch does it all.
 size_t int8_linear_workspace_bytes(int64_t M, int64_t, int64_t K) {
-  return M == 1 && K <= int8_gemv_max_k() ? 0 : up256((size_t)(M * K)) + (size_t)M * 4;
+  return M <= int8_linear_max_rows(K) ? 0 : up256((size_t)(M * K)) + (size_t)M * 4;
 }
 
 hipError_t launch_int8_linear(const void* X, int xdtype, const float* act_scale, const void* W, const float* w_scales,
                               const float* bias, int64_t M, int64_t N, int64_t K, void* Y, void* workspace, hipStream_t stream) {
-  if (M == 1 && K <= int8_gemv_max_k()) return launch_int8_linear_row(X, xdtype, act_scale, W, w_scales, bias, N, K, Y, stream);
+  if (M <= int8_linear_max_rows(K)) return launch_int8_linear_rows(X, xdtype, act_scale, W, w_scales, bias, M, N, K, Y, stream);
   float* const scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up256((size_t)(M * K)));
   const hipError_t e = launch_int8_quantize(X, xdtype, act_scale, false, M, K, workspace, scales, stream);
   if (e != hipSuccess) return e;

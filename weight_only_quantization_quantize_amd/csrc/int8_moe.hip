@@ -289,7 +289,11 @@ hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, co
   float* const products = reinterpret_cast<float*>(ws + l.products);
   float* const h_scales = reinterpret_cast<float*>(ws + l.h_scales);
   float* const x_scales = reinterpret_cast<float*>(ws + l.scales);
-  const Int8RowsPlan p = int8_rows_plan(T, H);
+  Int8RowsPlan p = int8_rows_plan(T, H);
+  if (choices >= 2048) {  // large workgroups, for the one that plans (2048 tokens, four each: @@)
+    p.rows = kRowMaxWaves / p.W;
+    p.groups = (unsigned)((T + p.rows - 1) / p.rows);
+  }
   auto prepare = [&](auto tag) {
     using XT = decltype(tag);
     auto* const f = p.per <= 1 ? int8_moe_prepare_kernel<XT, 1> : (p.per <= 2 ? int8_moe_prepare_kernel<XT, 2> : int8_moe_prepare_kernel<XT, 4>);

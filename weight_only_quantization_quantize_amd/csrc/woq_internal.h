@@ -181,12 +181,13 @@ hipError_t launch_int8_quantize(const void* x, int xdtype, const float* act_scal
                                 void* codes, float* scales, hipStream_t stream);
 hipError_t launch_int8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, const float* bias,
                             int64_t M, int64_t N, int64_t K, int ydtype, void* Y, hipStream_t stream);
-// One row, K <= int8_gemv_max_k(): of codes, or of 16-bit activations.
-int64_t int8_gemv_max_k();
+// Up to int8_gemv_max_rows(K) rows of codes, int8_linear_max_rows(K) of 16-bit activations.
+int64_t int8_gemv_max_rows(int64_t K);
+int64_t int8_linear_max_rows(int64_t K);
 hipError_t launch_int8_gemv(const void* codes, const float* a_scales, const void* W, const float* w_scales, const float* bias,
-                            int64_t N, int64_t K, int ydtype, void* y, hipStream_t stream);
-hipError_t launch_int8_linear_row(const void* x, int xdtype, const float* act_scale, const void* W, const float* w_scales,
-                                  const float* bias, int64_t N, int64_t K, void* y, hipStream_t stream);
+                            int64_t M, int64_t N, int64_t K, int ydtype, void* y, hipStream_t stream);
+hipError_t launch_int8_linear_rows(const void* x, int xdtype, const float* act_scale, const void* W, const float* w_scales,
+                                   const float* bias, int64_t M, int64_t N, int64_t K, void* y, hipStream_t stream);
 size_t int8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_linear(const void* X, int xdtype, const float* act_scale, const void* W, const float* w_scales,
                               const float* bias, int64_t M, int64_t N, int64_t K, void* Y, void* workspace, hipStream_t stream);

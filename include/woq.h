@@ -359,8 +359,8 @@ woq_status woq_mxfp4_moe(const void* X, int32_t xdtype, const void* router, cons
 /* 8-bit integers with a scale a row (W8A8).
  *
  * Format of a matrix [M, K], K a multiple of 16 and at most 131056 (sums of K
- * products of two codes are exact in 32 bits): codes int8 [M, K], scales fp32
- * [M]; the element k of row m stands for codes[m, k] scales[m].  Quantization of
+ * products of two codes are exact in 32 bits), M at most 2^28: codes int8 [M, K],
+ * scales fp32 [M]; the element k of row m stands for codes[m, k] scales[m].  Quantization of
  * a row y, a = max|y|:
  *   scale = a / 127
  *   code  = the integer nearest to 127 y / a, ties to the even one, exactly
@@ -396,7 +396,7 @@ woq_status woq_int8_linear(const void* X, int32_t xdtype, const float* act_scale
                            const float* scales, const float* bias, int64_t M, int64_t N, int64_t K, void* Y,
                            void* workspace, size_t workspace_bytes, void* stream);
 
-/* Routing of tokens to experts (E <= 512, top_k <= 64).  Of a token's logits x [E]:
+/* Routing of up to 2^24 tokens to experts (E <= 512, top_k <= 64).  Of a token's logits x [E]:
  *   s       = softmax(x) (WOQ_SOFTMAX) or 1 / (1 + exp(-x)) (WOQ_SIGMOID)
  *   key     = x, or, with a bias b [E], s + b computed in 64 bits
  *   groups  : E / groups neighbours each.  Only the top_groups groups with the

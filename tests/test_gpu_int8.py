@@ -235,6 +235,40 @@ def test_gemm_writes_into_out_and_nothing_else():
         assert torch.equal(big[:M], ops.int8_gemm(*args, dtype=F32))
 
 
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_products_of_weights_past_32_bits(M):
+    """5.2 GB of weights, all zeros but rows in the first and the last bytes."""
+    N, K = 40000, 131056
+    g = rng(19, M)
+    w = torch.zeros(N, K, dtype=torch.int8, device=DEV)
+    rows = np.array([0, 1, 16386, 16387, 32772, 32773, N - 2, N - 1])
+    wr = g.integers(-127, 128, (len(rows), K)).astype(np.int8)
+    w[torch.from_numpy(rows).to(DEV)] = tensor(wr, torch.int8)
+    a = g.integers(-127, 128, (M, K)).astype(np.int8)
+    one = torch.ones(N, device=DEV)
+    y = ops.int8_gemm(tensor(a, torch.int8), torch.full((M,), 2.0 ** -20, device=DEV), w, one, dtype=F32)
+    ref = O.gemm(a, np.full(M, 2.0 ** -20), wr, np.ones(len(rows)))
+    close(host(y)[:, rows], ref, 4 * U * np.abs(ref) + 2.0 ** -149, f"far weights, {M}")
+    y[:, torch.from_numpy(rows).to(DEV)] = 0
+    assert not y.any()
+
+
+def test_quantize_past_32_bits():
+    """2.1 billion elements and one row more; rows of 16384 with other waves' shares."""
+    for M, K in ((131073, 16400), (9000000, 272)):
+        x = torch.zeros(M, K, dtype=F16, device=DEV)
+        rows = np.array([0, M // 2, M - 1])
+        v = rng(20).normal(size=(3, K)).astype(np.float16)
+        x[torch.from_numpy(rows).to(DEV)] = tensor(v, F16)
+        codes, scales = ops.int8_quantize(x)
+        q, s = O.quantize(v.astype(np.float64))
+        assert np.array_equal(raw(codes[torch.from_numpy(rows).to(DEV)]), q)
+        close(host(scales)[rows], s, U * ABOVE * s, "scales")
+        codes[torch.from_numpy(rows).to(DEV)] = 0
+        assert not codes.any()
+        del x, codes
+
+
 # ---------------------------------------------------------------------------
 # Routing
 # ---------------------------------------------------------------------------
@@ -409,6 +443,27 @@ def test_moe_bits_do_not_depend_on_the_other_tokens(T):
     assert torch.equal(y[::7], one)
     order = torch.from_numpy(g.permutation(T)).to(DEV)
     assert torch.equal(y[order], ops.int8_moe(x[order].contiguous(), e[order].contiguous(), w[order].contiguous(), *weights))
+
+
+@pytest.mark.parametrize("T", [1, 5, 300])
+def test_moe_of_weights_past_32_bits(T):
+    """4.8 GB of up rows: the experts at both ends."""
+    g, H, I, E = rng(21, T), 8192, 4096, 72
+    up, down = torch.zeros(E, 2 * I, H, dtype=torch.int8, device=DEV), torch.zeros(E, H, I, dtype=torch.int8, device=DEV)
+    ends = [0, E - 1]
+    few = layer(5, H, I, 2)
+    for i, e in enumerate(ends):
+        up[e], down[e] = tensor(few[0][i], torch.int8), tensor(few[2][i], torch.int8)
+    su, sd = torch.zeros(E, 2 * I, device=DEV), torch.zeros(E, H, device=DEV)
+    su[ends], sd[ends] = tensor(few[1]), tensor(few[3])
+    x = tensor(g.normal(size=(T, H)), BF16)
+    which = g.integers(0, 2, (T, 2))
+    w = tensor(g.random((T, 2)).astype(np.float32))
+    y = ops.int8_moe(x, tensor(which * (E - 1), torch.int32), w, up, su, down, sd)
+    rows = np.arange(min(T, 3))
+    ref, reach, parts = O.moe(host(x)[rows], which[rows], host(w)[rows], *few, slack=SLACK)
+    err = (reach + (SLACK / 127 + 7 * U) * parts + HALF[BF16] * np.abs(ref)) * ABOVE + HALF[BF16] * reach + TINY[BF16]
+    close(host(y)[rows], ref, err, f"far experts, {T}")
 
 
 def test_moe_writes_into_out_and_nothing_else():

@@ -217,7 +217,7 @@ ABI = [
     ("woq_int8_gemm", GEMM, INVALID, [dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(Y=None), dict(Y=P(5) + 8),
                                       dict(w=P(2) + 4), dict(bias=P(4) + 2), dict(M=0), dict(N=0), dict(K=8), dict(ydtype=5),
                                       dict(Y=P(0)), dict(Y=P(1)), dict(Y=P(2) + 304), dict(Y=P(3)), dict(Y=P(4))]),
-    ("woq_int8_gemm", GEMM, UNSUPPORTED, [dict(K=131072), dict(M=1 << 28, N=1 << 28)]),
+    ("woq_int8_gemm", GEMM, UNSUPPORTED, [dict(K=131072), dict(M=1 << 28, N=1 << 28), dict(M=1 << 22, N=1 << 16)]),
     ("woq_int8_linear", LINEAR, INVALID, [dict(X=None), dict(xdtype=2), dict(Y=None), dict(ws=None), dict(ws=P(6) + 16),
                                           dict(ws_bytes=100), dict(Y=P(0)), dict(ws=P(5)), dict(ws=P(0)), dict(act_scale=P(1) + 8)]),
     ("woq_moe_route", ROUTE, INVALID, [dict(logits=None), dict(logits=P(0) + 1), dict(dtype=9), dict(T=0), dict(E=0), dict(top_k=0),
@@ -225,14 +225,14 @@ ABI = [
                                        dict(top_groups=0), dict(group_top=3), dict(group_top=0), dict(groups=8, group_top=2),
                                        dict(bias=P(1) + 1), dict(experts=None), dict(weights=None), dict(experts=P(0)),
                                        dict(weights=P(2) + 28)]),
-    ("woq_moe_route", ROUTE, UNSUPPORTED, [dict(E=1024), dict(E=512, groups=1, top_k=65), dict(T=(1 << 28) + 1)]),
+    ("woq_moe_route", ROUTE, UNSUPPORTED, [dict(E=1024), dict(E=512, groups=1, top_k=65), dict(T=(1 << 24) + 1)]),
     ("woq_moe_route_backward", BACKWARD, INVALID, [dict(logits=None), dict(experts=None), dict(dweights=None), dict(dlogits=None),
                                                    dict(dlogits=P(0)), dict(dlogits=P(1)), dict(dlogits=P(2)), dict(dtype=1, dlogits=P(3) + 1)]),
     ("woq_int8_moe", MOE, INVALID, [dict(X=None), dict(xdtype=2), dict(experts=None), dict(weights=P(2) + 2), dict(up=None), dict(su=None),
                                     dict(down=P(5) + 8), dict(sd=None), dict(T=0), dict(H=40), dict(I=8), dict(top_k=0), dict(Y=P(0)),
                                     dict(Y=P(3)), dict(ws=P(7)), dict(ws=None), dict(ws_bytes=1000), dict(Y=None)]),
     ("woq_int8_moe", MOE, UNSUPPORTED, [dict(E=513), dict(top_k=65), dict(H=1 << 16, I=1 << 16), dict(T=1 << 20, H=1 << 16),
-                                        dict(T=1 << 27, H=16, I=16, top_k=4)]),
+                                        dict(T=1 << 23, H=16, I=16, top_k=64), dict(T=(1 << 24) + 1, H=16, I=16, top_k=1)]),
 ]
 
 

@@ -14,16 +14,20 @@ namespace {
 template <class XT, Fold F, int STEPS>
 __global__ __launch_bounds__(kRowMaxWaves * 64) void int8_quantize_kernel(const void* __restrict__ x,
                                                                          const float* __restrict__ s, int64_t M, int K, int W,
-                                                                         int rounds, int8_t* __restrict__ codes,
+                                                                         int rounds, unsigned groups, int8_t* __restrict__ codes,
                                                                          float* __restrict__ scales) {
-  int8_quantize_rows<XT, F, STEPS>(x, s, M, K, W, rounds, blockIdx.x, codes, scales);
+  for (unsigned g = blockIdx.x; g < groups; g += gridDim.x) {
+    int8_quantize_rows<XT, F, STEPS>(x, s, M, K, W, rounds, g, codes, scales);
+    if (g + gridDim.x < groups) __syncthreads();  // the waves' largest magnitudes were read
+  }
 }
 
 template <class XT, Fold F>
 hipError_t launch(const void* x, const float* s, int64_t M, int K, void* codes, float* scales, hipStream_t stream) {
   const Int8RowsPlan p = int8_rows_plan(M, K);
   auto* const f = p.per <= 1 ? int8_quantize_kernel<XT, F, 1> : (p.per <= 2 ? int8_quantize_kernel<XT, F, 2> : int8_quantize_kernel<XT, F, 4>);
-  f<<<p.groups, (unsigned)p.threads(), 0, stream>>>(x, s, M, K, p.W, p.rounds(), static_cast<int8_t*>(codes), scales);
+  const unsigned grid = p.groups < kMostGroups ? p.groups : kMostGroups;
+  f<<<grid, (unsigned)p.threads(), 0, stream>>>(x, s, M, K, p.W, p.rounds(), p.groups, static_cast<int8_t*>(codes), scales);
   return hipGetLastError();
 }
 

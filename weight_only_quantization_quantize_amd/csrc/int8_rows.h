@@ -129,7 +129,9 @@ __device__ __forceinline__ void int8_quantize_rows(const void* __restrict__ x, c
   }
 }
 
-// How a matrix's rows are shared out: W, rounds and rows a workgroup.
+// How a matrix's rows are shared out: W, rounds and rows a workgroup.  A launch has fewer than
+// 2^32 threads: workgroups of more rows than that go around (kMostGroups of up to 1024 threads).
+constexpr unsigned kMostGroups = 1u << 21;
 struct Int8RowsPlan {
   int W, per, rows;
   unsigned groups;

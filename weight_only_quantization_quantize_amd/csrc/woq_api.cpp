@@ -239,7 +239,8 @@ int64_t dtype_bytes(int32_t dtype) { return dtype == WOQ_F32 ? 4 : 2; }
 woq_status check_int8_gemm(int64_t M, int64_t N, int64_t K) {
   WOQ_TRY(check_int8_shape(M, K, "M"));
   WOQ_TRY(check_int8_shape(N, K, "N"));
-  if ((M + 63) / 64 * ((N + 63) / 64) > INT32_MAX - 8)
+  // tiles of at least 64 x 64 at such sizes, the threads of a launch counted in 32 bits
+  if ((M + 63) / 64 * ((N + 63) / 64) > (1 << 25))
     return fail(WOQ_ERR_UNSUPPORTED, "product too large for this library (M=%lld, N=%lld)", (long long)M, (long long)N);
   return WOQ_OK;
 }
@@ -257,8 +258,8 @@ woq_status check_route(int64_t T, int64_t E, int32_t top_k, int32_t dtype, int32
   WOQ_TRY(check_any_dtype(dtype, "dtype"));
   if (scoring != WOQ_SOFTMAX && scoring != WOQ_SIGMOID)
     return fail(WOQ_ERR_INVALID_ARGUMENT, "scoring must be WOQ_SOFTMAX or WOQ_SIGMOID (got %d)", scoring);
-  if (T > (1 << 28) || E > woq::moe_route_max_experts() || top_k > woq::moe_route_max_top_k())
-    return fail(WOQ_ERR_UNSUPPORTED, "a routing takes up to 2^28 tokens, %d experts and a top_k of %d (got %lld, %lld, %d)",
+  if (T > (1 << 24) || E > woq::moe_route_max_experts() || top_k > woq::moe_route_max_top_k())
+    return fail(WOQ_ERR_UNSUPPORTED, "a routing takes up to 2^24 tokens, %d experts and a top_k of %d (got %lld, %lld, %d)",
                 woq::moe_route_max_experts(), woq::moe_route_max_top_k(), (long long)T, (long long)E, top_k);
   return WOQ_OK;
 }
@@ -271,8 +272,9 @@ woq_status check_int8_moe(int64_t T, int64_t H, int64_t I, int64_t E, int32_t to
     return fail(WOQ_ERR_UNSUPPORTED, "int8_moe takes up to %d experts and a top_k of %d (got %lld, %d)",
                 woq::int8_moe_max_experts(), woq::moe_route_max_top_k(), (long long)E, top_k);
   // rows of X and of an expert at 32-bit offsets; tiles of 64 rows and columns counted in 32 bits
-  const int64_t wide = (H > I ? H : I) / 64 + 1;
-  if (T * H > UINT32_MAX || 2 * I * H > UINT32_MAX || T * top_k > (1 << 28) || (T * top_k / 64 + E) * wide > INT32_MAX)
+  const int64_t wide = (H > I ? H : I) / 64 + 9;
+  if (T > (1 << 24) || T * H > UINT32_MAX || 2 * I * H > UINT32_MAX || T * top_k > (1 << 28) ||
+      (T * top_k / 64 + E) * wide > (1 << 30))
     return fail(WOQ_ERR_UNSUPPORTED, "layer too large for this library (T=%lld, H=%lld, I=%lld, top_k=%d)", (long long)T,
                 (long long)H, (long long)I, top_k);
   return WOQ_OK;

@@ -181,6 +181,13 @@ def test_gemm_of_many_tiles(M, N, K):
     check_gemm(*gemm_inputs(M, N, K, False), BF16, f"{M} x {N} x {K}")
 
 
+@pytest.mark.parametrize("M,N,K", [(1500, 6001, 80), (2040, 6001, 80), (2040, 6001, 1040), (2040, 11000, 80), (2040, 11001, 400)])
+@pytest.mark.parametrize("dtype,bias", [(F16, True), (BF16, False), (F32, True)])
+def test_gemm_of_large_tiles(M, N, K, dtype, bias):
+    """Outputs that give every compute unit tiles of 192 and 256 rows, the last ones cut short."""
+    check_gemm(*gemm_inputs(M, N, K, bias), dtype, f"{M} x {N} x {K}")
+
+
 @pytest.mark.parametrize("M", [1, 2, 16, 40, 130])
 def test_gemm_largest_sums(M):
     """All codes at -128 or 127: sums up to 2^31 - 2^18 in magnitude."""

@@ -5,8 +5,8 @@
 //   q = the integer nearest to 127 y / a, ties to the even one, decided exactly.
 // y r with r = fl(127 / a) is off by at most 127 2^-24 < 2^-17 (and 2^-18 more where it is
 // rounded), so it decides every element but those within kNear of a tie; there the sign of
-// 254 |y| - (2 floor(|y| r) + 1) a decides.  Both products are exact as a float and its error term (fmaf), their
-// difference next to a tie is exact too, and 0 only at a tie.
+// 254 |y| - (2 floor(|y| r) + 1) a decides.  Both products are exact as a float and its error
+// term (fmaf), their difference next to a tie is exact too, and 0 only at a tie.
 #pragma once
 
 #include <type_traits>

@@ -1,6 +1,8 @@
 // Products of two 8-bit integer matrices with a scale for each row of either:
 //   Y[m, n] = (acc sa[m]) sw[n] + bias[n],  acc = sum_k a[m, k] w[n, k]
-// The sums are exact (int8_tile.h); the scales multiply in fp32, Y is rounded once.
+// The sums are exact (int8_tile.h, which says what bounds them); the scales multiply in fp32,
+// Y is rounded once.  Up to four rows go to the kernel that streams the weights past them
+// (int8_gemv.hip).
 #include "int8_tile.h"
 #include "woq_internal.h"
 
@@ -76,11 +78,11 @@ hipError_t launch_tiles(const int8_t* A, const float* sa, const int8_t* W, const
 // The tile with the smallest time by a model of what was measured (weights out of HBM, 327
 // sizes from 2 x 36 x 64 to 4096 x 11008 x 4096, and 260 small ones), in us for r tiles a
 // compute unit and s stages of 128 K:  fixed + r (tile + stage s).  The choice takes 3% more
-// than the fastest of all in the mean, of the small ones 0.5%.  Large tiles read LDS least for a matrix instruction (2048 x 11008
-// x 4096: 256 x 384 85 us, 192 x 256 95, 128 x 128 107, 256 x 256, whose 344 tiles fill two
-// rounds badly, 111; 8192 x 8192 x 8192: 459, 510, 539 and 450); small ones are there for
-// outputs of few tiles, where K is split between four groups of waves and many stages are in
-// flight (16 x 4096 x 11008: 32 x 32 16.4 us, 64 x 32 18.1, 64 x 64 23.7; 128 x 4096 x 4096:
+// than the fastest of all in the mean, of the small ones 0.5%.  Large tiles read LDS least for
+// a matrix instruction (2048 x 11008 x 4096: 256 x 384 85 us, 192 x 256 95, 128 x 128 107,
+// 256 x 256, whose 344 tiles fill two rounds badly, 111; 8192 x 8192 x 8192: 459, 510, 539 and
+// 450); small ones are there for outputs of few tiles, where K is split between four groups
+// of waves and many stages are in flight (16 x 4096 x 11008: 32 x 32 16.4 us, 64 x 32 18.1, 64 x 64 23.7; 128 x 4096 x 4096:
 // 15, 9.3 and 10.4; 16 x 28672 x 8192: 55, 58 and 45.5).
 struct Model {
   int bm, bn;
@@ -90,12 +92,10 @@ constexpr Model kModels[] = {{256, 256, 0.0, 7.95, 1.24}, {256, 384, 0.0, 11.08,
                              {128, 256, 0.0, 5.91, 0.75}, {128, 128, 0.0, 5.17, 0.47},  {64, 128, 0.19, 3.24, 0.35},
                              {64, 64, 1.9, 1.3, 0.24},    {32, 64, 2.44, 1.08, 0.22},   {64, 32, 0.85, 3.46, 0.18},
                              {32, 32, 1.19, 2.84, 0.15}};
-// wide: the second tile too (its registers hold the sums and 16-bit outputs, not fp32 ones)
-int choose(int64_t M, int64_t N, int64_t K, bool wide) {
+int choose(int64_t M, int64_t N, int64_t K) {
   int best = 0;
   double least = 0.0;
   for (int i = 0; i < (int)(sizeof(kModels) / sizeof(kModels[0])); ++i) {
-    if (i == 1 && !wide) continue;
     const Model& m = kModels[i];
     const double r = (double)(((M + m.bm - 1) / m.bm * ((N + m.bn - 1) / m.bn) + 255) / 256);
     const double t = m.fixed + r * (m.tile + m.stage * (double)((K + 127) / 128));
@@ -108,12 +108,9 @@ template <class YT>
 hipError_t launch(const int8_t* A, const float* sa, const int8_t* W, const float* sw, const float* bias, int64_t M,
                   int64_t N, int64_t K, void* Y, hipStream_t stream) {
   auto run = [&](auto tag) { return launch_tiles<YT, decltype(tag)>(A, sa, W, sw, bias, M, N, K, Y, stream); };
-  constexpr bool kWide = !std::is_same_v<YT, F32>;
-  switch (choose(M, N, K, kWide)) {
+  switch (choose(M, N, K)) {
     case 0: return run(Int8Tile<4, 2, 4, 4, 1, 2>{});
-    case 1:
-      if constexpr (kWide) return run(Int8Tile<4, 3, 4, 4, 1, 2>{});
-      [[fallthrough]];
+    case 1: return run(Int8Tile<4, 3, 4, 4, 1, 2>{});
     case 2: return run(Int8Tile<3, 2, 4, 4, 1, 2>{});
     case 3: return run(Int8Tile<2, 2, 4, 4, 1, 3>{});
     case 4: return run(Int8Tile<2, 2, 2, 4, 1, 4, 1>{});

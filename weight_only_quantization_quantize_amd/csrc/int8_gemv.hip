@@ -5,11 +5,14 @@
 // needs the codes of the very 16 elements that it quantizes, and all that passes between
 // lanes is the largest magnitude.
 //
-// Bound by streaming the weights once.  A lane owns 16 k (CH times), 16 bytes of a row; a
-// row's chunks are spread over `team` lanes (a power of two up to 64; longer rows over
-// `segs` waves, the slots of a workgroup being 8 / segs rows).  Workgroup b takes the row
-// groups b, b + B, ..., so the whole GPU reads one window of rows at a time, kSteps of them
-// a batch, the next batch on its way while one is multiplied (v_dot4) and summed.
+// Bound by streaming the weights once: 8192 x 8192 14 .. 15 us (4.7 TB/s) with the
+// quantization in it, 19.5 with a launch before for the codes.
+//
+// A lane owns 16 k (CH times), 16 bytes of a row; a row's chunks are spread over `team` lanes
+// (a power of two up to 64; longer rows over `segs` waves, the slots of a workgroup being
+// 8 / segs rows).  Workgroup b takes the row groups b, b + B, ..., so the whole GPU reads one
+// window of rows at a time, kSteps of them a batch, the next batch on its way while one is
+// multiplied (v_dot4) and summed.
 #include "int8_row.h"
 #include "woq_internal.h"
 

@@ -21,8 +21,9 @@
 // weights 115 .. 130), so an expert's weights should come out of HBM once: its row tiles of
 // one column tile are neighbours in the run of one XCD, are multiplied at the same time and
 // share the weights in its L2.  The column tiles go around the XCDs, which so have the same
-// work.  2048 tokens of 32 experts 4096 x 2048, four each, whole layer: 389 us; each XCD an
-// eighth of all tiles, experts in a row, 412, with the idle ones helping out 417.
+// work.  2048 tokens of 32 experts 4096 x 2048, four each, whole layer: 389 us when this was
+// chosen; each XCD an eighth of all tiles, experts in a row, 412, with the idle ones helping
+// out 417.
 #include "int8_rows.h"
 #include "int8_tile.h"
 #include "woq_internal.h"
@@ -289,11 +290,7 @@ hipError_t launch_int8_moe(const void* X, int xdtype, const int32_t* experts, co
   float* const products = reinterpret_cast<float*>(ws + l.products);
   float* const h_scales = reinterpret_cast<float*>(ws + l.h_scales);
   float* const x_scales = reinterpret_cast<float*>(ws + l.scales);
-  Int8RowsPlan p = int8_rows_plan(T, H);
-  if (choices >= 2048) {  // large workgroups, for the one that plans (2048 tokens, four each: @@)
-    p.rows = kRowMaxWaves / p.W;
-    p.groups = (unsigned)((T + p.rows - 1) / p.rows);
-  }
+  const Int8RowsPlan p = int8_rows_plan(T, H);
   auto prepare = [&](auto tag) {
     using XT = decltype(tag);
     auto* const f = p.per <= 1 ? int8_moe_prepare_kernel<XT, 1> : (p.per <= 2 ? int8_moe_prepare_kernel<XT, 2> : int8_moe_prepare_kernel<XT, 4>);

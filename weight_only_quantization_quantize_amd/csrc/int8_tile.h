@@ -6,14 +6,25 @@
 // through LDS at the end.
 //
 // Pipeline.  K goes in stages of 32 KS, two or more of them in LDS, filled by direct loads
-// (global_load_lds: no registers, no instructions to write LDS).  At the top of a turn a
-// wave waits until its own loads of this stage are done, meets the others at the barrier,
-// which also says that everybody is through with the previous stage, starts the loads of
-// the stage kStages - 1 ahead into that one's place, and multiplies.  The loads are written
-// out in assembly because the compiler would wait for all of them before every read of
-// LDS; their counter is waited for by hand, and there is no other vector memory access
+// (global_load_lds: no registers, no instructions to write LDS).  A turn multiplies a
+// stage.  Before its last units, whose operands are in registers by then, a wave waits until
+// its own loads of the next stage are done, meets the others at the barrier, which also says
+// that everybody has read this stage, starts the loads of a later stage into its place, and
+// reads the next stage's first operands; the units left cover those reads.  The loads are
+// written out in assembly because the compiler would wait for all of them before every read
+// of LDS; their counter is waited for by hand, and there is no other vector memory access
 // inside the loop.  Loads past a row's end repeat its last 16 bytes; the last stage masks
 // them on W's side.
+//
+// What bounds it.  On registers alone the matrix units make 5.0 P op/s of zeros, 3.3 P of
+// random codes and, with the LDS reads of a 128 x 64 wave tile beside them, 2.8 P (the
+// clock falling with the power, it seems: zeros keep 4.2 P with the same reads).  The products
+// reach 2.3 .. 2.4 P (8192 x 8192 x 8192 450 us, a library product 526; 2048 x 11008 x 4096
+// 80 .. 85, 104).  LDS is the other limit: a 256 x 256 tile of 8 waves reads 192 KB and takes in
+// 64 KB for each 2048 cycles of matrix instructions, 128 bytes a cycle.  Reading operands a
+// unit ahead, and past the barrier, took 8192 x 8192 x 8192 from 474 to 450 us; stages
+// of 64 K take 498, wave tiles of 128 x 128 on 4 waves 484, and a third stage of W alone
+// changes nothing.
 //
 // LDS layout: a row's 32 KS bytes of a stage are chunks of 16, chunk c at position
 // c ^ swizzle(row), so that 16 rows read at one chunk lie in 16 different 16-byte slots of
@@ -60,7 +71,7 @@ struct Int8Tile {
   static constexpr int kWUnits = BN / kUnitRows;
   // LDS: NS stages of whole tiles, or all of it where a second workgroup has no place anyway.
   // A tile of few rows has shorter stages, and more of them: it has less to hide its loads
-  // behind (a layer of 2048 tokens, where two tiles of three are short ones: @@).
+  // behind (a layer of 2048 tokens, where two tiles of three are short: 404 us, 414 without).
   __host__ __device__ static constexpr int stage_bytes(int blocks) { return (32 * WM * blocks + BN) * kRow; }
   static constexpr int kWhole = KG * NS_ * stage_bytes(TM);
   static constexpr int kMost = 159 * 1024;  // of the 160 KB; the rest is the caller's

@@ -418,6 +418,14 @@ def test_moe(T, H, I, E, k, dtype):
     check_moe(x, e, w, layer(1, H, I, E), f"T {T} H {H} I {I} E {E} k {k}")
 
 
+@pytest.mark.parametrize("counts", [(320, 321, 0, 64, 65, 641, 1, 255, 256), (1, 0, 1900), (129, 193, 257, 385, 449, 640), (97, 98, 99)])
+def test_moe_of_rows_at_the_edges_of_tiles(counts):
+    g, H, I, E, T = rng(21, *counts), 144, 80, len(counts), sum(counts)
+    x = tensor(g.normal(size=(T, H)), BF16)
+    e = tensor(g.permutation(np.repeat(np.arange(E), counts)).astype(np.int32)[:, None], torch.int32)
+    check_moe(x, e, tensor(g.random((T, 1)).astype(np.float32)), layer(5, H, I, E), f"experts of {counts} rows")
+
+
 @pytest.mark.parametrize("T", [1, 6, 90])
 def test_moe_of_left_out_choices_empty_experts_and_spoilt_tokens(T):
     g, H, I, E, k = rng(14, T), 144, 80, 9, 3

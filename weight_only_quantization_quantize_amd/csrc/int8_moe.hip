@@ -24,6 +24,15 @@
 // work.  2048 tokens of 32 experts 4096 x 2048, four each, whole layer: 389 us when this was
 // chosen; each XCD an eighth of all tiles, experts in a row, 412, with the idle ones helping
 // out 417.
+//
+// An expert's second tile reads the weights again, so tiles of many rows are 320 high, all
+// that registers and LDS hold, and an expert's rows are spread evenly over its tiles, in whole
+// row blocks.  The same layer, routed evenly (unevenly: logits with a normal bias for each
+// expert), T tokens, tiles of 256 rows with a short last one before it:
+//   T     1500         2048         3000         4096
+//   now   305 (348)    356 (385)    478 (498)    602 (643) us
+//   256   305 (331)    382 (430)    500 (513)    642 (659)
+// (320 rows with a short last tile: 550 for 3000 tokens; 256 rows, even: 384 for 2048.)
 #include "int8_rows.h"
 #include "int8_tile.h"
 #include "woq_internal.h"
@@ -33,6 +42,7 @@ namespace {
 
 constexpr int kMaxExperts = 512;
 constexpr int kXcds = 8;
+constexpr int kRowBlock = 64;  // tiles' rows are multiplied by as many (int8_tile.h; 32 of each of two waves)
 
 // Up to BM rows of an expert, whose rank by rows is `rank`.
 struct Tile {
@@ -79,7 +89,10 @@ __device__ void int8_moe_plan(const int32_t* __restrict__ experts, int choices, 
     const int lane = threadIdx.x;
     int rows = 0, of = 0;
     for (int r0 = 0; r0 < E; r0 += 64) {
-      const int r = r0 + lane, e = by_rank[r < E ? r : 0], n = r < E ? count[e] : 0, m = (n + BM - 1) / BM;
+      const int r = r0 + lane, e = by_rank[r < E ? r : 0], n = r < E ? count[e] : 0;
+      // an expert's tiles are of one height, in whole row blocks, but for the last one
+      const int least = (n + BM - 1) / BM, height = n ? (n + kRowBlock * least - 1) / (kRowBlock * least) * kRowBlock : BM;
+      const int m = (n + height - 1) / height;
       int a = n, b = m;
       for (int off = 1; off < 64; off <<= 1) {
         const int p = __shfl_up(a, off, 64), q = __shfl_up(b, off, 64);
@@ -89,7 +102,7 @@ __device__ void int8_moe_plan(const int32_t* __restrict__ experts, int choices, 
         const int row = rows + a - n;
         first[e] = row;
         for (int i = 0; i < m; ++i)
-          tiles[of + b - m + i] = Tile{e, row + i * BM, n - i * BM < BM ? n - i * BM : BM, r};
+          tiles[of + b - m + i] = Tile{e, row + i * height, n - i * height < height ? n - i * height : height, r};
       }
       rows += __shfl(a, 63, 64);
       of += __shfl(b, 63, 64);
@@ -235,7 +248,7 @@ __global__ __launch_bounds__(256) void int8_moe_combine_kernel(const float* __re
 
 typedef Int8Tile<1, 2, 2, 4, 1, 3> Small;
 typedef Int8Tile<2, 2, 2, 4, 1, 4, 1> Middle;
-typedef Int8Tile<4, 2, 4, 4, 1, 2> Large;
+typedef Int8Tile<5, 2, 4, 4, 1, 2> Large;
 
 // Tiles of rows, at most: one for each expert that is taken and one for each further BM.
 int64_t most_tiles(int64_t choices, int64_t E, int64_t BM) { return (choices < E ? choices : E) + choices / BM; }

@@ -256,6 +256,8 @@ struct Int8Tile {
   template <class F>
   __device__ __forceinline__ static void for_blocks(int rows, F&& f) {
     const int n = blocks(rows);
+    if constexpr (TM > 4)
+      if (n == 4) return f(std::integral_constant<int, 4>{});
     if constexpr (TM > 3)
       if (n == 3) return f(std::integral_constant<int, 3>{});
     if constexpr (TM > 2)

@@ -426,6 +426,26 @@ def test_moe_of_rows_at_the_edges_of_tiles(counts):
     check_moe(x, e, tensor(g.random((T, 1)).astype(np.float32)), layer(5, H, I, E), f"experts of {counts} rows")
 
 
+@pytest.mark.parametrize("counts,H,I", [((320, 321, 0, 64, 65, 641, 1, 255, 256), 144, 2816), ((1, 0, 1900), 80, 4112), ((97, 98, 99), 48, 11008),
+                                        ((129, 193, 257, 385, 449, 640), 272, 2064)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_moe_of_large_tiles(counts, H, I, dtype):
+    """Layers with tiles for the whole GPU, which take 320 rows at a time."""
+    g, E, T = rng(22, *counts), len(counts), sum(counts) + 3
+    x = tensor(g.normal(size=(T, H)), dtype)
+    e = np.concatenate([np.repeat(np.arange(E), counts), [-1, E, -7]])  # the last ones of no expert
+    e = tensor(g.permutation(e).astype(np.int32)[:, None], torch.int32)
+    w, weights = tensor(g.random((T, 1)).astype(np.float32)), layer(6, H, I, E)
+    x[5, 3] = float("nan")
+    e[5] = 0
+    rows = np.array([t for t in range(T) if t != 5])
+    y = check_moe(x, e, w, weights, f"experts of {counts} rows, I {I}", rows)
+    assert torch.isnan(y[5]).all()
+    gpu = on_gpu(*weights)
+    for t in (0, 1, T // 2, T - 1):
+        assert torch.equal(y[t:t + 1], ops.int8_moe(x[t:t + 1], e[t:t + 1], w[t:t + 1], *gpu)), t
+
+
 @pytest.mark.parametrize("T", [1, 6, 90])
 def test_moe_of_left_out_choices_empty_experts_and_spoilt_tokens(T):
     g, H, I, E, k = rng(14, T), 144, 80, 9, 3

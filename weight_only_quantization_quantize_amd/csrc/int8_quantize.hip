@@ -1,8 +1,8 @@
 // Rows to 8-bit integers with a scale each (int8_device.h): y = x, x s or x / s of the
 // channel scales s, rounded to fp32; scale = max|y| / 127; codes.
 //
-// Bound by reading x and writing the codes: 28672 x 8192 fp16 with folded scales 156 us, 4.5
-// TB/s, where a copy makes 5.1 (192 us with the rounding's steps one by one; int8_device.h).
+// Bound by reading x and writing the codes: 28672 x 8192 fp16 with folded scales 156 .. 162 us,
+// 4.4 TB/s, where a copy makes 5.1 (192 us with the rounding's steps one by one; int8_device.h).
 //
 // A row stays in the registers of its W waves
 // between the search for its largest magnitude and the rounding (8 elements a lane and

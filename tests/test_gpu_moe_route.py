@@ -1,0 +1,69 @@
+"""GPU parity of the routing to experts where its numbers cancel or lie far from 1.
+
+Tolerances: choices equal; weights and gradients are computed in 64 bits and rounded once,
+1 % more for the 64-bit functions.  Inputs are such that nothing cancels but what the kernel
+has to keep from cancelling, unless a bound says otherwise.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8_oracle as O
+from tests.test_gpu_int8 import BF16, F16, F32, HALF, TINY, U, check_route, close, host, raw, rng, tensor
+from weight_only_quantization_quantize_amd import ops
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Groups whose two best keys nearly cancel
+# ---------------------------------------------------------------------------
+def opposite(seed, scoring, E, groups, T, size):
+    """Logits [T, E] and a bias that raises one expert of each group and lowers another one by as much, by another value for
+    each group, and the rest of it by more: the groups' sums of two keys are of the order of the scores, and all keys are far
+    from each other.  Only tokens whose sums are further apart than 64 bits round them (2^-52 of the size in all) are kept."""
+    g, per = rng(31, seed, E, int(size)), E // groups
+    x = g.normal(size=(T, E)).astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    for i in range(groups):
+        at, far = per * i + g.permutation(per), np.float32(size * (1 + i / groups))
+        bias[at[0]], bias[at[1]] = far, -far
+        bias[at[2:]] = -size * (3 + np.arange(per - 2) + i / groups)
+    key = O.scores(x, scoring) + bias.astype(np.float64)
+    two = np.sort(key.reshape(T, groups, per), 2)[:, :, -2:].sum(2)
+    x = x[(np.diff(np.sort(two, 1)) > 2.0 ** -50 * size).all(1)]
+    assert len(x) > T // 2
+    return x, bias
+
+
+@pytest.mark.parametrize("size", [300, 10 ** 4, 10 ** 5, 10 ** 6])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(32, 8), (64, 4), (256, 8), (512, 16)])
+def test_groups_of_opposite_biases(E, groups, scoring, size):
+    x, bias = opposite(1, scoring, E, groups, 1500, size)
+    check_route(tensor(x), 2, f"{scoring} {E} {size}", bias, scoring=scoring, groups=groups, top_groups=groups // 2, group_top=2)
+
+
+def test_groups_of_one_opposite_pair():
+    """Sums of 1.017362 and 1.017373: the second group, by 11e-6 beside two keys of 1000 and -999."""
+    x = np.zeros((1, 16), np.float32)
+    x[0, [0, 1, 8, 9]] = [-0.08407006, 0.15377067, 0.2157111, -0.14564292]
+    bias = -5000 - 100 * np.arange(16, dtype=np.float32)
+    bias[[0, 1, 8, 9]] = 1000, -1000, 0, 0
+    e = check_route(tensor(x), 1, "one pair", bias, scoring="sigmoid", groups=2, top_groups=1, group_top=2)
+    assert raw(e).tolist() == [[8]]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("low", [-1e9, -3e38, -np.inf, 3e38])
+def test_groups_of_extreme_biases(scoring, low):
+    """Experts held back by the type's lowest values, groups of nothing else among them; sums of two that 32 bits cannot hold."""
+    g, E, groups = rng(32), 64, 8
+    x = g.normal(size=(40, E)).astype(np.float32)
+    bias = (0.1 * g.normal(size=E)).astype(np.float32)
+    bias[:16] = low
+    bias[17:24] = low
+    bias[30] = bias[33] = low
+    x[5, 40:48] = -np.inf
+    for top in (1, 2):
+        check_route(tensor(x), 6, f"{scoring} {low}", bias, scoring=scoring, groups=groups, top_groups=4, group_top=top)

@@ -369,15 +369,21 @@ __device__ __forceinline__ bool route_row(const void* __restrict__ logits, int64
       best = fmaxf(best, b);
     }
     const float rank = r.group_top > 1 ? best + next : best;
+    // By how much the rank may be off: its scores' errors, and each key's and the sum's rounding, 2^-24 of the keys and not of
+    // what is left of them where they cancel.  A best logit is exact, and so is -infinity of masked experts.
+    const float size = r.group_top > 1 ? fabsf(best) + fabsf(next) : fabsf(best);
+    const bool exact = !scored || is_masked(r.group_top > 1 ? next : best);
+    const float off = exact ? 0.0f : kClose + 0x1p-22f * size;
     int before = 0;
 #pragma unroll
     for (int n = 1; n < kRow; ++n) before += row_rotated(rank, n) > rank ? 1 : 0;
     bool kept = before < r.top_groups * lanes;
-    const float last = -row_all(kept ? -rank : -inf, larger), first = row_all(kept ? -inf : rank, larger);
-    // (a best logit is exact, but equal ones are not told apart here)
-    const float close = scored ? 2.0f * kClose * (1.0f + fabsf(last)) : 0.0f;
+    // (sums past 32 bits' range are infinite, and so is what they may be off by: never told apart)
+    const float high = off < inf ? rank + off : inf, low = off < inf ? rank - off : -inf;
+    const float last = -row_all(kept ? -low : -inf, larger), first = row_all(kept ? -inf : high, larger);
+    // (equal ranks are not told apart here)
     const int keeps = row_all(kept ? 1 : 0, [](int a, int b) { return a + b; });
-    const bool told = r.top_groups == r.groups || (last - first > close && keeps == r.top_groups * lanes);
+    const bool told = r.top_groups == r.groups || (last > first && keeps == r.top_groups * lanes);
     if (__any(!told)) {  // the groups' sums in 64 bits
       const double total = scored && !r.sigmoid ? softmax_sum(x, max) : 1.0;
       double best = -inf, next = -inf;

@@ -380,9 +380,10 @@ woq_status woq_int8_quantize(const void* x, int32_t xdtype, const float* act_sca
                              int64_t K, void* codes, float* scales, void* stream);
 
 /* Y[m, n] = (acc a_scales[m]) scales[n] + bias[n], acc = sum_k a[m, k] w[n, k]
- * over the codes of a [M, K] and w [N, K], exact; fp32 from there, Y [M, N] of
- * ydtype (WOQ_F16, WOQ_BF16 or WOQ_F32) rounded once.
- *   bias : fp32 [N] or NULL. */
+ * over the codes of a [M, K] and w [N, K], exact; fp32 from there (the second
+ * product and the sum are one fma), Y [M, N] of ydtype (WOQ_F16, WOQ_BF16 or
+ * WOQ_F32) rounded once.  A row's bits do not depend on the other rows.
+ *   bias : fp32 [N] or NULL (0). */
 woq_status woq_int8_gemm(const void* a_codes, const float* a_scales, const void* codes, const float* scales,
                          const float* bias, int64_t M, int64_t N, int64_t K, int32_t ydtype, void* Y, void* stream);
 

@@ -1,8 +1,9 @@
 // Products of two 8-bit integer matrices with a scale for each row of either:
 //   Y[m, n] = (acc sa[m]) sw[n] + bias[n],  acc = sum_k a[m, k] w[n, k]
-// The sums are exact (int8_tile.h, which says what bounds them); the scales multiply in fp32,
-// Y is rounded once.  Up to four rows go to the kernel that streams the weights past them
-// (int8_gemv.hip).
+// The sums are exact (int8_tile.h, which says what bounds them); the first scale multiplies in
+// fp32, the second one and the bias (0 where there is none) in one fma, here and in
+// int8_gemv.hip, so that an element has the same bits whichever kernel takes it; Y is rounded
+// once.  Up to four rows go to the kernel that streams the weights past them (int8_gemv.hip).
 #include "int8_tile.h"
 #include "woq_internal.h"
 
@@ -58,7 +59,7 @@ __global__ __launch_bounds__(C::kThreads, C::kOccupancy) void int8_gemm_kernel(
         const float4_t t = *reinterpret_cast<const float4_t*>(cols + kCols + 8 * b + 4 * half);
         float4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][b / 4][4 * (b % 4) + e] * f * s[e] + t[e];
+        for (int e = 0; e < 4; ++e) v[e] = fmaf((float)acc[i][b / 4][4 * (b % 4) + e] * f, s[e], t[e]);
         return v;
       });
     }

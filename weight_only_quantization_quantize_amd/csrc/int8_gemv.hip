@@ -92,8 +92,7 @@ __global__ __launch_bounds__(kWaves * 64) void int8_gemv_kernel(const void* __re
 #pragma unroll
     for (int m = 0; m < MR; ++m) scales[m] = scale[m];
   auto store = [&](int m, int n, int sum, float by) {
-    float v = (float)sum * by * sw[n];
-    if (bias) v += bias[n];
+    const float v = fmaf((float)sum * by, sw[n], bias ? bias[n] : 0.0f);  // as the tiles do (int8_gemm.hip)
     if (m < M) y[(int64_t)m * N + n] = Int8Out<YT>::of(v);
   };
   const int batches = (N + stride * kSteps - 1) / (stride * kSteps);

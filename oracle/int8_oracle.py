@@ -128,8 +128,9 @@ def route_backward(x, experts, dweights, scoring="softmax", renormalize=True, sc
                 dense[e] += v
             out[t] = s * (dense - (dense * s).sum())
         else:
+            rest = scores(-x[t:t + 1], scoring)[0]  # 1 - s, which would cancel next to 1
             for v, (_, e) in zip(ds, ids):
-                out[t, e] += v * s[e] * (1 - s[e])
+                out[t, e] += v * s[e] * rest[e]
     return out
 
 

@@ -67,3 +67,26 @@ def test_groups_of_extreme_biases(scoring, low):
     x[5, 40:48] = -np.inf
     for top in (1, 2):
         check_route(tensor(x), 6, f"{scoring} {low}", bias, scoring=scoring, groups=groups, top_groups=4, group_top=top)
+
+
+# ---------------------------------------------------------------------------
+# Gradients of logits far from 0
+# ---------------------------------------------------------------------------
+def check_backward(x, e, d, scoring, renormalize, label):
+    got = ops.moe_route_backward(x, tensor(e, torch.int32), tensor(d), scoring, renormalize, 1.5)
+    ref = O.route_backward(host(x), e, host(tensor(d)), scoring, renormalize, 1.5)
+    close(host(got), ref, 1.01 * HALF[x.dtype] * np.abs(ref) + TINY[x.dtype], label)
+
+
+@pytest.mark.parametrize("E", [8, 100, 512])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_gradient_of_far_sigmoid_logits(E, renormalize, dtype):
+    """Scores of 1 - 2^-36 .. 1 - 2^-115 and their counterparts: s (1 - s) is the larger one's distance from 1."""
+    g, T, k = rng(33, E), 24, 4
+    sign = 1.0 if renormalize else np.where(g.random((T, 1)) < 0.3, -1.0, 1.0)
+    x = tensor(g.uniform(25, 80, (T, E)) * sign, dtype)
+    e = np.stack([g.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    # renormalised weights are 1/4 each: the values are 0.6 or more of their size away from their mean
+    d = (np.array([[1.0, -2.0, 4.0, -8.0]]) * (1 + g.random((T, 1)))).astype(np.float32)
+    check_backward(x, e, d, "sigmoid", renormalize, f"{E} experts")

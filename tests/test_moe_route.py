@@ -1,0 +1,53 @@
+"""The oracle's gradient of a routing against 60 decimal digits, where its terms cancel or lie far from 1."""
+from decimal import Decimal, getcontext
+
+import numpy as np
+import pytest
+
+from oracle import int8_oracle as O
+
+getcontext().prec = 60
+
+
+def sigmoid(x):
+    return 1 / (1 + (-Decimal(float(x))).exp())
+
+
+def gradient(x, ids, d, scoring, renormalize, scale):
+    """Of one token, as sums over pairs; 60 digits leave what cancels."""
+    x, d, scale = [Decimal(float(v)) for v in x], [Decimal(float(v)) for v in d], Decimal(float(scale))
+    if scoring == "sigmoid":
+        s = [sigmoid(v) for v in x]
+        ds = [v * (1 - v) for v in s]
+    else:
+        top = max(x)
+        e = [(v - top).exp() for v in x]
+        s = [v / sum(e) for v in e]
+    total = sum(s[i] for i in ids)
+    out = []
+    for i in range(len(x)):
+        v = Decimal(0)
+        for c, j in enumerate(ids):  # dw_c / dx_i
+            if scoring == "sigmoid":
+                if renormalize:
+                    v += d[c] * ds[i] * ((j == i) * total - ids.count(i) * s[j]) / total ** 2
+                else:
+                    v += d[c] * ds[i] * (j == i)
+            elif renormalize:
+                v += d[c] * s[j] / total * ((j == i) - ids.count(i) * s[i] / total)
+            else:
+                v += d[c] * s[j] * ((j == i) - s[i])
+        out.append(float(scale * v))
+    return np.array(out)
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_oracle_gradient_of_far_sigmoid_logits(renormalize):
+    """Within a few 2^-53 of every sum's terms; values 0.6 or more of their size away from their mean."""
+    g = np.random.default_rng(51)
+    x = g.uniform(25, 80, (6, 9)) * (1.0 if renormalize else np.where(np.arange(6)[:, None] < 2, -1.0, 1.0))
+    e = np.stack([g.permutation(9)[:4] for _ in range(6)])
+    d = np.array([[1.0, -2.0, 4.0, -8.0]]) * (1 + g.random((6, 1)))
+    got = O.route_backward(x, e, d, "sigmoid", renormalize, 1.5)
+    for t in range(6):
+        np.testing.assert_allclose(got[t], gradient(x[t], e[t].tolist(), d[t], "sigmoid", renormalize, 1.5), rtol=1e-13, atol=0)

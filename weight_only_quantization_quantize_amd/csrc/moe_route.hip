@@ -504,7 +504,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_wide_kernel(const void*
 // dx[e] from dw: through w = scale s or scale s / (sum of the chosen s), and s.
 //   softmax, renormalised: dx_c = scale p_c (dw_c - sum p dw), p = the weights over scale
 //   softmax              : dx_e = s_e (scale dw_e - sum over the chosen of scale s dw)
-//   sigmoid              : dx_c = ds_c s_c (1 - s_c), ds_c = scale dw_c, renormalised
+//   sigmoid              : dx_c = ds_c s(x_c) s(-x_c), ds_c = scale dw_c, renormalised
 //                          scale (dw_c - sum p dw) / (sum of s)
 // Lane c works the chosen expert c out; then every expert adds up what names it.
 template <class XT, int NJ>
@@ -547,12 +547,12 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const v
   } else if (!sigmoid) {
     d = p * (dw - dot);
   } else {
-    const double score = used ? sigmoid64(xc) : 0.0;
+    const double score = used ? sigmoid64(xc) : 0.0, rest = used ? sigmoid64(-xc) : 0.0;  // 1 - s, which would cancel next to 1
     if (renormalize) {
       const double total = wave_sum(score);
-      d = total == 0.0 ? 0.0 : (dw - dot) / total * score * (1.0 - score);
+      d = total == 0.0 ? 0.0 : (dw - dot) / total * score * rest;
     } else {
-      d = dw * score * (1.0 - score);
+      d = dw * score * rest;
     }
   }
   double dx[NJ] = {};

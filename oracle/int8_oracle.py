@@ -111,26 +111,17 @@ def route_backward(x, experts, dweights, scoring="softmax", renormalize=True, sc
     for t in range(x.shape[0]):
         ids = [(c, e) for c, e in enumerate(experts[t]) if 0 <= e < x.shape[1]]
         s = scores(x[t:t + 1], scoring)[0]
-        if renormalize:
+        rest = scores(-x[t:t + 1], scoring)[0] if scoring == "sigmoid" else np.ones_like(s)  # 1 - s, which would cancel next to 1
+        if renormalize:  # (dw - dot) / total s, the last two of them the weight, times ds / s
             w = _weights(x[t], s, [e for _, e in ids], scoring, True, 1.0)
             dot = sum(wc * d[t, c] for wc, (c, _) in zip(w, ids))
-            if scoring == "softmax":
-                for wc, (c, e) in zip(w, ids):
-                    out[t, e] += scale * wc * (d[t, c] - dot)
-                continue
-            total = sum(s[e] for _, e in ids)
-            ds = [0.0 if total == 0 else scale * (d[t, c] - dot) / total for c, _ in ids]
-        else:
-            ds = [scale * d[t, c] for c, _ in ids]
-        if scoring == "softmax":
-            dense = np.zeros_like(s)
-            for v, (_, e) in zip(ds, ids):
-                dense[e] += v
-            out[t] = s * (dense - (dense * s).sum())
-        else:
-            rest = scores(-x[t:t + 1], scoring)[0]  # 1 - s, which would cancel next to 1
-            for v, (_, e) in zip(ds, ids):
-                out[t, e] += v * s[e] * rest[e]
+            for wc, (c, e) in zip(w, ids):
+                out[t, e] += scale * wc * (d[t, c] - dot) * rest[e]
+            continue
+        dense = np.zeros_like(s)
+        for c, e in ids:
+            dense[e] += scale * d[t, c]
+        out[t] = s * (dense - (dense * s).sum()) if scoring == "softmax" else dense * s * rest
     return out
 
 

@@ -90,3 +90,13 @@ def test_gradient_of_far_sigmoid_logits(E, renormalize, dtype):
     # renormalised weights are 1/4 each: the values are 0.6 or more of their size away from their mean
     d = (np.array([[1.0, -2.0, 4.0, -8.0]]) * (1 + g.random((T, 1)))).astype(np.float32)
     check_backward(x, e, d, "sigmoid", renormalize, f"{E} experts")
+
+
+def test_gradient_of_the_smallest_sigmoid_scores():
+    """Scores of 10^-304 .. 10^-299 and values of 10^20: their quotients are past 64 bits' range, the gradient is not."""
+    g, T, k = rng(36), 20, 4
+    x, e = g.uniform(-700, -690, (T, 40)), np.stack([g.permutation(40)[:k] for _ in range(T)]).astype(np.int32)
+    x[np.arange(T)[:, None], e] = g.uniform(-696, -695, (T, k))  # weights of 0.1 .. 0.5
+    d = (np.array([[1e20, -2e20, 4e20, -8e20]]) * (1 + g.random((T, 1)))).astype(np.float32)
+    for dtype in (F32, BF16):
+        check_backward(tensor(x, dtype), e, d, "sigmoid", True, "smallest scores")

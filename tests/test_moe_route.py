@@ -51,3 +51,11 @@ def test_oracle_gradient_of_far_sigmoid_logits(renormalize):
     got = O.route_backward(x, e, d, "sigmoid", renormalize, 1.5)
     for t in range(6):
         np.testing.assert_allclose(got[t], gradient(x[t], e[t].tolist(), d[t], "sigmoid", renormalize, 1.5), rtol=1e-13, atol=0)
+
+
+def test_oracle_gradient_of_the_smallest_sigmoid_scores():
+    g = np.random.default_rng(52)
+    x, d = g.uniform(-696, -695, 5), np.array([1e20, -2e20, 4e20, -8e20])
+    got = O.route_backward(x[None], np.array([[0, 2, 3, 4]]), d[None], "sigmoid", True, 1.5)
+    # (the exponential of a number of this size is off by 2^-53 of it, relative)
+    np.testing.assert_allclose(got[0], gradient(x, [0, 2, 3, 4], d, "sigmoid", True, 1.5), rtol=1e-12, atol=0)

@@ -504,8 +504,8 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_wide_kernel(const void*
 // dx[e] from dw: through w = scale s or scale s / (sum of the chosen s), and s.
 //   softmax, renormalised: dx_c = scale p_c (dw_c - sum p dw), p = the weights over scale
 //   softmax              : dx_e = s_e (scale dw_e - sum over the chosen of scale s dw)
-//   sigmoid              : dx_c = ds_c s(x_c) s(-x_c), ds_c = scale dw_c, renormalised
-//                          scale (dw_c - sum p dw) / (sum of s)
+//   sigmoid              : dx_c = scale dw_c s(x_c) s(-x_c), renormalised
+//                          scale p_c (dw_c - sum p dw) s(-x_c)
 // Lane c works the chosen expert c out; then every expert adds up what names it.
 template <class XT, int NJ>
 __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const void* __restrict__ logits,
@@ -547,13 +547,7 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const v
   } else if (!sigmoid) {
     d = p * (dw - dot);
   } else {
-    const double score = used ? sigmoid64(xc) : 0.0, rest = used ? sigmoid64(-xc) : 0.0;  // 1 - s, which would cancel next to 1
-    if (renormalize) {
-      const double total = wave_sum(score);
-      d = total == 0.0 ? 0.0 : (dw - dot) / total * score * rest;
-    } else {
-      d = dw * score * rest;
-    }
+    d = p * (renormalize ? dw - dot : dw) * sigmoid64(-xc);  // 1 - s would cancel next to 1
   }
   double dx[NJ] = {};
   for (int c = 0; c < top_k; ++c) {

@@ -112,16 +112,16 @@ def route_backward(x, experts, dweights, scoring="softmax", renormalize=True, sc
         ids = [(c, e) for c, e in enumerate(experts[t]) if 0 <= e < x.shape[1]]
         s = scores(x[t:t + 1], scoring)[0]
         rest = scores(-x[t:t + 1], scoring)[0] if scoring == "sigmoid" else np.ones_like(s)  # 1 - s, which would cancel next to 1
-        if renormalize:  # (dw - dot) / total s, the last two of them the weight, times ds / s
+        # dw_c - sum p dw as sum p_j (dw_c - dw_j) (the p add up to 1): next to a weight of nearly 1 the former would cancel
+        if renormalize:  # by total, with s the weight, times ds / s
             w = _weights(x[t], s, [e for _, e in ids], scoring, True, 1.0)
-            dot = sum(wc * d[t, c] for wc, (c, _) in zip(w, ids))
             for wc, (c, e) in zip(w, ids):
-                out[t, e] += scale * wc * (d[t, c] - dot) * rest[e]
+                out[t, e] += scale * wc * sum(wj * (d[t, c] - d[t, j]) for wj, (j, _) in zip(w, ids)) * rest[e]
             continue
         dense = np.zeros_like(s)
         for c, e in ids:
             dense[e] += scale * d[t, c]
-        out[t] = s * (dense - (dense * s).sum()) if scoring == "softmax" else dense * s * rest
+        out[t] = s * ((dense[:, None] - dense) @ s) if scoring == "softmax" else dense * s * rest
     return out
 
 

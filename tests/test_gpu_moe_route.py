@@ -100,3 +100,30 @@ def test_gradient_of_the_smallest_sigmoid_scores():
     d = (np.array([[1e20, -2e20, 4e20, -8e20]]) * (1 + g.random((T, 1)))).astype(np.float32)
     for dtype in (F32, BF16):
         check_backward(tensor(x, dtype), e, d, "sigmoid", True, "smallest scores")
+
+
+@pytest.mark.parametrize("E", [8, 100, 512])
+@pytest.mark.parametrize("scoring,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_gradient_beside_a_weight_of_nearly_one(E, scoring, renormalize, dtype):
+    """One expert's logit 25 .. 60 above all others: its own gradient is the sum of the others' shares, 2^-36 .. 2^-86 of the
+    values.  Its value is the largest, and all are positive, so that no sum of shares cancels."""
+    g, T, k = rng(34, E), 30, 5
+    x = -g.uniform(25, 60, (T, E))
+    e = np.stack([g.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    place = g.integers(0, k, T)
+    x[np.arange(T), e[np.arange(T), place]] = g.normal(size=T)
+    d = g.uniform(0.1, 1.0, (T, k)).astype(np.float32)
+    d[np.arange(T), place] = 2.0
+    e[3, place[3]] = -1  # the large one is kept elsewhere
+    e[4] = np.where(np.arange(k) == place[4], e[4], -1)  # nothing but the large one
+    check_backward(tensor(x, dtype), e, d, scoring, renormalize, f"{scoring} {E}")
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_equal_values_have_no_gradient(scoring):
+    """The renormalised weights add up to 1."""
+    g = rng(35)
+    x, e = tensor(g.normal(size=(50, 40))), np.stack([g.permutation(40)[:7] for _ in range(50)]).astype(np.int32)
+    d = tensor(np.repeat(g.normal(size=(50, 1)), 7, 1).astype(np.float32))
+    assert not ops.moe_route_backward(x, tensor(e, torch.int32), d, scoring).any()

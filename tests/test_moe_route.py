@@ -59,3 +59,14 @@ def test_oracle_gradient_of_the_smallest_sigmoid_scores():
     got = O.route_backward(x[None], np.array([[0, 2, 3, 4]]), d[None], "sigmoid", True, 1.5)
     # (the exponential of a number of this size is off by 2^-53 of it, relative)
     np.testing.assert_allclose(got[0], gradient(x, [0, 2, 3, 4], d, "sigmoid", True, 1.5), rtol=1e-12, atol=0)
+
+
+@pytest.mark.parametrize("scoring,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_oracle_gradient_beside_a_weight_of_nearly_one(scoring, renormalize):
+    """One logit 25 .. 60 above all others, with the largest of the positive values: no sum of shares cancels."""
+    g = np.random.default_rng(53)
+    for t in range(6):
+        x, ids, d = -g.uniform(25, 60, 12), g.permutation(12)[:5], g.uniform(0.1, 1.0, 5)
+        x[ids[t % 5]], d[t % 5] = g.normal(), 2.0
+        got = O.route_backward(x[None], ids[None], d[None], scoring, renormalize, 1.5)
+        np.testing.assert_allclose(got[0], gradient(x, ids.tolist(), d, scoring, renormalize, 1.5), rtol=1e-13, atol=0)

@@ -62,16 +62,16 @@ __device__ inline bool is_masked(float x) { return x == -__builtin_inff(); }
 __device__ inline double sigmoid64(float x) { return 1.0 / (1.0 + exp(-(double)x)); }
 
 // The weights of the chosen experts' logits, lane c of TEAM lanes holding the c-th (used: c <
-// top_k); max, sum: of the row, as softmax without renormalisation needs them.
+// top_k); max, sum: of the row, as softmax without renormalisation needs them, or, where given
+// says so, max of the chosen ones.
 template <int TEAM = 64>
-__device__ inline double weight_of(float x, bool used, bool sigmoid, bool renormalize, float max, double sum) {
+__device__ inline double weight_of(float x, bool used, bool sigmoid, bool renormalize, float max, double sum, bool given = false) {
   double s = 0.0;
   if (sigmoid) {
     if (used) s = sigmoid64(x);
   } else {
     if (renormalize) {  // the row's sum cancels
-      max = used ? x : -__builtin_inff();
-      max = team_max(max, TEAM);
+      if (!given) max = team_max(used ? x : -__builtin_inff(), TEAM);
       max = is_masked(max) ? 0.0f : max;
     }
     if (used) s = exp((double)x - (double)max);
@@ -506,6 +506,9 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_wide_kernel(const void*
 //   softmax              : dx_e = s_e (scale dw_e - sum over the chosen of scale s dw)
 //   sigmoid              : dx_c = scale dw_c s(x_c) s(-x_c), renormalised
 //                          scale p_c (dw_c - sum p dw) s(-x_c)
+// The differences dw_c - sum p dw (the p add up to 1) are taken with every dw as its distance
+// from the largest logit's: where that one's p is nearly 1, its own difference is the sum of the
+// others' small shares, and dw less a sum of nearly as much would leave nothing of it.
 // Lane c works the chosen expert c out; then every expert adds up what names it.
 template <class XT, int NJ>
 __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const void* __restrict__ logits,
@@ -539,15 +542,16 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const v
     }
     sum = wave_sum(sum);
   }
-  const double p = weight_of(xc, used, sigmoid, renormalize, max, sum);
-  const double dot = wave_sum(used ? p * dw : 0.0);
-  double d;  // of the lane's chosen expert
-  if (all) {
-    d = dw;
-  } else if (!sigmoid) {
-    d = p * (dw - dot);
-  } else {
-    d = p * (renormalize ? dw - dot : dw) * sigmoid64(-xc);  // 1 - s would cancel next to 1
+  double d = dw;  // of the lane's chosen expert
+  if (!all) {
+    const float top = renormalize ? team_max(xc, 64) : 0.0f;
+    const double p = weight_of(xc, used, sigmoid, renormalize, top, sum, true);
+    if (renormalize) {
+      const uint64_t at = __ballot(used && xc == top);
+      const double from = dw - (at ? __shfl(dw, __builtin_ctzll(at), 64) : 0.0);
+      d = from - wave_sum(used ? p * from : 0.0);
+    }
+    d *= sigmoid ? p * sigmoid64(-xc) : p;  // 1 - s would cancel next to 1
   }
   double dx[NJ] = {};
   for (int c = 0; c < top_k; ++c) {
@@ -556,10 +560,26 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const v
 #pragma unroll
     for (int j = 0; j < NJ; ++j) dx[j] += e == 64 * j + lane ? v : 0.0;
   }
+  if (all) {
+    double base = 0.0, dot = 0.0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const uint64_t at = __ballot(x[j] == max);
+      if (at && !found) base = __shfl(dx[j], __builtin_ctzll(at), 64), found = true;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      dx[j] -= base;
+      dot += s[j] * dx[j];
+    }
+    dot = sum == 0.0 ? 0.0 : wave_sum(dot) / sum;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) dx[j] = sum == 0.0 ? 0.0 : s[j] / sum * (dx[j] - dot);
+  }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int e = 64 * j + lane;
-    if (all) dx[j] = sum == 0.0 ? 0.0 : s[j] / sum * (dx[j] - dot);
     if (e < E) dlogits[t * E + e] = Int8Out<XT>::of((float)dx[j]);
   }
 }

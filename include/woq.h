@@ -438,10 +438,11 @@ woq_status woq_moe_route_backward(const void* logits, int32_t dtype, const int32
  *   [T, top_k] (woq_moe_route); up codes [E, 2 I, H], scales [E, 2 I] (rows 0 .. I-1
  *   gate, I .. 2I-1 up), down codes [E, H, I], scales [E, H]; H and I multiples of 16.
  * A choice outside 0 .. E - 1 (an expert kept elsewhere) takes no part; a token
- * without any has a row of zeros.  Products are exact sums times the two scales,
- * as above; the choices are added in their order in fp32, Y is rounded once.  The
- * same inputs give the same bits, whatever the other tokens are.  workspace as
- * above. */
+ * without any has a row of zeros; choices elsewhere count in the workspace and in
+ * the choice of kernels all the same.  T H and 2 I H stay below 2^32, T top_k at
+ * most 2^28.  Products are exact sums times the two scales, as above; the choices
+ * are added in their order in fp32, Y is rounded once.  The same inputs give the
+ * same bits, whatever the other tokens are.  workspace as above. */
 size_t woq_int8_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int32_t top_k);
 woq_status woq_int8_moe(const void* X, int32_t xdtype, const int32_t* experts, const float* weights,
                         const void* up_codes, const float* up_scales, const void* down_codes, const float* down_scales,

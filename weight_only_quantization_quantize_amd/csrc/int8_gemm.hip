@@ -3,7 +3,8 @@
 // The sums are exact (int8_tile.h, which says what bounds them); the first scale multiplies in
 // fp32, the second one and the bias (0 where there is none) in one fma, here and in
 // int8_gemv.hip, so that an element has the same bits whichever kernel takes it; Y is rounded
-// once.  Up to four rows go to the kernel that streams the weights past them (int8_gemv.hip).
+// once.  Few rows go to the kernel that streams the weights past them (int8_gemv.hip): up to
+// four with K <= 8192, one with K <= 32768.
 #include "int8_tile.h"
 #include "woq_internal.h"
 

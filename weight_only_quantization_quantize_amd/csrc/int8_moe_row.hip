@@ -6,7 +6,7 @@
 //         elements of them, and takes columns of y: a row of every choice's expert
 // The results are the tile path's to the last bit: exact sums, the same fp32 steps.
 // bf16, H = 4096, I = 2048, 4 of 32 experts (101 MB): 23 .. 25 us (up 13 .. 15, 67 MB; down
-// 9, 34 MB); the six launches of the tile path 46.
+// 9, 34 MB); the five launches of the tile path 43 .. 44.
 #include "int8_row.h"
 #include "woq_internal.h"
 

@@ -7,7 +7,8 @@
 //   w = scale s, over the sum of the chosen experts' s where that is asked for
 //
 // Bound by vector instructions: a logit is 2 or 4 bytes, its score and its part in the
-// choice some dozens of instructions.  So the usual routing (route_row) has four tokens a
+// choice 85 instructions (16384 tokens of 256 experts, 8 groups, a bias: 1370 a wave of 1024
+// logits, four waves a SIMD, which issue one 60% of the time; 20.5 us).  So the usual routing (route_row) has four tokens a
 // wave, 16 lanes each, neighbouring experts in a lane, and decides in 32 bits what they decide:
 //   scores p = 1 / (1 + 2^(-x log2 e)) are off by at most 2^-21, 2^((x - max) log2 e) / sum
 //   by 2^-19, s + b by 2^-24 of itself more;
@@ -510,6 +511,9 @@ __global__ __launch_bounds__(kWaves * 64) void moe_route_wide_kernel(const void*
 // from the largest logit's: where that one's p is nearly 1, its own difference is the sum of the
 // others' small shares, and dw less a sum of nearly as much would leave nothing of it.
 // Lane c works the chosen expert c out; then every expert adds up what names it.
+// Bound by instructions, not by bytes: 8192 tokens of 64 experts, 6 of them, fp32 (4.8 MB, a
+// microsecond) take 6.9 us (softmax; 230 vector instructions and 50 between lanes a token,
+// which is a wave's), renormalised 6.7 (sigmoid 7.0).
 template <class XT, int NJ>
 __global__ __launch_bounds__(kWaves * 64) void moe_route_backward_kernel(const void* __restrict__ logits,
                                                                          const int32_t* __restrict__ experts,
